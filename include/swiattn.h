@@ -54,7 +54,9 @@ typedef enum {
     SWIATTN_ETIMEOUT = 4       /* a device-side bounded wait expired (from get_device_error) */
 } swiattn_status;
 
-typedef enum { SWIATTN_F32 = 0, SWIATTN_BF16 = 1 } swiattn_dtype;
+/* SWIATTN_E4M3: 8-bit cache pages (swiattn_append_paged, swiattn_decode_paged_e4m3),
+ * never the dtype of a call's q, k, v or o. */
+typedef enum { SWIATTN_F32 = 0, SWIATTN_BF16 = 1, SWIATTN_E4M3 = 2 } swiattn_dtype;
 
 /* Router GEMV and hard gate (report section 2, router design; one scalar per
  * token per layer, shared by every head):
@@ -316,6 +318,85 @@ int swiattn_route_backward(const void* h, const void* w, const float* logits, co
                            float* d_logits, void* dh, float* dw, float* db, void* workspace,
                            size_t workspace_bytes, void* stream);
 
+/* Rotary position encoding of q and k, for the calls above, whose q and k
+ * arrive position-encoded (the report's section 2 trains with rotary positions
+ * scaled for long contexts).  With w_f = inv_freq[f] (fp64, radians a
+ * position, f < rot_dim/2) and p a token's position, the pair (x_a, x_b) of a
+ * head's dimensions becomes
+ *   x_a' = factor * (x_a cos(p w_f) - x_b sin(p w_f)),
+ *   x_b' = factor * (x_b cos(p w_f) + x_a sin(p w_f)),
+ * with (a, b) = (f, f + rot_dim/2), or (2f, 2f+1) when interleaved != 0;
+ * dimensions rot_dim .. d-1 are copied.  Any scaling of the frequencies is in
+ * inv_freq, that of their amplitude in factor (1: none; finite).  Angles are
+ * reduced exactly: far positions cost no precision.
+ * q [B,N,Hq,d], k [B,N,Hkv,d] of `dtype`; positions int32 [B,N], any sign
+ * (NULL: 0..N-1 in every sequence).  Token t = b*N + i of q starts at element
+ * t * q_stride, and likewise for k, q_out, k_out, so views of a fused
+ * projection serve; a stride is at least heads * d and a multiple of 16 bytes.
+ * q_out may be q itself with the same stride (in place), k_out k; they must
+ * not overlap the inputs otherwise.  q and q_out may both be NULL (Hq is then
+ * ignored), or k and k_out (Hkv ignored), not both pairs.  Hq and Hkv need not
+ * divide one another.
+ * d in {64, 128}; rot_dim a multiple of 16 in [16, d]; B*N < 2^31. */
+int swiattn_rope(const void* q, const void* k, const int32_t* positions, const double* inv_freq,
+                 void* q_out, void* k_out, int B, int N, int Hq, int Hkv, int d, int rot_dim,
+                 int interleaved, float factor, int64_t q_stride, int64_t k_stride,
+                 int64_t q_out_stride, int64_t k_out_stride, int dtype, void* stream);
+
+/* Gradient of swiattn_rope: given dq_rot = dLoss/dq_out and dk_rot =
+ * dLoss/dk_out (what swiattn_prefill_backward returns for rotated q, k),
+ * dq = dLoss/dq and dk = dLoss/dk, each pair by the transposed map
+ *   dx_a = factor * (dx_a' cos + dx_b' sin),  dx_b = factor * (dx_b' cos - dx_a' sin).
+ * The map is linear, so nothing of the forward is needed but its arguments.
+ * Arguments as for swiattn_rope. */
+int swiattn_rope_backward(const void* dq_rot, const void* dk_rot, const int32_t* positions,
+                          const double* inv_freq, void* dq, void* dk, int B, int N, int Hq,
+                          int Hkv, int d, int rot_dim, int interleaved, float factor,
+                          int64_t q_stride, int64_t k_stride, int64_t q_out_stride,
+                          int64_t k_out_stride, int dtype, void* stream);
+
+/* Appends new tokens' keys and values to a paged cache, rotating q and k on
+ * the way (swiattn_rope's map), for a prompt, a chunk of one, or a decode
+ * step.  The cache is that of swiattn_decode_paged.
+ *  - T new tokens, packed: sequence b owns tokens [starts[b], starts[b+1])
+ *    (int32 [B+1], non-decreasing, starts[0] >= 0, starts[B] <= T), the last
+ *    of its seq_lens[b] tokens: token t sits at position
+ *    seq_lens[b] - (starts[b+1] - t).  seq_lens (int32 [B]) counts the new
+ *    tokens, so the same array goes to the decode call after this one.
+ *    starts == NULL: one token for each sequence (T == B), a decode step.
+ *  - q [T,Hq,d], k, v [T,Hkv,d] of `dtype`, tokens q_stride, k_stride and
+ *    v_stride elements apart (as swiattn_rope).  q_out [T,Hq,d], contiguous,
+ *    receives the rotated q, and must not overlap q unless it is q itself,
+ *    contiguous; q and q_out may both be NULL (Hq ignored).
+ *  - rot_dim 0: no rotation (q is copied, inv_freq may be NULL, interleaved and
+ *    factor are ignored), e.g. for keys that swiattn_rope rotated for the
+ *    prefill.  Otherwise rot_dim, interleaved, inv_freq and factor as there.
+ *  - k_pages, v_pages [num_pages, page_size, Hkv, d] of page_dtype: `dtype`
+ *    (k_exp and v_exp unused, may be NULL), or, with bf16 inputs, SWIATTN_E4M3.
+ *    An e4m3 row (one token, one KV head, d values) holds x * 2^-e rounded to
+ *    the nearest e4m3 (ties to even) with e the smallest integer in
+ *    [-126, 127] for which the row's largest |x| is at most 448 * 2^e, x
+ *    being the fp32 rotated value (infinities count as the largest value a
+ *    row can hold, a NaN stays one and does not enter e); the byte
+ *    k_exp[(page * Hkv + h) * page_size + slot] = e + 127 of
+ *    uint8 [num_pages, Hkv, page_size] says so, and v_exp for v.
+ * Only the rows of new tokens are written.  Tokens before starts[0] or from
+ * starts[B] on (padding) and those of a sequence with seq_lens[b] == 0 (an
+ * empty slot) are passed over: neither pages nor their q_out rows are
+ * touched.  A token whose position is negative or past max_pages * page_size,
+ * or whose table entry lies outside [0, num_pages), is passed over too, and
+ * swiattn_get_device_error then reports SWIATTN_EINVAL.  Two tokens must not
+ * go to one row of the pool.  Nothing else of the pool is read or written.
+ * d in {64, 128}; page_size a power of two with max_pages * page_size <= 2^30;
+ * B <= 2^30; T == 0 is a valid no-op.  No workspace. */
+int swiattn_append_paged(const void* q, const void* k, const void* v, const int32_t* starts,
+                         const int32_t* seq_lens, const int32_t* block_table,
+                         const double* inv_freq, void* q_out, void* k_pages, void* v_pages,
+                         uint8_t* k_exp, uint8_t* v_exp, int T, int B, int max_pages,
+                         int page_size, int num_pages, int Hq, int Hkv, int d, int rot_dim,
+                         int interleaved, float factor, int64_t q_stride, int64_t k_stride,
+                         int64_t v_stride, int dtype, int page_dtype, void* stream);
+
 /* Synchronises `stream`, then returns and clears the device error word of the
  * current device: SWIATTN_OK, SWIATTN_ETIMEOUT if a bounded device wait
  * expired since the last query, or SWIATTN_ECUDA if the synchronisation itself
@@ -328,8 +409,9 @@ int swiattn_get_device_error(void* stream);
 const char* swiattn_status_string(int status);
 
 /* Timing hook.  When both are non-NULL, every later swiattn_prefill,
- * swiattn_decode, swiattn_dual_branch, swiattn_prefill_backward, swiattn_route
- * and swiattn_route_backward call records `start` (a cudaEvent_t passed as
+ * swiattn_decode, swiattn_dual_branch, swiattn_prefill_backward, swiattn_route,
+ * swiattn_route_backward, swiattn_rope(_backward), swiattn_append_paged and
+ * swiattn_decode_paged_e4m3 call records `start` (a cudaEvent_t passed as
  * void*) on its stream immediately before launching its dominant kernel (the
  * attention kernel, the decode split kernel, the backward's two attention
  * kernels, dK/dV then dQ, the router GEMV, or the router backward's three

@@ -21,10 +21,11 @@ __all__ = [
     "prefill_workspace", "decode_workspace", "dual_branch_workspace", "get_device_error",
     "status_string", "num_sms", "set_profile_events", "EXPORTS", "prefill_backward",
     "prefill_backward_workspace", "route_backward", "route_backward_workspace", "decode_paged",
-    "decode_paged_workspace", "decode_anchored", "decode_anchored_workspace",
+    "decode_paged_workspace", "decode_anchored", "decode_anchored_workspace", "rope",
+    "rope_backward", "append_paged",
 ]
 
-F32, BF16 = 0, 1
+F32, BF16, E4M3 = 0, 1, 2
 _DT = {torch.float32: F32, torch.bfloat16: BF16}
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libswiattn.so")
@@ -41,7 +42,8 @@ EXPORTS = (
     "swiattn_decode_anchored", "swiattn_prefill_anchored", "swiattn_route_prefill_workspace",
     "swiattn_route_prefill", "swiattn_prefill_host_workspace", "swiattn_prefill_host",
     "swiattn_get_device_error", "swiattn_status_string", "swiattn_set_profile_events",
-    "swiattn_num_sms", "swiattn_set_wait_limit_ns",
+    "swiattn_num_sms", "swiattn_set_wait_limit_ns", "swiattn_rope", "swiattn_rope_backward",
+    "swiattn_append_paged",
 )
 
 
@@ -98,6 +100,10 @@ def _load() -> ctypes.CDLL:
             lib.swiattn_route_prefill_workspace.restype = sz
             lib.swiattn_route_prefill.argtypes = ([vp, vp, f32, i32] + [vp] * 7 + [i32] * 7 +
                                                   [f32, i32, vp, sz, vp])
+            for name in ("swiattn_rope", "swiattn_rope_backward"):
+                getattr(lib, name).argtypes = [vp] * 6 + [i32] * 7 + [f32] + [i64] * 4 + [i32, vp]
+            lib.swiattn_append_paged.argtypes = ([vp] * 12 + [i32] * 10 + [f32] + [i64] * 3
+                                                 + [i32, i32, vp])
             lib.swiattn_get_device_error.argtypes = [vp]
             lib.swiattn_status_string.argtypes = [i32]
             lib.swiattn_status_string.restype = ctypes.c_char_p
@@ -110,7 +116,8 @@ def _load() -> ctypes.CDLL:
                          "swiattn_prefill_backward", "swiattn_route_backward",
                          "swiattn_decode_paged", "swiattn_decode_anchored",
                          "swiattn_prefill_anchored", "swiattn_route_prefill",
-                         "swiattn_prefill_host"):
+                         "swiattn_prefill_host", "swiattn_rope", "swiattn_rope_backward",
+                         "swiattn_append_paged"):
                 getattr(lib, name).restype = ctypes.c_int
             _lib = lib
     return _lib
@@ -476,3 +483,183 @@ def decode_paged(q, k_pages, v_pages, block_table, seq_lens, gate, W: int,
         _ptr(o), _ptr(lse), B, max_pages, page_size, num_pages, Hq, Hkv, d, W, n_anchor,
         float(scale), _DT[q.dtype], _ptr(ws), ws.numel(), _stream()), "swiattn_decode_paged")
     return (o, lse) if want_lse else o
+
+
+def _tokens(t: torch.Tensor, name: str, lead, dtype=None):
+    """Check q/k/v of one call, [*lead, heads, d] on a GPU with packed heads and one distance
+    between tokens (a view of a fused projection is fine); returns that distance in elements."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    shape, stride = t.shape, t.stride()
+    n = len(lead)
+    if len(shape) != n + 2 or tuple(shape[:n]) != tuple(lead):
+        raise ValueError(f"{name} must be {list(lead)} + [heads, d], got {list(shape)}")
+    heads, d = shape[n], shape[n + 1]
+    if stride[n + 1] != 1 or (heads > 1 and stride[n] != d):
+        raise ValueError(f"{name}: heads and their elements must be contiguous")
+    step, rows = heads * d, 1
+    for i in range(n - 1, -1, -1):   # dimensions of size 1 may have any stride
+        if shape[i] > 1:
+            if rows == 1:
+                step = stride[i]
+            elif stride[i] != rows * step:
+                raise ValueError(f"{name}: tokens must be evenly spaced")
+            rows *= shape[i]
+    return step
+
+
+def _one_device(first: torch.Tensor, **tensors):
+    device = first.device
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return device
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _launch(where: str, device: torch.device, *args):
+    """Call library function `where` with the tensors' device current, on its current stream."""
+    fn = getattr(_lib or _load(), where)
+    if device.index == torch.cuda.current_device():
+        status = fn(*args, torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, torch.cuda.current_stream().cuda_stream)
+    if status != 0:
+        raise SwiAttnError(status, where)
+
+
+def _rope(where, q, k, inv_freq, positions, interleaved, factor, out):
+    some = q if q is not None else k
+    if some is None:
+        raise ValueError("q and k are both None")
+    B, N, _, d = some.shape
+    q_out, k_out = out if out is not None else (None, None)
+    strides = []
+    for name, t, o in (("q", q, q_out), ("k", k, k_out)):
+        if t is None:
+            if o is not None:
+                raise ValueError(f"out for {name}, which is None")
+            strides.append((0, 0, 0))
+            continue
+        step = _tokens(t, name, (B, N), some.dtype)
+        if t.shape[3] != d:
+            raise ValueError("q and k must have one head size")
+        if o is None:
+            strides.append((t.shape[2], step, t.shape[2] * d))
+        else:
+            if o.shape != t.shape:
+                raise ValueError(f"out for {name} must be {list(t.shape)}, got {list(o.shape)}")
+            strides.append((t.shape[2], step, _tokens(o, f"out for {name}", (B, N), some.dtype)))
+    _dev(inv_freq, "inv_freq", torch.float64)
+    if positions is not None:
+        _dev(positions, "positions", torch.int32)
+        if positions.numel() != B * N:
+            raise ValueError(f"positions must be [{B}, {N}]")
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    device = _one_device(some, k=k, inv_freq=inv_freq, positions=positions, out=q_out, out_k=k_out)
+    (Hq, qs, qos), (Hkv, ks, kos) = strides
+    if some.numel():
+        _launch(where, device, _addr(q), _addr(k), _addr(positions), inv_freq.data_ptr(),
+                _addr(q_out), _addr(k_out), B, N, Hq, Hkv, d, 2 * inv_freq.numel(),
+                int(interleaved), float(factor), qs, ks, qos, kos, _DT[some.dtype])
+    return q_out, k_out
+
+
+def rope(q, k, inv_freq, positions=None, interleaved: bool = False, factor: float = 1.0, out=None):
+    """Rotary position encoding of q [B,N,Hq,d] and k [B,N,Hkv,d] (either may be None), for
+    prefill, dual_branch and the rest, whose q and k arrive position-encoded.  inv_freq fp64
+    [rot_dim/2], radians a position; positions int32 [B,N] (None: 0..N-1); interleaved: pairs
+    (2f, 2f+1) instead of (f, f + rot_dim/2); factor multiplies cosines and sines.  q and k may
+    be views of a fused projection.  Returns (q_out, k_out), contiguous unless given as out,
+    which may be (q, k) themselves (in place)."""
+    return _rope("swiattn_rope", q, k, inv_freq, positions, interleaved, factor, out)
+
+
+def rope_backward(dq_rot, dk_rot, inv_freq, positions=None, interleaved: bool = False,
+                  factor: float = 1.0, out=None):
+    """Gradient of rope: (dq, dk) from the gradients of its outputs.  Arguments as for rope."""
+    return _rope("swiattn_rope_backward", dq_rot, dk_rot, inv_freq, positions, interleaved, factor,
+                 out)
+
+
+def _exponents(t, name: str, pages: torch.Tensor):
+    if t is None or not t.is_cuda or not t.is_contiguous() or t.dtype not in (
+            torch.uint8, torch.float8_e8m0fnu):
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of uint8 or float8_e8m0fnu")
+    if tuple(t.shape) != (pages.shape[0], pages.shape[2], pages.shape[1]):
+        raise ValueError(f"{name} must be [num_pages, Hkv, page_size], got {list(t.shape)}")
+
+
+def append_paged(q, k, v, k_pages, v_pages, block_table, seq_lens, inv_freq=None, starts=None,
+                 interleaved: bool = False, factor: float = 1.0, k_exp=None, v_exp=None, out=None):
+    """Append new tokens to a paged cache, rotating q and k on the way.  q [T,Hq,d] (or None),
+    k, v [T,Hkv,d], packed; sequence b owns tokens starts[b] .. starts[b+1]-1 (int32 [B+1]; None:
+    one token each, T == B), the last of its seq_lens[b] (int32 [B], new tokens included).
+    k_pages, v_pages [num_pages, page_size, Hkv, d] of q's type, or float8_e4m3fn with k_exp,
+    v_exp [num_pages, Hkv, page_size] (uint8 or float8_e8m0fnu); block_table int32 [B, max_pages].
+    inv_freq, interleaved, factor as for rope (inv_freq None: no rotation).  The pages are written
+    in place; returns the rotated q [T,Hq,d] (None without q).  Rows of q's result that no
+    sequence owns are left as they were (a result allocated here: undefined)."""
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be [T, Hkv, d]")
+    T, Hkv, d = k.shape
+    dtype = k.dtype
+    ks = _tokens(k, "k", (T,))
+    vs = _tokens(v, "v", (T,), dtype)
+    if v.shape != k.shape:
+        raise ValueError("k and v must have one shape")
+    Hq, qs = 0, 0
+    if q is not None:
+        qs = _tokens(q, "q", (T,), dtype)
+        Hq = q.shape[1]
+        if q.shape[2] != d:
+            raise ValueError("q and k must have one head size")
+        if out is None:
+            out = torch.empty((T, Hq, d), dtype=dtype, device=q.device)
+        else:
+            _dev(out, "out", dtype)
+            if out.shape != q.shape:
+                raise ValueError(f"out must be {list(q.shape)}, got {list(out.shape)}")
+    elif out is not None:
+        raise ValueError("out without q")
+    e4m3 = k_pages.dtype == torch.float8_e4m3fn
+    _dev(k_pages, "k_pages", None if e4m3 else dtype)
+    _dev(v_pages, "v_pages", k_pages.dtype)
+    if k_pages.dim() != 4 or tuple(k_pages.shape[2:]) != (Hkv, d) or v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must be [num_pages, page_size, Hkv, d]")
+    if e4m3:
+        _exponents(k_exp, "k_exp", k_pages)
+        _exponents(v_exp, "v_exp", k_pages)
+    _dev(block_table, "block_table", torch.int32)
+    _dev(seq_lens, "seq_lens", torch.int32)
+    B = seq_lens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must be [{B}, max_pages]")
+    if starts is not None:
+        _dev(starts, "starts", torch.int32)
+        if starts.numel() != B + 1:
+            raise ValueError(f"starts must hold {B + 1} values")
+    rot_dim = 0
+    if inv_freq is not None:
+        _dev(inv_freq, "inv_freq", torch.float64)
+        rot_dim = 2 * inv_freq.numel()
+    device = _one_device(k, q=q, v=v, out=out, k_pages=k_pages, v_pages=v_pages, k_exp=k_exp,
+                         v_exp=v_exp, block_table=block_table, seq_lens=seq_lens, starts=starts,
+                         inv_freq=inv_freq)
+    num_pages, page_size = k_pages.shape[0], k_pages.shape[1]
+    _launch("swiattn_append_paged", device, _addr(q), k.data_ptr(), v.data_ptr(), _addr(starts),
+            seq_lens.data_ptr(), block_table.data_ptr(), _addr(inv_freq), _addr(out),
+            k_pages.data_ptr(), v_pages.data_ptr(), _addr(k_exp) if e4m3 else None,
+            _addr(v_exp) if e4m3 else None, T, B, block_table.shape[1], page_size, num_pages, Hq,
+            Hkv, d, rot_dim, int(interleaved), float(factor), qs, ks, vs, _DT[dtype],
+            E4M3 if e4m3 else _DT[dtype])
+    return out

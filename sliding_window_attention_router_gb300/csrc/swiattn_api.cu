@@ -683,4 +683,147 @@ int swiattn_route_backward(const void* h, const void* w, const float* logits, co
     return launched(e);
 }
 
+namespace {
+
+// Token stride of a [tokens, heads, d] operand: whole 16-byte steps, no overlap.
+bool token_stride_ok(int64_t stride, int heads, int d, int dtype) {
+    return stride >= (int64_t)heads * d && stride % (dtype == SWIATTN_BF16 ? 8 : 4) == 0 &&
+           stride < (int64_t(1) << 40);
+}
+bool rot_dim_ok(int rot_dim, int d) { return rot_dim >= 16 && rot_dim <= d && rot_dim % 16 == 0; }
+bool heads_ok(int heads) { return heads > 0 && heads <= (1 << 16); }
+
+int rope_call(const void* q, const void* k, const int32_t* positions, const double* inv_freq,
+              void* q_out, void* k_out, int B, int N, int Hq, int Hkv, int d, int rot_dim,
+              int interleaved, float factor, int64_t q_stride, int64_t k_stride,
+              int64_t q_out_stride, int64_t k_out_stride, int dtype, bool backward, void* stream) {
+    if (B <= 0 || N <= 0 || (d != 64 && d != 128) || !rot_dim_ok(rot_dim, d)) return SWIATTN_EINVAL;
+    if (dtype != SWIATTN_BF16 && dtype != SWIATTN_F32) return SWIATTN_EINVAL;
+    if ((int64_t)B * N >= (int64_t(1) << 31)) return SWIATTN_EINVAL;
+    if (!inv_freq || (q == nullptr) != (q_out == nullptr) || (k == nullptr) != (k_out == nullptr) ||
+        (!q && !k))
+        return SWIATTN_EINVAL;
+    if (!(factor - factor == 0.f)) return SWIATTN_EINVAL;   // not finite
+    if (q && (!heads_ok(Hq) || !aligned16(q) || !aligned16(q_out) ||
+              !token_stride_ok(q_stride, Hq, d, dtype) ||
+              !token_stride_ok(q_out_stride, Hq, d, dtype) ||
+              (q == q_out && q_stride != q_out_stride)))
+        return SWIATTN_EINVAL;
+    if (k && (!heads_ok(Hkv) || !aligned16(k) || !aligned16(k_out) ||
+              !token_stride_ok(k_stride, Hkv, d, dtype) ||
+              !token_stride_ok(k_out_stride, Hkv, d, dtype) ||
+              (k == k_out && k_stride != k_out_stride)))
+        return SWIATTN_EINVAL;
+    RopeArgs a;
+    a.q = q;
+    a.k = k;
+    a.positions = positions;
+    a.inv_freq = inv_freq;
+    a.q_out = q_out;
+    a.k_out = k_out;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.q_out_stride = q_out_stride;
+    a.k_out_stride = k_out_stride;
+    a.tokens = (int64_t)B * N;
+    a.N = N;
+    a.Hq = q ? Hq : 0;
+    a.Hkv = k ? Hkv : 0;
+    a.d = d;
+    a.rot = rot_dim;
+    a.interleaved = interleaved != 0;
+    a.factor = factor;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    prof_start(s);
+    const cudaError_t e = launch_rope(a, dtype, backward, s);
+    prof_stop(s);
+    return launched(e);
+}
+
+}  // namespace
+
+int swiattn_rope(const void* q, const void* k, const int32_t* positions, const double* inv_freq,
+                 void* q_out, void* k_out, int B, int N, int Hq, int Hkv, int d, int rot_dim,
+                 int interleaved, float factor, int64_t q_stride, int64_t k_stride,
+                 int64_t q_out_stride, int64_t k_out_stride, int dtype, void* stream) {
+    return rope_call(q, k, positions, inv_freq, q_out, k_out, B, N, Hq, Hkv, d, rot_dim, interleaved,
+                     factor, q_stride, k_stride, q_out_stride, k_out_stride, dtype, false, stream);
+}
+
+int swiattn_rope_backward(const void* dq_rot, const void* dk_rot, const int32_t* positions,
+                          const double* inv_freq, void* dq, void* dk, int B, int N, int Hq,
+                          int Hkv, int d, int rot_dim, int interleaved, float factor,
+                          int64_t q_stride, int64_t k_stride, int64_t q_out_stride,
+                          int64_t k_out_stride, int dtype, void* stream) {
+    return rope_call(dq_rot, dk_rot, positions, inv_freq, dq, dk, B, N, Hq, Hkv, d, rot_dim,
+                     interleaved, factor, q_stride, k_stride, q_out_stride, k_out_stride, dtype,
+                     true, stream);
+}
+
+int swiattn_append_paged(const void* q, const void* k, const void* v, const int32_t* starts,
+                         const int32_t* seq_lens, const int32_t* block_table,
+                         const double* inv_freq, void* q_out, void* k_pages, void* v_pages,
+                         uint8_t* k_exp, uint8_t* v_exp, int T, int B, int max_pages,
+                         int page_size, int num_pages, int Hq, int Hkv, int d, int rot_dim,
+                         int interleaved, float factor, int64_t q_stride, int64_t k_stride,
+                         int64_t v_stride, int dtype, int page_dtype, void* stream) {
+    if (T < 0 || B <= 0 || B > (1 << 30) || !heads_ok(Hkv) || (d != 64 && d != 128)) return SWIATTN_EINVAL;
+    if (page_size <= 0 || (page_size & (page_size - 1)) != 0 || max_pages <= 0 || num_pages <= 0 ||
+        (int64_t)max_pages * page_size > (1 << 30))
+        return SWIATTN_EINVAL;
+    if (dtype != SWIATTN_BF16 && dtype != SWIATTN_F32) return SWIATTN_EINVAL;
+    if (page_dtype != dtype && page_dtype != SWIATTN_E4M3) return SWIATTN_EINVAL;
+    if (page_dtype == SWIATTN_E4M3 && dtype != SWIATTN_BF16) return SWIATTN_EUNSUPPORTED;
+    if (rot_dim != 0 && (!rot_dim_ok(rot_dim, d) || !(factor - factor == 0.f))) return SWIATTN_EINVAL;
+    if (!starts && T != B) return SWIATTN_EINVAL;
+    if (T == 0) return SWIATTN_OK;
+    if (!k || !v || !seq_lens || !block_table || !k_pages || !v_pages ||
+        (q == nullptr) != (q_out == nullptr) || (rot_dim != 0 && !inv_freq))
+        return SWIATTN_EINVAL;
+    if (page_dtype == SWIATTN_E4M3 && (!k_exp || !v_exp)) return SWIATTN_EINVAL;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_pages) || !aligned16(v_pages))
+        return SWIATTN_EINVAL;
+    if (!token_stride_ok(k_stride, Hkv, d, dtype) || !token_stride_ok(v_stride, Hkv, d, dtype))
+        return SWIATTN_EINVAL;
+    if (q && (!heads_ok(Hq) || !aligned16(q) || !aligned16(q_out) ||
+              !token_stride_ok(q_stride, Hq, d, dtype) ||
+              (q == q_out && q_stride != (int64_t)Hq * d)))
+        return SWIATTN_EINVAL;
+    DeviceInfo di;
+    if (!device_info(di)) return SWIATTN_ECUDA;
+    AppendArgs a;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.starts = starts;
+    a.seq_lens = seq_lens;
+    a.block_table = block_table;
+    a.inv_freq = inv_freq;
+    a.q_out = q_out;
+    a.k_pages = k_pages;
+    a.v_pages = v_pages;
+    a.k_exp = k_exp;
+    a.v_exp = v_exp;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.tokens = T;
+    a.B = B;
+    a.max_pages = max_pages;
+    a.page_lg = 0;
+    while ((1 << a.page_lg) < page_size) ++a.page_lg;
+    a.num_pages = num_pages;
+    a.Hq = q ? Hq : 0;
+    a.Hkv = Hkv;
+    a.d = d;
+    a.rot = rot_dim;
+    a.interleaved = interleaved != 0;
+    a.factor = factor;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    prof_start(s);
+    const cudaError_t e = launch_append(a, dtype, page_dtype, di.err, s);
+    prof_stop(s);
+    return launched(e);
+}
+
 }  // extern "C"

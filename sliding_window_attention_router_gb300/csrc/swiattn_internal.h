@@ -272,6 +272,43 @@ cudaError_t launch_decode_paged(const void* q, const void* kp, const void* vp,
                                 float scale, int dtype, const DecodeWs& L, char* ws,
                                 unsigned int* err, cudaStream_t s);
 
+// ------------------------------------------- rotation and paged append ------
+struct RopeArgs {
+    const void* q;              // [tokens, Hq, d], q_stride elements from token to token
+    const void* k;
+    const int32_t* positions;   // nullptr: token t of sequences of N is at t % N
+    const double* inv_freq;     // [rot/2]
+    void* q_out;
+    void* k_out;
+    int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+    int64_t tokens;
+    int N, Hq, Hkv, d, rot;     // Hq or Hkv 0: that tensor is absent
+    int interleaved;
+    float factor;
+};
+cudaError_t launch_rope(const RopeArgs& a, int dtype, bool backward, cudaStream_t s);
+
+struct AppendArgs {
+    const void* q;              // [tokens, Hq, d] (Hq 0: absent), q_stride elements a token
+    const void* k;              // [tokens, Hkv, d]
+    const void* v;
+    const int32_t* starts;      // [B+1] first token of each sequence; nullptr: one token each
+    const int32_t* seq_lens;    // [B] lengths with the new tokens
+    const int32_t* block_table; // [B, max_pages]
+    const double* inv_freq;     // [rot/2]
+    void* q_out;                // [tokens, Hq, d]
+    void* k_pages;              // [num_pages, 1 << page_lg, Hkv, d]
+    void* v_pages;
+    uint8_t* k_exp;             // e4m3 pages: [num_pages, Hkv, 1 << page_lg]
+    uint8_t* v_exp;
+    int64_t q_stride, k_stride, v_stride;
+    int tokens, B, max_pages, page_lg, num_pages, Hq, Hkv, d, rot;
+    int interleaved;
+    float factor;
+};
+cudaError_t launch_append(const AppendArgs& a, int dtype, int page_dtype, unsigned int* err,
+                          cudaStream_t s);
+
 // Timing hook around the dominant kernel of a call (no-ops unless set).
 void prof_start(cudaStream_t s);
 void prof_stop(cudaStream_t s);
