@@ -397,6 +397,40 @@ int swiattn_append_paged(const void* q, const void* k, const void* v, const int3
                          int interleaved, float factor, int64_t q_stride, int64_t k_stride,
                          int64_t v_stride, int dtype, int page_dtype, void* stream);
 
+/* Bytes of device workspace swiattn_decode_paged_e4m3 needs for these sizes
+ * (0 for invalid sizes). */
+size_t swiattn_decode_paged_e4m3_workspace(int B, int max_pages, int page_size, int Hq, int Hkv,
+                                           int d, int W, int n_anchor);
+
+/* swiattn_decode_paged over the 8-bit pages that swiattn_append_paged writes:
+ * k_pages, v_pages e4m3 [num_pages, page_size, Hkv, d] with exponent bytes
+ * k_exp, v_exp uint8 [num_pages, Hkv, page_size], a row standing for its
+ * values times 2^(byte - 127); bytes 1 to 254.  The query of sequence b sits
+ * at position seq_lens[b] - 1 and reads the entries swiattn_decode_paged
+ * would: gate[b] != 0 all, else the last W and the first n_anchor.
+ *  - seq_lens[b] == 0 is an empty slot: o[b] = 0, lse[b] = -inf, nothing read.
+ *    A seq_lens[b] outside [0, max_pages * page_size] is clamped into it, a
+ *    table entry the call reads outside [0, num_pages) is read as page 0, and
+ *    swiattn_get_device_error then reports SWIATTN_EINVAL.
+ *  - Entries that are not visited are not read, so whatever they hold (NaN
+ *    included) does not reach the result; a NaN in a visited row does.
+ *  - q, o bf16 [B,Hq,d] (dtype SWIATTN_BF16; SWIATTN_F32 returns
+ *    SWIATTN_EUNSUPPORTED); lse (nullable) fp32 [B,Hq].  d in {64, 128};
+ *    Hq / Hkv any whole number up to 16 (larger: SWIATTN_EUNSUPPORTED);
+ *    B and Hkv up to 65535; page_size a power of two, max_pages * page_size
+ *    <= 2^30.
+ *  - A sequence's result does not depend on the rest of the batch, and is
+ *    bitwise repeatable.
+ * workspace: at least swiattn_decode_paged_e4m3_workspace(...) bytes, 256-byte
+ * aligned, scratch only; calls that share one must not overlap in time. */
+int swiattn_decode_paged_e4m3(const void* q, const void* k_pages, const void* v_pages,
+                              const uint8_t* k_exp, const uint8_t* v_exp,
+                              const int32_t* block_table, const int32_t* seq_lens,
+                              const uint8_t* gate, void* o, float* lse, int B, int max_pages,
+                              int page_size, int num_pages, int Hq, int Hkv, int d, int W,
+                              int n_anchor, float scale, int dtype, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
 /* Synchronises `stream`, then returns and clears the device error word of the
  * current device: SWIATTN_OK, SWIATTN_ETIMEOUT if a bounded device wait
  * expired since the last query, or SWIATTN_ECUDA if the synchronisation itself

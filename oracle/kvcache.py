@@ -114,3 +114,34 @@ def contiguous(pages, block_table):
     """[B, max_pages * page_size, Hkv, d] out of a pool [P, page_size, Hkv, d]."""
     B, max_pages = block_table.shape
     return pages[np.asarray(block_table)].reshape(B, max_pages * pages.shape[1], *pages.shape[2:])
+
+
+def visited(length, gate, W, S):
+    """The cache entries that the query at the end of `length` tokens reads."""
+    lo = 0 if gate else max(0, length - W)
+    return np.concatenate([np.arange(min(S, lo)), np.arange(lo, length)]).astype(np.int64)
+
+
+def decode(q, k, v, v_exps, seq_lens, gate, W, S, scale):
+    """Decode over values k, v [B, L, Hkv, d] (v_exps [B, L, Hkv]: the exponent bytes of v's rows).
+    Returns o, lse and, for tolerances: sum_j p_j |v_j| [B, Hq, d]; the largest weight of a row of
+    8-bit values, max_j p_j 2^(byte - 127) [B, Hq]; and max_j scale sum_c |q_c k_jc| [B, Hq]."""
+    B, Hq, d = q.shape
+    Hkv = k.shape[2]
+    o, absum = np.zeros((B, Hq, d)), np.zeros((B, Hq, d))
+    lse, peak, size = np.full((B, Hq), -np.inf), np.zeros((B, Hq)), np.zeros((B, Hq))
+    for b in range(B):
+        at = visited(int(seq_lens[b]), gate[b], W, S)
+        if len(at) == 0:
+            continue
+        for h in range(Hq):
+            kk, vv = k[b, at, h // (Hq // Hkv)], v[b, at, h // (Hq // Hkv)]
+            s = scale * (kk @ q[b, h])
+            m = s.max()
+            e = np.exp(s - m)
+            p = e / e.sum()
+            lse[b, h] = m + np.log(e.sum())
+            o[b, h], absum[b, h] = p @ vv, p @ np.abs(vv)
+            peak[b, h] = np.max(p * np.ldexp(1.0, v_exps[b, at, h // (Hq // Hkv)].astype(np.int64) - 127))
+            size[b, h] = scale * np.max(np.abs(kk) @ np.abs(q[b, h]))
+    return o, lse, absum, peak, size

@@ -22,7 +22,7 @@ __all__ = [
     "status_string", "num_sms", "set_profile_events", "EXPORTS", "prefill_backward",
     "prefill_backward_workspace", "route_backward", "route_backward_workspace", "decode_paged",
     "decode_paged_workspace", "decode_anchored", "decode_anchored_workspace", "rope",
-    "rope_backward", "append_paged",
+    "rope_backward", "append_paged", "decode_paged_e4m3", "decode_paged_e4m3_workspace",
 ]
 
 F32, BF16, E4M3 = 0, 1, 2
@@ -43,7 +43,7 @@ EXPORTS = (
     "swiattn_route_prefill", "swiattn_prefill_host_workspace", "swiattn_prefill_host",
     "swiattn_get_device_error", "swiattn_status_string", "swiattn_set_profile_events",
     "swiattn_num_sms", "swiattn_set_wait_limit_ns", "swiattn_rope", "swiattn_rope_backward",
-    "swiattn_append_paged",
+    "swiattn_append_paged", "swiattn_decode_paged_e4m3_workspace", "swiattn_decode_paged_e4m3",
 )
 
 
@@ -104,6 +104,9 @@ def _load() -> ctypes.CDLL:
                 getattr(lib, name).argtypes = [vp] * 6 + [i32] * 7 + [f32] + [i64] * 4 + [i32, vp]
             lib.swiattn_append_paged.argtypes = ([vp] * 12 + [i32] * 10 + [f32] + [i64] * 3
                                                  + [i32, i32, vp])
+            lib.swiattn_decode_paged_e4m3_workspace.argtypes = [i32] * 8
+            lib.swiattn_decode_paged_e4m3_workspace.restype = sz
+            lib.swiattn_decode_paged_e4m3.argtypes = [vp] * 10 + [i32] * 9 + [f32, i32, vp, sz, vp]
             lib.swiattn_get_device_error.argtypes = [vp]
             lib.swiattn_status_string.argtypes = [i32]
             lib.swiattn_status_string.restype = ctypes.c_char_p
@@ -117,7 +120,7 @@ def _load() -> ctypes.CDLL:
                          "swiattn_decode_paged", "swiattn_decode_anchored",
                          "swiattn_prefill_anchored", "swiattn_route_prefill",
                          "swiattn_prefill_host", "swiattn_rope", "swiattn_rope_backward",
-                         "swiattn_append_paged"):
+                         "swiattn_append_paged", "swiattn_decode_paged_e4m3"):
                 getattr(lib, name).restype = ctypes.c_int
             _lib = lib
     return _lib
@@ -663,3 +666,51 @@ def append_paged(q, k, v, k_pages, v_pages, block_table, seq_lens, inv_freq=None
             Hkv, d, rot_dim, int(interleaved), float(factor), qs, ks, vs, _DT[dtype],
             E4M3 if e4m3 else _DT[dtype])
     return out
+
+
+def decode_paged_e4m3_workspace(B, max_pages, page_size, Hq, Hkv, d, W, n_anchor=0) -> int:
+    return int(_load().swiattn_decode_paged_e4m3_workspace(B, max_pages, page_size, Hq, Hkv, d, W,
+                                                           n_anchor))
+
+
+def decode_paged_e4m3(q, k_pages, v_pages, k_exp, v_exp, block_table, seq_lens, gate, W: int,
+                      scale: Optional[float] = None, out=None, want_lse=False, workspace=None,
+                      n_anchor: int = 0):
+    """decode_paged over 8-bit pages (as append_paged writes them).  q bf16 [B,Hq,d];
+    k_pages, v_pages float8_e4m3fn [num_pages, page_size, Hkv, d]; k_exp, v_exp
+    [num_pages, Hkv, page_size] (uint8 or float8_e8m0fnu); block_table int32 [B, max_pages];
+    seq_lens int32 [B] (0: an empty slot, o = 0 and lse = -inf); gate uint8 [B].
+    Hq/Hkv any whole number up to 16."""
+    _dev(q, "q")
+    _dev(k_pages, "k_pages", torch.float8_e4m3fn)
+    _dev(v_pages, "v_pages", torch.float8_e4m3fn)
+    B, Hq, d = q.shape
+    num_pages, page_size, Hkv, dk = k_pages.shape
+    if dk != d or v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must be [num_pages, page_size, Hkv, d]")
+    _exponents(k_exp, "k_exp", k_pages)
+    _exponents(v_exp, "v_exp", k_pages)
+    _dev(block_table, "block_table", torch.int32)
+    _dev(seq_lens, "seq_lens", torch.int32)
+    _dev(gate, "gate", torch.uint8)
+    if block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.numel() != B or gate.numel() != B:
+        raise ValueError(f"block_table, seq_lens and gate must hold {B} sequences")
+    max_pages = block_table.shape[1]
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    if out is None:
+        out = torch.empty_like(q)
+    elif _dev(out, "out", q.dtype).shape != q.shape:
+        raise ValueError(f"out must be {list(q.shape)}, got {list(out.shape)}")
+    lse = torch.empty((B, Hq), device=q.device, dtype=torch.float32) if want_lse else None
+    if workspace is None:
+        workspace = _workspace(decode_paged_e4m3_workspace(B, max_pages, page_size, Hq, Hkv, d, W,
+                                                           n_anchor), q.device, None)
+    device = _one_device(q, k_pages=k_pages, v_pages=v_pages, k_exp=k_exp, v_exp=v_exp,
+                         block_table=block_table, seq_lens=seq_lens, gate=gate, out=out,
+                         workspace=workspace)
+    _launch("swiattn_decode_paged_e4m3", device, q.data_ptr(), k_pages.data_ptr(),
+            v_pages.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), block_table.data_ptr(),
+            seq_lens.data_ptr(), gate.data_ptr(), out.data_ptr(), _addr(lse), B, max_pages,
+            page_size, num_pages, Hq, Hkv, d, W, n_anchor, float(scale), _DT[q.dtype],
+            workspace.data_ptr(), workspace.numel())
+    return (out, lse) if want_lse else out

@@ -826,4 +826,77 @@ int swiattn_append_paged(const void* q, const void* k, const void* v, const int3
     return launched(e);
 }
 
+namespace {
+
+// Sizes of a decode over e4m3 pages: SWIATTN_OK, or why not.
+int decode_e4m3_sizes_ok(int B, int max_pages, int page_size, int Hq, int Hkv, int d, int W,
+                         int n_anchor) {
+    if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || (d != 64 && d != 128) || W <= 0 ||
+        n_anchor < 0)
+        return SWIATTN_EINVAL;
+    if (page_size <= 0 || (page_size & (page_size - 1)) != 0 || max_pages <= 0 ||
+        (int64_t)max_pages * page_size > (1 << 30))
+        return SWIATTN_EINVAL;
+    if (Hq / Hkv > 16 || B > 65535 || Hkv > 65535) return SWIATTN_EUNSUPPORTED;
+    return SWIATTN_OK;
+}
+
+}  // namespace
+
+size_t swiattn_decode_paged_e4m3_workspace(int B, int max_pages, int page_size, int Hq, int Hkv,
+                                           int d, int W, int n_anchor) {
+    if (decode_e4m3_sizes_ok(B, max_pages, page_size, Hq, Hkv, d, W, n_anchor) != SWIATTN_OK)
+        return 0;
+    return decode_e4m3_workspace_bytes(
+        B, Hq, d, decode_e4m3_max_chunks((int64_t)max_pages * page_size, n_anchor, Hkv));
+}
+
+int swiattn_decode_paged_e4m3(const void* q, const void* k_pages, const void* v_pages,
+                              const uint8_t* k_exp, const uint8_t* v_exp,
+                              const int32_t* block_table, const int32_t* seq_lens,
+                              const uint8_t* gate, void* o, float* lse, int B, int max_pages,
+                              int page_size, int num_pages, int Hq, int Hkv, int d, int W,
+                              int n_anchor, float scale, int dtype, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+    const int ok = decode_e4m3_sizes_ok(B, max_pages, page_size, Hq, Hkv, d, W, n_anchor);
+    if (ok == SWIATTN_EINVAL || num_pages <= 0) return SWIATTN_EINVAL;
+    if (!q || !k_pages || !v_pages || !k_exp || !v_exp || !block_table || !seq_lens || !gate || !o)
+        return SWIATTN_EINVAL;
+    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o))
+        return SWIATTN_EINVAL;
+    if (!(scale > 0.f) || !(scale - scale == 0.f)) return SWIATTN_EINVAL;
+    if (dtype != SWIATTN_BF16 && dtype != SWIATTN_F32) return SWIATTN_EINVAL;
+    if (ok != SWIATTN_OK || dtype != SWIATTN_BF16) return SWIATTN_EUNSUPPORTED;
+    DecodeE4m3Args a;
+    a.max_chunks = decode_e4m3_max_chunks((int64_t)max_pages * page_size, n_anchor, Hkv);
+    if (!workspace || !aligned256(workspace) ||
+        workspace_bytes < decode_e4m3_workspace_bytes(B, Hq, d, a.max_chunks))
+        return SWIATTN_EINVAL;
+    DeviceInfo di;
+    if (!device_info(di)) return SWIATTN_ECUDA;
+    a.q = q;
+    a.k_pages = static_cast<const uint8_t*>(k_pages);
+    a.v_pages = static_cast<const uint8_t*>(v_pages);
+    a.k_exp = k_exp;
+    a.v_exp = v_exp;
+    a.block_table = block_table;
+    a.seq_lens = seq_lens;
+    a.gate = gate;
+    a.o = o;
+    a.lse = lse;
+    a.part = static_cast<float*>(workspace);
+    a.err = di.err;
+    a.B = B;
+    a.max_pages = max_pages;
+    a.page_lg = 0;
+    while ((1 << a.page_lg) < page_size) ++a.page_lg;
+    a.num_pages = num_pages;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.W = W;
+    a.n_anchor = n_anchor;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    return launched(launch_decode_e4m3(a, d, static_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -309,6 +309,27 @@ struct AppendArgs {
 cudaError_t launch_append(const AppendArgs& a, int dtype, int page_dtype, unsigned int* err,
                           cudaStream_t s);
 
+// -------------------------------------------------- decode over e4m3 pages ---
+struct DecodeE4m3Args {
+    const void* q;              // bf16 [B, Hq, d]
+    const uint8_t* k_pages;     // e4m3 [num_pages, 1 << page_lg, Hkv, d]
+    const uint8_t* v_pages;
+    const uint8_t* k_exp;       // [num_pages, Hkv, 1 << page_lg]
+    const uint8_t* v_exp;
+    const int32_t* block_table; // [B, max_pages]
+    const int32_t* seq_lens;    // [B]
+    const uint8_t* gate;        // [B]
+    void* o;                    // bf16 [B, Hq, d]
+    float* lse;                 // [B, Hq], nullable
+    float* part;                // [B, Hq, max_chunks, d + 4]
+    unsigned int* err;
+    int B, max_pages, page_lg, num_pages, Hq, Hkv, W, n_anchor, max_chunks;
+    float scale_log2;           // softmax scale times log2(e)
+};
+int decode_e4m3_max_chunks(int64_t max_len, int n_anchor, int Hkv);
+size_t decode_e4m3_workspace_bytes(int B, int Hq, int d, int max_chunks);
+cudaError_t launch_decode_e4m3(const DecodeE4m3Args& a, int d, cudaStream_t s);
+
 // Timing hook around the dominant kernel of a call (no-ops unless set).
 void prof_start(cudaStream_t s);
 void prof_stop(cudaStream_t s);

@@ -85,3 +85,18 @@ def test_row_exponent_is_the_smallest():
     # half a step of a normal value, or of a subnormal one
     err = np.abs(got - x)
     assert np.all((err <= 2.0 ** -4 * np.abs(x) + np.ldexp(2.0 ** -10, e)[:, None]) | np.isnan(x))
+
+
+def test_decode_equals_the_oracles():
+    """On plain values, against the oracle's decode (itself pinned)."""
+    import oracle
+    g = rng(5)
+    B, L, Hq, Hkv, d, W, S = 3, 40, 6, 3, 8, 7, 5
+    q, k, v = g.standard_normal((B, Hq, d)), g.standard_normal((B, L, Hkv, d)), g.standard_normal((B, L, Hkv, d))
+    lens, gate = np.array([40, 9, 1], np.int32), np.array([0, 0, 1], np.uint8)
+    exps = np.full((B, L, Hkv), 127, np.uint8)
+    o, lse, *_ = ref.decode(q, k, v, exps, lens, gate, W, S, 0.3)
+    want, want_lse = oracle.decode_anchored(q, k, v, lens, gate, W, S, 0.3, want_lse=True)
+    np.testing.assert_allclose(o, want, atol=1e-12)
+    np.testing.assert_allclose(lse, want_lse, atol=1e-12)
+    assert np.all(ref.decode(q, k, v, exps, [0, 0, 0], gate, W, S, 0.3)[0] == 0)
