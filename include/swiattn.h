@@ -418,7 +418,7 @@ size_t swiattn_decode_paged_e4m3_workspace(int B, int max_pages, int page_size, 
  *    SWIATTN_EUNSUPPORTED); lse (nullable) fp32 [B,Hq].  d in {64, 128};
  *    Hq / Hkv any whole number up to 16 (larger: SWIATTN_EUNSUPPORTED);
  *    B and Hkv up to 65535; page_size a power of two, max_pages * page_size
- *    <= 2^30.
+ *    <= 2^30, num_pages * page_size <= 2^32 (larger: SWIATTN_EUNSUPPORTED).
  *  - A sequence's result does not depend on the rest of the batch, and is
  *    bitwise repeatable.
  * workspace: at least swiattn_decode_paged_e4m3_workspace(...) bytes, 256-byte

@@ -488,18 +488,44 @@ def decode_paged(q, k_pages, v_pages, block_table, seq_lens, gate, W: int,
     return (o, lse) if want_lse else o
 
 
-def _tokens(t: torch.Tensor, name: str, lead, dtype=None):
-    """Check q/k/v of one call, [*lead, heads, d] on a GPU with packed heads and one distance
-    between tokens (a view of a fused projection is fine); returns that distance in elements."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+# The address of the current stream of a device, without building a Stream object each call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _gpu(t, name: str) -> int:
+    """The index of the device that tensor t, the first of a call, is on."""
+    index = t.get_device() if isinstance(t, torch.Tensor) and t.is_cuda else -1
+    if index < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if dtype is not None and t.dtype != dtype:
+    return index
+
+
+def _same(t, name: str, index: int, dtype=None):
+    """Check a further tensor of a call on device `index`: contiguous, of `dtype`."""
+    if isinstance(t, torch.Tensor) and t.get_device() == index and t.is_contiguous() and (
+            dtype is None or t.dtype is dtype):
+        return t
+    _dev(t, name, dtype)
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+
+
+def _tokens(t, name: str, lead, index: int, dtype):
+    """Check q/k/v of one call, [*lead, heads, d] on device `index` with packed heads and one
+    distance between tokens (a view of a fused projection is fine); returns (heads, d, that
+    distance in elements)."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != index:
+        raise ValueError(f"{name} must be a tensor on cuda:{index}")
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    shape, stride = t.shape, t.stride()
+    shape = t.shape
     n = len(lead)
-    if len(shape) != n + 2 or tuple(shape[:n]) != tuple(lead):
+    if len(shape) != n + 2 or shape[:n] != lead:
         raise ValueError(f"{name} must be {list(lead)} + [heads, d], got {list(shape)}")
-    heads, d = shape[n], shape[n + 1]
+    heads, d = shape[n:]
+    if t.is_contiguous():
+        return heads, d, heads * d
+    stride = t.stride()
     if stride[n + 1] != 1 or (heads > 1 and stride[n] != d):
         raise ValueError(f"{name}: heads and their elements must be contiguous")
     step, rows = heads * d, 1
@@ -510,71 +536,60 @@ def _tokens(t: torch.Tensor, name: str, lead, dtype=None):
             elif stride[i] != rows * step:
                 raise ValueError(f"{name}: tokens must be evenly spaced")
             rows *= shape[i]
-    return step
-
-
-def _one_device(first: torch.Tensor, **tensors):
-    device = first.device
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
-    return device
+    return heads, d, step
 
 
 def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _launch(where: str, device: torch.device, *args):
-    """Call library function `where` with the tensors' device current, on its current stream."""
+def _launch(where: str, index: int, *args):
+    """Call library function `where` with device `index` current, on its current stream."""
     fn = getattr(_lib or _load(), where)
-    if device.index == torch.cuda.current_device():
-        status = fn(*args, torch.cuda.current_stream().cuda_stream)
+    if index == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(device):
-            status = fn(*args, torch.cuda.current_stream().cuda_stream)
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
     if status != 0:
         raise SwiAttnError(status, where)
 
 
 def _rope(where, q, k, inv_freq, positions, interleaved, factor, out):
     some = q if q is not None else k
-    if some is None:
-        raise ValueError("q and k are both None")
-    B, N, _, d = some.shape
-    q_out, k_out = out if out is not None else (None, None)
-    strides = []
-    for name, t, o in (("q", q, q_out), ("k", k, k_out)):
+    index = _gpu(some, "q and k")
+    if some.dim() != 4:
+        raise ValueError(f"q and k must be [B, N, heads, d], got {list(some.shape)}")
+    lead, d, dtype = some.shape[:2], some.shape[3], some.dtype
+    results, sizes = [], []
+    for name, t, o in (("q", q, out and out[0]), ("k", k, out and out[1])):
         if t is None:
             if o is not None:
                 raise ValueError(f"out for {name}, which is None")
-            strides.append((0, 0, 0))
+            results.append(None)
+            sizes.append((0, 0, 0))
             continue
-        step = _tokens(t, name, (B, N), some.dtype)
-        if t.shape[3] != d:
+        heads, dt, step = _tokens(t, name, lead, index, dtype)
+        if dt != d:
             raise ValueError("q and k must have one head size")
         if o is None:
-            strides.append((t.shape[2], step, t.shape[2] * d))
+            o, out_step = torch.empty(t.shape, dtype=dtype, device=t.device), heads * d
         else:
-            if o.shape != t.shape:
+            oh, od, out_step = _tokens(o, f"out for {name}", lead, index, dtype)
+            if oh != heads or od != d:
                 raise ValueError(f"out for {name} must be {list(t.shape)}, got {list(o.shape)}")
-            strides.append((t.shape[2], step, _tokens(o, f"out for {name}", (B, N), some.dtype)))
-    _dev(inv_freq, "inv_freq", torch.float64)
-    if positions is not None:
-        _dev(positions, "positions", torch.int32)
-        if positions.numel() != B * N:
-            raise ValueError(f"positions must be [{B}, {N}]")
-    if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    device = _one_device(some, k=k, inv_freq=inv_freq, positions=positions, out=q_out, out_k=k_out)
-    (Hq, qs, qos), (Hkv, ks, kos) = strides
+        results.append(o)
+        sizes.append((heads, step, out_step))
+    _same(inv_freq, "inv_freq", index, torch.float64)
+    B, N = lead
+    if positions is not None and _same(positions, "positions", index, torch.int32).numel() != B * N:
+        raise ValueError(f"positions must be [{B}, {N}]")
+    (Hq, qs, qos), (Hkv, ks, kos) = sizes
     if some.numel():
-        _launch(where, device, _addr(q), _addr(k), _addr(positions), inv_freq.data_ptr(),
-                _addr(q_out), _addr(k_out), B, N, Hq, Hkv, d, 2 * inv_freq.numel(),
-                int(interleaved), float(factor), qs, ks, qos, kos, _DT[some.dtype])
-    return q_out, k_out
+        _launch(where, index, _addr(q), _addr(k), _addr(positions), inv_freq.data_ptr(),
+                _addr(results[0]), _addr(results[1]), B, N, Hq, Hkv, d, 2 * inv_freq.numel(),
+                bool(interleaved), factor, qs, ks, qos, kos, _DT[dtype])
+    return results[0], results[1]
 
 
 def rope(q, k, inv_freq, positions=None, interleaved: bool = False, factor: float = 1.0, out=None):
@@ -594,11 +609,15 @@ def rope_backward(dq_rot, dk_rot, inv_freq, positions=None, interleaved: bool = 
                  out)
 
 
-def _exponents(t, name: str, pages: torch.Tensor):
-    if t is None or not t.is_cuda or not t.is_contiguous() or t.dtype not in (
-            torch.uint8, torch.float8_e8m0fnu):
-        raise ValueError(f"{name} must be a contiguous CUDA tensor of uint8 or float8_e8m0fnu")
-    if tuple(t.shape) != (pages.shape[0], pages.shape[2], pages.shape[1]):
+_EXPONENTS = (torch.uint8, torch.float8_e8m0fnu)
+
+
+def _exponents(t, name: str, index: int, shape):
+    if not isinstance(t, torch.Tensor) or t.get_device() != index or t.dtype not in _EXPONENTS or (
+            not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous tensor of uint8 or float8_e8m0fnu on "
+                         f"cuda:{index}")
+    if t.shape != shape:
         raise ValueError(f"{name} must be [num_pages, Hkv, page_size], got {list(t.shape)}")
 
 
@@ -612,59 +631,49 @@ def append_paged(q, k, v, k_pages, v_pages, block_table, seq_lens, inv_freq=None
     inv_freq, interleaved, factor as for rope (inv_freq None: no rotation).  The pages are written
     in place; returns the rotated q [T,Hq,d] (None without q).  Rows of q's result that no
     sequence owns are left as they were (a result allocated here: undefined)."""
-    if not isinstance(k, torch.Tensor) or k.dim() != 3:
-        raise ValueError("k must be [T, Hkv, d]")
-    T, Hkv, d = k.shape
-    dtype = k.dtype
-    ks = _tokens(k, "k", (T,))
-    vs = _tokens(v, "v", (T,), dtype)
-    if v.shape != k.shape:
+    index = _gpu(k, "k")
+    lead, dtype = k.shape[:1], k.dtype
+    Hkv, d, ks = _tokens(k, "k", lead, index, dtype)
+    vh, vd, vs = _tokens(v, "v", lead, index, dtype)
+    if vh != Hkv or vd != d:
         raise ValueError("k and v must have one shape")
     Hq, qs = 0, 0
     if q is not None:
-        qs = _tokens(q, "q", (T,), dtype)
-        Hq = q.shape[1]
-        if q.shape[2] != d:
+        Hq, qd, qs = _tokens(q, "q", lead, index, dtype)
+        if qd != d:
             raise ValueError("q and k must have one head size")
         if out is None:
-            out = torch.empty((T, Hq, d), dtype=dtype, device=q.device)
-        else:
-            _dev(out, "out", dtype)
-            if out.shape != q.shape:
-                raise ValueError(f"out must be {list(q.shape)}, got {list(out.shape)}")
+            out = torch.empty(q.shape, dtype=dtype, device=q.device)
+        elif _same(out, "out", index, dtype).shape != q.shape:
+            raise ValueError(f"out must be {list(q.shape)}, got {list(out.shape)}")
     elif out is not None:
         raise ValueError("out without q")
-    e4m3 = k_pages.dtype == torch.float8_e4m3fn
-    _dev(k_pages, "k_pages", None if e4m3 else dtype)
-    _dev(v_pages, "v_pages", k_pages.dtype)
-    if k_pages.dim() != 4 or tuple(k_pages.shape[2:]) != (Hkv, d) or v_pages.shape != k_pages.shape:
+    page_dtype = _same(k_pages, "k_pages", index).dtype
+    _same(v_pages, "v_pages", index, page_dtype)
+    shape = k_pages.shape
+    if len(shape) != 4 or shape[2] != Hkv or shape[3] != d or v_pages.shape != shape:
         raise ValueError("k_pages and v_pages must be [num_pages, page_size, Hkv, d]")
-    if e4m3:
-        _exponents(k_exp, "k_exp", k_pages)
-        _exponents(v_exp, "v_exp", k_pages)
-    _dev(block_table, "block_table", torch.int32)
-    _dev(seq_lens, "seq_lens", torch.int32)
-    B = seq_lens.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != B:
+    if page_dtype is torch.float8_e4m3fn:
+        _exponents(k_exp, "k_exp", index, (shape[0], Hkv, shape[1]))
+        _exponents(v_exp, "v_exp", index, (shape[0], Hkv, shape[1]))
+        kind, ke, ve = E4M3, k_exp.data_ptr(), v_exp.data_ptr()
+    elif page_dtype is dtype:
+        kind, ke, ve = _DT[dtype], None, None
+    else:
+        raise ValueError(f"pages must be {dtype} or float8_e4m3fn, got {page_dtype}")
+    B = _same(seq_lens, "seq_lens", index, torch.int32).numel()
+    table = _same(block_table, "block_table", index, torch.int32).shape
+    if len(table) != 2 or table[0] != B:
         raise ValueError(f"block_table must be [{B}, max_pages]")
-    if starts is not None:
-        _dev(starts, "starts", torch.int32)
-        if starts.numel() != B + 1:
-            raise ValueError(f"starts must hold {B + 1} values")
+    if starts is not None and _same(starts, "starts", index, torch.int32).numel() != B + 1:
+        raise ValueError(f"starts must hold {B + 1} values")
     rot_dim = 0
     if inv_freq is not None:
-        _dev(inv_freq, "inv_freq", torch.float64)
-        rot_dim = 2 * inv_freq.numel()
-    device = _one_device(k, q=q, v=v, out=out, k_pages=k_pages, v_pages=v_pages, k_exp=k_exp,
-                         v_exp=v_exp, block_table=block_table, seq_lens=seq_lens, starts=starts,
-                         inv_freq=inv_freq)
-    num_pages, page_size = k_pages.shape[0], k_pages.shape[1]
-    _launch("swiattn_append_paged", device, _addr(q), k.data_ptr(), v.data_ptr(), _addr(starts),
+        rot_dim = 2 * _same(inv_freq, "inv_freq", index, torch.float64).numel()
+    _launch("swiattn_append_paged", index, _addr(q), k.data_ptr(), v.data_ptr(), _addr(starts),
             seq_lens.data_ptr(), block_table.data_ptr(), _addr(inv_freq), _addr(out),
-            k_pages.data_ptr(), v_pages.data_ptr(), _addr(k_exp) if e4m3 else None,
-            _addr(v_exp) if e4m3 else None, T, B, block_table.shape[1], page_size, num_pages, Hq,
-            Hkv, d, rot_dim, int(interleaved), float(factor), qs, ks, vs, _DT[dtype],
-            E4M3 if e4m3 else _DT[dtype])
+            k_pages.data_ptr(), v_pages.data_ptr(), ke, ve, lead[0], B, table[1], shape[1],
+            shape[0], Hq, Hkv, d, rot_dim, bool(interleaved), factor, qs, ks, vs, _DT[dtype], kind)
     return out
 
 
@@ -681,36 +690,36 @@ def decode_paged_e4m3(q, k_pages, v_pages, k_exp, v_exp, block_table, seq_lens, 
     [num_pages, Hkv, page_size] (uint8 or float8_e8m0fnu); block_table int32 [B, max_pages];
     seq_lens int32 [B] (0: an empty slot, o = 0 and lse = -inf); gate uint8 [B].
     Hq/Hkv any whole number up to 16."""
-    _dev(q, "q")
-    _dev(k_pages, "k_pages", torch.float8_e4m3fn)
-    _dev(v_pages, "v_pages", torch.float8_e4m3fn)
+    index = _gpu(q, "q")
+    _same(q, "q", index)
     B, Hq, d = q.shape
-    num_pages, page_size, Hkv, dk = k_pages.shape
-    if dk != d or v_pages.shape != k_pages.shape:
+    shape = _same(k_pages, "k_pages", index, torch.float8_e4m3fn).shape
+    if len(shape) != 4 or shape[3] != d or (
+            _same(v_pages, "v_pages", index, torch.float8_e4m3fn).shape != shape):
         raise ValueError("k_pages and v_pages must be [num_pages, page_size, Hkv, d]")
-    _exponents(k_exp, "k_exp", k_pages)
-    _exponents(v_exp, "v_exp", k_pages)
-    _dev(block_table, "block_table", torch.int32)
-    _dev(seq_lens, "seq_lens", torch.int32)
-    _dev(gate, "gate", torch.uint8)
-    if block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.numel() != B or gate.numel() != B:
+    num_pages, page_size, Hkv, _ = shape
+    _exponents(k_exp, "k_exp", index, (num_pages, Hkv, page_size))
+    _exponents(v_exp, "v_exp", index, (num_pages, Hkv, page_size))
+    table = _same(block_table, "block_table", index, torch.int32).shape
+    if len(table) != 2 or table[0] != B or (
+            _same(seq_lens, "seq_lens", index, torch.int32).numel() != B) or (
+            _same(gate, "gate", index, torch.uint8).numel() != B):
         raise ValueError(f"block_table, seq_lens and gate must hold {B} sequences")
-    max_pages = block_table.shape[1]
-    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
     if out is None:
         out = torch.empty_like(q)
-    elif _dev(out, "out", q.dtype).shape != q.shape:
+    elif _same(out, "out", index, q.dtype).shape != q.shape:
         raise ValueError(f"out must be {list(q.shape)}, got {list(out.shape)}")
     lse = torch.empty((B, Hq), device=q.device, dtype=torch.float32) if want_lse else None
     if workspace is None:
-        workspace = _workspace(decode_paged_e4m3_workspace(B, max_pages, page_size, Hq, Hkv, d, W,
+        workspace = _workspace(decode_paged_e4m3_workspace(B, table[1], page_size, Hq, Hkv, d, W,
                                                            n_anchor), q.device, None)
-    device = _one_device(q, k_pages=k_pages, v_pages=v_pages, k_exp=k_exp, v_exp=v_exp,
-                         block_table=block_table, seq_lens=seq_lens, gate=gate, out=out,
-                         workspace=workspace)
-    _launch("swiattn_decode_paged_e4m3", device, q.data_ptr(), k_pages.data_ptr(),
+    else:
+        _same(workspace, "workspace", index, torch.uint8)
+    _launch("swiattn_decode_paged_e4m3", index, q.data_ptr(), k_pages.data_ptr(),
             v_pages.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), block_table.data_ptr(),
-            seq_lens.data_ptr(), gate.data_ptr(), out.data_ptr(), _addr(lse), B, max_pages,
-            page_size, num_pages, Hq, Hkv, d, W, n_anchor, float(scale), _DT[q.dtype],
+            seq_lens.data_ptr(), gate.data_ptr(), out.data_ptr(), _addr(lse), B, table[1],
+            page_size, num_pages, Hq, Hkv, d, W, n_anchor, scale, _DT[q.dtype],
             workspace.data_ptr(), workspace.numel())
     return (out, lse) if want_lse else out

@@ -848,7 +848,7 @@ size_t swiattn_decode_paged_e4m3_workspace(int B, int max_pages, int page_size, 
     if (decode_e4m3_sizes_ok(B, max_pages, page_size, Hq, Hkv, d, W, n_anchor) != SWIATTN_OK)
         return 0;
     return decode_e4m3_workspace_bytes(
-        B, Hq, d, decode_e4m3_max_chunks((int64_t)max_pages * page_size, n_anchor, Hkv));
+        B, Hq, d, decode_e4m3_max_chunks((int64_t)max_pages * page_size, n_anchor));
 }
 
 int swiattn_decode_paged_e4m3(const void* q, const void* k_pages, const void* v_pages,
@@ -867,8 +867,9 @@ int swiattn_decode_paged_e4m3(const void* q, const void* k_pages, const void* v_
     if (!(scale > 0.f) || !(scale - scale == 0.f)) return SWIATTN_EINVAL;
     if (dtype != SWIATTN_BF16 && dtype != SWIATTN_F32) return SWIATTN_EINVAL;
     if (ok != SWIATTN_OK || dtype != SWIATTN_BF16) return SWIATTN_EUNSUPPORTED;
+    if ((int64_t)num_pages * page_size > (int64_t(1) << 32)) return SWIATTN_EUNSUPPORTED;
     DecodeE4m3Args a;
-    a.max_chunks = decode_e4m3_max_chunks((int64_t)max_pages * page_size, n_anchor, Hkv);
+    a.max_chunks = decode_e4m3_max_chunks((int64_t)max_pages * page_size, n_anchor);
     if (!workspace || !aligned256(workspace) ||
         workspace_bytes < decode_e4m3_workspace_bytes(B, Hq, d, a.max_chunks))
         return SWIATTN_EINVAL;
@@ -896,7 +897,7 @@ int swiattn_decode_paged_e4m3(const void* q, const void* k_pages, const void* v_
     a.W = W;
     a.n_anchor = n_anchor;
     a.scale_log2 = scale * 1.4426950408889634f;
-    return launched(launch_decode_e4m3(a, d, static_cast<cudaStream_t>(stream)));
+    return launched(launch_decode_e4m3(a, d, di.sms, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -326,9 +326,9 @@ struct DecodeE4m3Args {
     int B, max_pages, page_lg, num_pages, Hq, Hkv, W, n_anchor, max_chunks;
     float scale_log2;           // softmax scale times log2(e)
 };
-int decode_e4m3_max_chunks(int64_t max_len, int n_anchor, int Hkv);
+int decode_e4m3_max_chunks(int64_t max_len, int n_anchor);
 size_t decode_e4m3_workspace_bytes(int B, int Hq, int d, int max_chunks);
-cudaError_t launch_decode_e4m3(const DecodeE4m3Args& a, int d, cudaStream_t s);
+cudaError_t launch_decode_e4m3(const DecodeE4m3Args& a, int d, int sms, cudaStream_t s);
 
 // Timing hook around the dominant kernel of a call (no-ops unless set).
 void prof_start(cudaStream_t s);
