@@ -404,23 +404,23 @@ size_t swiattn_decode_paged_e4m3_workspace(int B, int max_pages, int page_size, 
 
 /* swiattn_decode_paged over the 8-bit pages that swiattn_append_paged writes:
  * k_pages, v_pages e4m3 [num_pages, page_size, Hkv, d] with exponent bytes
- * k_exp, v_exp uint8 [num_pages, Hkv, page_size], a row standing for its
- * values times 2^(byte - 127); bytes 1 to 254.  The query of sequence b sits
+ * k_exp, v_exp uint8 [num_pages, Hkv, page_size] (16-byte aligned), a row
+ * standing for its values times 2^(byte - 127); bytes 1 to 254.  The query of sequence b sits
  * at position seq_lens[b] - 1 and reads the entries swiattn_decode_paged
  * would: gate[b] != 0 all, else the last W and the first n_anchor.
  *  - seq_lens[b] == 0 is an empty slot: o[b] = 0, lse[b] = -inf, nothing read.
  *    A seq_lens[b] outside [0, max_pages * page_size] is clamped into it, a
  *    table entry the call reads outside [0, num_pages) is read as page 0, and
  *    swiattn_get_device_error then reports SWIATTN_EINVAL.
- *  - Entries that are not visited are not read, so whatever they hold (NaN
- *    included) does not reach the result; a NaN in a visited row does.
+ *  - Whatever entries that are not visited hold (NaN included) does not reach
+ *    the result; a NaN in a visited row does.
  *  - q, o bf16 [B,Hq,d] (dtype SWIATTN_BF16; SWIATTN_F32 returns
  *    SWIATTN_EUNSUPPORTED); lse (nullable) fp32 [B,Hq].  d in {64, 128};
  *    Hq / Hkv any whole number up to 16 (larger: SWIATTN_EUNSUPPORTED);
- *    B and Hkv up to 65535; page_size a power of two, max_pages * page_size
+ *    B <= 65535, B * Hkv <= 2^30; page_size a power of two, max_pages * page_size
  *    <= 2^30, num_pages * page_size <= 2^32 (larger: SWIATTN_EUNSUPPORTED).
- *  - A sequence's result does not depend on the rest of the batch, and is
- *    bitwise repeatable.
+ *  - The call is bitwise repeatable.  How a sequence's keys are split for the
+ *    GPU depends on the whole batch, so the last bits of its result may.
  * workspace: at least swiattn_decode_paged_e4m3_workspace(...) bytes, 256-byte
  * aligned, scratch only; calls that share one must not overlap in time. */
 int swiattn_decode_paged_e4m3(const void* q, const void* k_pages, const void* v_pages,
@@ -460,7 +460,7 @@ int swiattn_num_sms(void);
 
 /* Failure-detection aid with no counterpart in the paper: sets, on the
  * current device, how long a device-side wait of the tensor-core kernels
- * (routed prefill, dual branch, backward) may last before the kernel gives up,
+ * (routed prefill, dual branch, backward) and of the decode over e4m3 pages may last before the kernel gives up,
  * records SWIATTN_ETIMEOUT for swiattn_get_device_error and returns early
  * without computing the rest of its work; ns = 0 restores the default of 2 s.
  * A tiny limit lets a test make such a wait run out on purpose and check that

@@ -29,24 +29,26 @@
 //   transposes inside the warp.
 
 #include "swiattn.h"
+#include "ptx.cuh"
 #include "swiattn_internal.h"
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 #include <math.h>
+#include <algorithm>
 #include <atomic>
+#include <cstring>
 
 namespace swi {
 namespace {
 
 constexpr int kTile = 16;        // keys of one product tile
-constexpr int kWarps = 4;        // warps of a block; they take a chunk's tiles in turn
-constexpr int kStages = 3;       // tiles a warp holds: one at work, two on their way
-constexpr int kBlocksPerSm = 4;
-constexpr int kMinChunk = 64;    // keys of a chunk (one block's work at a time)
-constexpr int kMaxChunk = 512;
-constexpr int kChunksWanted = 8; // of a visit shorter than kChunksWanted * kMaxChunk
+constexpr int kWarps = 4;        // warps of a block (they share nothing)
+constexpr int kStages = 2;       // tiles a warp holds: one at work, one on its way
+template <int NH>
+constexpr int kBlocksPerSm = NH == 1 ? 4 : 2;   // by registers: 128 or 255 a thread
+constexpr int kMaxWarps = 152 * 4 * kWarps;     // workers of one call: what fills a GB300
+constexpr int kMinRun = 2;       // tiles a warp takes at least
 constexpr float kSlack = 8.f;    // base-2 units a score may pass its reference (weights up to 256)
 
 __device__ __forceinline__ float ex2f(float x) {
@@ -55,9 +57,9 @@ __device__ __forceinline__ float ex2f(float x) {
     return y;
 }
 
-// What to subtract from scores whose maximum is x: a maximum of -inf (no key
-// yet, or scores that are all -inf or NaN) must not make -inf - -inf.
-__device__ __forceinline__ float finite_or_0(float x) { return x == -INFINITY ? 0.f : x; }
+// Where references and maxima start: below every score, yet finite, so that
+// no difference of two of them is a NaN (scores that are all -inf leave it).
+constexpr float kLow = -3e38f;
 
 __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -73,11 +75,11 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     return y;
 }
 
-// Two e4m3 bytes (the low or high half of w) as a pair of fp16.
-__device__ __forceinline__ uint32_t half2_of(uint32_t w, int high) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(high ? w >> 16 : w & 0xffffu),
-                                                     __NV_E4M3);
-    return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+// Four e4m3 bytes as two pairs of fp16 (exact).
+__device__ __forceinline__ void halves_of(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
 }
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
@@ -86,510 +88,525 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 }
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {   // zeros where not on
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void copy8(uint32_t dst, const void* src, bool on) {
-    asm volatile("cp.async.ca.shared.global.L2::128B [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(on ? 8 : 0)
-                 : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
 
-// Keys sequence b visits: anchors [0, na) and [lo, len).  Chunks are runs of
-// `tiles` 16-key tiles at multiples of 16 from the cache's start, so that a
-// tile never straddles a page of 16 or more; the first nca chunks are
-// anchors'.  The chunk length depends on the visit alone, so a sequence's
-// result does not depend on the rest of the batch.
+// What sequence b's query visits: anchors [0, na) and [lo, len), as 16-key
+// tiles at multiples of 16 from the cache's start (so a tile never straddles a
+// page of 16 or more): `ta` anchor tiles, then the others, `tiles` in all.
 struct Visit {
     int len, lo, na;
-    int tiles;      // tiles of a chunk
-    int nca, nc;    // chunks: anchors', all
+    int ta, tiles;
 };
-__device__ __forceinline__ Visit visit_of(const DecodeE4m3Args& a, int raw_len, int gate) {
+__device__ __forceinline__ Visit visit_of(const DecodeE4m3Args& a, int b) {
     Visit v;
-    v.len = min(max(raw_len, 0), a.max_pages << a.page_lg);
-    v.lo = gate ? 0 : max(0, v.len - a.W);
+    v.len = min(max(a.seq_lens[b], 0), a.max_pages << a.page_lg);
+    v.lo = a.gate[b] ? 0 : max(0, v.len - a.W);
     v.na = min(a.n_anchor, v.lo);
-    const int m = v.na + v.len - v.lo;
-    int chunk = kMinChunk;
-    while (chunk < kMaxChunk && chunk * kChunksWanted < m) chunk <<= 1;
-    v.tiles = chunk / kTile;
-    const int ta = (v.na + kTile - 1) / kTile;
-    const int tw = v.len > 0 ? (v.len + kTile - 1) / kTile - v.lo / kTile : 0;
-    v.nca = (ta + v.tiles - 1) / v.tiles;
-    v.nc = v.nca + (tw + v.tiles - 1) / v.tiles;
+    v.ta = (v.na + kTile - 1) / kTile;
+    v.tiles = v.ta + (v.len > 0 ? (v.len + kTile - 1) / kTile - v.lo / kTile : 0);
     return v;
 }
 
-// Shared memory of a block: each thread's own queue of the 16-byte pieces it
-// loads (piece p of stage s of a warp: 32 lanes side by side), so nothing is
-// exchanged through it and no bank is met twice; after the last tile the same
-// bytes hold the warps' sums.
-template <int D>
-constexpr int kStageBytes = kTile * 2 * D;   // of one warp
-template <int D>
-constexpr int kSharedBytes = kWarps * kStages * kStageBytes<D>;
-
-// A unit of work: chunk c of KV head h of sequence b.  Blocks are persistent
-// and take units blockIdx.x, blockIdx.x + gridDim.x, ... of the batch's (a
-// unit's heads side by side, so that neighbouring blocks read neighbouring
-// bytes of the same tokens).  Each warp finds its block's units by itself: it
-// holds the visits of 32 sequences, one a lane, and moves on to the next 32
-// when the unit lies behind them.
-struct Units {
-    Visit mine;        // of sequence first + lane
-    int first;         // first sequence held
-    int before, total; // chunks of the held sequences: before this lane's, of all
-    unsigned c;        // the unit: chunk index from the first held sequence's first
-    int h;
-
-    __device__ void hold(const DecodeE4m3Args& a, int from) {
-        const int lane = threadIdx.x & 31, b = from + lane;
-        first = from;
-        mine = visit_of(a, b < a.B ? a.seq_lens[b] : 0, b < a.B ? a.gate[b] : 0);
-        int sum = mine.nc;
+// The work: every sequence's tiles are cut into blocks of `run` tiles, and a
+// warp takes one block of one KV head at a time: item (blocks before it) * Hkv +
+// head.  So neighbouring warps read neighbouring heads of the same tokens,
+// which the memory serves from the same open rows (runs cut without regard to
+// the heads moved 5.2 TB/s where these move TB/s).  `run` is the least
+// that gives each warp one item, where the batch has fewer (sequence, head)s
+// than half the warps, and balances their number otherwise.  Items' sums are
+// joined in the order of the blocks.
+//
+// The plan that the split kernel leaves for the join: plan[b] blocks of the
+// sequences before b, plan[B] tiles of a block.
+__device__ __forceinline__ int inclusive_sum(int x) {   // over the warp's lanes
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += y;
-        }
-        before = sum - mine.nc;
-        total = __shfl_sync(0xffffffffu, sum, 31);
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if ((threadIdx.x & 31) >= o) x += y;
     }
-    // Finds the unit's sequence; false: there are no more.
-    __device__ bool find(const DecodeE4m3Args& a, int& b, int& chunk, Visit& v) {
-        while (c >= static_cast<unsigned>(total)) {
-            c -= total;
-            if (first + 32 >= a.B) return false;
-            hold(a, first + 32);
-        }
-        const int ci = static_cast<int>(c);
-        const int at = __ffs(__ballot_sync(0xffffffffu, ci >= before && ci < before + mine.nc)) - 1;
-        b = first + at;
-        chunk = ci - __shfl_sync(0xffffffffu, before, at);
-        v.len = __shfl_sync(0xffffffffu, mine.len, at);
-        v.lo = __shfl_sync(0xffffffffu, mine.lo, at);
-        v.na = __shfl_sync(0xffffffffu, mine.na, at);
-        v.tiles = __shfl_sync(0xffffffffu, mine.tiles, at);
-        v.nca = __shfl_sync(0xffffffffu, mine.nca, at);
-        return true;
-    }
-};
+    return x;
+}
 
-// NH: groups of eight query heads (1: Hq/Hkv <= 8, 2: <= 16).
-template <int D, int NH>
-__global__ void __launch_bounds__(kWarps * 32, NH == 1 ? kBlocksPerSm : 2) decode_e4m3_split_kernel(DecodeE4m3Args a) {
+// Shared memory of a warp: a ring of tiles, each 16 key rows, then 16 value
+// rows, of D bytes.  A row's 16-byte pieces lie swizzled, as a tile copy of
+// that width leaves them (128-byte rows: piece ^ (row & 7); 64-byte rows: piece ^
+// (row / 2 & 3)), so that the eight rows a quarter of a warp reads at once
+// spread over the banks.
+template <int D>
+constexpr int kStageBytes = kTile * 2 * D;
+template <int D>
+constexpr int kSharedBytes = kWarps * kStages * kStageBytes<D> + 1024;   // and room to align
+template <int D>
+__device__ __forceinline__ int piece_at(int row, int piece) {
+    return row * D + ((D == 128 ? piece ^ (row & 7) : piece ^ ((row >> 1) & 3)) << 4);
+}
+
+// NH: groups of eight query heads (1: Hq/Hkv <= 8, 2: <= 16).  WIDE: pages of
+// 16 tokens or more, where a tile's rows follow one another.
+template <int D, int NH, bool WIDE>
+__global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm<NH>) decode_e4m3_split_kernel(const __grid_constant__ DecodeE4m3Args a,
+                         const __grid_constant__ CUtensorMap k_map,
+                         const __grid_constant__ CUtensorMap v_map) {
     constexpr int KS = D / 16;    // 16-deep steps of the score product, and 16-row tiles of O^T
     constexpr int KW = D / 64;    // 16-byte pieces of a key row a thread holds
-    extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ uint8_t s_exp[kWarps][kStages][32];
-    __shared__ float s_m[kWarps][NH * 8], s_n[kWarps][NH * 8], s_l[kWarps][NH * 8];
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ __align__(16) uint8_t s_exp[kWarps][kStages][32];   // of a tile's 16 K rows, then V rows
+    __shared__ uint64_t s_full[kWarps][kStages];
+    __shared__ int s_abort[kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     const int G = a.Hq / a.Hkv;
-    uint8_t* const queue = smem + warp * kStages * kStageBytes<D>;
-    const uint32_t queue_s = static_cast<uint32_t>(__cvta_generic_to_shared(queue));
-
-    if (blockIdx.x == 0)   // lengths that are clamped
-        for (int i = threadIdx.x; i < a.B; i += kWarps * 32) {
-            const int raw = a.seq_lens[i];
-            if (raw < 0 || raw > (a.max_pages << a.page_lg)) atomicOr(a.err, kDevErrInput);
-        }
-
-    Units unit;
-    unit.hold(a, 0);
-    unit.c = blockIdx.x / a.Hkv;
-    unit.h = blockIdx.x % a.Hkv;
-    const unsigned step_c = gridDim.x / a.Hkv;
-    const int step_h = gridDim.x % a.Hkv;
-    int b, c;
-    Visit vis;
-    for (; unit.find(a, b, c, vis);) {
-    const int h = unit.h;
-    unit.c += step_c;
-    unit.h += step_h;
-    if (unit.h >= a.Hkv) {
-        unit.h -= a.Hkv;
-        ++unit.c;
+    uint8_t* const queue = smem + ((1024 - (smem_u32(smem) & 1023)) & 1023) + warp * kStages * kStageBytes<D>;
+    const uint32_t queue_s = smem_u32(queue);
+    const uint32_t mask = (1u << a.page_lg) - 1;
+    const size_t token_bytes = static_cast<size_t>(a.Hkv) * D;
+    if (WIDE && lane == 0) {
+#pragma unroll
+        for (int i = 0; i < kStages; ++i) mbar_init(&s_full[warp][i], 1);
+        s_abort[warp] = 0;
+        fence_barrier_init();
+        fence_proxy_async_smem();
     }
+    __syncwarp();
 
-    // This chunk's tiles and the keys of them that are visited, [from, to);
-    // this warp's are tile0, tile0 + kWarps, ..., `count` of them.
-    int tile0, from, to;
-    if (c < vis.nca) {
-        from = 0;
-        to = vis.na;
-        tile0 = c * vis.tiles;
-    } else {
-        from = vis.lo;
-        to = vis.len;
-        tile0 = vis.lo / kTile + (c - vis.nca) * vis.tiles;
-    }
-    const int tile1 = min(tile0 + vis.tiles, (to + kTile - 1) / kTile);
-    tile0 += warp;
-    const int count = max(0, (tile1 - tile0 + kWarps - 1) / kWarps);
+    // The length of a block, from all sequences' tiles.
+    int64_t total = 0;
+    for (int i = lane; i < a.B; i += 32) total += visit_of(a, i).tiles;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    const int worker = blockIdx.x * kWarps + warp, workers = gridDim.x * kWarps;
+    const int64_t share = max(workers - static_cast<int64_t>(a.B) * a.Hkv, static_cast<int64_t>(workers) / 2);
+    const int run = static_cast<int>(
+        min(max((total * a.Hkv + share - 1) / share, static_cast<int64_t>(kMinRun)), static_cast<int64_t>(1) << 27));
 
-    // Pool row of key (lane & 15) of this warp's i-th tile (a key that is not
-    // visited: of one that is, and its bytes are not copied).
-    const int32_t* table = a.block_table + static_cast<size_t>(b) * a.max_pages;
-    auto row_of = [&](int i) -> uint32_t {
-        const int tok = min(max((tile0 + i * kWarps) * kTile + (lane & 15), from), to - 1);
-        int p = table[tok >> a.page_lg];
-        if (p < 0 || p >= a.num_pages) {
-            atomicOr(a.err, kDevErrInput);
-            p = 0;
-        }
-        return (static_cast<uint32_t>(p) << a.page_lg) + (tok & ((1 << a.page_lg) - 1));
-    };
-    // Starts the copies of tile i, whose rows are `row` (lane by lane).
-    auto issue = [&](int i, uint32_t row) {
-        const int base = (tile0 + i * kWarps) * kTile;
-        const uint32_t dst = queue_s + (i % kStages) * kStageBytes<D>;
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {   // keys g and 8 + g
-            const int j = g + 8 * r;
-            const size_t at = static_cast<size_t>(__shfl_sync(0xffffffffu, row, j)) * a.Hkv + h;
-            const bool on = base + j >= from && base + j < to;
-#pragma unroll
-            for (int w = 0; w < KW; ++w)
-                copy16(dst + ((r * KW + w) * 32 + lane) * 16, a.k_pages + at * D + w * 64 + t * 16, on);
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {   // values of keys 2t, 2t + 1, 2t + 8, 2t + 9
-            const int j = 2 * t + (r & 1) + 8 * (r >> 1);
-            const size_t at = static_cast<size_t>(__shfl_sync(0xffffffffu, row, j)) * a.Hkv + h;
-            const bool on = base + j >= from && base + j < to;
-            const uint8_t* src = a.v_pages + at * D + g * (D / 8);
-            const uint32_t to_s = dst + 2 * KW * 512 + (r * 32 + lane) * (D / 8);
-            if constexpr (D == 128) copy16(to_s, src, on);
-            else copy8(to_s, src, on);
-        }
-    };
-    // Exponent byte of key (lane & 15): of its K row in lanes 0-15, its V row in 16-31.
-    auto exponent_of = [&](uint32_t row) -> uint32_t {
-        const size_t at = ((static_cast<size_t>(row >> a.page_lg) * a.Hkv + h) << a.page_lg) +
-                          (row & ((1u << a.page_lg) - 1));
-        return (lane < 16 ? a.k_exp : a.v_exp)[at];
-    };
-
-    uint32_t first_row[kStages - 1], next_row = 0;
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) first_row[i] = i < count ? row_of(i) : 0;
-    if (kStages - 1 < count) next_row = row_of(kStages - 1);
-
-    // Query fragments: head g (and 8 + g), dims 16 t .. 16 t + 15 of each 64.
-    uint32_t qf[NH][KS][2];
-    float fs[NH][2];   // scale log2(e) 2^-qe of the thread's columns, heads 2t and 2t + 1
-#pragma unroll
-    for (int n = 0; n < NH; ++n) {
-        const int head = n * 8 + g;
-        float x[KW * 16];
-        float amax = 0.f;
-#pragma unroll
-        for (int w = 0; w < KW; ++w) {
-            uint4 u[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-            if (head < G) {
-                const uint4* src = reinterpret_cast<const uint4*>(
-                    static_cast<const __nv_bfloat16*>(a.q) + (static_cast<size_t>(b) * a.Hq + h * G + head) * D + w * 64 + t * 16);
-                u[0] = src[0];
-                u[1] = src[1];
+    int slot = 0;             // stage of the next tile to work on,
+    uint32_t phase = 0;       // and the parity its barrier completes with
+    for (int item = worker;; item += workers) {
+        // The item's sequence, block and head; the first warp passes over all
+        // sequences once, leaves the plan for the join and reports lengths.
+        const int h = item % a.Hkv;
+        const bool planner = item == 0;
+        int left = item / a.Hkv, block = 0;   // blocks from the scanned ones' end on
+        int b = -1;
+        for (int from = 0; from < a.B; from += 32) {
+            const int i = from + lane;
+            const int n = i < a.B ? (visit_of(a, i).tiles + run - 1) / run : 0;
+            const int sum = inclusive_sum(n);
+            if (planner && i < a.B) {
+                a.plan[i] = sum - n - left;
+                if (a.seq_lens[i] < 0 || a.seq_lens[i] > (a.max_pages << a.page_lg)) atomicOr(a.err, kDevErrInput);
             }
-            const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(u);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float2 f = __bfloat1622float2(p[e]);
-                x[w * 16 + 2 * e] = f.x;
-                x[w * 16 + 2 * e + 1] = f.y;
-                amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+            const unsigned hit = __ballot_sync(0xffffffffu, left < sum);
+            if (hit && b < 0) {
+                const int who = __ffs(hit) - 1;
+                block = left - __shfl_sync(0xffffffffu, sum - n, who);
+                b = from + who;
+                if (!planner) break;
             }
+            left -= __shfl_sync(0xffffffffu, sum, 31);
         }
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        // 2^qe takes the head's largest element to [2^14, 2^15).
-        const int qe = min(126, 14 + 127 - static_cast<int>(__float_as_uint(amax) >> 23));
-        const float up = __uint_as_float(static_cast<uint32_t>(qe + 127) << 23);
-#pragma unroll
-        for (int s = 0; s < KS; ++s)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) qf[n][s][r] = pack_half2(x[4 * s + 2 * r] * up, x[4 * s + 2 * r + 1] * up);
-        const float down = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - qe) << 23);
-        fs[n][0] = __shfl_sync(0xffffffffu, down, (2 * t) * 4);
-        fs[n][1] = __shfl_sync(0xffffffffu, down, (2 * t + 1) * 4);
-    }
-
-    float acc[NH][KS][4];
-    float m[NH][2], nmax[NH][2], l[NH][2];
-#pragma unroll
-    for (int n = 0; n < NH; ++n) {
-#pragma unroll
-        for (int j = 0; j < KS; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[n][j][e] = 0.f;
-        m[n][0] = m[n][1] = nmax[n][0] = nmax[n][1] = -INFINITY;
-        l[n][0] = l[n][1] = 0.f;
-    }
-
-    uint32_t last_exp = 0;
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-        if (i < count) issue(i, first_row[i]);
-        if (i > 0 && i - 1 < count) s_exp[warp][i - 1][lane] = static_cast<uint8_t>(last_exp);
-        if (i < count) last_exp = exponent_of(first_row[i]);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    }
-
-    for (int i = 0; i < count; ++i) {
-        // The exponents of the tile issued last have arrived by now; then the
-        // next tile's copies start, in the stage that the last one left.
-        const int ahead = i + kStages - 1;
-        if (ahead - 1 < count) s_exp[warp][(ahead - 1) % kStages][lane] = static_cast<uint8_t>(last_exp);
-        if (ahead < count) {
-            issue(ahead, next_row);
-            last_exp = exponent_of(next_row);
-            if (ahead + 1 < count) next_row = row_of(ahead + 1);
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-        __syncwarp();
-        const int base = (tile0 + i * kWarps) * kTile;
-        const uint8_t* stage = queue + (i % kStages) * kStageBytes<D>;
-        uint4 kw[2][KW];
-        uint32_t vw[4][D / 32];
-        int ku[2], vu[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-#pragma unroll
-            for (int w = 0; w < KW; ++w)
-                kw[r][w] = *reinterpret_cast<const uint4*>(stage + ((r * KW + w) * 32 + lane) * 16);
-            ku[r] = s_exp[warp][i % kStages][g + 8 * r];
-            vu[r] = s_exp[warp][i % kStages][16 + g + 8 * r];
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const uint8_t* src = stage + 2 * KW * 512 + (r * 32 + lane) * (D / 8);
-            if constexpr (D == 128) {
-                const uint4 u = *reinterpret_cast<const uint4*>(src);
-                vw[r][0] = u.x, vw[r][1] = u.y, vw[r][2] = u.z, vw[r][3] = u.w;
-            } else {
-                const uint2 u = *reinterpret_cast<const uint2*>(src);
-                vw[r][0] = u.x, vw[r][1] = u.y;
-            }
-        }
-        __syncwarp();   // every lane has read the stage's exponents
-
-        // Scores: rows key g and 8 + g, columns heads 2t and 2t + 1.
-        float s[NH][4];
-#pragma unroll
-        for (int n = 0; n < NH; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-        const uint32_t* k0 = reinterpret_cast<const uint32_t*>(kw[0]);
-        const uint32_t* k1 = reinterpret_cast<const uint32_t*>(kw[1]);
-#pragma unroll
-        for (int i = 0; i < KS; ++i) {
-            const uint32_t a0 = half2_of(k0[i], 0), a1 = half2_of(k1[i], 0);
-            const uint32_t a2 = half2_of(k0[i], 1), a3 = half2_of(k1[i], 1);
-#pragma unroll
-            for (int n = 0; n < NH; ++n) mma_f16(s[n], a0, a1, a2, a3, qf[n][i][0], qf[n][i][1]);
-        }
-        // s_j and t_j, and whether one is over kSlack above the reference it
-        // would be subtracted from.
-        float x[NH][4], y[NH][4];
-        bool over = false;
+        if (planner && lane == 0) a.plan[a.B] = run;
+        if (b < 0) break;
+        const Visit vis = visit_of(a, b);
+        const int at = block * run;   // first tile of the block
+        const int count = min(run, vis.tiles - at);
+        // The query's head g (and 8 + g), dims 16 t .. 16 t + 15 of each 64.
+        uint4 q_raw[NH][2 * KW];
 #pragma unroll
         for (int n = 0; n < NH; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int r = e >> 1, tok = base + g + 8 * r;
-                const bool on = tok >= from && tok < to;
-                x[n][e] = on ? s[n][e] * fs[n][e & 1] * __uint_as_float(static_cast<uint32_t>(ku[r]) << 23) : -INFINITY;
-                y[n][e] = x[n][e] + static_cast<float>(vu[r] - 127);
-                over |= x[n][e] > m[n][e & 1] + kSlack || y[n][e] > nmax[n][e & 1] + kSlack;
+            for (int p = 0; p < 2 * KW; ++p) {
+                q_raw[n][p] = make_uint4(0, 0, 0, 0);
+                if (n * 8 + g < G)
+                    q_raw[n][p] = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                        (static_cast<size_t>(b) * a.Hq + h * G + n * 8 + g) * D + (p / 2) * 64 + t * 16)[p % 2];
             }
-        if (__any_sync(0xffffffffu, over)) {
-#pragma unroll
-            for (int n = 0; n < NH; ++n)
-#pragma unroll
-                for (int col = 0; col < 2; ++col) {
-                    float xm = fmaxf(x[n][col], x[n][col + 2]), ym = fmaxf(y[n][col], y[n][col + 2]);
-#pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) {
-                        xm = fmaxf(xm, __shfl_xor_sync(0xffffffffu, xm, o));
-                        ym = fmaxf(ym, __shfl_xor_sync(0xffffffffu, ym, o));
-                    }
-                    const float mn = fmaxf(m[n][col], xm), nn = fmaxf(nmax[n][col], ym);
-                    l[n][col] *= ex2f(m[n][col] - finite_or_0(mn));
-                    const float ca = ex2f(nmax[n][col] - finite_or_0(nn));
-#pragma unroll
-                    for (int j = 0; j < KS; ++j) {
-                        acc[n][j][col] *= ca;
-                        acc[n][j][col + 2] *= ca;
-                    }
-                    m[n][col] = mn;
-                    nmax[n][col] = nn;
+        struct Keys {
+            int base, from, to;   // first key of the tile; visited: [from, to)
+        };
+        auto keys_of = [&](int i) -> Keys {
+            const int j = at + i;
+            if (j < vis.ta) return {j * kTile, 0, vis.na};
+            return {(vis.lo / kTile + j - vis.ta) * kTile, vis.lo, vis.len};
+        };
+        // Page of a token (a bad table entry: page 0).
+        auto page_of = [&](int tok) -> int {
+            const int p = a.block_table[static_cast<size_t>(b) * a.max_pages + (tok >> a.page_lg)];
+            if (p >= 0 && p < a.num_pages) return p;
+            atomicOr(a.err, kDevErrInput);
+            return 0;
+        };
+        // WIDE: lane i holds the page of tile i (from the last multiple of 32 on),
+        // looked up 32 tiles at once.  Otherwise: of key (lane & 15) of one tile, a
+        // key not visited standing for one that is (its bytes are not copied).
+        int pages = 0;
+        // Starts the copies of tile i into stage `slot`.
+        auto issue = [&](int i, int slot) {
+            const Keys k = keys_of(i);
+            const uint32_t dst = queue_s + slot * kStageBytes<D>;
+            if constexpr (WIDE) {
+                if (i % 32 == 0) pages = i + lane < count ? page_of(keys_of(i + lane).base) : 0;
+                const int page = __shfl_sync(0xffffffffu, pages, i % 32);
+                if (lane == 0) {
+                    const int at_page = k.base & mask;
+                    const size_t ex = ((static_cast<size_t>(page) * a.Hkv + h) << a.page_lg) + at_page;
+                    uint64_t* bar = &s_full[warp][slot];
+                    mbar_arrive_expect_tx(bar, kStageBytes<D> + 32);
+                    tma_load_3d(dst, &k_map, bar, h * D, at_page, page);
+                    tma_load_3d(dst + kTile * D, &v_map, bar, h * D, at_page, page);
+                    bulk_load(smem_u32(s_exp[warp][slot]), a.k_exp + ex, 16, bar);
+                    bulk_load(smem_u32(s_exp[warp][slot]) + 16, a.v_exp + ex, 16, bar);
                 }
+            } else {
+                const int tok = min(max(k.base + (lane & 15), k.from), k.to - 1);
+                pages = page_of(tok);
+                const size_t row = (static_cast<size_t>(pages) << a.page_lg) + (tok & mask);
+                constexpr int P = D / 16;   // pieces of a row
+#pragma unroll
+                for (int x = 0; x < P / 2; ++x) {
+                    const int j = x * (32 / P) + lane / P, piece = lane % P;
+                    const bool on = k.base + j >= k.from && k.base + j < k.to;
+                    const size_t src = __shfl_sync(0xffffffffu, row, j) * token_bytes + h * D + piece * 16;
+                    copy16(dst + piece_at<D>(j, piece), a.k_pages + src, on);
+                    copy16(dst + kTile * D + piece_at<D>(j, piece), a.v_pages + src, on);
+                }
+                const size_t ex = ((static_cast<size_t>(pages) * a.Hkv + h) << a.page_lg) + (tok & mask);
+                s_exp[warp][slot][lane] = (lane < 16 ? a.k_exp : a.v_exp)[ex];
+            }
+        };
+
+        // The first tiles, from stage `slot` on.
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) {
+            if (i < count) issue(i, slot + i < kStages ? slot + i : slot + i - kStages);
+            if (!WIDE) asm volatile("cp.async.commit_group;" ::: "memory");
         }
-        uint32_t wt[NH][2];
+
+        // Query fragments and the factors of their scores.
+        uint32_t qf[NH][KS][2];
+        float fs[NH][2];   // scale log2(e) 2^-qe of the thread's columns, heads 2t and 2t + 1
+#pragma unroll
+        for (int n = 0; n < NH; ++n) {
+            float x[KW * 16];
+            float amax = 0.f;
+            const __nv_bfloat162* pairs = reinterpret_cast<const __nv_bfloat162*>(q_raw[n]);
+#pragma unroll
+            for (int e = 0; e < KW * 8; ++e) {
+                const float2 f = __bfloat1622float2(pairs[e]);
+                x[2 * e] = f.x;
+                x[2 * e + 1] = f.y;
+                amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            // 2^qe takes the head's largest element to [2^14, 2^15).
+            const int qe = min(126, 14 + 127 - static_cast<int>(__float_as_uint(amax) >> 23));
+            const float up = __uint_as_float(static_cast<uint32_t>(qe + 127) << 23);
+    #pragma unroll
+            for (int s = 0; s < KS; ++s)
+    #pragma unroll
+                for (int r = 0; r < 2; ++r) qf[n][s][r] = pack_half2(x[4 * s + 2 * r] * up, x[4 * s + 2 * r + 1] * up);
+            const float down = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - qe) << 23);
+            fs[n][0] = __shfl_sync(0xffffffffu, down, (2 * t) * 4);
+            fs[n][1] = __shfl_sync(0xffffffffu, down, (2 * t + 1) * 4);
+        }
+    
+        float acc[NH][KS][4];
+        float m[NH][2], nmax[NH][2], l[NH][2];   // references of s and t, and the sum
 #pragma unroll
         for (int n = 0; n < NH; ++n) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int col = e & 1;
-                l[n][col] += ex2f(x[n][e] - finite_or_0(m[n][col]));
-                y[n][e] = ex2f(y[n][e] - finite_or_0(nmax[n][col]));
-            }
-            wt[n][0] = transpose8x8(pack_half2(y[n][0], y[n][1]));
-            wt[n][1] = transpose8x8(pack_half2(y[n][2], y[n][3]));
-        }
-        // O^T: tile i holds dims D/8 g + 2 i (rows g) and + 1 (rows 8 + g).
+            for (int j = 0; j < KS; ++j)
 #pragma unroll
-        for (int i = 0; i < KS; ++i) {
-            const uint32_t sel = (i & 1) ? 0x7362 : 0x5140;
-            const uint32_t lo = __byte_perm(vw[0][i / 2], vw[1][i / 2], sel);
-            const uint32_t hi = __byte_perm(vw[2][i / 2], vw[3][i / 2], sel);
-            const uint32_t a0 = half2_of(lo, 0), a1 = half2_of(lo, 1), a2 = half2_of(hi, 0), a3 = half2_of(hi, 1);
-#pragma unroll
-            for (int n = 0; n < NH; ++n) mma_f16(acc[n][i], a0, a1, a2, a3, wt[n][0], wt[n][1]);
+                for (int e = 0; e < 4; ++e) acc[n][j][e] = 0.f;
+            m[n][0] = m[n][1] = nmax[n][0] = nmax[n][1] = kLow;
+            l[n][0] = l[n][1] = 0.f;
         }
-    }
 
-    // Join the warps: their references, then their sums relative to the
-    // block's, through the queue's bytes.
-    float* part = a.part + ((static_cast<size_t>(b) * a.Hq + h * G) * a.max_chunks + c) * (D + 4);
-    const size_t head_step = static_cast<size_t>(a.max_chunks) * (D + 4);
-    float* const s_acc = reinterpret_cast<float*>(smem);
-    static_assert(kSharedBytes<D> >= kWarps * 8 * D * 4, "the sums of eight heads fit the queue");
-#pragma unroll
-    for (int n = 0; n < NH; ++n)
-#pragma unroll
-        for (int col = 0; col < 2; ++col) {
-            float ls = l[n][col];
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
-            if (g == 0) {
-                s_m[warp][n * 8 + 2 * t + col] = m[n][col];
-                s_n[warp][n * 8 + 2 * t + col] = nmax[n][col];
-                s_l[warp][n * 8 + 2 * t + col] = ls;
+        for (int i = 0; i < count; ++i) {
+            // The next tile's copies start, in the stage that the last one left.
+            const int ahead = i + kStages - 1;
+            if (ahead < count) issue(ahead, slot == 0 ? kStages - 1 : slot - 1);
+            if constexpr (WIDE) {
+                // One lane's time-out is every lane's: the warp leaves together.
+                if (!__all_sync(0xffffffffu, mbar_wait(&s_full[warp][slot], phase, &s_abort[warp], a.err))) {
+                    for (int j = i; j < min(ahead + 1, count); ++j) {   // the copies in flight
+                        mbar_drain(&s_full[warp][slot], phase);
+                        if (++slot == kStages) slot = 0, phase ^= 1;
+                    }
+                    return;
+                }
+            } else {
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+                __syncwarp();
             }
-        }
-    __syncthreads();
+            const uint8_t* stage = queue + slot * kStageBytes<D>;
+            const Keys keys = keys_of(i);
+            uint4 kw[2][KW];
+            uint32_t vw[4][D / 32];
+            int ku[2], vu[2];
 #pragma unroll
-    for (int n = 0; n < NH; ++n) {
+            for (int r = 0; r < 2; ++r) {
+                const int row = g + 8 * r;
 #pragma unroll
-        for (int col = 0; col < 2; ++col) {
-            const int head = 2 * t + col;
-            float top = s_n[0][n * 8 + head];
+                for (int p = 0; p < KW; ++p)
+                    kw[r][p] = *reinterpret_cast<const uint4*>(stage + piece_at<D>(row, 4 * p + t));
+                ku[r] = s_exp[warp][slot][row];
+                vu[r] = s_exp[warp][slot][16 + row];
+            }
 #pragma unroll
-            for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_n[w][n * 8 + head]);
-            const float f = ex2f(nmax[n][col] - finite_or_0(top));   // 0 for a warp without a tile
-            if (n * 8 + head < G) {
-#pragma unroll
-                for (int j = 0; j < KS; ++j) {
-                    s_acc[(warp * 8 + head) * D + g * (D / 8) + 2 * j] = acc[n][j][col] * f;
-                    s_acc[(warp * 8 + head) * D + g * (D / 8) + 2 * j + 1] = acc[n][j][col + 2] * f;
+            for (int r = 0; r < 4; ++r) {   // value rows 2t, 2t + 1, 2t + 8, 2t + 9
+                const int row = 2 * t + (r & 1) + 8 * (r >> 1);
+                if constexpr (D == 128) {
+                    const uint4 u = *reinterpret_cast<const uint4*>(stage + kTile * D + piece_at<D>(row, g));
+                    vw[r][0] = u.x, vw[r][1] = u.y, vw[r][2] = u.z, vw[r][3] = u.w;
+                } else {
+                    const uint2 u = *reinterpret_cast<const uint2*>(stage + kTile * D + piece_at<D>(row, g / 2) + (g & 1) * 8);
+                    vw[r][0] = u.x, vw[r][1] = u.y;
                 }
             }
-        }
-        __syncthreads();
-        const int heads = min(8, G - n * 8);
-        for (int i = threadIdx.x; i < heads * D; i += kWarps * 32) {
-            const int head = i / D, col = i % D;
-            float sum = 0.f;
+            __syncwarp();   // every lane has read the stage
+            if (++slot == kStages) slot = 0, phase ^= 1;
+            if (keys.base < keys.from || keys.base + kTile > keys.to) {
+                // Rows that are not visited: a weight of zero would not cancel a NaN.
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) sum += s_acc[(w * 8 + head) * D + col];
-            part[(n * 8 + head) * head_step + col] = sum;
+                for (int r = 0; r < 4; ++r) {
+                    const int tok = keys.base + 2 * t + (r & 1) + 8 * (r >> 1);
+                    if (tok < keys.from || tok >= keys.to) {
+#pragma unroll
+                        for (int w = 0; w < D / 32; ++w) vw[r][w] = 0;
+                    }
+                }
+            }
+
+            // Scores: rows key g and 8 + g, columns heads 2t and 2t + 1.
+            // Two chains of products, to wait less on either.
+            float s[NH][4], s2[NH][4];
+#pragma unroll
+            for (int n = 0; n < NH; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.f;
+            const uint32_t* k0 = reinterpret_cast<const uint32_t*>(kw[0]);
+            const uint32_t* k1 = reinterpret_cast<const uint32_t*>(kw[1]);
+#pragma unroll
+            for (int j = 0; j < KS; ++j) {
+                uint32_t a0, a1, a2, a3;
+                halves_of(k0[j], a0, a2);
+                halves_of(k1[j], a1, a3);
+#pragma unroll
+                for (int n = 0; n < NH; ++n) mma_f16(j & 1 ? s2[n] : s[n], a0, a1, a2, a3, qf[n][j][0], qf[n][j][1]);
+            }
+            // s_j and t_j, and whether one is over kSlack above the reference it
+            // would be subtracted from.
+            float x[NH][4], y[NH][4];
+            bool over = false;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int tok = keys.base + g + 8 * r;
+                const bool on = static_cast<unsigned>(tok - keys.from) < static_cast<unsigned>(keys.to - keys.from);
+                const float kf = __uint_as_float(static_cast<uint32_t>(ku[r]) << 23), ve = static_cast<float>(vu[r] - 127);
+#pragma unroll
+                for (int n = 0; n < NH; ++n)
+#pragma unroll
+                    for (int col = 0; col < 2; ++col) {
+                        const int e = 2 * r + col;
+                        x[n][e] = on ? (s[n][e] + s2[n][e]) * fs[n][col] * kf : -INFINITY;
+                        y[n][e] = x[n][e] + ve;
+                        over |= x[n][e] > m[n][col] + kSlack || y[n][e] > nmax[n][col] + kSlack;
+                    }
+            }
+            if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+                for (int n = 0; n < NH; ++n)
+#pragma unroll
+                    for (int col = 0; col < 2; ++col) {
+                        float xm = fmaxf(x[n][col], x[n][col + 2]), ym = fmaxf(y[n][col], y[n][col + 2]);
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) {
+                            xm = fmaxf(xm, __shfl_xor_sync(0xffffffffu, xm, o));
+                            ym = fmaxf(ym, __shfl_xor_sync(0xffffffffu, ym, o));
+                        }
+                        const float mn = fmaxf(m[n][col], xm), nn = fmaxf(nmax[n][col], ym);
+                        l[n][col] *= ex2f(m[n][col] - mn);
+                        const float ca = ex2f(nmax[n][col] - nn);
+#pragma unroll
+                        for (int j = 0; j < KS; ++j) {
+                            acc[n][j][col] *= ca;
+                            acc[n][j][col + 2] *= ca;
+                        }
+                        m[n][col] = mn;
+                        nmax[n][col] = nn;
+                    }
+            }
+            uint32_t wt[NH][2];
+#pragma unroll
+            for (int n = 0; n < NH; ++n) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    l[n][e & 1] += ex2f(x[n][e] - m[n][e & 1]);
+                    y[n][e] = ex2f(y[n][e] - nmax[n][e & 1]);
+                }
+                wt[n][0] = transpose8x8(pack_half2(y[n][0], y[n][1]));
+                wt[n][1] = transpose8x8(pack_half2(y[n][2], y[n][3]));
+            }
+            // O^T: tile j holds dims D/8 g + 2 j (rows g) and + 1 (rows 8 + g).
+#pragma unroll
+            for (int j = 0; j < KS; ++j) {
+                const uint32_t sel = (j & 1) ? 0x7362 : 0x5140;
+                uint32_t a0, a1, a2, a3;
+                halves_of(__byte_perm(vw[0][j / 2], vw[1][j / 2], sel), a0, a1);
+                halves_of(__byte_perm(vw[2][j / 2], vw[3][j / 2], sel), a2, a3);
+#pragma unroll
+                for (int n = 0; n < NH; ++n) mma_f16(acc[n][j], a0, a1, a2, a3, wt[n][0], wt[n][1]);
+            }
         }
-        __syncthreads();
+
+        // The item's part.
+        float* part = a.part + static_cast<size_t>(item) * G * (D + 4);
+#pragma unroll
+        for (int n = 0; n < NH; ++n)
+#pragma unroll
+            for (int col = 0; col < 2; ++col) {
+                float ls = l[n][col];
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+                const int head = n * 8 + 2 * t + col;
+                if (head < G) {
+                    float* dst = part + head * (D + 4);
+#pragma unroll
+                    for (int j = 0; j < KS; j += 2)
+                        *reinterpret_cast<float4*>(dst + g * (D / 8) + 2 * j) =
+                            make_float4(acc[n][j][col], acc[n][j][col + 2], acc[n][j + 1][col], acc[n][j + 1][col + 2]);
+                    if (g == 0) *reinterpret_cast<float4*>(dst + D) = make_float4(m[n][col], nmax[n][col], ls, 0.f);
+                }
+            }
     }
-    if (threadIdx.x < G) {
-        const int head = threadIdx.x;
-        float top = s_m[0][head], topn = s_n[0][head];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) {
-            top = fmaxf(top, s_m[w][head]);
-            topn = fmaxf(topn, s_n[w][head]);
-        }
-        float sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) sum += s_l[w][head] * ex2f(s_m[w][head] - finite_or_0(top));
-        float* dst = part + head * head_step + D;
-        dst[0] = top;
-        dst[1] = topn;
-        dst[2] = sum;
-    }
-    __syncthreads();   // s_m, s_n, s_l and the queue are free again
-    }   // next unit
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Joins the chunks of one (query head, sequence): block (hq, b), kJoin groups
-// of D threads; group i sums chunks i, i + kJoin, ..., and the groups' sums are
-// added in order.  Launched as a programmatic dependent of the split kernel:
-// it reads the visit, an input, and then waits for that grid's memory.
-constexpr int kJoin = 4;
+// Joins the parts of one (query head, sequence), block (hq, b): groups of D/4
+// threads, four dimensions a thread.  A group takes every kJoinThreads/(D/4)-th
+// part, kAtOnce of them loaded together, with running maxima; the groups join
+// in order.  Launched as a programmatic dependent of the split kernel: it reads
+// the visit, an input, and then waits for that grid's memory.
+constexpr int kJoinThreads = 256;
+constexpr int kAtOnce = 2;
 template <int D>
-__global__ void __launch_bounds__(kJoin * D) decode_e4m3_join_kernel(DecodeE4m3Args a) {
-    __shared__ float s_top[2][kJoin * D / 32];
-    __shared__ float s_sum[kJoin][D], s_l[kJoin];
-    const int hq = blockIdx.x, b = blockIdx.y, col = threadIdx.x % D, grp = threadIdx.x / D;
-    const Visit vis = visit_of(a, a.seq_lens[b], a.gate[b]);
-    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + (static_cast<size_t>(b) * a.Hq + hq) * D;
-    const float* part = a.part + (static_cast<size_t>(b) * a.Hq + hq) * a.max_chunks * (D + 4);
+__global__ void __launch_bounds__(kJoinThreads) decode_e4m3_join_kernel(const __grid_constant__ DecodeE4m3Args a) {
+    constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes;
+    __shared__ float4 s_sum[kGroups][kLanes];
+    __shared__ float3 s_top[kGroups];
+    const int hq = blockIdx.x, b = blockIdx.y, col = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
+    const int G = a.Hq / a.Hkv, h = hq / G;
+    const int tiles = visit_of(a, b).tiles;
+    uint2* o = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + (static_cast<size_t>(b) * a.Hq + hq) * D) + col;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (vis.nc == 0) {   // an empty slot
-        if (grp == 0) o[col] = __float2bfloat16_rn(0.f);
+    if (tiles == 0) {   // an empty slot
+        if (grp == 0) *o = make_uint2(0, 0);
         if (a.lse && threadIdx.x == 0) a.lse[static_cast<size_t>(b) * a.Hq + hq] = -INFINITY;
         return;
     }
-    float m = -INFINITY, n = -INFINITY;
-    for (int c = threadIdx.x; c < vis.nc; c += kJoin * D) {
-        const float2 p = *reinterpret_cast<const float2*>(part + static_cast<size_t>(c) * (D + 4) + D);
-        m = fmaxf(m, p.x);
-        n = fmaxf(n, p.y);
-    }
+    const int run = a.plan[a.B], parts = (tiles + run - 1) / run;
+    const size_t step = static_cast<size_t>(a.Hkv) * G * (D + 4);   // from block to block
+    const float* part = a.part + (static_cast<size_t>(a.plan[b]) * a.Hkv + h) * G * (D + 4) + (hq % G) * (D + 4);
+    float m = kLow, n = kLow, l = 0.f;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int c0 = grp; c0 < parts; c0 += kGroups * kAtOnce) {
+        float4 st[kAtOnce], v[kAtOnce];
 #pragma unroll
-    for (int i = 16; i > 0; i >>= 1) {
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
-        n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, i));
-    }
-    if ((threadIdx.x & 31) == 0) {
-        s_top[0][threadIdx.x / 32] = m;
-        s_top[1][threadIdx.x / 32] = n;
-    }
-    __syncthreads();
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int c = c0 + i * kGroups;
+            st[i] = make_float4(kLow, kLow, 0.f, 0.f);
+            v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (c < parts) {
+                const float4* p = reinterpret_cast<const float4*>(part + c * step);
+                st[i] = __ldcg(p + kLanes);
+                v[i] = __ldcg(p + col);
+            }
+        }
+        float mn = m, nn = n;
 #pragma unroll
-    for (int i = 0; i < kJoin * D / 32; ++i) {
-        m = fmaxf(m, s_top[0][i]);
-        n = fmaxf(n, s_top[1][i]);
+        for (int i = 0; i < kAtOnce; ++i) {
+            mn = fmaxf(mn, st[i].x);
+            nn = fmaxf(nn, st[i].y);
+        }
+        l *= ex2f(m - mn);
+        const float f = ex2f(n - nn);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] *= f;
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            l += st[i].z * ex2f(st[i].x - mn);
+            const float w = ex2f(st[i].y - nn);
+            sum[0] += v[i].x * w;
+            sum[1] += v[i].y * w;
+            sum[2] += v[i].z * w;
+            sum[3] += v[i].w * w;
+        }
+        m = mn;
+        n = nn;
     }
-    const float mr = finite_or_0(m), nr = finite_or_0(n);
-    float l = 0.f, sum = 0.f;
-#pragma unroll 4
-    for (int c = grp; c < vis.nc; c += kJoin) {
-        const float* p = part + static_cast<size_t>(c) * (D + 4);
-        const float4 st = *reinterpret_cast<const float4*>(p + D);
-        l += st.z * ex2f(st.x - mr);
-        sum += p[col] * ex2f(st.y - nr);
+    if (parts > 1) {   // else group 0 has it all
+        s_sum[grp][col] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+        if (col == 0) s_top[grp] = make_float3(m, n, l);
+        __syncthreads();
+        if (grp != 0) return;
+        float mn = m, nn = n;
+#pragma unroll
+        for (int i = 1; i < kGroups; ++i) {
+            mn = fmaxf(mn, s_top[i].x);
+            nn = fmaxf(nn, s_top[i].y);
+        }
+        l *= ex2f(m - mn);
+        const float f = ex2f(n - nn);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] *= f;
+#pragma unroll
+        for (int i = 1; i < kGroups; ++i) {
+            l += s_top[i].z * ex2f(s_top[i].x - mn);
+            const float w = ex2f(s_top[i].y - nn);
+            const float4 v = s_sum[i][col];
+            sum[0] += v.x * w;
+            sum[1] += v.y * w;
+            sum[2] += v.z * w;
+            sum[3] += v.w * w;
+        }
+        m = mn;
+        n = nn;
     }
-    s_sum[grp][col] = sum;
-    if (col == 0) s_l[grp] = l;
-    __syncthreads();
     if (grp != 0) return;
-#pragma unroll
-    for (int i = 1; i < kJoin; ++i) {
-        sum += s_sum[i][col];
-        l += s_l[i];
-    }
-    o[col] = __float2bfloat16_rn(sum / l * ex2f(n - m));
+    const float f = ex2f(n - m);
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(sum[0] / l * f, sum[1] / l * f);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(sum[2] / l * f, sum[3] / l * f);
+    *o = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     if (a.lse && col == 0) a.lse[static_cast<size_t>(b) * a.Hq + hq] = (m + __log2f(l)) * 0.69314718055994531f;
+}
+
+template <int D, int NH, bool WIDE>
+cudaError_t launch_split(const DecodeE4m3Args& a, int sms, cudaStream_t s) {
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_dynamic_smem(decode_e4m3_split_kernel<D, NH, WIDE>, kSharedBytes<D>, done);
+    if (e != cudaSuccess) return e;
+    // At most what is resident at once, and what the longest visits can use.
+    const int64_t visit = (static_cast<int64_t>(a.max_pages) << a.page_lg) / kTile + 1;
+    const int64_t units = (visit * a.B * a.Hkv + kMinRun * kWarps - 1) / (kMinRun * kWarps);
+    const int64_t most = std::min<int64_t>(static_cast<int64_t>(sms) * kBlocksPerSm<NH>, kMaxWarps / kWarps);
+    CUtensorMap k_map, v_map;
+    std::memset(&k_map, 0, sizeof(k_map));
+    std::memset(&v_map, 0, sizeof(v_map));
+    if (WIDE && (!make_tmap_pages_u8(&k_map, a.k_pages, static_cast<uint64_t>(a.Hkv) * D, 1ull << a.page_lg, a.num_pages, D, kTile) ||
+                 !make_tmap_pages_u8(&v_map, a.v_pages, static_cast<uint64_t>(a.Hkv) * D, 1ull << a.page_lg, a.num_pages, D, kTile)))
+        return cudaErrorInvalidValue;
+    decode_e4m3_split_kernel<D, NH, WIDE>
+        <<<static_cast<unsigned>(units < most ? units : most), kWarps * 32, kSharedBytes<D>, s>>>(a, k_map, v_map);
+    return cudaGetLastError();
 }
 
 template <int D, int NH>
 cudaError_t launch_split(const DecodeE4m3Args& a, int sms, cudaStream_t s) {
-    static std::atomic<uint64_t> done{0};
-    cudaError_t e = allow_dynamic_smem(decode_e4m3_split_kernel<D, NH>, kSharedBytes<D>, done);
-    if (e != cudaSuccess) return e;
-    const int64_t units = static_cast<int64_t>(a.B) * a.Hkv * a.max_chunks;
-    const int64_t most = static_cast<int64_t>(sms) * kBlocksPerSm;
-    decode_e4m3_split_kernel<D, NH><<<static_cast<unsigned>(units < most ? units : most), kWarps * 32, kSharedBytes<D>, s>>>(a);
-    return cudaGetLastError();
+    return (1 << a.page_lg) >= kTile ? launch_split<D, NH, true>(a, sms, s) : launch_split<D, NH, false>(a, sms, s);
 }
 
 template <int D>
@@ -600,7 +617,7 @@ cudaError_t launch_d(const DecodeE4m3Args& a, int sms, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.Hq, a.B);
-    cfg.blockDim = dim3(kJoin * D);
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -613,20 +630,17 @@ cudaError_t launch_d(const DecodeE4m3Args& a, int sms, cudaStream_t s) {
 
 }  // namespace
 
-// A visit of v keys (v <= max_len + min(n_anchor, max_len)) has at most
-// v / chunk + 2.75 chunks (two segments, each cut at multiples of 16 keys, of
-// at least four tiles a chunk): kChunksWanted + 2 where the chunk is below
-// kMaxChunk (then kChunksWanted chunks hold v), else ceil(v / kMaxChunk) + 2.
-int decode_e4m3_max_chunks(int64_t max_len, int n_anchor) {
-    const int64_t v = max_len + (n_anchor < max_len ? n_anchor : max_len);
-    const int64_t longest = (v + kMaxChunk - 1) / kMaxChunk;
-    return static_cast<int>((longest > kChunksWanted ? longest : kChunksWanted) + 3);
+// The parts, then the plan: prefix tiles of every sequence and a run's length.
+DecodeE4m3Ws decode_e4m3_ws_layout(int B, int Hq, int Hkv, int d) {
+    DecodeE4m3Ws L;
+    const size_t parts = static_cast<size_t>(kMaxWarps) + static_cast<size_t>(B) * Hkv;
+    L.plan = sizeof(float) * parts * (Hq / Hkv) * (d + 4);
+    L.plan = (L.plan + 255) & ~static_cast<size_t>(255);
+    L.total = (L.plan + sizeof(int) * (static_cast<size_t>(B) + 1) + 255) & ~static_cast<size_t>(255);
+    return L;
 }
 
-size_t decode_e4m3_workspace_bytes(int B, int Hq, int d, int max_chunks) {
-    const size_t n = sizeof(float) * static_cast<size_t>(B) * Hq * max_chunks * (d + 4);
-    return (n + 255) & ~static_cast<size_t>(255);
-}
+cudaError_t decode_e4m3_set_wait_limit(uint64_t ns) { return set_wait_limit_of_unit(ns); }
 
 cudaError_t launch_decode_e4m3(const DecodeE4m3Args& a, int d, int sms, cudaStream_t s) {
     return d == 128 ? launch_d<128>(a, sms, s) : launch_d<64>(a, sms, s);

@@ -101,6 +101,20 @@ bool make_tmap_4d_bf16(CUtensorMap* map, const void* base, uint64_t d0, uint64_t
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_tmap_pages_u8(CUtensorMap* map, const void* base, uint64_t token_bytes, uint64_t page_size,
+                        uint64_t num_pages, uint32_t box_bytes, uint32_t box_tokens) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {token_bytes, page_size, num_pages};
+    const cuuint64_t strides[2] = {token_bytes, token_bytes * page_size};
+    const cuuint32_t box[3] = {box_bytes, box_tokens, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE,
+              box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 DualWs dual_ws_layout(int B, int N, int Hq, int d, int dtype) {
     auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
     DualWs L;
@@ -142,7 +156,7 @@ void swiattn_set_profile_events(void* start, void* stop) {
 
 int swiattn_set_wait_limit_ns(uint64_t ns) {
     if (prefill_set_wait_limit(ns) != cudaSuccess || dual_set_wait_limit(ns) != cudaSuccess ||
-        bwd_set_wait_limit(ns) != cudaSuccess)
+        bwd_set_wait_limit(ns) != cudaSuccess || decode_e4m3_set_wait_limit(ns) != cudaSuccess)
         return SWIATTN_ECUDA;
     return SWIATTN_OK;
 }
@@ -837,7 +851,7 @@ int decode_e4m3_sizes_ok(int B, int max_pages, int page_size, int Hq, int Hkv, i
     if (page_size <= 0 || (page_size & (page_size - 1)) != 0 || max_pages <= 0 ||
         (int64_t)max_pages * page_size > (1 << 30))
         return SWIATTN_EINVAL;
-    if (Hq / Hkv > 16 || B > 65535 || Hkv > 65535) return SWIATTN_EUNSUPPORTED;
+    if (Hq / Hkv > 16 || B > 65535 || (int64_t)B * Hkv > (1 << 30)) return SWIATTN_EUNSUPPORTED;
     return SWIATTN_OK;
 }
 
@@ -847,8 +861,7 @@ size_t swiattn_decode_paged_e4m3_workspace(int B, int max_pages, int page_size, 
                                            int d, int W, int n_anchor) {
     if (decode_e4m3_sizes_ok(B, max_pages, page_size, Hq, Hkv, d, W, n_anchor) != SWIATTN_OK)
         return 0;
-    return decode_e4m3_workspace_bytes(
-        B, Hq, d, decode_e4m3_max_chunks((int64_t)max_pages * page_size, n_anchor));
+    return decode_e4m3_ws_layout(B, Hq, Hkv, d).total;
 }
 
 int swiattn_decode_paged_e4m3(const void* q, const void* k_pages, const void* v_pages,
@@ -862,19 +875,18 @@ int swiattn_decode_paged_e4m3(const void* q, const void* k_pages, const void* v_
     if (ok == SWIATTN_EINVAL || num_pages <= 0) return SWIATTN_EINVAL;
     if (!q || !k_pages || !v_pages || !k_exp || !v_exp || !block_table || !seq_lens || !gate || !o)
         return SWIATTN_EINVAL;
-    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o))
+    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(k_exp) ||
+        !aligned16(v_exp) || !aligned16(o))
         return SWIATTN_EINVAL;
     if (!(scale > 0.f) || !(scale - scale == 0.f)) return SWIATTN_EINVAL;
     if (dtype != SWIATTN_BF16 && dtype != SWIATTN_F32) return SWIATTN_EINVAL;
     if (ok != SWIATTN_OK || dtype != SWIATTN_BF16) return SWIATTN_EUNSUPPORTED;
     if ((int64_t)num_pages * page_size > (int64_t(1) << 32)) return SWIATTN_EUNSUPPORTED;
-    DecodeE4m3Args a;
-    a.max_chunks = decode_e4m3_max_chunks((int64_t)max_pages * page_size, n_anchor);
-    if (!workspace || !aligned256(workspace) ||
-        workspace_bytes < decode_e4m3_workspace_bytes(B, Hq, d, a.max_chunks))
-        return SWIATTN_EINVAL;
+    const DecodeE4m3Ws L = decode_e4m3_ws_layout(B, Hq, Hkv, d);
+    if (!workspace || !aligned256(workspace) || workspace_bytes < L.total) return SWIATTN_EINVAL;
     DeviceInfo di;
     if (!device_info(di)) return SWIATTN_ECUDA;
+    DecodeE4m3Args a;
     a.q = q;
     a.k_pages = static_cast<const uint8_t*>(k_pages);
     a.v_pages = static_cast<const uint8_t*>(v_pages);
@@ -886,6 +898,7 @@ int swiattn_decode_paged_e4m3(const void* q, const void* k_pages, const void* v_
     a.o = o;
     a.lse = lse;
     a.part = static_cast<float*>(workspace);
+    a.plan = reinterpret_cast<int*>(static_cast<char*>(workspace) + L.plan);
     a.err = di.err;
     a.B = B;
     a.max_pages = max_pages;

@@ -22,10 +22,12 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;   // 2 s
 constexpr uint64_t kDrainLimitNs = 100000000ull;   // 0.1 s, waits while aborting
 
 // Per translation unit setters of the wait limit (current device; 0 restores
-// the default): the routed prefill, the dual-branch forward, the backward.
+// the default): the routed prefill, the dual-branch forward, the backward,
+// decode over e4m3 pages.
 cudaError_t prefill_set_wait_limit(uint64_t ns);
 cudaError_t dual_set_wait_limit(uint64_t ns);
 cudaError_t bwd_set_wait_limit(uint64_t ns);
+cudaError_t decode_e4m3_set_wait_limit(uint64_t ns);
 
 // Lets `kernel` use `bytes` of dynamic shared memory on the current device.
 // The attribute belongs to the device's context, so it is set once per
@@ -321,13 +323,17 @@ struct DecodeE4m3Args {
     const uint8_t* gate;        // [B]
     void* o;                    // bf16 [B, Hq, d]
     float* lse;                 // [B, Hq], nullable
-    float* part;                // [B, Hq, max_chunks, d + 4]
+    float* part;                // workspace, as DecodeE4m3Ws
+    int* plan;
     unsigned int* err;
-    int B, max_pages, page_lg, num_pages, Hq, Hkv, W, n_anchor, max_chunks;
+    int B, max_pages, page_lg, num_pages, Hq, Hkv, W, n_anchor;
     float scale_log2;           // softmax scale times log2(e)
 };
-int decode_e4m3_max_chunks(int64_t max_len, int n_anchor);
-size_t decode_e4m3_workspace_bytes(int B, int Hq, int d, int max_chunks);
+struct DecodeE4m3Ws {
+    size_t plan;   // int [B + 1], after the parts (d + 4 floats for each query head of one)
+    size_t total;
+};
+DecodeE4m3Ws decode_e4m3_ws_layout(int B, int Hq, int Hkv, int d);
 cudaError_t launch_decode_e4m3(const DecodeE4m3Args& a, int d, int sms, cudaStream_t s);
 
 // Timing hook around the dominant kernel of a call (no-ops unless set).
@@ -337,5 +343,9 @@ void prof_stop(cudaStream_t s);
 // TMA descriptor creation through the driver entry point (no libcuda link).
 bool make_tmap_4d_bf16(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                        uint64_t d3, uint32_t box0, uint32_t box2);
+// Pages [num_pages, page_size] of token_bytes each, loaded box_tokens tokens of
+// box_bytes (64 or 128, the swizzle span) at a time.
+bool make_tmap_pages_u8(CUtensorMap* map, const void* base, uint64_t token_bytes, uint64_t page_size,
+                        uint64_t num_pages, uint32_t box_bytes, uint32_t box_tokens);
 
 }  // namespace swi
