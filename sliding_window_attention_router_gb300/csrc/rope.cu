@@ -20,30 +20,47 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
+#include <algorithm>
+#include <atomic>
 
 namespace swi {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxHalf = 64;   // rotated pairs of a head: d <= 128
+constexpr int kMaxHalf = 64;     // rotated pairs of a head: d <= 128
+constexpr int kMaxTile = 16;     // tokens of a tile
+template <typename T>
+constexpr int kAtOnce = sizeof(T) == 2 ? 4 : 2;   // slots a thread loads before it rotates one (64 bytes each in fp32)
 
-// ---- eight elements of T as floats -----------------------------------------
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
+// ---- eight elements of T: as loaded, as floats ------------------------------
+template <typename T>
+struct Eight;
+template <>
+struct Eight<__nv_bfloat16> {
+    uint4 u;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void get(float* x) const {
+        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __bfloat1622float2(h[i]);
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __bfloat1622float2(h[i]);
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+        }
     }
-}
-__device__ __forceinline__ void load8(const float* p, float* x) {
-    const float4 a = *reinterpret_cast<const float4*>(p);
-    const float4 b = *reinterpret_cast<const float4*>(p + 4);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
+};
+template <>
+struct Eight<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = __ldcs(reinterpret_cast<const float4*>(p));
+        b = __ldcs(reinterpret_cast<const float4*>(p + 4));
+    }
+    __device__ __forceinline__ void get(float* x) const {
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+        x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
+};
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
     uint4 u;
     __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
@@ -96,64 +113,7 @@ __device__ __forceinline__ float2 cos_sin(uint64_t F, int p, float m) {
     return make_float2(m * c, m * s);
 }
 
-// A slot is 16 elements of one head: lane `sub` of the head's d/16 lanes.
-// Rotated slots (sub < rot/16) hold eight pairs, the others pass through.
-struct Slot {
-    int lo, hi;   // element offsets of its two groups of eight
-};
-__device__ __forceinline__ Slot slot_of(int sub, int rot, bool interleaved) {
-    if (!interleaved && sub * 16 < rot) return {sub * 8, rot / 2 + sub * 8};
-    return {sub * 16, sub * 16 + 8};
-}
-
-// Rotates the 16 elements of a slot; cs holds (m cos, m sin) of its eight pairs.
-template <bool BACKWARD>
-__device__ __forceinline__ void rotate(float* x, const float2* cs, bool interleaved) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float c = cs[e].x, s = BACKWARD ? -cs[e].y : cs[e].y;
-        if (interleaved) {
-            const float a = x[2 * e], b = x[2 * e + 1];
-            x[2 * e] = a * c - b * s;
-            x[2 * e + 1] = b * c + a * s;
-        } else {
-            const float a = x[e], b = x[8 + e];
-            x[e] = a * c - b * s;
-            x[8 + e] = b * c + a * s;
-        }
-    }
-}
-
-// ---- rotation of q and k ---------------------------------------------------
-// One token a block: the block's first threads take the token's cosines and
-// sines, then each thread rotates slot after slot of its heads.
-template <typename T, bool BACKWARD>
-__global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a) {
-    __shared__ float2 cs[kMaxHalf];
-    const int64_t t = blockIdx.x;
-    const int pos = a.positions ? a.positions[t] : static_cast<int>(t % a.N);
-    if (threadIdx.x < a.rot / 2) cs[threadIdx.x] = cos_sin(turn_fraction(a.inv_freq[threadIdx.x]), pos, a.factor);
-    __syncthreads();
-    const int lph = a.d / 16;
-    const int slots = (a.Hq + a.Hkv) * lph;
-    for (int i = threadIdx.x; i < slots; i += kThreads) {
-        const int head = i / lph, sub = i % lph;
-        const Slot sl = slot_of(sub, a.rot, a.interleaved);
-        const bool isq = head < a.Hq;
-        const T* src = isq ? static_cast<const T*>(a.q) + t * a.q_stride + head * a.d
-                           : static_cast<const T*>(a.k) + t * a.k_stride + (head - a.Hq) * a.d;
-        T* dst = isq ? static_cast<T*>(a.q_out) + t * a.q_out_stride + head * a.d
-                     : static_cast<T*>(a.k_out) + t * a.k_out_stride + (head - a.Hq) * a.d;
-        float x[16];
-        load8(src + sl.lo, x);
-        load8(src + sl.hi, x + 8);
-        if (sub * 16 < a.rot) rotate<BACKWARD>(x, cs + sub * 8, a.interleaved);
-        store8(dst + sl.lo, x);
-        store8(dst + sl.hi, x + 8);
-    }
-}
-
-// ---- append ----------------------------------------------------------------
+// ---- where a new token goes --------------------------------------------------
 // Largest b in [0, B) with starts[b] <= t, by one warp (32 probes a step), or
 // -1.  Every probe is inside [0, B) whatever the array holds.
 __device__ __forceinline__ int find_sequence(const int32_t* starts, int B, int t) {
@@ -178,7 +138,7 @@ struct Place {
     int pos;
     int64_t row;
 };
-__device__ __forceinline__ Place place_of(const AppendArgs& a, int t, unsigned int* err) {
+__device__ __forceinline__ Place place_of(const RotateArgs& a, int t) {
     int b = t, after = 1;   // tokens of the sequence from t on
     if (a.starts) {
         b = find_sequence(a.starts, a.B, t);
@@ -195,7 +155,7 @@ __device__ __forceinline__ Place place_of(const AppendArgs& a, int t, unsigned i
             return {static_cast<int>(pos),
                     (static_cast<int64_t>(page) << a.page_lg) + (pos & ((1 << a.page_lg) - 1))};
     }
-    if ((threadIdx.x & 31) == 0) atomicOr(err, kDevErrInput);
+    if ((threadIdx.x & 31) == 0) atomicOr(a.err, kDevErrInput);
     return {0, -1};
 }
 
@@ -207,102 +167,220 @@ __device__ __forceinline__ int row_exponent(float amax) {
     return max(-126, min(127, e));
 }
 
-// One token a block.
-template <typename T, bool E4M3>
-__global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a, unsigned int* err) {
-    __shared__ float2 cs[kMaxHalf];
-    __shared__ Place where;
-    const int t = blockIdx.x;
-    if (threadIdx.x < 32) {
-        const Place p = place_of(a, t, err);
-        if (threadIdx.x == 0) where = p;
-    }
-    __syncthreads();
-    const int pos = where.pos;
-    const int64_t row = where.row;
-    if (row < 0) return;
-    if (threadIdx.x < a.rot / 2) cs[threadIdx.x] = cos_sin(turn_fraction(a.inv_freq[threadIdx.x]), pos, a.factor);
-    __syncthreads();
+// ---- the kernel ------------------------------------------------------------
+// A token's heads (q's, k's, v's) are cut into slots of 16 elements, d/16 to a
+// head: a rotated slot holds eight whole pairs, as two groups of eight
+// elements (rot/2 apart, or side by side when interleaved), the others two
+// groups that pass through.  One thread loads a slot with two 16-byte loads (bf16).
+//
+// HBM-bound: 6 operations on 4 bytes.  A block takes tiles of `tile` tokens,
+// one after another (so the frequencies' 64-bit fractions are taken once a
+// block), and per tile
+//   1. starts the loads of kAtOnce slots a thread, which need no position,
+//   2. works out the tile's cosines and sines in shared memory, one for all
+//      heads, and the places of the next tile's tokens,
+//   3. after one barrier rotates, converts and stores.
+// One barrier a tile is enough: a warp that is ahead writes the table of a tile
+// on (two tables) and the places of two tiles on (three) while others still read.
+enum Mode { kRope, kRopeBackward, kAppend, kAppendE4m3 };
+
+// Where a thread's slot is within a tile; the same for every tile.
+struct Slot {
+    int token;    // in the tile; -1: none
+    int which;    // 0 q, 1 k, 2 v
+    int head, sub;
+    int lo, hi;   // element offsets of its two groups within the head
+    bool turned;
+};
+__device__ __forceinline__ Slot slot_of(int i, int slots, const RotateArgs& a) {
+    const int lph = a.d / 16, nq = a.Hq * lph, nk = a.Hkv * lph;
+    Slot s;
+    s.token = i / slots;
+    const int j = i - s.token * slots;
+    s.which = j < nq ? 0 : j < nq + nk ? 1 : 2;
+    const int k = s.which == 0 ? j : s.which == 1 ? j - nq : j - nq - nk;
+    s.head = k / lph;
+    s.sub = k - s.head * lph;
+    s.turned = s.which < 2 && s.sub * 16 < a.rot;
+    const bool apart = s.turned && !a.interleaved;
+    s.lo = apart ? s.sub * 8 : s.sub * 16;
+    s.hi = apart ? a.rot / 2 + s.sub * 8 : s.sub * 16 + 8;
+    if (s.token >= a.tile) s.token = -1;
+    return s;
+}
+
+// (m cos, m sin) of frequency f of a token, two frequencies to 16 bytes, laid
+// out so that the lanes of a head read neighbouring 16 bytes.
+__device__ __forceinline__ int table_at(int f) { return ((f & 7) >> 1) * 16 + (f >> 3) * 2 + (f & 1); }
+
+template <typename T, int MODE>
+__global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant__ RotateArgs a) {
+    constexpr bool kStored = MODE == kAppend || MODE == kAppendE4m3;   // k and v go to pages
+    constexpr int U = kAtOnce<T>;
+    __shared__ __align__(16) float2 s_table[2][kMaxTile][kMaxHalf];
+    __shared__ Place s_place[3][kMaxTile];
+    __shared__ uint64_t s_freq[kMaxHalf];
     const int lph = a.d / 16;
-    const int nq = a.Hq * lph, nk = a.Hkv * lph;
-    const int slots = nq + 2 * nk;
-    // Whole warps go round together, for the shuffles of the row maximum.
-    for (int i0 = threadIdx.x & ~31; i0 < slots; i0 += kThreads) {
-        const int i = i0 + (threadIdx.x & 31);
-        const bool active = i < slots;
-        const int which = i < nq ? 0 : i < nq + nk ? 1 : 2;
-        const int j = which == 0 ? i : which == 1 ? i - nq : i - nq - nk;
-        const int head = j / lph, sub = j % lph;
-        const Slot sl = slot_of(sub, which == 2 ? 0 : a.rot, a.interleaved);
-        float x[16];
-        if (active) {
-            const T* src = which == 0   ? static_cast<const T*>(a.q) + t * a.q_stride
-                           : which == 1 ? static_cast<const T*>(a.k) + t * a.k_stride
-                                        : static_cast<const T*>(a.v) + t * a.v_stride;
-            src += head * a.d;
-            load8(src + sl.lo, x);
-            load8(src + sl.hi, x + 8);
-            if (which < 2 && sub * 16 < a.rot) rotate<false>(x, cs + sub * 8, a.interleaved);
-        }
-        if (which == 0) {
-            if (active) {
-                T* dst = static_cast<T*>(a.q_out) + (static_cast<int64_t>(t) * a.Hq + head) * a.d;
-                store8(dst + sl.lo, x);
-                store8(dst + sl.hi, x + 8);
+    const int slots = (a.Hq + (kStored ? 2 : 1) * a.Hkv) * lph;
+    const int tiles = (a.tokens - 1) / a.tile + 1;
+    const int warp = threadIdx.x / 32;
+
+    auto places = [&](int tile, int at) {   // of a tile's tokens, a warp a token
+        for (int j = warp; j < a.tile; j += kThreads / 32) {
+            const int t = tile * a.tile + j;
+            Place p = {0, -1};
+            if (t < a.tokens) {
+                if (kStored) p = place_of(a, t);
+                else p = {a.positions ? a.positions[t] : t % a.N, 0};
             }
+            if (threadIdx.x % 32 == 0) s_place[at][j] = p;
         }
-        if constexpr (E4M3) {
-            float amax = 0.f;   // a NaN does not enter it
-            if (active) {
+    };
+    if (static_cast<int>(threadIdx.x) < a.rot / 2) s_freq[threadIdx.x] = turn_fraction(a.inv_freq[threadIdx.x]);
+    places(blockIdx.x, 0);
+    __syncthreads();
+
+    int buf = 0, now = 0;   // this tile's table and places
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1, now = now == 2 ? 0 : now + 1) {
+        const int64_t t0 = static_cast<int64_t>(tile) * a.tile;
+        const int left = a.tokens - tile * a.tile;   // tokens from t0 on
+        for (int i0 = 0; i0 < a.tile * slots; i0 += U * kThreads) {
+            Slot slot[U];
+            Eight<T> raw[U][2];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e]));
-            }
-            for (int o = lph / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            if (active && which > 0) {
-                const int e = row_exponent(amax);
-                const float inv = __uint_as_float(static_cast<uint32_t>(127 - max(e, -126)) << 23);
-                uint8_t* dst = static_cast<uint8_t*>(which == 1 ? a.k_pages : a.v_pages) + (row * a.Hkv + head) * a.d;
-#pragma unroll
-                for (int c = 0; c < 16; ++c) x[c] *= inv;
-                store8_e4m3(dst + sl.lo, x);
-                store8_e4m3(dst + sl.hi, x + 8);
-                if (sub == 0) {
-                    uint8_t* ex = which == 1 ? a.k_exp : a.v_exp;
-                    const int64_t page = row >> a.page_lg, slot = row & ((1 << a.page_lg) - 1);
-                    ex[((page * a.Hkv + head) << a.page_lg) + slot] = static_cast<uint8_t>(e + 127);
+            for (int u = 0; u < U; ++u) {
+                slot[u] = slot_of(i0 + u * kThreads + threadIdx.x, slots, a);
+                if (slot[u].token >= left) slot[u].token = -1;
+                if (slot[u].token >= 0) {
+                    const int64_t t = t0 + slot[u].token;
+                    const T* src = slot[u].which == 0   ? static_cast<const T*>(a.q) + t * a.q_stride
+                                   : slot[u].which == 1 ? static_cast<const T*>(a.k) + t * a.k_stride
+                                                        : static_cast<const T*>(a.v) + t * a.v_stride;
+                    src += slot[u].head * a.d;
+                    raw[u][0].load(src + slot[u].lo);
+                    raw[u][1].load(src + slot[u].hi);
                 }
             }
-        } else {
-            if (active && which > 0) {
-                T* dst = static_cast<T*>(which == 1 ? a.k_pages : a.v_pages) + (row * a.Hkv + head) * a.d;
-                store8(dst + sl.lo, x);
-                store8(dst + sl.hi, x + 8);
+            if (i0 == 0) {
+                const int half = a.rot / 2, n = min(left, a.tile) * half;
+                for (int i = threadIdx.x; i < n; i += kThreads) {
+                    const int j = i / half, f = i - j * half;
+                    s_table[buf][j][table_at(f)] = cos_sin(s_freq[f], s_place[now][j].pos, a.factor);
+                }
+                if (tile + gridDim.x < tiles) places(tile + gridDim.x, now == 2 ? 0 : now + 1);
+                __syncthreads();
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const Slot& s = slot[u];
+                float x[16];
+                const int64_t row = s.token >= 0 ? s_place[now][s.token].row : -1;
+                if (s.token >= 0) {
+                    raw[u][0].get(x);
+                    raw[u][1].get(x + 8);
+                }
+                if (s.token >= 0 && s.turned) {
+                    const float4* table = reinterpret_cast<const float4*>(s_table[buf][s.token]) + s.sub;
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) {
+                        const float4 cs = table[e / 2 * 8];
+                        const float c[2] = {cs.x, cs.z};
+                        const float sn[2] = {MODE == kRopeBackward ? -cs.y : cs.y, MODE == kRopeBackward ? -cs.w : cs.w};
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            if (a.interleaved) {
+                                float &p = x[2 * (e + r)], &q = x[2 * (e + r) + 1];
+                                const float y = p * c[r] - q * sn[r];
+                                q = q * c[r] + p * sn[r];
+                                p = y;
+                            } else {
+                                float &p = x[e + r], &q = x[8 + e + r];
+                                const float y = p * c[r] - q * sn[r];
+                                q = q * c[r] + p * sn[r];
+                                p = y;
+                            }
+                        }
+                    }
+                }
+                const int64_t t = t0 + s.token;
+                if (s.which == 0 || !kStored) {
+                    if (row >= 0) {
+                        T* dst = s.which == 0 ? static_cast<T*>(a.q_out) + t * a.q_out_stride
+                                              : static_cast<T*>(a.k_out) + t * a.k_out_stride;
+                        dst += s.head * a.d;
+                        store8(dst + s.lo, x);
+                        store8(dst + s.hi, x + 8);
+                    }
+                }
+                if constexpr (MODE == kAppend) {
+                    if (s.which > 0 && row >= 0) {
+                        T* dst = static_cast<T*>(s.which == 1 ? a.k_out : a.v_out) + (row * a.Hkv + s.head) * a.d;
+                        store8(dst + s.lo, x);
+                        store8(dst + s.hi, x + 8);
+                    }
+                }
+                if constexpr (MODE == kAppendE4m3) {
+                    float amax = 0.f;   // a NaN does not enter it
+                    if (s.token >= 0) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e]));
+                    }
+                    for (int o = lph / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                    if (s.which > 0 && row >= 0) {
+                        const int e = row_exponent(amax);
+                        const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                        uint8_t* dst = static_cast<uint8_t*>(s.which == 1 ? a.k_out : a.v_out) + (row * a.Hkv + s.head) * a.d;
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) x[c] *= inv;
+                        store8_e4m3(dst + s.lo, x);
+                        store8_e4m3(dst + s.hi, x + 8);
+                        if (s.sub == 0) {
+                            const int64_t page = row >> a.page_lg, at = row & ((1 << a.page_lg) - 1);
+                            (s.which == 1 ? a.k_exp : a.v_exp)[((page * a.Hkv + s.head) << a.page_lg) + at] =
+                                static_cast<uint8_t>(e + 127);
+                        }
+                    }
+                }
             }
         }
+        if (tile + gridDim.x >= tiles) break;
     }
+}
+
+// Tokens of a tile: what kAtOnce slots a thread cover, less where that would
+// leave SMs without a tile.  Blocks: what is resident at once.
+template <typename T, int MODE>
+cudaError_t launch(RotateArgs a, int sms, cudaStream_t s) {
+    const int slots = (a.Hq + (MODE >= kAppend ? 2 : 1) * a.Hkv) * (a.d / 16);
+    int tile = std::max(1, std::min(kMaxTile, kAtOnce<T> * kThreads / slots));
+    a.tile = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(tile, a.tokens / (2 * sms))));
+    static std::atomic<int> resident[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    int per_sm = dev < 64 ? resident[dev].load(std::memory_order_relaxed) : 0;
+    if (per_sm == 0) {
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, rotate_kernel<T, MODE>, kThreads, 0);
+        if (e != cudaSuccess) return e;
+        per_sm = std::max(per_sm, 1);
+        if (dev < 64) resident[dev].store(per_sm, std::memory_order_relaxed);
+    }
+    const int64_t tiles = (a.tokens - 1) / a.tile + 1;
+    rotate_kernel<T, MODE><<<static_cast<unsigned>(std::min<int64_t>(tiles, static_cast<int64_t>(sms) * per_sm)), kThreads, 0, s>>>(a);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_rope(const RopeArgs& a, int dtype, bool backward, cudaStream_t s) {
-    const unsigned grid = static_cast<unsigned>(a.tokens);
-    if (dtype == SWIATTN_BF16) {
-        if (backward) rope_kernel<__nv_bfloat16, true><<<grid, kThreads, 0, s>>>(a);
-        else rope_kernel<__nv_bfloat16, false><<<grid, kThreads, 0, s>>>(a);
-    } else {
-        if (backward) rope_kernel<float, true><<<grid, kThreads, 0, s>>>(a);
-        else rope_kernel<float, false><<<grid, kThreads, 0, s>>>(a);
-    }
-    return cudaGetLastError();
+cudaError_t launch_rope(const RotateArgs& a, int dtype, bool backward, int sms, cudaStream_t s) {
+    if (dtype == SWIATTN_BF16)
+        return backward ? launch<__nv_bfloat16, kRopeBackward>(a, sms, s) : launch<__nv_bfloat16, kRope>(a, sms, s);
+    return backward ? launch<float, kRopeBackward>(a, sms, s) : launch<float, kRope>(a, sms, s);
 }
 
-cudaError_t launch_append(const AppendArgs& a, int dtype, int page_dtype, unsigned int* err,
-                          cudaStream_t s) {
-    const unsigned grid = static_cast<unsigned>(a.tokens);
-    if (page_dtype == SWIATTN_E4M3) append_kernel<__nv_bfloat16, true><<<grid, kThreads, 0, s>>>(a, err);
-    else if (dtype == SWIATTN_BF16) append_kernel<__nv_bfloat16, false><<<grid, kThreads, 0, s>>>(a, err);
-    else append_kernel<float, false><<<grid, kThreads, 0, s>>>(a, err);
-    return cudaGetLastError();
+cudaError_t launch_append(const RotateArgs& a, int dtype, int page_dtype, int sms, cudaStream_t s) {
+    if (page_dtype == SWIATTN_E4M3) return launch<__nv_bfloat16, kAppendE4m3>(a, sms, s);
+    return dtype == SWIATTN_BF16 ? launch<__nv_bfloat16, kAppend>(a, sms, s) : launch<float, kAppend>(a, sms, s);
 }
 
 }  // namespace swi

@@ -728,7 +728,9 @@ int rope_call(const void* q, const void* k, const int32_t* positions, const doub
               !token_stride_ok(k_out_stride, Hkv, d, dtype) ||
               (k == k_out && k_stride != k_out_stride)))
         return SWIATTN_EINVAL;
-    RopeArgs a;
+    DeviceInfo di;
+    if (!device_info(di)) return SWIATTN_ECUDA;
+    RotateArgs a = {};
     a.q = q;
     a.k = k;
     a.positions = positions;
@@ -739,7 +741,7 @@ int rope_call(const void* q, const void* k, const int32_t* positions, const doub
     a.k_stride = k_stride;
     a.q_out_stride = q_out_stride;
     a.k_out_stride = k_out_stride;
-    a.tokens = (int64_t)B * N;
+    a.tokens = B * N;
     a.N = N;
     a.Hq = q ? Hq : 0;
     a.Hkv = k ? Hkv : 0;
@@ -749,7 +751,7 @@ int rope_call(const void* q, const void* k, const int32_t* positions, const doub
     a.factor = factor;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     prof_start(s);
-    const cudaError_t e = launch_rope(a, dtype, backward, s);
+    const cudaError_t e = launch_rope(a, dtype, backward, di.sms, s);
     prof_stop(s);
     return launched(e);
 }
@@ -805,7 +807,7 @@ int swiattn_append_paged(const void* q, const void* k, const void* v, const int3
         return SWIATTN_EINVAL;
     DeviceInfo di;
     if (!device_info(di)) return SWIATTN_ECUDA;
-    AppendArgs a;
+    RotateArgs a = {};
     a.q = q;
     a.k = k;
     a.v = v;
@@ -814,10 +816,12 @@ int swiattn_append_paged(const void* q, const void* k, const void* v, const int3
     a.block_table = block_table;
     a.inv_freq = inv_freq;
     a.q_out = q_out;
-    a.k_pages = k_pages;
-    a.v_pages = v_pages;
+    a.k_out = k_pages;
+    a.v_out = v_pages;
     a.k_exp = k_exp;
     a.v_exp = v_exp;
+    a.err = di.err;
+    a.q_out_stride = (int64_t)Hq * d;
     a.q_stride = q_stride;
     a.k_stride = k_stride;
     a.v_stride = v_stride;
@@ -835,7 +839,7 @@ int swiattn_append_paged(const void* q, const void* k, const void* v, const int3
     a.factor = factor;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     prof_start(s);
-    const cudaError_t e = launch_append(a, dtype, page_dtype, di.err, s);
+    const cudaError_t e = launch_append(a, dtype, page_dtype, di.sms, s);
     prof_stop(s);
     return launched(e);
 }

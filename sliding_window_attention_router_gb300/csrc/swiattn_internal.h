@@ -275,41 +275,33 @@ cudaError_t launch_decode_paged(const void* q, const void* kp, const void* vp,
                                 unsigned int* err, cudaStream_t s);
 
 // ------------------------------------------- rotation and paged append ------
-struct RopeArgs {
+struct RotateArgs {
     const void* q;              // [tokens, Hq, d], q_stride elements from token to token
-    const void* k;
-    const int32_t* positions;   // nullptr: token t of sequences of N is at t % N
+    const void* k;              // [tokens, Hkv, d]; Hq or Hkv 0: that tensor is absent
+    const void* v;              // append: [tokens, Hkv, d]
     const double* inv_freq;     // [rot/2]
     void* q_out;
-    void* k_out;
-    int64_t q_stride, k_stride, q_out_stride, k_out_stride;
-    int64_t tokens;
-    int N, Hq, Hkv, d, rot;     // Hq or Hkv 0: that tensor is absent
+    void* k_out;                // append: pages [num_pages, 1 << page_lg, Hkv, d]
+    void* v_out;
+    int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
+    int tokens, Hq, Hkv, d, rot;
     int interleaved;
     float factor;
-};
-cudaError_t launch_rope(const RopeArgs& a, int dtype, bool backward, cudaStream_t s);
-
-struct AppendArgs {
-    const void* q;              // [tokens, Hq, d] (Hq 0: absent), q_stride elements a token
-    const void* k;              // [tokens, Hkv, d]
-    const void* v;
+    int tile;                   // tokens of a tile, set by the launcher
+    // rope
+    const int32_t* positions;   // nullptr: token t of sequences of N is at t % N
+    int N;
+    // append
     const int32_t* starts;      // [B+1] first token of each sequence; nullptr: one token each
     const int32_t* seq_lens;    // [B] lengths with the new tokens
     const int32_t* block_table; // [B, max_pages]
-    const double* inv_freq;     // [rot/2]
-    void* q_out;                // [tokens, Hq, d]
-    void* k_pages;              // [num_pages, 1 << page_lg, Hkv, d]
-    void* v_pages;
     uint8_t* k_exp;             // e4m3 pages: [num_pages, Hkv, 1 << page_lg]
     uint8_t* v_exp;
-    int64_t q_stride, k_stride, v_stride;
-    int tokens, B, max_pages, page_lg, num_pages, Hq, Hkv, d, rot;
-    int interleaved;
-    float factor;
+    unsigned int* err;
+    int B, max_pages, page_lg, num_pages;
 };
-cudaError_t launch_append(const AppendArgs& a, int dtype, int page_dtype, unsigned int* err,
-                          cudaStream_t s);
+cudaError_t launch_rope(const RotateArgs& a, int dtype, bool backward, int sms, cudaStream_t s);
+cudaError_t launch_append(const RotateArgs& a, int dtype, int page_dtype, int sms, cudaStream_t s);
 
 // -------------------------------------------------- decode over e4m3 pages ---
 struct DecodeE4m3Args {
