@@ -11,9 +11,9 @@
 // The angle: w_f / 2pi is held as a 64-bit binary fraction of a turn F, so
 // p F mod 2^64 is the angle modulo a whole turn without any rounding (a float
 // product would be off by p w_f 2^-24: 0.06 rad at position 10^6).  The nearest
-// quarter turn comes off its top 32 bits as a whole number, so what goes to
-// sincospif is within an eighth of a turn and its rounding to a float costs
-// at most 2^-28 of a turn.
+// quarter turn comes off its top 32 bits as a whole number; what is left is
+// within an eighth of a turn, where rounding it to a float costs at most 2^-28
+// of a turn, and goes to the Taylor polynomials of sine and cosine.
 
 #include "swiattn.h"
 #include "swiattn_internal.h"
@@ -21,16 +21,13 @@
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <algorithm>
-#include <atomic>
 
 namespace swi {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kMaxHalf = 64;     // rotated pairs of a head: d <= 128
-constexpr int kMaxTile = 16;     // tokens of a tile
-template <typename T>
-constexpr int kAtOnce = sizeof(T) == 2 ? 4 : 2;   // slots a thread loads before it rotates one (64 bytes each in fp32)
+constexpr int kMaxThreads = 256;  // of a block
+constexpr int kMaxHalf = 64;      // rotated pairs of a head: d <= 128
+constexpr int kMaxTokens = 8;     // of a block
 
 // ---- eight elements of T: as loaded, as floats ------------------------------
 template <typename T>
@@ -86,24 +83,37 @@ __device__ __forceinline__ void store8_e4m3(uint8_t* p, const float* x) {
 
 // ---- angles ----------------------------------------------------------------
 // Frequency w (radians a position) as a 64-bit fraction of a turn, modulo a
-// whole turn (positions are whole numbers, so whole turns do not matter).
-// 1/2pi is held in two doubles, so the fraction is right to 2^-63 for |w| <= 1.
+// whole turn (positions are whole numbers, so whole turns do not matter).  With
+// w = M 2^E, M of 53 bits, it is M * (2^66 / 2pi) * 2^(E - 2), a 128-bit whole
+// number shifted; |w| <= 1 keeps it right to the last bit but one.  Whole-number
+// arithmetic, as the double-precision pipe is a sixty-fourth as wide.
 __device__ __forceinline__ uint64_t turn_fraction(double w) {
-    constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;   // 1/2pi = kHi + kLo
-    const double p = w * kHi;
-    const double e = fma(w, kHi, -p) + w * kLo;
-    const double f = p - floor(p);                     // exact, in [0, 1)
-    const double hi = floor(f * 4294967296.0);         // first 32 bits
-    const double lo = (f * 4294967296.0 - hi) * 4294967296.0 + e * 18446744073709551616.0;
-    return (static_cast<uint64_t>(hi) << 32) + static_cast<uint64_t>(static_cast<int64_t>(rint(lo)));
+    const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(w));
+    const int e = static_cast<int>(bits >> 52 & 2047);
+    const uint64_t m = (bits & 0xfffffffffffffull) | (e ? 1ull << 52 : 0ull);
+    constexpr uint64_t kInv = 0xa2f9836e4e44152aull;   // 2^66 / 2pi
+    const uint64_t hi = __umul64hi(m, kInv), lo = m * kInv;
+    const int shift = 1077 - (e ? e : 1);   // right, 2 - E
+    uint64_t f;
+    if (shift >= 128) f = 0;
+    else if (shift >= 64) f = hi >> (shift - 64);
+    else if (shift > 0) f = (hi << (64 - shift)) | (lo >> shift);
+    else f = shift > -64 ? lo << -shift : 0;
+    return bits >> 63 ? 0 - f : f;
 }
-// m cos and m sin of position p times frequency F.
+// m cos and m sin of position p times frequency F.  With |z| <= pi/4 the first
+// terms left out are z^11/11! < 2^-29 of the sine and z^12/12! < 2^-32.  (The
+// library's sincospif in their place took 7 times the instructions, half as
+// many as the whole rotation of 16 + 16 heads.)
 __device__ __forceinline__ float2 cos_sin(uint64_t F, int p, float m) {
     const uint64_t turn = F * static_cast<uint64_t>(static_cast<int64_t>(p));
     const uint32_t top = static_cast<uint32_t>(turn >> 32);
     const uint32_t quarter = (top + 0x20000000u) >> 30;
-    float s, c;
-    sincospif(static_cast<float>(static_cast<int32_t>(top - (quarter << 30))) * 0x1p-31f, &s, &c);
+    const float z = static_cast<float>(static_cast<int32_t>(top - (quarter << 30))) * 1.46291807927e-9f;   // 2 pi 2^-32
+    const float q = z * z;
+    const float sp = fmaf(q, fmaf(q, fmaf(q, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6);
+    const float cp = fmaf(q, fmaf(q, fmaf(q, fmaf(q, -1.f / 3628800, 1.f / 40320), -1.f / 720), 1.f / 24), -0.5f);
+    float s = fmaf(z * q, sp, z), c = fmaf(q, cp, 1.f);
     if (quarter & 1) {   // a quarter turn on: (c, s) -> (-s, c)
         const float o = c;
         c = -s;
@@ -131,32 +141,36 @@ __device__ __forceinline__ int find_sequence(const int32_t* starts, int B, int t
     }
 }
 
-// Position and pool row (page * page_size + slot) of new token t; row < 0: the
-// token is not stored (a padding row, an empty slot, or bad input, which is
-// reported).  Called by a whole warp.
+// New token t: its sequence b and position; b < 0 where it is not stored (a
+// padding row, an empty slot, or a position off the table, which is reported).
+// Called by a whole warp.  Up to 32 sequences take one round trip to memory.
 struct Place {
-    int pos;
-    int64_t row;
+    int b, pos;
 };
 __device__ __forceinline__ Place place_of(const RotateArgs& a, int t) {
-    int b = t, after = 1;   // tokens of the sequence from t on
-    if (a.starts) {
+    int b = t, after = 1, len;   // tokens of the sequence from t on, its length
+    if (!a.starts) {
+        len = a.seq_lens[t];
+    } else if (a.B <= 32) {
+        const int lane = threadIdx.x & 31, i = min(lane, a.B - 1);
+        const int from = a.starts[i], to = a.starts[i + 1], mine = a.seq_lens[i];
+        const unsigned hit = __ballot_sync(0xffffffffu, lane < a.B && from <= t && t < to);
+        if (hit == 0) return {-1, 0};
+        b = 31 - __clz(hit);
+        after = __shfl_sync(0xffffffffu, to, b) - t;
+        len = __shfl_sync(0xffffffffu, mine, b);
+    } else {
         b = find_sequence(a.starts, a.B, t);
-        if (b < 0) return {0, -1};
+        if (b < 0) return {-1, 0};
         after = a.starts[b + 1] - t;
-        if (after <= 0) return {0, -1};
+        len = a.seq_lens[b];
+        if (after <= 0) return {-1, 0};
     }
-    const int len = a.seq_lens[b];
-    if (len == 0) return {0, -1};
+    if (len == 0) return {-1, 0};
     const int64_t pos = static_cast<int64_t>(len) - after;
-    if (pos >= 0 && (pos >> a.page_lg) < a.max_pages) {
-        const int32_t page = a.block_table[static_cast<int64_t>(b) * a.max_pages + (pos >> a.page_lg)];
-        if (page >= 0 && page < a.num_pages)
-            return {static_cast<int>(pos),
-                    (static_cast<int64_t>(page) << a.page_lg) + (pos & ((1 << a.page_lg) - 1))};
-    }
+    if (pos >= 0 && (pos >> a.page_lg) < a.max_pages) return {b, static_cast<int>(pos)};
     if ((threadIdx.x & 31) == 0) atomicOr(a.err, kDevErrInput);
-    return {0, -1};
+    return {-1, 0};
 }
 
 // Exponent e of the smallest power of two with amax <= 448 * 2^e, within
@@ -171,216 +185,194 @@ __device__ __forceinline__ int row_exponent(float amax) {
 // A token's heads (q's, k's, v's) are cut into slots of 16 elements, d/16 to a
 // head: a rotated slot holds eight whole pairs, as two groups of eight
 // elements (rot/2 apart, or side by side when interleaved), the others two
-// groups that pass through.  One thread loads a slot with two 16-byte loads (bf16).
+// groups that pass through.
 //
-// HBM-bound: 6 operations on 4 bytes.  A block takes tiles of `tile` tokens,
-// one after another (so the frequencies' 64-bit fractions are taken once a
-// block), and per tile
-//   1. starts the loads of kAtOnce slots a thread, which need no position,
-//   2. works out the tile's cosines and sines in shared memory, one for all
-//      heads, and the places of the next tile's tokens,
+// HBM-bound: 6 operations on 4 bytes.  A block takes U tokens a thread of one
+// slot, `span` tokens side by side, and
+//   1. starts all its loads, which need no position,
+//   2. finds the tokens' places and their cosines and sines, once for all
+//      heads, in shared memory (a warp a token and 32 frequencies),
 //   3. after one barrier rotates, converts and stores.
-// One barrier a tile is enough: a warp that is ahead writes the table of a tile
-// on (two tables) and the places of two tiles on (three) while others still read.
+// Blocks are small and many: while some wait in 2, others load and store.
 enum Mode { kRope, kRopeBackward, kAppend, kAppendE4m3 };
 
-// Where a thread's slot is within a tile; the same for every tile.
-struct Slot {
-    int token;    // in the tile; -1: none
-    int which;    // 0 q, 1 k, 2 v
-    int head, sub;
-    int lo, hi;   // element offsets of its two groups within the head
-    bool turned;
-};
-__device__ __forceinline__ Slot slot_of(int i, int slots, const RotateArgs& a) {
-    const int lph = a.d / 16, nq = a.Hq * lph, nk = a.Hkv * lph;
-    Slot s;
-    s.token = i / slots;
-    const int j = i - s.token * slots;
-    s.which = j < nq ? 0 : j < nq + nk ? 1 : 2;
-    const int k = s.which == 0 ? j : s.which == 1 ? j - nq : j - nq - nk;
-    s.head = k / lph;
-    s.sub = k - s.head * lph;
-    s.turned = s.which < 2 && s.sub * 16 < a.rot;
-    const bool apart = s.turned && !a.interleaved;
-    s.lo = apart ? s.sub * 8 : s.sub * 16;
-    s.hi = apart ? a.rot / 2 + s.sub * 8 : s.sub * 16 + 8;
-    if (s.token >= a.tile) s.token = -1;
-    return s;
+template <typename T, int MODE>
+constexpr int kAtOnce = sizeof(T) == 4 ? 1 : MODE == kAppendE4m3 ? 4 : 2;   // U
+
+// cos and sin of frequency f: two frequencies (c, c, s, s) to 16 bytes, laid out
+// so that the lanes of a head read neighbouring 16 bytes.
+__device__ __forceinline__ int table_at(int f) { return ((f & 7) >> 1) * 32 + (f >> 3) * 4 + (f & 1); }
+
+template <bool BACKWARD>
+__device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
+    if (BACKWARD) s = -s;
+    const float y = a * c - b * s;
+    b = b * c + a * s;
+    a = y;
 }
 
-// (m cos, m sin) of frequency f of a token, two frequencies to 16 bytes, laid
-// out so that the lanes of a head read neighbouring 16 bytes.
-__device__ __forceinline__ int table_at(int f) { return ((f & 7) >> 1) * 16 + (f >> 3) * 2 + (f & 1); }
+template <typename T, int MODE, int D>
+__global__ void __launch_bounds__(kMaxThreads) rotate_kernel(const __grid_constant__ RotateArgs a) {
+    constexpr bool kStored = MODE >= kAppend;   // k and v go to pages
+    constexpr bool kBackward = MODE == kRopeBackward;
+    constexpr int U = kAtOnce<T, MODE>, lph = D / 16;
+    __shared__ __align__(16) float s_table[kMaxTokens][2 * kMaxHalf];
+    __shared__ int64_t s_row[kMaxTokens];
+    const int half = a.rot / 2;
+    const int t0 = blockIdx.x * (U * a.span), part = blockIdx.y;
+    const int tokens = min(a.tokens - t0, U * a.span);
 
-template <typename T, int MODE>
-__global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant__ RotateArgs a) {
-    constexpr bool kStored = MODE == kAppend || MODE == kAppendE4m3;   // k and v go to pages
-    constexpr int U = kAtOnce<T>;
-    __shared__ __align__(16) float2 s_table[2][kMaxTile][kMaxHalf];
-    __shared__ Place s_place[3][kMaxTile];
-    __shared__ uint64_t s_freq[kMaxHalf];
-    const int lph = a.d / 16;
-    const int slots = (a.Hq + (kStored ? 2 : 1) * a.Hkv) * lph;
-    const int tiles = (a.tokens - 1) / a.tile + 1;
-    const int warp = threadIdx.x / 32;
+    // This thread's slot: of the part's slots, side by side with other tokens'.
+    const int beside = a.span == 1 ? threadIdx.x >= a.part_slots : threadIdx.x / a.part_slots;   // token of the span
+    const int i = part * a.part_slots + threadIdx.x - beside * a.part_slots;
+    int head = i / lph;   // q's, then k's, then v's
+    const int sub = i % lph;
+    const bool on = beside < a.span && head < a.Hq + (kStored ? 2 : 1) * a.Hkv;
+    const int which = head < a.Hq ? 0 : head < a.Hq + a.Hkv ? 1 : 2;
+    head -= which == 0 ? 0 : which == 1 ? a.Hq : a.Hq + a.Hkv;
+    const bool turned = which < 2 && sub * 16 < a.rot;
+    const bool apart = turned && !a.interleaved;
+    const int lo = head * D + (apart ? sub * 8 : sub * 16), apart_by = apart ? half : 8;
 
-    auto places = [&](int tile, int at) {   // of a tile's tokens, a warp a token
-        for (int j = warp; j < a.tile; j += kThreads / 32) {
-            const int t = tile * a.tile + j;
-            Place p = {0, -1};
-            if (t < a.tokens) {
-                if (kStored) p = place_of(a, t);
-                else p = {a.positions ? a.positions[t] : t % a.N, 0};
+    Eight<T> raw[U][2];
+    {
+        const int64_t stride = which == 0 ? a.q_stride : which == 1 ? a.k_stride : a.v_stride;
+        const T* src = static_cast<const T*>(which == 0 ? a.q : which == 1 ? a.k : a.v) + (t0 + beside) * stride + lo;
+#pragma unroll
+        for (int u = 0; u < U; ++u, src += a.span * stride)
+            if (on && u * a.span + beside < tokens) {
+                raw[u][0].load(src);
+                raw[u][1].load(src + apart_by);
             }
-            if (threadIdx.x % 32 == 0) s_place[at][j] = p;
+    }
+
+    // Places and tables: task x is token x / pieces, frequencies 32 (x % pieces) on.
+    const bool table_used = part * (a.part_slots / lph) < a.Hq + a.Hkv;   // a part may hold values alone
+    const int pieces = table_used ? max((half + 31) / 32, 1) : 1;
+    for (int x = threadIdx.x / 32; x < tokens * pieces; x += blockDim.x / 32) {
+        const int j = pieces == 2 ? x >> 1 : x, f = (pieces == 2 ? (x & 1) * 32 : 0) + (threadIdx.x & 31);
+        const int t = t0 + j;
+        Place place = {0, 0};
+        int page = 0;
+        if (kStored) {
+            place = place_of(a, t);
+            page = place.b < 0 ? -1 : a.block_table[static_cast<int64_t>(place.b) * a.max_pages + (place.pos >> a.page_lg)];
+        } else {
+            place.pos = a.positions ? a.positions[t] : t % a.N;
         }
-    };
-    if (static_cast<int>(threadIdx.x) < a.rot / 2) s_freq[threadIdx.x] = turn_fraction(a.inv_freq[threadIdx.x]);
-    places(blockIdx.x, 0);
+        if (table_used && f < half) {   // while the page number is on its way
+            const float2 cs = cos_sin(turn_fraction(a.inv_freq[f]), place.pos, a.factor);
+            s_table[j][table_at(f)] = cs.x;
+            s_table[j][table_at(f) + 2] = cs.y;
+        }
+        if ((threadIdx.x & 31) == 0) {   // the pieces of a token agree
+            int64_t row = 0;
+            if (kStored) {
+                row = page < 0 || page >= a.num_pages ? -1 : (static_cast<int64_t>(page) << a.page_lg) + (place.pos & ((1 << a.page_lg) - 1));
+                if (row < 0 && place.b >= 0) atomicOr(a.err, kDevErrInput);
+            }
+            s_row[j] = row;
+        }
+    }
     __syncthreads();
 
-    int buf = 0, now = 0;   // this tile's table and places
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1, now = now == 2 ? 0 : now + 1) {
-        const int64_t t0 = static_cast<int64_t>(tile) * a.tile;
-        const int left = a.tokens - tile * a.tile;   // tokens from t0 on
-        for (int i0 = 0; i0 < a.tile * slots; i0 += U * kThreads) {
-            Slot slot[U];
-            Eight<T> raw[U][2];
+    const bool paged = kStored && which > 0;
+    const int size = MODE == kAppendE4m3 && paged ? 1 : static_cast<int>(sizeof(T));
+    char* const dst = static_cast<char*>(which == 0 ? a.q_out : which == 1 ? a.k_out : a.v_out) + lo * size;
+    const int64_t out_stride = (paged ? a.Hkv * D : which == 0 ? a.q_out_stride : a.k_out_stride) * size;
+    const unsigned paged_lanes = MODE == kAppendE4m3 ? __ballot_sync(0xffffffffu, paged) : 0;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                slot[u] = slot_of(i0 + u * kThreads + threadIdx.x, slots, a);
-                if (slot[u].token >= left) slot[u].token = -1;
-                if (slot[u].token >= 0) {
-                    const int64_t t = t0 + slot[u].token;
-                    const T* src = slot[u].which == 0   ? static_cast<const T*>(a.q) + t * a.q_stride
-                                   : slot[u].which == 1 ? static_cast<const T*>(a.k) + t * a.k_stride
-                                                        : static_cast<const T*>(a.v) + t * a.v_stride;
-                    src += slot[u].head * a.d;
-                    raw[u][0].load(src + slot[u].lo);
-                    raw[u][1].load(src + slot[u].hi);
-                }
-            }
-            if (i0 == 0) {
-                const int half = a.rot / 2, n = min(left, a.tile) * half;
-                for (int i = threadIdx.x; i < n; i += kThreads) {
-                    const int j = i / half, f = i - j * half;
-                    s_table[buf][j][table_at(f)] = cos_sin(s_freq[f], s_place[now][j].pos, a.factor);
-                }
-                if (tile + gridDim.x < tiles) places(tile + gridDim.x, now == 2 ? 0 : now + 1);
-                __syncthreads();
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const Slot& s = slot[u];
-                float x[16];
-                const int64_t row = s.token >= 0 ? s_place[now][s.token].row : -1;
-                if (s.token >= 0) {
-                    raw[u][0].get(x);
-                    raw[u][1].get(x + 8);
-                }
-                if (s.token >= 0 && s.turned) {
-                    const float4* table = reinterpret_cast<const float4*>(s_table[buf][s.token]) + s.sub;
+    for (int u = 0; u < U; ++u) {
+        const int token = u * a.span + beside;
+        const bool mine = on && token < tokens;
+        float x[16];
+        int64_t row = -1;
+        if (mine) {
+            row = s_row[token];
+            raw[u][0].get(x);
+            raw[u][1].get(x + 8);
+            if (turned) {
+                const float4* table = reinterpret_cast<const float4*>(s_table[token]) + sub;
+                if (a.interleaved) {
 #pragma unroll
                     for (int e = 0; e < 8; e += 2) {
                         const float4 cs = table[e / 2 * 8];
-                        const float c[2] = {cs.x, cs.z};
-                        const float sn[2] = {MODE == kRopeBackward ? -cs.y : cs.y, MODE == kRopeBackward ? -cs.w : cs.w};
+                        turn<kBackward>(x[2 * e], x[2 * e + 1], cs.x, cs.z);
+                        turn<kBackward>(x[2 * e + 2], x[2 * e + 3], cs.y, cs.w);
+                    }
+                } else {
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            if (a.interleaved) {
-                                float &p = x[2 * (e + r)], &q = x[2 * (e + r) + 1];
-                                const float y = p * c[r] - q * sn[r];
-                                q = q * c[r] + p * sn[r];
-                                p = y;
-                            } else {
-                                float &p = x[e + r], &q = x[8 + e + r];
-                                const float y = p * c[r] - q * sn[r];
-                                q = q * c[r] + p * sn[r];
-                                p = y;
-                            }
-                        }
-                    }
-                }
-                const int64_t t = t0 + s.token;
-                if (s.which == 0 || !kStored) {
-                    if (row >= 0) {
-                        T* dst = s.which == 0 ? static_cast<T*>(a.q_out) + t * a.q_out_stride
-                                              : static_cast<T*>(a.k_out) + t * a.k_out_stride;
-                        dst += s.head * a.d;
-                        store8(dst + s.lo, x);
-                        store8(dst + s.hi, x + 8);
-                    }
-                }
-                if constexpr (MODE == kAppend) {
-                    if (s.which > 0 && row >= 0) {
-                        T* dst = static_cast<T*>(s.which == 1 ? a.k_out : a.v_out) + (row * a.Hkv + s.head) * a.d;
-                        store8(dst + s.lo, x);
-                        store8(dst + s.hi, x + 8);
-                    }
-                }
-                if constexpr (MODE == kAppendE4m3) {
-                    float amax = 0.f;   // a NaN does not enter it
-                    if (s.token >= 0) {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e]));
-                    }
-                    for (int o = lph / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                    if (s.which > 0 && row >= 0) {
-                        const int e = row_exponent(amax);
-                        const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                        uint8_t* dst = static_cast<uint8_t*>(s.which == 1 ? a.k_out : a.v_out) + (row * a.Hkv + s.head) * a.d;
-#pragma unroll
-                        for (int c = 0; c < 16; ++c) x[c] *= inv;
-                        store8_e4m3(dst + s.lo, x);
-                        store8_e4m3(dst + s.hi, x + 8);
-                        if (s.sub == 0) {
-                            const int64_t page = row >> a.page_lg, at = row & ((1 << a.page_lg) - 1);
-                            (s.which == 1 ? a.k_exp : a.v_exp)[((page * a.Hkv + s.head) << a.page_lg) + at] =
-                                static_cast<uint8_t>(e + 127);
-                        }
+                    for (int e = 0; e < 8; e += 2) {
+                        const float4 cs = table[e / 2 * 8];
+                        turn<kBackward>(x[e], x[8 + e], cs.x, cs.z);
+                        turn<kBackward>(x[e + 1], x[9 + e], cs.y, cs.w);
                     }
                 }
             }
         }
-        if (tile + gridDim.x >= tiles) break;
+        if (MODE == kAppendE4m3 && paged) {
+            float amax = 0.f;   // a NaN does not enter it
+            if (mine) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e]));
+            }
+#pragma unroll
+            for (int o = lph / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(paged_lanes, amax, o));
+            if (row >= 0) {
+                const int e = row_exponent(amax);
+                const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) x[c] *= inv;
+                uint8_t* to = reinterpret_cast<uint8_t*>(dst + row * out_stride);
+                store8_e4m3(to, x);
+                store8_e4m3(to + apart_by, x + 8);
+                if (sub == 0) {
+                    const int64_t page = row >> a.page_lg, at = row & ((1 << a.page_lg) - 1);
+                    (which == 1 ? a.k_exp : a.v_exp)[((page * a.Hkv + head) << a.page_lg) + at] = static_cast<uint8_t>(e + 127);
+                }
+            }
+        } else if (row >= 0) {
+            T* to = reinterpret_cast<T*>(dst + (paged ? row : t0 + token) * out_stride);
+            store8(to, x);
+            store8(to + apart_by, x + 8);
+        }
     }
 }
 
-// Tokens of a tile: what kAtOnce slots a thread cover, less where that would
-// leave SMs without a tile.  Blocks: what is resident at once.
-template <typename T, int MODE>
-cudaError_t launch(RotateArgs a, int sms, cudaStream_t s) {
-    const int slots = (a.Hq + (MODE >= kAppend ? 2 : 1) * a.Hkv) * (a.d / 16);
-    int tile = std::max(1, std::min(kMaxTile, kAtOnce<T> * kThreads / slots));
-    a.tile = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(tile, a.tokens / (2 * sms))));
-    static std::atomic<int> resident[64];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    int per_sm = dev < 64 ? resident[dev].load(std::memory_order_relaxed) : 0;
-    if (per_sm == 0) {
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, rotate_kernel<T, MODE>, kThreads, 0);
-        if (e != cudaSuccess) return e;
-        per_sm = std::max(per_sm, 1);
-        if (dev < 64) resident[dev].store(per_sm, std::memory_order_relaxed);
-    }
-    const int64_t tiles = (a.tokens - 1) / a.tile + 1;
-    rotate_kernel<T, MODE><<<static_cast<unsigned>(std::min<int64_t>(tiles, static_cast<int64_t>(sms) * per_sm)), kThreads, 0, s>>>(a);
+// A block covers all slots of a token, as many tokens side by side as 128
+// threads hold; more than kMaxThreads slots are cut into parts of whole heads
+// and at most 128 slots (16 + 16 + 16 heads: bf16 append 126 us, in two parts 130,
+// whole 161, as then only two blocks fit an SM; 16 + 4 heads: whole 27 us, in two
+// parts 29).
+template <typename T, int MODE, int D>
+cudaError_t launch(RotateArgs a, cudaStream_t s) {
+    constexpr int U = kAtOnce<T, MODE>, lph = D / 16;
+    const int heads = a.Hq + (MODE >= kAppend ? 2 : 1) * a.Hkv;
+    const int parts = heads * lph <= kMaxThreads ? 1 : (heads * lph + 127) / 128;
+    a.part_slots = (heads + parts - 1) / parts * lph;
+    a.span = std::max(1, std::min({128 / a.part_slots, kMaxTokens / U, (a.tokens + U - 1) / U}));
+    const int threads = (a.part_slots * a.span + 31) / 32 * 32;
+    const dim3 grid((a.tokens - 1) / (U * a.span) + 1, parts);
+    rotate_kernel<T, MODE, D><<<grid, threads, 0, s>>>(a);
     return cudaGetLastError();
+}
+
+template <typename T, int MODE>
+cudaError_t launch(const RotateArgs& a, cudaStream_t s) {
+    return a.d == 128 ? launch<T, MODE, 128>(a, s) : launch<T, MODE, 64>(a, s);
 }
 
 }  // namespace
 
-cudaError_t launch_rope(const RotateArgs& a, int dtype, bool backward, int sms, cudaStream_t s) {
+cudaError_t launch_rope(const RotateArgs& a, int dtype, bool backward, cudaStream_t s) {
     if (dtype == SWIATTN_BF16)
-        return backward ? launch<__nv_bfloat16, kRopeBackward>(a, sms, s) : launch<__nv_bfloat16, kRope>(a, sms, s);
-    return backward ? launch<float, kRopeBackward>(a, sms, s) : launch<float, kRope>(a, sms, s);
+        return backward ? launch<__nv_bfloat16, kRopeBackward>(a, s) : launch<__nv_bfloat16, kRope>(a, s);
+    return backward ? launch<float, kRopeBackward>(a, s) : launch<float, kRope>(a, s);
 }
 
-cudaError_t launch_append(const RotateArgs& a, int dtype, int page_dtype, int sms, cudaStream_t s) {
-    if (page_dtype == SWIATTN_E4M3) return launch<__nv_bfloat16, kAppendE4m3>(a, sms, s);
-    return dtype == SWIATTN_BF16 ? launch<__nv_bfloat16, kAppend>(a, sms, s) : launch<float, kAppend>(a, sms, s);
+cudaError_t launch_append(const RotateArgs& a, int dtype, int page_dtype, cudaStream_t s) {
+    if (page_dtype == SWIATTN_E4M3) return launch<__nv_bfloat16, kAppendE4m3>(a, s);
+    return dtype == SWIATTN_BF16 ? launch<__nv_bfloat16, kAppend>(a, s) : launch<float, kAppend>(a, s);
 }
 
 }  // namespace swi

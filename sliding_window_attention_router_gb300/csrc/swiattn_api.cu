@@ -728,8 +728,6 @@ int rope_call(const void* q, const void* k, const int32_t* positions, const doub
               !token_stride_ok(k_out_stride, Hkv, d, dtype) ||
               (k == k_out && k_stride != k_out_stride)))
         return SWIATTN_EINVAL;
-    DeviceInfo di;
-    if (!device_info(di)) return SWIATTN_ECUDA;
     RotateArgs a = {};
     a.q = q;
     a.k = k;
@@ -751,7 +749,7 @@ int rope_call(const void* q, const void* k, const int32_t* positions, const doub
     a.factor = factor;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     prof_start(s);
-    const cudaError_t e = launch_rope(a, dtype, backward, di.sms, s);
+    const cudaError_t e = launch_rope(a, dtype, backward, s);
     prof_stop(s);
     return launched(e);
 }
@@ -839,7 +837,7 @@ int swiattn_append_paged(const void* q, const void* k, const void* v, const int3
     a.factor = factor;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     prof_start(s);
-    const cudaError_t e = launch_append(a, dtype, page_dtype, di.sms, s);
+    const cudaError_t e = launch_append(a, dtype, page_dtype, s);
     prof_stop(s);
     return launched(e);
 }

@@ -287,7 +287,7 @@ struct RotateArgs {
     int tokens, Hq, Hkv, d, rot;
     int interleaved;
     float factor;
-    int tile;                   // tokens of a tile, set by the launcher
+    int part_slots, span;   // how the work is cut, set by the launcher
     // rope
     const int32_t* positions;   // nullptr: token t of sequences of N is at t % N
     int N;
@@ -300,8 +300,8 @@ struct RotateArgs {
     unsigned int* err;
     int B, max_pages, page_lg, num_pages;
 };
-cudaError_t launch_rope(const RotateArgs& a, int dtype, bool backward, int sms, cudaStream_t s);
-cudaError_t launch_append(const RotateArgs& a, int dtype, int page_dtype, int sms, cudaStream_t s);
+cudaError_t launch_rope(const RotateArgs& a, int dtype, bool backward, cudaStream_t s);
+cudaError_t launch_append(const RotateArgs& a, int dtype, int page_dtype, cudaStream_t s);
 
 // -------------------------------------------------- decode over e4m3 pages ---
 struct DecodeE4m3Args {
