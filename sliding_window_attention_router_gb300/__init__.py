@@ -511,31 +511,29 @@ def _same(t, name: str, index: int, dtype=None):
 
 
 def _tokens(t, name: str, lead, index: int, dtype):
-    """Check q/k/v of one call, [*lead, heads, d] on device `index` with packed heads and one
+    """Check q/k/v of one call, lead + [heads, d] on device `index` with packed heads and one
     distance between tokens (a view of a fused projection is fine); returns (heads, d, that
     distance in elements)."""
     if not isinstance(t, torch.Tensor) or t.get_device() != index:
         raise ValueError(f"{name} must be a tensor on cuda:{index}")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    shape = t.shape
-    n = len(lead)
-    if len(shape) != n + 2 or shape[:n] != lead:
-        raise ValueError(f"{name} must be {list(lead)} + [heads, d], got {list(shape)}")
-    heads, d = shape[n:]
+    *rows, heads, d = t.shape
+    if rows != lead:
+        raise ValueError(f"{name} must be {lead} + [heads, d], got {list(t.shape)}")
     if t.is_contiguous():
         return heads, d, heads * d
-    stride = t.stride()
-    if stride[n + 1] != 1 or (heads > 1 and stride[n] != d):
+    *strides, head_step, last = t.stride()
+    if last != 1 or (heads > 1 and head_step != d):
         raise ValueError(f"{name}: heads and their elements must be contiguous")
-    step, rows = heads * d, 1
-    for i in range(n - 1, -1, -1):   # dimensions of size 1 may have any stride
-        if shape[i] > 1:
-            if rows == 1:
-                step = stride[i]
-            elif stride[i] != rows * step:
+    step, count = heads * d, 1
+    for size, stride in zip(reversed(rows), reversed(strides)):
+        if size > 1:   # dimensions of size 1 may have any stride
+            if count == 1:
+                step = stride
+            elif stride != count * step:
                 raise ValueError(f"{name}: tokens must be evenly spaced")
-            rows *= shape[i]
+            count *= size
     return heads, d, step
 
 
@@ -560,7 +558,8 @@ def _rope(where, q, k, inv_freq, positions, interleaved, factor, out):
     index = _gpu(some, "q and k")
     if some.dim() != 4:
         raise ValueError(f"q and k must be [B, N, heads, d], got {list(some.shape)}")
-    lead, d, dtype = some.shape[:2], some.shape[3], some.dtype
+    B, N, _, d = some.shape
+    lead, dtype = [B, N], some.dtype
     results, sizes = [], []
     for name, t, o in (("q", q, out and out[0]), ("k", k, out and out[1])):
         if t is None:
@@ -581,7 +580,6 @@ def _rope(where, q, k, inv_freq, positions, interleaved, factor, out):
         results.append(o)
         sizes.append((heads, step, out_step))
     _same(inv_freq, "inv_freq", index, torch.float64)
-    B, N = lead
     if positions is not None and _same(positions, "positions", index, torch.int32).numel() != B * N:
         raise ValueError(f"positions must be [{B}, {N}]")
     (Hq, qs, qos), (Hkv, ks, kos) = sizes
@@ -632,7 +630,8 @@ def append_paged(q, k, v, k_pages, v_pages, block_table, seq_lens, inv_freq=None
     in place; returns the rotated q [T,Hq,d] (None without q).  Rows of q's result that no
     sequence owns are left as they were (a result allocated here: undefined)."""
     index = _gpu(k, "k")
-    lead, dtype = k.shape[:1], k.dtype
+    T, dtype = k.shape[0], k.dtype
+    lead = [T]
     Hkv, d, ks = _tokens(k, "k", lead, index, dtype)
     vh, vd, vs = _tokens(v, "v", lead, index, dtype)
     if vh != Hkv or vd != d:
@@ -672,7 +671,7 @@ def append_paged(q, k, v, k_pages, v_pages, block_table, seq_lens, inv_freq=None
         rot_dim = 2 * _same(inv_freq, "inv_freq", index, torch.float64).numel()
     _launch("swiattn_append_paged", index, _addr(q), k.data_ptr(), v.data_ptr(), _addr(starts),
             seq_lens.data_ptr(), block_table.data_ptr(), _addr(inv_freq), _addr(out),
-            k_pages.data_ptr(), v_pages.data_ptr(), ke, ve, lead[0], B, table[1], shape[1],
+            k_pages.data_ptr(), v_pages.data_ptr(), ke, ve, T, B, table[1], shape[1],
             shape[0], Hq, Hkv, d, rot_dim, bool(interleaved), factor, qs, ks, vs, _DT[dtype], kind)
     return out
 

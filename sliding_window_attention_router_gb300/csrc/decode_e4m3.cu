@@ -12,21 +12,34 @@
 // order 1 at the largest contribution, whatever the rows' sizes.  Parts (m,
 // n, l, a) of the key set join by their maxima.
 //
-// The products run on mma.sync m16n8k16 (fp16 in, fp32 accumulate).  An e4m3
-// value is exact in fp16, and q is made so by a power of two per head (exact
-// for every element within 2^31 of the head's largest).  The weights are
-// rounded to fp16, 2^-11 of each, under the bf16 result's own 2^-8.  The
-// bound is the cache's bytes, not the products: 16 keys of one head (4 KiB at
-// d = 128) take 16 products for up to 8 query heads, a small part of the
-// tensor rate, so the register path (no shared-memory staging, no TMEM) is
-// the short one:
-//   S^T [16 keys x 8 heads] = K Q^T: a thread's 16-byte pieces of two key rows
-//   are its A fragments after conversion, the order of d being free as long
-//   as q's fragments follow it;
-//   O^T [d x 8 heads] += V^T W^T: a thread's 16-byte pieces of four value rows
-//   are its A fragments after pairing bytes of neighbouring rows (one byte
-//   permute for two registers), and W^T comes from S^T by two 8 x 8
-//   transposes inside the warp.
+// The bound is the cache's bytes: 16 keys of one head are 4 KiB (d = 128), and
+// with up to 8 query heads to a key head 16 tensor-core products.  So the work
+// is to keep bytes on their way, and the instructions per byte few:
+//  - a warp streams tiles of 16 keys of one head, key and value rows and their
+//    exponents by asynchronous copies (TMA where pages hold a whole tile) into a
+//    ring of its own; it waits for no other warp.  Copies by the threads
+//    themselves (16 bytes each) took 145 requests to the L2 a tile and 68 us
+//    where these take 58 (8 sequences of 32K, 4 key heads, all visited).
+//  - the products are mma.sync m16n8k16, fp16 with fp32 accumulation, and not
+//    tcgen05: an e4m3 value is exact in fp16, a tcgen05 product of e4m3 would want
+//    q and the weights in e4m3 too, and the tensor pipe is busy 16 % of the time.
+//    q is made exact by a power of two per head (every element within 2^31 of
+//    the head's largest); the weights are rounded to fp16, 2^-11 of each, under
+//    the bf16 result's own 2^-8.
+//      S^T [16 keys x 8 heads] = K Q^T: a thread's 16-byte pieces of two key rows
+//      are its A fragments after conversion, the order of d being free as long
+//      as q's fragments follow it;
+//      O^T [d x 8 heads] += V^T W^T: a thread's 16-byte pieces of four value
+//      rows are its A fragments after pairing bytes of neighbouring rows (one
+//      byte permute for two registers), and W^T comes from S^T by two 8 x 8
+//      transposes inside the warp.
+//
+// Measured (one GB300, copy rate 6787 GB/s): 16 sequences of 32K, 16 heads, two
+// of them whole and fourteen in windows of 1024, 330 MB: 58 us, of which this
+// kernel 52 (first data after 3 us, then 6.6 TB/s, warps ending within 3 us of
+// one another) and the join the rest; 8 whole sequences of 32K with 16 query and
+// 4 key heads, 271 MB: 50 us.  One sequence of 777 tokens: 8.2 us, a chain of
+// dependent reads (lengths, page numbers, rows) and two launches.
 
 #include "swiattn.h"
 #include "ptx.cuh"
@@ -44,11 +57,11 @@ namespace {
 
 constexpr int kTile = 16;        // keys of one product tile
 constexpr int kWarps = 4;        // warps of a block (they share nothing)
-constexpr int kStages = 2;       // tiles a warp holds: one at work, one on its way
+constexpr int kStages = 2;       // tiles a warp holds: one at work, one on its way (3: 59.1 us become 61.0)
 template <int NH>
-constexpr int kBlocksPerSm = NH == 1 ? 4 : 2;   // by registers: 128 or 255 a thread
+constexpr int kBlocksPerSm = NH == 1 ? 4 : 2;   // by registers, 128 or 255 a thread (5 at 96, spilling: 58 us become 78)
 constexpr int kMaxWarps = 152 * 4 * kWarps;     // workers of one call: what fills a GB300
-constexpr int kMinRun = 2;       // tiles a warp takes at least
+constexpr int kMinRun = 2;       // tiles a warp takes at least (one sequence of 777 tokens: 8.2 us, at 4 10.3, at 8 12.3)
 constexpr float kSlack = 8.f;    // base-2 units a score may pass its reference (weights up to 256)
 
 __device__ __forceinline__ float ex2f(float x) {
@@ -111,11 +124,11 @@ __device__ __forceinline__ Visit visit_of(const DecodeE4m3Args& a, int b) {
 // The work: every sequence's tiles are cut into blocks of `run` tiles, and a
 // warp takes one block of one KV head at a time: item (blocks before it) * Hkv +
 // head.  So neighbouring warps read neighbouring heads of the same tokens,
-// which the memory serves from the same open rows (runs cut without regard to
-// the heads moved 5.2 TB/s where these move TB/s).  `run` is the least
-// that gives each warp one item, where the batch has fewer (sequence, head)s
-// than half the warps, and balances their number otherwise.  Items' sums are
-// joined in the order of the blocks.
+// which lie side by side in memory (16 heads: 66 us, against 74 with equal runs
+// cut without regard to the heads).  `run` is the least that gives each warp at
+// most one item, where the batch has fewer (sequence, head)s than half the
+// warps; else items come round by round.  Items' sums are joined in the order
+// of the blocks.
 //
 // The plan that the split kernel leaves for the join: plan[b] blocks of the
 // sequences before b, plan[B] tiles of a block.
@@ -145,8 +158,8 @@ __device__ __forceinline__ int piece_at(int row, int piece) {
 // NH: groups of eight query heads (1: Hq/Hkv <= 8, 2: <= 16).  WIDE: pages of
 // 16 tokens or more, where a tile's rows follow one another.
 template <int D, int NH, bool WIDE>
-__global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm<NH>) decode_e4m3_split_kernel(const __grid_constant__ DecodeE4m3Args a,
-                         const __grid_constant__ CUtensorMap k_map,
+__global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm<NH>)
+decode_e4m3_split_kernel(const __grid_constant__ DecodeE4m3Args a, const __grid_constant__ CUtensorMap k_map,
                          const __grid_constant__ CUtensorMap v_map) {
     constexpr int KS = D / 16;    // 16-deep steps of the score product, and 16-row tiles of O^T
     constexpr int KW = D / 64;    // 16-byte pieces of a key row a thread holds
@@ -180,33 +193,46 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm<NH>) decode_e4m3_spl
     const int run = static_cast<int>(
         min(max((total * a.Hkv + share - 1) / share, static_cast<int64_t>(kMinRun)), static_cast<int64_t>(1) << 27));
 
-    int slot = 0;             // stage of the next tile to work on,
-    uint32_t phase = 0;       // and the parity its barrier completes with
-    for (int item = worker;; item += workers) {
-        // The item's sequence, block and head; the first warp passes over all
-        // sequences once, leaves the plan for the join and reports lengths.
-        const int h = item % a.Hkv;
-        const bool planner = item == 0;
-        int left = item / a.Hkv, block = 0;   // blocks from the scanned ones' end on
-        int b = -1;
+    // Blocks of sequence from + lane, and of all up to it.
+    auto blocks_of = [&](int from, int& sum) {
+        const int i = from + lane, n = i < a.B ? (visit_of(a, i).tiles + run - 1) / run : 0;
+        sum = inclusive_sum(n);
+        return n;
+    };
+    if (worker == 0) {   // leaves the plan and reports lengths that are clamped
+        int before = 0;
         for (int from = 0; from < a.B; from += 32) {
             const int i = from + lane;
-            const int n = i < a.B ? (visit_of(a, i).tiles + run - 1) / run : 0;
-            const int sum = inclusive_sum(n);
-            if (planner && i < a.B) {
-                a.plan[i] = sum - n - left;
+            int sum;
+            const int n = blocks_of(from, sum);
+            if (i < a.B) {
+                a.plan[i] = before + sum - n;
                 if (a.seq_lens[i] < 0 || a.seq_lens[i] > (a.max_pages << a.page_lg)) atomicOr(a.err, kDevErrInput);
             }
+            before += __shfl_sync(0xffffffffu, sum, 31);
+        }
+        if (lane == 0) a.plan[a.B] = run;
+    }
+
+    int slot = 0;             // stage of the next tile to work on,
+    uint32_t phase = 0;       // and the parity its barrier completes with
+    int from = 0, before = 0; // the 32 sequences last looked at, and the blocks before them
+    for (int item = worker;; item += workers) {
+        // The item's head, sequence and block.
+        const int h = item % a.Hkv;
+        int b = -1, block = 0;
+        for (; from < a.B; from += 32) {
+            int sum;
+            const int n = blocks_of(from, sum), left = item / a.Hkv - before;
             const unsigned hit = __ballot_sync(0xffffffffu, left < sum);
-            if (hit && b < 0) {
+            if (hit) {
                 const int who = __ffs(hit) - 1;
                 block = left - __shfl_sync(0xffffffffu, sum - n, who);
                 b = from + who;
-                if (!planner) break;
+                break;
             }
-            left -= __shfl_sync(0xffffffffu, sum, 31);
+            before += __shfl_sync(0xffffffffu, sum, 31);
         }
-        if (planner && lane == 0) a.plan[a.B] = run;
         if (b < 0) break;
         const Visit vis = visit_of(a, b);
         const int at = block * run;   // first tile of the block
@@ -303,15 +329,15 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm<NH>) decode_e4m3_spl
             // 2^qe takes the head's largest element to [2^14, 2^15).
             const int qe = min(126, 14 + 127 - static_cast<int>(__float_as_uint(amax) >> 23));
             const float up = __uint_as_float(static_cast<uint32_t>(qe + 127) << 23);
-    #pragma unroll
+#pragma unroll
             for (int s = 0; s < KS; ++s)
-    #pragma unroll
+#pragma unroll
                 for (int r = 0; r < 2; ++r) qf[n][s][r] = pack_half2(x[4 * s + 2 * r] * up, x[4 * s + 2 * r + 1] * up);
             const float down = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - qe) << 23);
             fs[n][0] = __shfl_sync(0xffffffffu, down, (2 * t) * 4);
             fs[n][1] = __shfl_sync(0xffffffffu, down, (2 * t + 1) * 4);
         }
-    
+
         float acc[NH][KS][4];
         float m[NH][2], nmax[NH][2], l[NH][2];   // references of s and t, and the sum
 #pragma unroll
@@ -490,7 +516,9 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm<NH>) decode_e4m3_spl
 // threads, four dimensions a thread.  A group takes every kJoinThreads/(D/4)-th
 // part, kAtOnce of them loaded together, with running maxima; the groups join
 // in order.  Launched as a programmatic dependent of the split kernel: it reads
-// the visit, an input, and then waits for that grid's memory.
+// the visit, an input, and then waits for that grid's memory.  Bound by latency,
+// so small enough that 1024 blocks (64 sequences of 16 heads) run at once: 17.8
+// us for that batch, 20.8 with 8 parts at once, 28 with 512 threads.
 constexpr int kJoinThreads = 256;
 constexpr int kAtOnce = 2;
 template <int D>
@@ -630,7 +658,7 @@ cudaError_t launch_d(const DecodeE4m3Args& a, int sms, cudaStream_t s) {
 
 }  // namespace
 
-// The parts, then the plan: prefix tiles of every sequence and a run's length.
+// The parts of all items, then the plan.
 DecodeE4m3Ws decode_e4m3_ws_layout(int B, int Hq, int Hkv, int d) {
     DecodeE4m3Ws L;
     const size_t parts = static_cast<size_t>(kMaxWarps) + static_cast<size_t>(B) * Hkv;

@@ -150,6 +150,8 @@ KINDS = ["bf16", "e4m3", "f32"]
     ([130, 257], [130, 600], 4, 4, 128, 32, 96, False),
     ([1, 2, 3] * 15, [50, 2, 35] * 15, 5, 5, 64, 4, 32, True),     # more sequences than a warp
     ([40], [70000], 2, 2, 128, 256, 128, True),                    # far into a context
+    ([21, 9], [70, 9], 24, 8, 128, 16, 80, False),                 # more heads than one block takes
+    ([9, 4], [9, 4], 70, 3, 64, 8, 64, True),
 ])
 def test_append_matches_reference(swa, new, total, Hq, Hkv, d, page, rot, interleaved, kind):
     s = Setup(new, total, Hq, Hkv, d, page, kind, seed=sum(new) + rot)
@@ -299,3 +301,28 @@ def test_append_refusals(swa):
     empty = swa.append_paged(s.q[:0], s.k[:0], s.v[:0], *s.pages, s.table, s.seq_lens, w,
                              starts=torch.zeros_like(s.starts), k_exp=s.exps[0], v_exp=s.exps[1])
     assert empty.shape == (0, 2, 64)
+
+
+def test_append_past_32_bit_offsets(swa):
+    """A pool of over 2^32 values: its last pages."""
+    Hkv, d, page = 8, 128, 64
+    num_pages = (1 << 32) // (page * Hkv * d) + 3
+    s = Setup([90], [90], Hkv, Hkv, d, page, "e4m3", seed=12)   # decode wants Hq a multiple of Hkv
+    pages = [torch.empty((num_pages, page, Hkv, d), dtype=torch.float8_e4m3fn, device="cuda") for _ in "kv"]
+    exps = [torch.empty((num_pages, Hkv, page), dtype=torch.uint8, device="cuda") for _ in "kv"]
+    s.run(swa, freqs(128))
+    small = s.table.long()[0]
+    big = torch.tensor([num_pages - 1, num_pages - 2], device="cuda")
+    table = big.to(torch.int32)[None].contiguous()
+    q = swa.append_paged(s.q, s.k, s.v, *pages, table, s.seq_lens, freqs(128).cuda(), starts=s.starts, k_exp=exps[0],
+                         v_exp=exps[1])
+    assert swa.get_device_error() == 0
+    for which in (0, 1):
+        got = pages[which][big].view(torch.uint8).flatten(0, 1)[:90]
+        want = s.pages[which][small].view(torch.uint8).flatten(0, 1)[:90]
+        assert torch.equal(got, want)
+    gate, W = torch.ones(1, dtype=torch.uint8, device="cuda"), 5
+    last = q[-1:].contiguous()
+    o = swa.decode_paged_e4m3(last, *pages, *exps, table, s.seq_lens, gate, W)
+    want = swa.decode_paged_e4m3(last, *s.pages, *s.exps, s.table, s.seq_lens, gate, W)
+    assert swa.get_device_error() == 0 and torch.equal(o, want)

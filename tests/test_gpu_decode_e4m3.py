@@ -314,3 +314,17 @@ def test_refusals(swa):
         with pytest.raises((ValueError, swa.SwiAttnError)):
             swa.decode_paged_e4m3(**{**good, **change})
     assert swa.get_device_error() == 0
+
+
+def test_wait_limit(swa):
+    """With a tiny limit a wait for the cache's rows may run out: reported as SWIATTN_ETIMEOUT, the
+    context stays usable, and with the default limit the next call is right again."""
+    c = Cache([3000, 2500], [1, 1], 4, 2, 128, 64, 0, 16, seed=13)
+    a = c.args()
+    swa.set_wait_limit_ns(1)
+    try:
+        swa.decode_paged_e4m3(*a)
+        assert swa.get_device_error() in (0, 4)
+    finally:
+        swa.set_wait_limit_ns(0)
+    c.check(*run(swa, c))
