@@ -183,6 +183,8 @@ decode_e4m3_split_kernel(const __grid_constant__ DecodeE4m3Args a, const __grid_
     }
     __syncwarp();
 
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // for the kernel before this one
+
     // The length of a block, from all sequences' tiles.
     int64_t total = 0;
     for (int i = lane; i < a.B; i += 32) total += visit_of(a, i).tiles;
@@ -528,6 +530,7 @@ __global__ void __launch_bounds__(kJoinThreads) decode_e4m3_join_kernel(const __
     __shared__ float3 s_top[kGroups];
     const int hq = blockIdx.x, b = blockIdx.y, col = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
     const int G = a.Hq / a.Hkv, h = hq / G;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tiles = visit_of(a, b).tiles;
     uint2* o = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + (static_cast<size_t>(b) * a.Hq + hq) * D) + col;
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -627,8 +630,11 @@ cudaError_t launch_split(const DecodeE4m3Args& a, int sms, cudaStream_t s) {
     if (WIDE && (!make_tmap_pages_u8(&k_map, a.k_pages, static_cast<uint64_t>(a.Hkv) * D, 1ull << a.page_lg, a.num_pages, D, kTile) ||
                  !make_tmap_pages_u8(&v_map, a.v_pages, static_cast<uint64_t>(a.Hkv) * D, 1ull << a.page_lg, a.num_pages, D, kTile)))
         return cudaErrorInvalidValue;
-    decode_e4m3_split_kernel<D, NH, WIDE>
-        <<<static_cast<unsigned>(units < most ? units : most), kWarps * 32, kSharedBytes<D>, s>>>(a, k_map, v_map);
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = dependent_launch(static_cast<unsigned>(units < most ? units : most), kWarps * 32, s, attr);
+    cfg.dynamicSmemBytes = kSharedBytes<D>;
+    e = cudaLaunchKernelEx(&cfg, decode_e4m3_split_kernel<D, NH, WIDE>, a, k_map, v_map);
+    if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
 
@@ -643,15 +649,8 @@ cudaError_t launch_d(const DecodeE4m3Args& a, int sms, cudaStream_t s) {
     cudaError_t e = a.Hq / a.Hkv <= 8 ? launch_split<D, 1>(a, sms, s) : launch_split<D, 2>(a, sms, s);
     prof_stop(s);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.Hq, a.B);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = s;
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    const cudaLaunchConfig_t cfg = dependent_launch(dim3(a.Hq, a.B), kJoinThreads, s, attr);
     e = cudaLaunchKernelEx(&cfg, decode_e4m3_join_kernel<D>, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }

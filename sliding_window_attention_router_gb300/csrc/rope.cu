@@ -228,6 +228,10 @@ __global__ void __launch_bounds__(kMaxThreads) rotate_kernel(const __grid_consta
     constexpr int U = kAtOnce<T, MODE>, lph = D / 16;
     __shared__ __align__(16) float s_table[kMaxTokens][2 * kMaxHalf];
     __shared__ int64_t s_row[kMaxTokens];
+    // What waits for this grid may be set up now; this grid waits for the one
+    // before it.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int half = a.rot / 2;
     const int t0 = blockIdx.x * (U * a.span), part = blockIdx.y;
     const int tokens = min(a.tokens - t0, U * a.span);
@@ -363,8 +367,10 @@ cudaError_t launch(RotateArgs a, cudaStream_t s) {
     a.span = std::max(1, std::min({128 / a.part_slots, kMaxTokens / U, (a.tokens + U - 1) / U}));
     const int threads = (a.part_slots * a.span + 31) / 32 * 32;
     const dim3 grid((a.tokens - 1) / (U * a.span) + 1, parts);
-    rotate_kernel<T, MODE, D><<<grid, threads, 0, s>>>(a);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = dependent_launch(grid, threads, s, attr);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, rotate_kernel<T, MODE, D>, a);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <typename T, int MODE>

@@ -45,6 +45,21 @@ cudaError_t allow_dynamic_smem(K kernel, int bytes, std::atomic<uint64_t>& done)
     return e;
 }
 
+// A launch that may be set up while the kernel before it on the stream still
+// runs: the launched kernel has to execute griddepcontrol.wait before it touches
+// memory, which returns once that kernel is complete and its writes visible.
+inline cudaLaunchConfig_t dependent_launch(dim3 grid, unsigned threads, cudaStream_t s, cudaLaunchAttribute* attr) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
 // ------------------------------------------------------------ tiling --------
 constexpr int kBM = 128;   // query rows per tile (TMEM lanes)
 constexpr int kBN = 128;   // keys per tile
