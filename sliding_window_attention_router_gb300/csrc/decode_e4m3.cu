@@ -81,6 +81,14 @@ __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same onto zeros.
+__device__ __forceinline__ void mma_f16_first(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // Transposes the 8 x 8 matrix of 16-bit elements that the warp's registers hold.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
@@ -412,10 +420,6 @@ decode_e4m3_split_kernel(const __grid_constant__ DecodeE4m3Args a, const __grid_
             // Scores: rows key g and 8 + g, columns heads 2t and 2t + 1.
             // Two chains of products, to wait less on either.
             float s[NH][4], s2[NH][4];
-#pragma unroll
-            for (int n = 0; n < NH; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.f;
             const uint32_t* k0 = reinterpret_cast<const uint32_t*>(kw[0]);
             const uint32_t* k1 = reinterpret_cast<const uint32_t*>(kw[1]);
 #pragma unroll
@@ -424,33 +428,39 @@ decode_e4m3_split_kernel(const __grid_constant__ DecodeE4m3Args a, const __grid_
                 halves_of(k0[j], a0, a2);
                 halves_of(k1[j], a1, a3);
 #pragma unroll
-                for (int n = 0; n < NH; ++n) mma_f16(j & 1 ? s2[n] : s[n], a0, a1, a2, a3, qf[n][j][0], qf[n][j][1]);
+                for (int n = 0; n < NH; ++n) {
+                    float* chain = j & 1 ? s2[n] : s[n];
+                    if (j < 2) mma_f16_first(chain, a0, a1, a2, a3, qf[n][j][0], qf[n][j][1]);
+                    else mma_f16(chain, a0, a1, a2, a3, qf[n][j][0], qf[n][j][1]);
+                }
             }
-            // s_j and t_j, and whether one is over kSlack above the reference it
-            // would be subtracted from.
-            float x[NH][4], y[NH][4];
-            bool over = false;
+            // s_j and t_j less their references, which are raised first where one
+            // is over them by more than kSlack (a NaN is not).
+            float x[NH][4], y[NH][4], ve[2];
+            float over = -INFINITY;
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const int tok = keys.base + g + 8 * r;
                 const bool on = static_cast<unsigned>(tok - keys.from) < static_cast<unsigned>(keys.to - keys.from);
-                const float kf = __uint_as_float(static_cast<uint32_t>(ku[r]) << 23), ve = static_cast<float>(vu[r] - 127);
+                const float kf = __uint_as_float(static_cast<uint32_t>(ku[r]) << 23);
+                ve[r] = static_cast<float>(vu[r] - 127);
 #pragma unroll
                 for (int n = 0; n < NH; ++n)
 #pragma unroll
                     for (int col = 0; col < 2; ++col) {
                         const int e = 2 * r + col;
-                        x[n][e] = on ? (s[n][e] + s2[n][e]) * fs[n][col] * kf : -INFINITY;
-                        y[n][e] = x[n][e] + ve;
-                        over |= x[n][e] > m[n][col] + kSlack || y[n][e] > nmax[n][col] + kSlack;
+                        s[n][e] = on ? (s[n][e] + s2[n][e]) * fs[n][col] * kf : -INFINITY;
+                        x[n][e] = s[n][e] - m[n][col];
+                        y[n][e] = (s[n][e] + ve[r]) - nmax[n][col];
+                        over = fmaxf(over, fmaxf(x[n][e], y[n][e]));
                     }
             }
-            if (__any_sync(0xffffffffu, over)) {
+            if (__any_sync(0xffffffffu, over > kSlack)) {
 #pragma unroll
                 for (int n = 0; n < NH; ++n)
 #pragma unroll
                     for (int col = 0; col < 2; ++col) {
-                        float xm = fmaxf(x[n][col], x[n][col + 2]), ym = fmaxf(y[n][col], y[n][col + 2]);
+                        float xm = fmaxf(s[n][col], s[n][col + 2]), ym = fmaxf(s[n][col] + ve[0], s[n][col + 2] + ve[1]);
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) {
                             xm = fmaxf(xm, __shfl_xor_sync(0xffffffffu, xm, o));
@@ -466,6 +476,11 @@ decode_e4m3_split_kernel(const __grid_constant__ DecodeE4m3Args a, const __grid_
                         }
                         m[n][col] = mn;
                         nmax[n][col] = nn;
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            x[n][2 * r + col] = s[n][2 * r + col] - mn;
+                            y[n][2 * r + col] = (s[n][2 * r + col] + ve[r]) - nn;
+                        }
                     }
             }
             uint32_t wt[NH][2];
@@ -473,8 +488,8 @@ decode_e4m3_split_kernel(const __grid_constant__ DecodeE4m3Args a, const __grid_
             for (int n = 0; n < NH; ++n) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    l[n][e & 1] += ex2f(x[n][e] - m[n][e & 1]);
-                    y[n][e] = ex2f(y[n][e] - nmax[n][e & 1]);
+                    l[n][e & 1] += ex2f(x[n][e]);
+                    y[n][e] = ex2f(y[n][e]);
                 }
                 wt[n][0] = transpose8x8(pack_half2(y[n][0], y[n][1]));
                 wt[n][1] = transpose8x8(pack_half2(y[n][2], y[n][3]));
