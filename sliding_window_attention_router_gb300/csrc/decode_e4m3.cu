@@ -35,11 +35,12 @@
 //      transposes inside the warp.
 //
 // Measured (one GB300, copy rate 6787 GB/s): 16 sequences of 32K, 16 heads, two
-// of them whole and fourteen in windows of 1024, 330 MB: 58 us, of which this
+// of them whole and fourteen in windows of 1024, 330 MB: 57 us, of which this
 // kernel 52 (first data after 3 us, then 6.6 TB/s, warps ending within 3 us of
 // one another) and the join the rest; 8 whole sequences of 32K with 16 query and
-// 4 key heads, 271 MB: 50 us.  One sequence of 777 tokens: 8.2 us, a chain of
-// dependent reads (lengths, page numbers, rows) and two launches.
+// 4 key heads, 271 MB: 49 us.  One sequence of 777 tokens: 8.0 us, a chain of
+// dependent reads (lengths, page numbers, rows) and two launches.  A captured
+// graph of ten calls; 30 million warp instructions for the first (issue 51 %).
 
 #include "swiattn.h"
 #include "ptx.cuh"
