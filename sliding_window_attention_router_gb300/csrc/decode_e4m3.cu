@@ -48,6 +48,7 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <float.h>
 #include <math.h>
 #include <algorithm>
 #include <atomic>
@@ -71,9 +72,10 @@ __device__ __forceinline__ float ex2f(float x) {
     return y;
 }
 
-// Where references and maxima start: below every score, yet finite, so that
-// no difference of two of them is a NaN (scores that are all -inf leave it).
-constexpr float kLow = -3e38f;
+// Where references and maxima start: the lowest finite value, below no score
+// but -inf (scores that are all -inf leave it), and finite, so that no
+// difference of it and a score or a maximum is a NaN.
+constexpr float kLow = -FLT_MAX;
 
 __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {

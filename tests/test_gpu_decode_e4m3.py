@@ -328,3 +328,25 @@ def test_wait_limit(swa):
     finally:
         swa.set_wait_limit_ns(0)
     c.check(*run(swa, c))
+
+
+@pytest.mark.parametrize("sign", [-1, 1])
+@pytest.mark.parametrize("page", [4, 16])
+def test_scores_at_the_ends_of_fp32(swa, page, sign):
+    """Scores of +-3.24e38 in base 2 (3.39e38 * 7.5 * 128^-1/2 log2(e)), all alike: weights of one
+    each, so o is the value row that all keys share, without any rounding (40 equal terms of 4
+    significant bits), and lse is the score in base e to within its fp32 steps (6 roundings)."""
+    lens = [1, 40]
+    c = Cache(lens, [1, 1], 2, 1, 128, 64, 0, page, 5)
+    value = ref.e4m3_value(np.arange(0x30, 0x50, dtype=np.uint8))
+    for which in range(2):
+        c.codes[which][...] = 0
+        c.exps[which][...] = 127
+    c.codes[0][..., 7] = ref.e4m3_code(np.array(sign * 7.5))
+    c.codes[1][...] = np.tile(np.arange(0x30, 0x50, dtype=np.uint8), 4)
+    c.q.zero_()
+    c.q[..., 7] = torch.finfo(torch.bfloat16).max
+    o, lse = run(swa, c)
+    assert np.array_equal(f64(o), np.broadcast_to(np.tile(value, 4), o.shape))
+    want = sign * 7.5 * torch.finfo(torch.bfloat16).max / math.sqrt(128)
+    assert np.all(np.abs(f64(lse) - want) <= 6 * 2.0 ** -24 * abs(want))
