@@ -537,8 +537,9 @@ decode_e4m3_split_kernel(const __grid_constant__ DecodeE4m3Args a, const __grid_
 // part, kAtOnce of them loaded together, with running maxima; the groups join
 // in order.  Launched as a programmatic dependent of the split kernel: it reads
 // the visit, an input, and then waits for that grid's memory.  Bound by latency,
-// so small enough that 1024 blocks (64 sequences of 16 heads) run at once: 17.8
-// us for that batch, 20.8 with 8 parts at once, 28 with 512 threads.
+// so small enough that 1024 blocks (64 sequences of 16 heads) run at once: 16.9
+// us for that batch, 19.7 with 4 parts at once, 17.4 with 128 threads, 23.5 with
+// 512; 8 sequences of 32K: 49.4, 51.3, 51.2, 49.1.
 constexpr int kJoinThreads = 256;
 constexpr int kAtOnce = 2;
 template <int D>
