@@ -982,6 +982,11 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
+    // Nothing here reads what the dK/dV kernel writes, but this grid must not be
+    // complete before that one: a programmatic dependent after it waits for this
+    // grid alone, and reads dK and dV.  (Every dK/dV CTA is resident by now, so
+    // CTAs that wait here hold none up.)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 }  // namespace dqk
@@ -1062,7 +1067,7 @@ cudaError_t launch_bwd_dq(const TcBwdArgs& a, unsigned int* err, int num_sms, cu
     // the stream: the two read the same inputs and write disjoint outputs, so
     // dQ CTAs start on the SMs the dK/dV kernel's last items leave idle.  Its
     // own inputs (work list, compacted rows) are complete before any dK/dV
-    // CTA lets it launch.
+    // CTA lets it launch.  It waits for that grid only at its end.
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(num_sms);
     cfg.blockDim = dim3(kThreads);
