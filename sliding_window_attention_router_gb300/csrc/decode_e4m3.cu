@@ -3,14 +3,16 @@
 // e4m3 rows that each carry a power of two.
 //
 // The mathematics, for one query head and the visited keys j, in base 2:
-//   s_j = scale log2(e) 2^(ku_j - 127) <q, k8_j>,   t_j = s_j + vu_j - 127,
-//   l = sum_j 2^(s_j - m),      a = sum_j 2^(t_j - n) v8_j,
-//   o = 2^(n - m) a / l,        lse = ln 2 (m + log2 l),
-// with m and n the largest s_j and t_j.  Folding a value row's power of two
-// into its weight leaves the e4m3 bytes as they are; the weights then have a
-// maximum of their own, n, so that what is rounded to 16 bits is always of
-// order 1 at the largest contribution, whatever the rows' sizes.  Parts (m,
-// n, l, a) of the key set join by their maxima.
+//   s_j = scale log2(e) 2^(ku_j - 127) <q, k8_j>,   x_j = s_j - m,
+//   l = sum_j 2^x_j,            a = sum_j 2^(x_j + vu_j - 127 - n) v8_j,
+//   o = 2^n a / l,              lse = ln 2 (m + log2 l),
+// with m the largest s_j and n the largest x_j + vu_j - 127.  Folding a value
+// row's power of two into its weight leaves the e4m3 bytes as they are; the
+// weights then have a maximum of their own, n, so that what is rounded to 16
+// bits is always of order 1 at the largest contribution, whatever the rows'
+// sizes.  n is relative to m: beside a score of 2^24 and more a row's power of
+// two would be rounded away.  Parts (m, n, l, a) of the key set join by their
+// maxima; where m rises, n falls by as much.
 //
 // The bound is the cache's bytes: 16 keys of one head are 4 KiB (d = 128), and
 // with up to 8 query heads to a key head 16 tensor-core products.  So the work
@@ -352,14 +354,14 @@ decode_e4m3_split_kernel(const __grid_constant__ DecodeE4m3Args a, const __grid_
         }
 
         float acc[NH][KS][4];
-        float m[NH][2], nmax[NH][2], l[NH][2];   // references of s and t, and the sum
+        float m[NH][2], nr[NH][2], l[NH][2];   // reference of s, that of the values' weights beyond it, and the sum
 #pragma unroll
         for (int n = 0; n < NH; ++n) {
 #pragma unroll
             for (int j = 0; j < KS; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[n][j][e] = 0.f;
-            m[n][0] = m[n][1] = nmax[n][0] = nmax[n][1] = kLow;
+            m[n][0] = m[n][1] = nr[n][0] = nr[n][1] = kLow;
             l[n][0] = l[n][1] = 0.f;
         }
 
@@ -437,7 +439,7 @@ decode_e4m3_split_kernel(const __grid_constant__ DecodeE4m3Args a, const __grid_
                     else mma_f16(chain, a0, a1, a2, a3, qf[n][j][0], qf[n][j][1]);
                 }
             }
-            // s_j and t_j less their references, which are raised first where one
+            // Both exponents less their references, which are raised first where one
             // is over them by more than kSlack (a NaN is not).
             float x[NH][4], y[NH][4], ve[2];
             float over = -INFINITY;
@@ -454,7 +456,7 @@ decode_e4m3_split_kernel(const __grid_constant__ DecodeE4m3Args a, const __grid_
                         const int e = 2 * r + col;
                         s[n][e] = on ? (s[n][e] + s2[n][e]) * fs[n][col] * kf : -INFINITY;
                         x[n][e] = s[n][e] - m[n][col];
-                        y[n][e] = (s[n][e] + ve[r]) - nmax[n][col];
+                        y[n][e] = x[n][e] + (ve[r] - nr[n][col]);
                         over = fmaxf(over, fmaxf(x[n][e], y[n][e]));
                     }
             }
@@ -463,27 +465,27 @@ decode_e4m3_split_kernel(const __grid_constant__ DecodeE4m3Args a, const __grid_
                 for (int n = 0; n < NH; ++n)
 #pragma unroll
                     for (int col = 0; col < 2; ++col) {
-                        float xm = fmaxf(s[n][col], s[n][col + 2]), ym = fmaxf(s[n][col] + ve[0], s[n][col + 2] + ve[1]);
+                        float top = fmaxf(s[n][col], s[n][col + 2]);
 #pragma unroll
-                        for (int o = 4; o < 32; o <<= 1) {
-                            xm = fmaxf(xm, __shfl_xor_sync(0xffffffffu, xm, o));
-                            ym = fmaxf(ym, __shfl_xor_sync(0xffffffffu, ym, o));
-                        }
-                        const float mn = fmaxf(m[n][col], xm), nn = fmaxf(nmax[n][col], ym);
-                        l[n][col] *= ex2f(m[n][col] - mn);
-                        const float ca = ex2f(nmax[n][col] - nn);
+                        for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        const float mn = fmaxf(m[n][col], top), fall = m[n][col] - mn;
+                        x[n][col] = s[n][col] - mn;
+                        x[n][col + 2] = s[n][col + 2] - mn;
+                        top = fmaxf(x[n][col] + ve[0], x[n][col + 2] + ve[1]);
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        const float nn = fmaxf(nr[n][col] + fall, top);
+                        l[n][col] *= ex2f(fall);
+                        const float ca = ex2f(nr[n][col] + fall - nn);
 #pragma unroll
                         for (int j = 0; j < KS; ++j) {
                             acc[n][j][col] *= ca;
                             acc[n][j][col + 2] *= ca;
                         }
                         m[n][col] = mn;
-                        nmax[n][col] = nn;
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            x[n][2 * r + col] = s[n][2 * r + col] - mn;
-                            y[n][2 * r + col] = (s[n][2 * r + col] + ve[r]) - nn;
-                        }
+                        nr[n][col] = nn;
+                        y[n][col] = x[n][col] + (ve[0] - nn);
+                        y[n][col + 2] = x[n][col + 2] + (ve[1] - nn);
                     }
             }
             uint32_t wt[NH][2];
@@ -525,7 +527,7 @@ decode_e4m3_split_kernel(const __grid_constant__ DecodeE4m3Args a, const __grid_
                     for (int j = 0; j < KS; j += 2)
                         *reinterpret_cast<float4*>(dst + g * (D / 8) + 2 * j) =
                             make_float4(acc[n][j][col], acc[n][j][col + 2], acc[n][j + 1][col], acc[n][j + 1][col + 2]);
-                    if (g == 0) *reinterpret_cast<float4*>(dst + D) = make_float4(m[n][col], nmax[n][col], ls, 0.f);
+                    if (g == 0) *reinterpret_cast<float4*>(dst + D) = make_float4(m[n][col], nr[n][col], ls, 0.f);
                 }
             }
     }
@@ -576,12 +578,13 @@ __global__ void __launch_bounds__(kJoinThreads) decode_e4m3_join_kernel(const __
                 v[i] = __ldcg(p + col);
             }
         }
-        float mn = m, nn = n;
+        float mn = m;
 #pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-            mn = fmaxf(mn, st[i].x);
-            nn = fmaxf(nn, st[i].y);
-        }
+        for (int i = 0; i < kAtOnce; ++i) mn = fmaxf(mn, st[i].x);
+        n += m - mn;   // from here on beyond the new maximum
+        float nn = n;
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) nn = fmaxf(nn, st[i].y + (st[i].x - mn));
         l *= ex2f(m - mn);
         const float f = ex2f(n - nn);
 #pragma unroll
@@ -589,7 +592,7 @@ __global__ void __launch_bounds__(kJoinThreads) decode_e4m3_join_kernel(const __
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
             l += st[i].z * ex2f(st[i].x - mn);
-            const float w = ex2f(st[i].y - nn);
+            const float w = ex2f(st[i].y + (st[i].x - mn) - nn);
             sum[0] += v[i].x * w;
             sum[1] += v[i].y * w;
             sum[2] += v[i].z * w;
@@ -603,12 +606,13 @@ __global__ void __launch_bounds__(kJoinThreads) decode_e4m3_join_kernel(const __
         if (col == 0) s_top[grp] = make_float3(m, n, l);
         __syncthreads();
         if (grp != 0) return;
-        float mn = m, nn = n;
+        float mn = m;
 #pragma unroll
-        for (int i = 1; i < kGroups; ++i) {
-            mn = fmaxf(mn, s_top[i].x);
-            nn = fmaxf(nn, s_top[i].y);
-        }
+        for (int i = 1; i < kGroups; ++i) mn = fmaxf(mn, s_top[i].x);
+        n += m - mn;
+        float nn = n;
+#pragma unroll
+        for (int i = 1; i < kGroups; ++i) nn = fmaxf(nn, s_top[i].y + (s_top[i].x - mn));
         l *= ex2f(m - mn);
         const float f = ex2f(n - nn);
 #pragma unroll
@@ -616,7 +620,7 @@ __global__ void __launch_bounds__(kJoinThreads) decode_e4m3_join_kernel(const __
 #pragma unroll
         for (int i = 1; i < kGroups; ++i) {
             l += s_top[i].z * ex2f(s_top[i].x - mn);
-            const float w = ex2f(s_top[i].y - nn);
+            const float w = ex2f(s_top[i].y + (s_top[i].x - mn) - nn);
             const float4 v = s_sum[i][col];
             sum[0] += v.x * w;
             sum[1] += v.y * w;
@@ -627,7 +631,7 @@ __global__ void __launch_bounds__(kJoinThreads) decode_e4m3_join_kernel(const __
         n = nn;
     }
     if (grp != 0) return;
-    const float f = ex2f(n - m);
+    const float f = ex2f(n);
     const __nv_bfloat162 lo = __floats2bfloat162_rn(sum[0] / l * f, sum[1] / l * f);
     const __nv_bfloat162 hi = __floats2bfloat162_rn(sum[2] / l * f, sum[3] / l * f);
     *o = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
