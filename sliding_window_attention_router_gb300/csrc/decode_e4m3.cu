@@ -324,9 +324,13 @@ decode_e4m3_split_kernel(const __grid_constant__ DecodeE4m3Args a, const __grid_
             if (!WIDE) asm volatile("cp.async.commit_group;" ::: "memory");
         }
 
-        // Query fragments and the factors of their scores.
+        // Query fragments and the factors of their scores, scale log2(e) 2^-qe
+        // of the thread's columns, heads 2t and 2t + 1, as fa fb: a sum of
+        // products (2^-33 to 2^31) times fa, then times the key row's power of
+        // two, then times fb stays inside fp32 where the score is, and is off
+        // by no more than 2^-23 where one of the three is subnormal.
         uint32_t qf[NH][KS][2];
-        float fs[NH][2];   // scale log2(e) 2^-qe of the thread's columns, heads 2t and 2t + 1
+        float fa[NH][2], fb[NH][2];
 #pragma unroll
         for (int n = 0; n < NH; ++n) {
             float x[KW * 16];
@@ -348,9 +352,15 @@ decode_e4m3_split_kernel(const __grid_constant__ DecodeE4m3Args a, const __grid_
             for (int s = 0; s < KS; ++s)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) qf[n][s][r] = pack_half2(x[4 * s + 2 * r] * up, x[4 * s + 2 * r + 1] * up);
-            const float down = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - qe) << 23);
-            fs[n][0] = __shfl_sync(0xffffffffu, down, (2 * t) * 4);
-            fs[n][1] = __shfl_sync(0xffffffffu, down, (2 * t + 1) * 4);
+            const int down = a.scale_e - qe;   // large: after the key's power; small: some of it, as much as scores leave room
+            const int late = down < -90 ? -60 : min(max(down - 60, 0), 127);
+            const float f0 = a.scale_m * __uint_as_float(static_cast<uint32_t>(max(down - late, -126) + 127) << 23);
+            const float f1 = __uint_as_float(static_cast<uint32_t>(late + 127) << 23);
+#pragma unroll
+            for (int col = 0; col < 2; ++col) {
+                fa[n][col] = __shfl_sync(0xffffffffu, f0, (2 * t + col) * 4);
+                fb[n][col] = __shfl_sync(0xffffffffu, f1, (2 * t + col) * 4);
+            }
         }
 
         float acc[NH][KS][4];
@@ -454,8 +464,8 @@ decode_e4m3_split_kernel(const __grid_constant__ DecodeE4m3Args a, const __grid_
 #pragma unroll
                     for (int col = 0; col < 2; ++col) {
                         const int e = 2 * r + col;
-                        s[n][e] = on ? (s[n][e] + s2[n][e]) * fs[n][col] * kf : -INFINITY;
-                        x[n][e] = s[n][e] - m[n][col];
+                        s[n][e] = on ? (s[n][e] + s2[n][e]) * fa[n][col] * kf : -INFINITY;   // but for fb
+                        x[n][e] = fmaf(s[n][e], fb[n][col], -m[n][col]);
                         y[n][e] = x[n][e] + (ve[r] - nr[n][col]);
                         over = fmaxf(over, fmaxf(x[n][e], y[n][e]));
                     }
@@ -465,12 +475,12 @@ decode_e4m3_split_kernel(const __grid_constant__ DecodeE4m3Args a, const __grid_
                 for (int n = 0; n < NH; ++n)
 #pragma unroll
                     for (int col = 0; col < 2; ++col) {
-                        float top = fmaxf(s[n][col], s[n][col + 2]);
+                        float top = fmaxf(s[n][col], s[n][col + 2]) * fb[n][col];
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                         const float mn = fmaxf(m[n][col], top), fall = m[n][col] - mn;
-                        x[n][col] = s[n][col] - mn;
-                        x[n][col + 2] = s[n][col + 2] - mn;
+                        x[n][col] = fmaf(s[n][col], fb[n][col], -mn);
+                        x[n][col + 2] = fmaf(s[n][col + 2], fb[n][col], -mn);
                         top = fmaxf(x[n][col] + ve[0], x[n][col + 2] + ve[1]);
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));

@@ -7,6 +7,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <atomic>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 
@@ -911,7 +912,8 @@ int swiattn_decode_paged_e4m3(const void* q, const void* k_pages, const void* v_
     a.Hkv = Hkv;
     a.W = W;
     a.n_anchor = n_anchor;
-    a.scale_log2 = scale * 1.4426950408889634f;
+    a.scale_m = static_cast<float>(2 * std::frexp(scale * 1.4426950408889634, &a.scale_e));
+    --a.scale_e;
     return launched(launch_decode_e4m3(a, d, di.sms, static_cast<cudaStream_t>(stream)));
 }
 

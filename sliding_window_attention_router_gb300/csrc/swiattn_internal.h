@@ -334,7 +334,8 @@ struct DecodeE4m3Args {
     int* plan;
     unsigned int* err;
     int B, max_pages, page_lg, num_pages, Hq, Hkv, W, n_anchor;
-    float scale_log2;           // softmax scale times log2(e)
+    float scale_m;              // softmax scale times log2(e): scale_m 2^scale_e, scale_m in [1, 2]
+    int scale_e;
 };
 struct DecodeE4m3Ws {
     size_t plan;   // int [B + 1], after the parts (d + 4 floats for each query head of one)

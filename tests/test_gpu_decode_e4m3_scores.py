@@ -24,22 +24,24 @@ from test_gpu_decode_e4m3 import Cache, f64, swa  # noqa: F401  (the fixture)
 pytestmark = pytest.mark.gpu
 
 
-def scored(lens, Hq, Hkv, d, page, p, sign, q_up=0, k_up=0, seed=21):
-    """Scores sign * 2^p - j * step, j in 0 .. 4 by row, step 8 or what fp32 holds beside 2^p."""
+def scored(lens, Hq, Hkv, d, page, p, sign, q_up=0, k_up=0, code=1.0, seed=21):
+    """Scores sign * 2^p - j * step, j in 0 .. 4 by row, step 8 or what fp32 holds beside 2^p; the
+    factors 2^q_up and 2^k_up more in the query and the keys, the latter held as `code` (e4m3)."""
+    unit = min(code, 64.0)   # so that 4 of it are an e4m3 value
     c = Cache(lens, [1] * len(lens), Hq, Hkv, d, 64, 0, page, seed)
     r = np.random.default_rng(seed)
     seen = [np.swapaxes(e, 1, 2) != 255 for e in c.exps]   # [page, slot, head]
     k = np.zeros(c.codes[0].shape)
-    k[..., 7] = sign
-    k[..., 8] = -r.integers(0, 5, k.shape[:-1])
+    k[..., 7] = sign * code
+    k[..., 8] = -unit * r.integers(0, 5, k.shape[:-1])
     v = r.integers(0x30, 0x50, k.shape)
-    kb, vb = np.full(seen[0].shape, 127 + k_up), 127 + r.integers(-12, 13, seen[0].shape)
+    kb, vb = np.full(seen[0].shape, 127 + k_up - int(math.log2(code))), 127 + r.integers(-12, 13, seen[0].shape)
     for i, (codes, byte) in enumerate(((ref.e4m3_code(k), kb), (v, vb))):
         c.codes[i] = np.where(seen[i][..., None], codes, 0x7f).astype(np.uint8)
         c.exps[i] = np.ascontiguousarray(np.swapaxes(np.where(seen[i], byte, 255), 1, 2).astype(np.uint8))
     c.q.zero_()
     c.q[..., 7] = 2.0 ** (p + q_up)
-    c.q[..., 8] = 2.0 ** (max(3, p - 20) + q_up)
+    c.q[..., 8] = 2.0 ** (max(3, p - 20) + q_up) * (code / unit)
     return c
 
 
@@ -74,4 +76,26 @@ def test_value_exponents_at_large_scores(swa, lens, Hq, Hkv, d, page, p, sign): 
     the steps of fp32 are as large as the exponents)."""
     c = scored(lens, Hq, Hkv, d, page, min(p, 126), sign)
     scale = LN2 * (2.0 if p == 127 else 1.0)
+    check(c, scale, *run(swa, c, scale))
+
+
+@pytest.mark.parametrize("p,q_up,k_up,scale_up,code", [
+    (119, 8, -8, 0, 256),       # q to 2^127, keys as append writes them: codes of 256, a small power of two
+    (20, 100, -100, 0, 256),
+    (10, -120, 120, 0, 1),      # the reverse
+    (3, -129, 127, 2, 1),       # both at the ends of their types
+    (24, -60, -60, 120, 256),   # the scale makes up for both
+    (24, -130, 10, 120, 1),
+    (60, 60, 60, -120, 256),    # products past fp32, scores inside
+    (24, 90, 35, -125, 256),
+    (70, 57, -133, 76, 2.0 ** -9),
+])
+@pytest.mark.parametrize("lens,Hq,Hkv,d,page", SHAPES)
+def test_scores_inside_fp32_whatever_their_factors(swa, lens, Hq, Hkv, d, page, p, q_up, k_up, scale_up, code):  # noqa: F811
+    """Only the score has to be in the range of fp32, not the query, the key row's power of two and
+    the softmax scale multiplied in some order."""
+    scale = LN2 * 2.0 ** scale_up
+    c = scored(lens, Hq, Hkv, d, page, p, 1, q_up, k_up, code)
+    bits = c.q[0, 0, 7:9].float().log2().numpy()
+    assert np.all(bits == np.rint(bits)) and bits.min() >= -126   # powers of two, none rounded away
     check(c, scale, *run(swa, c, scale))
