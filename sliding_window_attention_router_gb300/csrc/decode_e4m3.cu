@@ -26,8 +26,8 @@
 //    tcgen05: an e4m3 value is exact in fp16, a tcgen05 product of e4m3 would want
 //    q and the weights in e4m3 too, and the tensor pipe is busy 16 % of the time.
 //    q is made exact by a power of two per head (every element within 2^31 of
-//    the head's largest); the weights are rounded to fp16, 2^-11 of each, under
-//    the bf16 result's own 2^-8.
+//    the head's largest); the weights are rounded to fp16, by 2^-11 of each where
+//    it is at least 2^-21 of the largest (kRoom), under the bf16 result's own 2^-8.
 //      S^T [16 keys x 8 heads] = K Q^T: a thread's 16-byte pieces of two key rows
 //      are its A fragments after conversion, the order of d being free as long
 //      as q's fragments follow it;
@@ -66,7 +66,13 @@ template <int NH>
 constexpr int kBlocksPerSm = NH == 1 ? 4 : 2;   // by registers, 128 or 255 a thread (5 at 96, spilling: 58 us become 78)
 constexpr int kMaxWarps = 152 * 4 * kWarps;     // workers of one call: what fills a GB300
 constexpr int kMinRun = 2;       // tiles a warp takes at least (one sequence of 777 tokens: 8.2 us, at 4 10.3, at 8 12.3)
-constexpr float kSlack = 8.f;    // base-2 units a score may pass its reference (weights up to 256)
+// The values' weights go to fp16: their reference lies kRoom below the largest
+// (base 2), and they pass it by up to kSlack before it is raised, so that they
+// end at 2^15 and those down to 2^-21 of the largest keep all 11 bits, down to
+// 2^-31 fewer (smaller ones are lost to the result, not to its sum of weights:
+// under a bf16 half step of it unless 2^23 such keys meet in one warp's part).
+constexpr float kRoom = 7.f;
+constexpr float kSlack = 15.f;
 
 __device__ __forceinline__ float ex2f(float x) {
     float y;
@@ -484,7 +490,7 @@ decode_e4m3_split_kernel(const __grid_constant__ DecodeE4m3Args a, const __grid_
                         top = fmaxf(x[n][col] + ve[0], x[n][col + 2] + ve[1]);
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                        const float nn = fmaxf(nr[n][col] + fall, top);
+                        const float nn = fmaxf(nr[n][col] + fall, top - kRoom);
                         l[n][col] *= ex2f(fall);
                         const float ca = ex2f(nr[n][col] + fall - nn);
 #pragma unroll
@@ -641,9 +647,10 @@ __global__ void __launch_bounds__(kJoinThreads) decode_e4m3_join_kernel(const __
         n = nn;
     }
     if (grp != 0) return;
-    const float f = ex2f(n);
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(sum[0] / l * f, sum[1] / l * f);
-    const __nv_bfloat162 hi = __floats2bfloat162_rn(sum[2] / l * f, sum[3] / l * f);
+    const float f = ex2f(n + kRoom);   // in [2^-126, 2^127], which 2^n is not
+    const float lr = l * (1 << static_cast<int>(kRoom));
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(sum[0] / lr * f, sum[1] / lr * f);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(sum[2] / lr * f, sum[3] / lr * f);
     *o = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     if (a.lse && col == 0) a.lse[static_cast<size_t>(b) * a.Hq + hq] = (m + __log2f(l)) * 0.69314718055994531f;
 }

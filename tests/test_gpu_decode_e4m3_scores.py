@@ -99,3 +99,30 @@ def test_scores_inside_fp32_whatever_their_factors(swa, lens, Hq, Hkv, d, page, 
     bits = c.q[0, 0, 7:9].float().log2().numpy()
     assert np.all(bits == np.rint(bits)) and bits.min() >= -126   # powers of two, none rounded away
     check(c, scale, *run(swa, c, scale))
+
+
+@pytest.mark.parametrize("first", [True, False])
+@pytest.mark.parametrize("below", [10, 20, 25, 28, 31])
+@pytest.mark.parametrize("lens,Hq,Hkv,d,page", [([320], 4, 1, 128, 16), ([600], 12, 1, 64, 4)])
+def test_small_weights_beside_a_large_one(swa, lens, Hq, Hkv, d, page, below, first):  # noqa: F811
+    """One key of score 0 whose value row is zero in the even dimensions; all others at -below with
+    positive values there.  The even dimensions come from weights of 2^-below of the largest alone,
+    powers of two, which 16 bits hold to 2^-31: they are right to a bf16 half step and the sums."""
+    c = scored(lens, Hq, Hkv, d, page, 3, 1)
+    top = 0 if first else lens[0] - 1
+    for b in range(len(lens)):
+        for t in range(lens[b]):
+            at = c.table[b, t // page], t % page
+            c.codes[0][at] = 0
+            c.codes[0][at][..., 8] = ref.e4m3_code(np.array(0.0 if t == top else -1.0))
+            c.codes[1][at] = 0x40 + t % 3 if t != top else np.tile([0, 0x40], d // 2)
+            c.exps[0][at[0], :, at[1]] = c.exps[1][at[0], :, at[1]] = 127
+    c.q[..., 7] = 0
+    c.q[..., 8] = below
+    o, lse = run(swa, c, LN2)
+    k, v = (ref.contiguous(np.nan_to_num(ref.page_values(x, e), nan=0.0, posinf=0.0), c.table) for x, e in zip(c.codes, c.exps))
+    ve = ref.contiguous(np.swapaxes(c.exps[1], 1, 2)[..., None], c.table)[..., 0]
+    want, want_lse, absum, _, _ = ref.decode(f64(c.q), k, v, ve, c.lens, c.gate, c.W, c.S, LN2)
+    err = np.abs(f64(o) - want)
+    assert np.all(want > 0) and np.all(err <= 2.0 ** -8 * want + 2.0 ** -16 * absum), np.max(err / want)
+    assert np.all(np.abs(f64(lse) - want_lse) <= 2.0 ** -16)
