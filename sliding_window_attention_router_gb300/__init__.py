@@ -26,7 +26,14 @@ __all__ = [
 ]
 
 F32, BF16, E4M3 = 0, 1, 2
-_DT = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+class _Types(dict):
+    def __missing__(self, dtype):
+        raise ValueError(f"dtype must be torch.float32 or torch.bfloat16, got {dtype}")
+
+
+_DT = _Types({torch.float32: F32, torch.bfloat16: BF16})
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libswiattn.so")
 _lock = threading.Lock()
@@ -560,6 +567,7 @@ def _rope(where, q, k, inv_freq, positions, interleaved, factor, out):
         raise ValueError(f"q and k must be [B, N, heads, d], got {list(some.shape)}")
     B, N, _, d = some.shape
     lead, dtype = [B, N], some.dtype
+    kind = _DT[dtype]
     results, sizes = [], []
     for name, t, o in (("q", q, out and out[0]), ("k", k, out and out[1])):
         if t is None:
@@ -586,7 +594,7 @@ def _rope(where, q, k, inv_freq, positions, interleaved, factor, out):
     if some.numel():
         _launch(where, index, _addr(q), _addr(k), _addr(positions), inv_freq.data_ptr(),
                 _addr(results[0]), _addr(results[1]), B, N, Hq, Hkv, d, 2 * inv_freq.numel(),
-                bool(interleaved), factor, qs, ks, qos, kos, _DT[dtype])
+                bool(interleaved), factor, qs, ks, qos, kos, kind)
     return results[0], results[1]
 
 
