@@ -328,7 +328,9 @@ int swiattn_route_backward(const void* h, const void* w, const float* logits, co
  * with (a, b) = (f, f + rot_dim/2), or (2f, 2f+1) when interleaved != 0;
  * dimensions rot_dim .. d-1 are copied.  Any scaling of the frequencies is in
  * inv_freq, that of their amplitude in factor (1: none; finite).  Angles are
- * reduced exactly: far positions cost no precision.
+ * reduced in 64 bits: far positions cost no precision (2^-32 of a turn at any
+ * position while |w_f| <= 1; 2^-63 of the turns made beyond).  A w_f that is not
+ * finite makes its pair NaN at every position.
  * q [B,N,Hq,d], k [B,N,Hkv,d] of `dtype`; positions int32 [B,N], any sign
  * (NULL: 0..N-1 in every sequence).  Token t = b*N + i of q starts at element
  * t * q_stride, and likewise for k, q_out, k_out, so views of a fused

@@ -85,7 +85,8 @@ __device__ __forceinline__ void store8_e4m3(uint8_t* p, const float* x) {
 // Frequency w (radians a position) as a 64-bit fraction of a turn, modulo a
 // whole turn (positions are whole numbers, so whole turns do not matter).  With
 // w = M 2^E, M of 53 bits, it is M * (2^66 / 2pi) * 2^(E - 2), a 128-bit whole
-// number shifted; |w| <= 1 keeps it right to the last bit but one.  Whole-number
+// number shifted, right to 2^-63 of the turns it stands for and, up to a radian a
+// position, to the last bit but one.  (w not finite: any.)  Whole-number
 // arithmetic, as the double-precision pipe is a sixty-fourth as wide.
 __device__ __forceinline__ uint64_t turn_fraction(double w) {
     const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(w));
@@ -275,7 +276,9 @@ __global__ void __launch_bounds__(kMaxThreads) rotate_kernel(const __grid_consta
             place.pos = a.positions ? a.positions[t] : t % a.N;
         }
         if (table_used && f < half) {   // while the page number is on its way
-            const float2 cs = cos_sin(turn_fraction(a.inv_freq[f]), place.pos, a.factor);
+            const double w = a.inv_freq[f];
+            float2 cs = cos_sin(turn_fraction(w), place.pos, a.factor);
+            if ((~__double2hiint(w) & 0x7ff00000) == 0) cs.x = cs.y = __int_as_float(0x7fffffff);   // w is not finite
             s_table[j][table_at(f)] = cs.x;
             s_table[j][table_at(f) + 2] = cs.y;
         }
