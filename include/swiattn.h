@@ -462,7 +462,8 @@ int swiattn_num_sms(void);
 
 /* Failure-detection aid with no counterpart in the paper: sets, on the
  * current device, how long a device-side wait of the tensor-core kernels
- * (routed prefill, dual branch, backward) and of the decode over e4m3 pages may last before the kernel gives up,
+ * (routed prefill, dual branch, backward) and of the decode over e4m3 pages
+ * (of 16 tokens and more) may last before the kernel gives up,
  * records SWIATTN_ETIMEOUT for swiattn_get_device_error and returns early
  * without computing the rest of its work; ns = 0 restores the default of 2 s.
  * A tiny limit lets a test make such a wait run out on purpose and check that

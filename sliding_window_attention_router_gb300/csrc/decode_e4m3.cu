@@ -386,8 +386,10 @@ decode_e4m3_split_kernel(const __grid_constant__ DecodeE4m3Args a, const __grid_
             const int ahead = i + kStages - 1;
             if (ahead < count) issue(ahead, slot == 0 ? kStages - 1 : slot - 1);
             if constexpr (WIDE) {
-                // One lane's time-out is every lane's: the warp leaves together.
-                if (!__all_sync(0xffffffffu, mbar_wait(&s_full[warp][slot], phase, &s_abort[warp], a.err))) {
+                // One lane's time-out is every lane's: the warp leaves together.  (With
+                // a first try that may suspend 16 x 32K takes 57.8 us in place of 58.1,
+                // but a lowered limit does not reach these waits.)
+                if (!__all_sync(0xffffffffu, mbar_wait_short(&s_full[warp][slot], phase, &s_abort[warp], a.err))) {
                     for (int j = i; j < min(ahead + 1, count); ++j) {   // the copies in flight
                         mbar_drain(&s_full[warp][slot], phase);
                         if (++slot == kStages) slot = 0, phase ^= 1;

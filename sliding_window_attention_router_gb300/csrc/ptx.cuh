@@ -98,19 +98,19 @@ static inline cudaError_t set_wait_limit_of_unit(uint64_t ns) {
     return cudaMemcpyToSymbol(g_wait_limit_ns, &v, sizeof(v));
 }
 
-// Bounded wait for the phase with the given parity.  Returns false when the
-// CTA-wide abort flag is raised or after g_wait_limit_ns; in the latter case
-// the waiter raises the abort flag and records SWIATTN_DEVERR_TIMEOUT in *err.
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                          unsigned int* err) {
-    if (mbar_try_wait(bar, parity)) return true;
+// Below this limit a waiter polls without suspending: a suspended one may sleep
+// until the phase completes, past such a limit.
+constexpr uint64_t kPollBelowNs = 100000;   // 0.1 ms
+
+// The rest of a bounded wait whose first try has not found the phase complete.
+__device__ __forceinline__ bool mbar_wait_on(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                             unsigned int* err) {
     const uint64_t t0 = globaltimer_ns();
     const uint64_t limit = g_wait_limit_ns;
-    // A limit below 0.1 ms polls without suspending (a suspended waiter may
-    // sleep until the phase completes, past such a limit) and also bounds the
-    // number of polls (the global timer may tick more coarsely than such a
-    // limit); otherwise the waiter suspends for up to 0.1 ms at a time.
-    const bool poll = limit < 100000ull;
+    // Polling also bounds the number of polls (the global timer may tick more
+    // coarsely than such a limit); otherwise the waiter suspends for up to 0.1 ms
+    // at a time.
+    const bool poll = limit < kPollBelowNs;
     for (uint64_t polls = 1;; ++polls) {
         if (poll ? mbar_test_wait(bar, parity) : mbar_try_wait_sleep(bar, parity, 100000u))
             return true;
@@ -121,6 +121,21 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
             return false;
         }
     }
+}
+
+// Bounded wait for the phase with the given parity.  Returns false when the
+// CTA-wide abort flag is raised or after g_wait_limit_ns; in the latter case
+// the waiter raises the abort flag and records SWIATTN_DEVERR_TIMEOUT in *err.
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                          unsigned int* err) {
+    return mbar_try_wait(bar, parity) || mbar_wait_on(bar, parity, abort_flag, err);
+}
+
+// The same with a first try that does not suspend, so that a limit that polls
+// reaches waits that would end within it.
+__device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                                unsigned int* err) {
+    return mbar_test_wait(bar, parity) || mbar_wait_on(bar, parity, abort_flag, err);
 }
 
 // Short bounded wait used while draining after an abort: never raises flags.
