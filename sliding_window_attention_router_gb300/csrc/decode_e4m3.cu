@@ -26,14 +26,16 @@
 //    tcgen05: an e4m3 value is exact in fp16, a tcgen05 product of e4m3 would want
 //    q and the weights in e4m3 too, and the tensor pipe is busy 16 % of the time.
 //    q is made exact by a power of two per head (every element within 2^31 of
-//    the head's largest); the weights are rounded to fp16, by 2^-11 of each where
-//    it is at least 2^-21 of the largest (kRoom), under the bf16 result's own 2^-8.
+//    the head's largest); the weights go in as two fp16, the nearest value and
+//    what it leaves, right to 2^-22 of each or 2^-32 of the largest (kRoom).  With
+//    the first alone, 2^-11 of each, one bf16 result in twenty was the neighbour
+//    of the one that fp32 weights give, for 16 x 32K in 58.1 us in place of 59.4.
 //      S^T [16 keys x 8 heads] = K Q^T: a thread's 16-byte pieces of two key rows
 //      are its A fragments after conversion, the order of d being free as long
 //      as q's fragments follow it;
 //      O^T [d x 8 heads] += V^T W^T: a thread's 16-byte pieces of four value
 //      rows are its A fragments after pairing bytes of neighbouring rows (one
-//      byte permute for two registers), and W^T comes from S^T by two 8 x 8
+//      byte permute for two registers), and W^T comes from S^T by 8 x 8
 //      transposes inside the warp.
 //
 // Measured (one GB300, copy rate 6787 GB/s): 16 sequences of 32K, 16 heads, two
@@ -68,9 +70,9 @@ constexpr int kMaxWarps = 152 * 4 * kWarps;     // workers of one call: what fil
 constexpr int kMinRun = 2;       // tiles a warp takes at least (one sequence of 777 tokens: 8.2 us, at 4 10.3, at 8 12.3)
 // The values' weights go to fp16: their reference lies kRoom below the largest
 // (base 2), and they pass it by up to kSlack before it is raised, so that they
-// end at 2^15 and those down to 2^-21 of the largest keep all 11 bits, down to
-// 2^-31 fewer (smaller ones are lost to the result, not to its sum of weights:
-// under a bf16 half step of it unless 2^23 such keys meet in one warp's part).
+// end at 2^15 and reach down to 2^-31 of the largest (smaller ones are lost to
+// the result, not to its sum of weights: under a bf16 half step of it unless
+// 2^23 such keys meet in one warp's part).
 constexpr float kRoom = 7.f;
 constexpr float kSlack = 15.f;
 
@@ -506,7 +508,7 @@ decode_e4m3_split_kernel(const __grid_constant__ DecodeE4m3Args a, const __grid_
                         y[n][col + 2] = x[n][col + 2] + (ve[1] - nn);
                     }
             }
-            uint32_t wt[NH][2];
+            uint32_t wt[NH][2], wl[NH][2];   // and what rounding left
 #pragma unroll
             for (int n = 0; n < NH; ++n) {
 #pragma unroll
@@ -514,8 +516,13 @@ decode_e4m3_split_kernel(const __grid_constant__ DecodeE4m3Args a, const __grid_
                     l[n][e & 1] += ex2f(x[n][e]);
                     y[n][e] = ex2f(y[n][e]);
                 }
-                wt[n][0] = transpose8x8(pack_half2(y[n][0], y[n][1]));
-                wt[n][1] = transpose8x8(pack_half2(y[n][2], y[n][3]));
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const uint32_t hi = pack_half2(y[n][2 * r], y[n][2 * r + 1]);
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+                    wt[n][r] = transpose8x8(hi);
+                    wl[n][r] = transpose8x8(pack_half2(y[n][2 * r] - f.x, y[n][2 * r + 1] - f.y));
+                }
             }
             // O^T: tile j holds dims D/8 g + 2 j (rows g) and + 1 (rows 8 + g).
 #pragma unroll
@@ -525,7 +532,10 @@ decode_e4m3_split_kernel(const __grid_constant__ DecodeE4m3Args a, const __grid_
                 halves_of(__byte_perm(vw[0][j / 2], vw[1][j / 2], sel), a0, a1);
                 halves_of(__byte_perm(vw[2][j / 2], vw[3][j / 2], sel), a2, a3);
 #pragma unroll
-                for (int n = 0; n < NH; ++n) mma_f16(acc[n][j], a0, a1, a2, a3, wt[n][0], wt[n][1]);
+                for (int n = 0; n < NH; ++n) {
+                    mma_f16(acc[n][j], a0, a1, a2, a3, wt[n][0], wt[n][1]);
+                    mma_f16(acc[n][j], a0, a1, a2, a3, wl[n][0], wl[n][1]);
+                }
             }
         }
 

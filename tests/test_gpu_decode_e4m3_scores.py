@@ -126,3 +126,24 @@ def test_small_weights_beside_a_large_one(swa, lens, Hq, Hkv, d, page, below, fi
     err = np.abs(f64(o) - want)
     assert np.all(want > 0) and np.all(err <= 2.0 ** -8 * want + 2.0 ** -16 * absum), np.max(err / want)
     assert np.all(np.abs(f64(lse) - want_lse) <= 2.0 ** -16)
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,d,page", SHAPES)
+def test_weights_as_exact_as_fp32(swa, lens, Hq, Hkv, d, page):  # noqa: F811
+    """Scores that are multiples of 5/8 in base 2, exact, so that the weights fill their mantissas; values
+    of both signs, so that results far below the sum of absolute terms show the weights' own error.
+    Left are the exponentials (2^-22 each, of weights and sum), the weights' two halves (2^-22) and fp32
+    sums of a part's few dozen terms (2^-19): 2^-17 of the sum of absolute terms, and a bf16 half step."""
+    c = scored(lens, Hq, Hkv, d, page, 3, 1)
+    r = np.random.default_rng(22)
+    c.codes[1] = np.where(c.codes[1] == 0x7f, 0x7f, c.codes[1] | (r.integers(0, 2, c.codes[1].shape) << 7)).astype(np.uint8)
+    c.q[..., 7] = 0.0
+    c.q[..., 8] = 0.625
+    o, lse = run(swa, c, LN2)
+    with np.errstate(invalid="ignore", over="ignore"):
+        k, v = (ref.contiguous(ref.page_values(x, e), c.table) for x, e in zip(c.codes, c.exps))
+    ve = ref.contiguous(np.swapaxes(c.exps[1], 1, 2)[..., None], c.table)[..., 0]
+    want, want_lse, absum, _, _ = ref.decode(f64(c.q), k, v, ve, c.lens, c.gate, c.W, c.S, LN2)
+    err = np.abs(f64(o) - want)
+    assert np.all(err <= 2.0 ** -8 * np.abs(want) + 2.0 ** -17 * absum), np.max(err / absum)
+    assert np.all(np.abs(f64(lse) - want_lse) <= 2.0 ** -17)
