@@ -86,14 +86,16 @@ __device__ __forceinline__ void store8_e4m3(uint8_t* p, const float* x) {
 // whole turn (positions are whole numbers, so whole turns do not matter).  With
 // w = M 2^E, M of 53 bits, it is M * (2^66 / 2pi) * 2^(E - 2), a 128-bit whole
 // number shifted, right to 2^-63 of the turns it stands for and, up to a radian a
-// position, to the last bit but one.  (w not finite: any.)  Whole-number
-// arithmetic, as the double-precision pipe is a sixty-fourth as wide.
-__device__ __forceinline__ uint64_t turn_fraction(double w) {
+// position, to the last bit but one.  Whole-number arithmetic, as the
+// double-precision pipe is a sixty-fourth as wide.  `factor`, of the cosine and
+// sine, becomes a NaN where w is not finite.
+__device__ __forceinline__ uint64_t turn_fraction(double w, float& factor) {
     const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(w));
     const int e = static_cast<int>(bits >> 52 & 2047);
     const uint64_t m = (bits & 0xfffffffffffffull) | (e ? 1ull << 52 : 0ull);
     constexpr uint64_t kInv = 0xa2f9836e4e44152aull;   // 2^66 / 2pi
     const uint64_t hi = __umul64hi(m, kInv), lo = m * kInv;
+    if (e == 2047) factor = __int_as_float(0x7fffffff);
     const int shift = 1077 - (e ? e : 1);   // right, 2 - E
     uint64_t f;
     if (shift >= 128) f = 0;
@@ -276,9 +278,9 @@ __global__ void __launch_bounds__(kMaxThreads) rotate_kernel(const __grid_consta
             place.pos = a.positions ? a.positions[t] : t % a.N;
         }
         if (table_used && f < half) {   // while the page number is on its way
-            const double w = a.inv_freq[f];
-            float2 cs = cos_sin(turn_fraction(w), place.pos, a.factor);
-            if ((~__double2hiint(w) & 0x7ff00000) == 0) cs.x = cs.y = __int_as_float(0x7fffffff);   // w is not finite
+            float factor = a.factor;
+            const uint64_t fraction = turn_fraction(a.inv_freq[f], factor);
+            const float2 cs = cos_sin(fraction, place.pos, factor);
             s_table[j][table_at(f)] = cs.x;
             s_table[j][table_at(f) + 2] = cs.y;
         }
