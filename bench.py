@@ -45,15 +45,15 @@ L2_FLUSH_BYTES = 256 << 20
 # has changed since reports null.
 MEASURED_TRAFFIC = {
     # prefill_kernel, long-context prefill N=32768 f=0.13 (far items head by head):
-    # 727 854 336 read + 121 214 976 written
-    ("prefill", "532909cf403d4c6c"): 727854336 + 121214976,
+    # 730 999 040 read + 121 548 800 written
+    ("prefill", "ad2ebe391d3eab42"): 730999040 + 121548800,
     # decode_split2_kernel (persistent CTAs), 16 x 32768 decode: 654 431 488 read + 4 102 656 written
     ("decode", "97db57687c228419"): 654431488 + 4102656,
-    # dual_kernel, dual-branch workload B=2 N=8192 GQA 16/4: 144 400 384 read + 270 856 192 written
-    ("dual", "0d140f1582e3c2ea"): 144400384 + 270856192,
-    # dkdv_kernel + dq_kernel, backward on the dual workload: (315 288 064 + 22 582 016)
-    # + (254 839 296 + 48 433 152)
-    ("backward", "789f57cbf56f040a"): 315288064 + 22582016 + 254839296 + 48433152,
+    # dual_kernel, dual-branch workload B=2 N=8192 GQA 16/4: 143 767 040 read + 271 276 288 written
+    ("dual", "c42c6d9de72c1154"): 143767040 + 271276288,
+    # dkdv_kernel + dq_kernel, backward on the dual workload: (315 331 584 + 22 627 584)
+    # + (254 837 248 + 47 843 584)
+    ("backward", "971f419b64acb641"): 315331584 + 22627584 + 254837248 + 47843584,
     # route_kernel, 32768 tokens x 2048: 134 248 192 read + 2 795 520 written
     ("route", "4a5c0b7bf6e2d8ed"): 134248192 + 2795520,
     # route_bwd_logit + dh + reduce kernels, 16384 tokens: (201 534 208 + 3 031 552)
