@@ -421,6 +421,11 @@ size_t swiattn_decode_paged_e4m3_workspace(int B, int max_pages, int page_size, 
  *    Hq / Hkv any whole number up to 16 (larger: SWIATTN_EUNSUPPORTED);
  *    B <= 65535, B * Hkv <= 2^30; page_size a power of two, max_pages * page_size
  *    <= 2^30, num_pages * page_size <= 2^32 (larger: SWIATTN_EUNSUPPORTED).
+ *  - Accuracy: that of fp32 scores and weights.  A score (times log2 e) has to be
+ *    in the range of fp32; q, the keys' powers of two and scale each may have any
+ *    size.  Of q, an element under 2^-31 of its head's largest loses bits.  A
+ *    key's weight times its value row's power of two counts down to 2^-31 of the
+ *    largest such product.
  *  - The call is bitwise repeatable.  How a sequence's keys are split for the
  *    GPU depends on the whole batch, so the last bits of its result may.
  * workspace: at least swiattn_decode_paged_e4m3_workspace(...) bytes, 256-byte

@@ -21,10 +21,11 @@
 //    exponents by asynchronous copies (TMA where pages hold a whole tile) into a
 //    ring of its own; it waits for no other warp.  Copies by the threads
 //    themselves (16 bytes each) took 145 requests to the L2 a tile and 68 us
-//    where these take 58 (8 sequences of 32K, 4 key heads, all visited).
+//    where these took 58 (8 sequences of 32K, 4 key heads, all visited; 50 us
+//    with what came after).
 //  - the products are mma.sync m16n8k16, fp16 with fp32 accumulation, and not
 //    tcgen05: an e4m3 value is exact in fp16, a tcgen05 product of e4m3 would want
-//    q and the weights in e4m3 too, and the tensor pipe is busy 16 % of the time.
+//    q and the weights in e4m3 too, and the tensor pipe is busy 25 % of the time.
 //    q is made exact by a power of two per head (every element within 2^31 of
 //    the head's largest); the weights go in as two fp16, the nearest value and
 //    what it leaves, right to 2^-22 of each or 2^-32 of the largest (kRoom).  With
@@ -39,12 +40,20 @@
 //      transposes inside the warp.
 //
 // Measured (one GB300, copy rate 6787 GB/s): 16 sequences of 32K, 16 heads, two
-// of them whole and fourteen in windows of 1024, 330 MB: 57 us, of which this
-// kernel 52 (first data after 3 us, then 6.6 TB/s, warps ending within 3 us of
-// one another) and the join the rest; 8 whole sequences of 32K with 16 query and
-// 4 key heads, 271 MB: 49 us.  One sequence of 777 tokens: 8.0 us, a chain of
-// dependent reads (lengths, page numbers, rows) and two launches.  A captured
-// graph of ten calls; 30 million warp instructions for the first (issue 51 %).
+// of them whole and fourteen in windows of 1024, 330 MB: 59.5 us, of which this
+// kernel 54 (first data after 3 us, warps ending within 3 us of one another) and
+// the join the rest; 8 whole sequences of 32K with 16 query and 4 key heads, 271
+// MB: 50.5 us.  One sequence of 777 tokens: 8.0 us, a chain of dependent reads
+// (lengths, page numbers, rows) and two launches.  A captured graph of ten calls;
+// 33 million warp instructions for the first (issue 54 %).  Further from their
+// bytes: two groups of heads (the second case with 48 query heads: 64 us; half
+// the warps, each with a ring of the same depth), pages under a tile (with pages
+// of 8, 4 and 1 tokens: 60, 61 and 66 us; page number and exponents waited for in
+// each tile), and batches whose (sequence, key head)s come near the number of
+// warps (64, 96 and 160 windows of 1024, 16 heads: 71, 94 and 147 us for 40, 60
+// and 100 us of bytes; blocks of unequal length, a last round of few).
+// Comparisons beside the constants below are of the time when they were chosen,
+// on the first case unless they say otherwise.
 
 #include "swiattn.h"
 #include "ptx.cuh"

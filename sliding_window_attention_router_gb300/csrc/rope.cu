@@ -201,10 +201,11 @@ __device__ __forceinline__ int row_exponent(float amax) {
 //
 // Measured (one GB300, copy rate 6787 GB/s): rotation of 32K tokens of 16 + 16
 // heads, 537 MB, 79 us, the copy rate; gradient of 2 x 8K tokens of 16 + 4 heads,
-// 168 MB, 27 us (92 % of it); append of five prompts, 8K tokens of 16 + 4 + 4 heads,
-// 57 MB, 10 us; append of 32K tokens of 16 + 16 + 16 heads to e4m3 pages, 672 MB,
+// 168 MB, 27 us (92 % of it); append of five prompts, 4.7K tokens of 16 + 4 + 4
+// heads, 57 MB, 10 us; append of 32K tokens of 16 + 16 + 16 heads to e4m3 pages, 672 MB,
 // 118 us (84 %; it issues in 71 % of the cycles: maxima, scaling and conversion
-// on top of the rotation); to bf16 pages, 805 MB, 126 us (94 %).  One token: 2.7 us.
+// on top of the rotation); to bf16 pages, 805 MB, 125 us (95 %);
+// fp32, one token a thread, to fp32 pages, 1611 MB, 264 us (90 %).  One token: 2.5 us.
 enum Mode { kRope, kRopeBackward, kAppend, kAppendE4m3 };
 
 // U.  The e4m3 append, bound by instructions, shares its addressing among four
