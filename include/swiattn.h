@@ -357,6 +357,30 @@ int swiattn_rope_backward(const void* dq_rot, const void* dk_rot, const int32_t*
                           int64_t q_stride, int64_t k_stride, int64_t q_out_stride,
                           int64_t k_out_stride, int dtype, void* stream);
 
+/* swiattn_rope with positions on several axes, as image and video tokens have
+ * them (time, height, width; the pages have no counterpart, their positions
+ * being those of text): token t has the n_axes positions
+ * positions[a * B*N + t] (int32 [n_axes,B,N], any sign), and frequency f turns by
+ * positions[axes[f] * B*N + t] * w_f.  axes is a HOST array uint8
+ * [rot_dim / 2], read before the call returns, every entry below n_axes; so
+ * sections of the frequencies, and axes dealt out to them in turn, are both
+ * possible.  1 <= n_axes <= 64.  A token whose positions all agree is rotated
+ * as by swiattn_rope at that position, bit for bit.  Other arguments as for
+ * swiattn_rope; positions and axes are not NULL. */
+int swiattn_rope_axes(const void* q, const void* k, const int32_t* positions, const uint8_t* axes,
+                      int n_axes, const double* inv_freq, void* q_out, void* k_out, int B, int N,
+                      int Hq, int Hkv, int d, int rot_dim, int interleaved, float factor,
+                      int64_t q_stride, int64_t k_stride, int64_t q_out_stride,
+                      int64_t k_out_stride, int dtype, void* stream);
+
+/* Gradient of swiattn_rope_axes, as swiattn_rope_backward is of swiattn_rope. */
+int swiattn_rope_axes_backward(const void* dq_rot, const void* dk_rot, const int32_t* positions,
+                               const uint8_t* axes, int n_axes, const double* inv_freq, void* dq,
+                               void* dk, int B, int N, int Hq, int Hkv, int d, int rot_dim,
+                               int interleaved, float factor, int64_t q_stride, int64_t k_stride,
+                               int64_t q_out_stride, int64_t k_out_stride, int dtype,
+                               void* stream);
+
 /* Appends new tokens' keys and values to a paged cache, rotating q and k on
  * the way (swiattn_rope's map), for a prompt, a chunk of one, or a decode
  * step.  The cache is that of swiattn_decode_paged.
@@ -398,6 +422,22 @@ int swiattn_append_paged(const void* q, const void* k, const void* v, const int3
                          int page_size, int num_pages, int Hq, int Hkv, int d, int rot_dim,
                          int interleaved, float factor, int64_t q_stride, int64_t k_stride,
                          int64_t v_stride, int dtype, int page_dtype, void* stream);
+
+/* swiattn_append_paged where a new token is rotated by positions of its own
+ * and not by its place in the cache, which stays what it was: for the tokens of
+ * a drafted tree (swiattn_decode_tree), whose positions follow their depth in
+ * it, and for image and video tokens, which have positions on several axes.
+ * positions int32 [n_axes, T], any sign; axes as for swiattn_rope_axes, or NULL
+ * with n_axes == 1.  The positions of tokens that are passed over do not matter.
+ * rot_dim is not 0; other arguments as for swiattn_append_paged. */
+int swiattn_append_paged_at(const void* q, const void* k, const void* v, const int32_t* starts,
+                            const int32_t* seq_lens, const int32_t* block_table,
+                            const int32_t* positions, const uint8_t* axes, int n_axes,
+                            const double* inv_freq, void* q_out, void* k_pages, void* v_pages,
+                            uint8_t* k_exp, uint8_t* v_exp, int T, int B, int max_pages,
+                            int page_size, int num_pages, int Hq, int Hkv, int d, int rot_dim,
+                            int interleaved, float factor, int64_t q_stride, int64_t k_stride,
+                            int64_t v_stride, int dtype, int page_dtype, void* stream);
 
 /* Bytes of device workspace swiattn_decode_paged_e4m3 needs for these sizes
  * (0 for invalid sizes). */

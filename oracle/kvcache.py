@@ -145,3 +145,13 @@ def decode(q, k, v, v_exps, seq_lens, gate, W, S, scale):
             peak[b, h] = np.max(p * np.ldexp(1.0, v_exps[b, at, h // (Hq // Hkv)].astype(np.int64) - 127))
             size[b, h] = scale * np.max(np.abs(kk) @ np.abs(q[b, h]))
     return o, lse, absum, peak, size
+
+
+def rotate_axes(x, positions, axes, inv_freq, interleaved=False, factor=1.0, transposed=False):
+    """rotate() with positions [A, ...]: frequency f turns by the position on axis axes[f].  The axes'
+    rotations concern different pairs, so they follow one another."""
+    y = np.asarray(x, dtype=np.float64)
+    for a, p in enumerate(positions):
+        mine = np.where(np.asarray(axes) == a, np.asarray(inv_freq, dtype=np.float64), 0.0)
+        y = rotate(y, p, mine, interleaved, factor if a == 0 else 1.0, transposed)
+    return y

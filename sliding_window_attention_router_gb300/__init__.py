@@ -51,6 +51,7 @@ EXPORTS = (
     "swiattn_get_device_error", "swiattn_status_string", "swiattn_set_profile_events",
     "swiattn_num_sms", "swiattn_set_wait_limit_ns", "swiattn_rope", "swiattn_rope_backward",
     "swiattn_append_paged", "swiattn_decode_paged_e4m3_workspace", "swiattn_decode_paged_e4m3",
+    "swiattn_rope_axes", "swiattn_rope_axes_backward", "swiattn_append_paged_at",
 )
 
 
@@ -109,8 +110,14 @@ def _load() -> ctypes.CDLL:
                                                   [f32, i32, vp, sz, vp])
             for name in ("swiattn_rope", "swiattn_rope_backward"):
                 getattr(lib, name).argtypes = [vp] * 6 + [i32] * 7 + [f32] + [i64] * 4 + [i32, vp]
+            u8s = ctypes.c_char_p   # a host array of bytes
+            for name in ("swiattn_rope_axes", "swiattn_rope_axes_backward"):
+                getattr(lib, name).argtypes = ([vp] * 3 + [u8s, i32] + [vp] * 3 + [i32] * 7 + [f32]
+                                               + [i64] * 4 + [i32, vp])
             lib.swiattn_append_paged.argtypes = ([vp] * 12 + [i32] * 10 + [f32] + [i64] * 3
                                                  + [i32, i32, vp])
+            lib.swiattn_append_paged_at.argtypes = ([vp] * 7 + [u8s, i32] + [vp] * 6 + [i32] * 10
+                                                    + [f32] + [i64] * 3 + [i32, i32, vp])
             lib.swiattn_decode_paged_e4m3_workspace.argtypes = [i32] * 8
             lib.swiattn_decode_paged_e4m3_workspace.restype = sz
             lib.swiattn_decode_paged_e4m3.argtypes = [vp] * 10 + [i32] * 9 + [f32, i32, vp, sz, vp]
@@ -127,7 +134,8 @@ def _load() -> ctypes.CDLL:
                          "swiattn_decode_paged", "swiattn_decode_anchored",
                          "swiattn_prefill_anchored", "swiattn_route_prefill",
                          "swiattn_prefill_host", "swiattn_rope", "swiattn_rope_backward",
-                         "swiattn_append_paged", "swiattn_decode_paged_e4m3"):
+                         "swiattn_append_paged", "swiattn_decode_paged_e4m3", "swiattn_rope_axes",
+                         "swiattn_rope_axes_backward", "swiattn_append_paged_at"):
                 getattr(lib, name).restype = ctypes.c_int
             _lib = lib
     return _lib
@@ -560,7 +568,17 @@ def _launch(where: str, index: int, *args):
         raise SwiAttnError(status, where)
 
 
-def _rope(where, q, k, inv_freq, positions, interleaved, factor, out):
+def _axes(axes, half: int) -> bytes:
+    """The axis of each of `half` frequencies, as the library takes them."""
+    if isinstance(axes, torch.Tensor):
+        axes = axes.tolist()
+    axes = bytes(axes)   # refuses what is no whole number of 0 to 255
+    if len(axes) != half:
+        raise ValueError(f"axes must hold {half} values, one for each frequency, got {len(axes)}")
+    return axes
+
+
+def _rope(where, q, k, inv_freq, positions, axes, interleaved, factor, out):
     some = q if q is not None else k
     index = _gpu(some, "q and k")
     if some.dim() != 4:
@@ -588,31 +606,44 @@ def _rope(where, q, k, inv_freq, positions, interleaved, factor, out):
         results.append(o)
         sizes.append((heads, step, out_step))
     _same(inv_freq, "inv_freq", index, torch.float64)
-    if positions is not None and _same(positions, "positions", index, torch.int32).numel() != B * N:
-        raise ValueError(f"positions must be [{B}, {N}]")
     (Hq, qs, qos), (Hkv, ks, kos) = sizes
+    more = ()
+    if axes is not None:
+        if positions is None:
+            raise ValueError("axes without positions")
+        shape = _same(positions, "positions", index, torch.int32).shape
+        if len(shape) != 3 or shape[1] != B or shape[2] != N:
+            raise ValueError(f"positions must be [axes, {B}, {N}], got {list(shape)}")
+        where = where.replace("rope", "rope_axes")
+        more = (_axes(axes, inv_freq.numel()), shape[0])
+    elif positions is not None and (
+            _same(positions, "positions", index, torch.int32).numel() != B * N):
+        raise ValueError(f"positions must be [{B}, {N}]")
     if some.numel():
-        _launch(where, index, _addr(q), _addr(k), _addr(positions), inv_freq.data_ptr(),
+        _launch(where, index, _addr(q), _addr(k), _addr(positions), *more, inv_freq.data_ptr(),
                 _addr(results[0]), _addr(results[1]), B, N, Hq, Hkv, d, 2 * inv_freq.numel(),
                 bool(interleaved), factor, qs, ks, qos, kos, kind)
     return results[0], results[1]
 
 
-def rope(q, k, inv_freq, positions=None, interleaved: bool = False, factor: float = 1.0, out=None):
+def rope(q, k, inv_freq, positions=None, interleaved: bool = False, factor: float = 1.0, out=None,
+         axes=None):
     """Rotary position encoding of q [B,N,Hq,d] and k [B,N,Hkv,d] (either may be None), for
     prefill, dual_branch and the rest, whose q and k arrive position-encoded.  inv_freq fp64
     [rot_dim/2], radians a position; positions int32 [B,N] (None: 0..N-1); interleaved: pairs
     (2f, 2f+1) instead of (f, f + rot_dim/2); factor multiplies cosines and sines.  q and k may
     be views of a fused projection.  Returns (q_out, k_out), contiguous unless given as out,
-    which may be (q, k) themselves (in place)."""
-    return _rope("swiattn_rope", q, k, inv_freq, positions, interleaved, factor, out)
+    which may be (q, k) themselves (in place).
+    axes: with positions int32 [A,B,N] on A axes (time, height, width), the axis that each
+    frequency turns by, a sequence of rot_dim/2 whole numbers below A."""
+    return _rope("swiattn_rope", q, k, inv_freq, positions, axes, interleaved, factor, out)
 
 
 def rope_backward(dq_rot, dk_rot, inv_freq, positions=None, interleaved: bool = False,
-                  factor: float = 1.0, out=None):
+                  factor: float = 1.0, out=None, axes=None):
     """Gradient of rope: (dq, dk) from the gradients of its outputs.  Arguments as for rope."""
-    return _rope("swiattn_rope_backward", dq_rot, dk_rot, inv_freq, positions, interleaved, factor,
-                 out)
+    return _rope("swiattn_rope_backward", dq_rot, dk_rot, inv_freq, positions, axes, interleaved,
+                 factor, out)
 
 
 _EXPONENTS = (torch.uint8, torch.float8_e8m0fnu)
@@ -628,7 +659,8 @@ def _exponents(t, name: str, index: int, shape):
 
 
 def append_paged(q, k, v, k_pages, v_pages, block_table, seq_lens, inv_freq=None, starts=None,
-                 interleaved: bool = False, factor: float = 1.0, k_exp=None, v_exp=None, out=None):
+                 interleaved: bool = False, factor: float = 1.0, k_exp=None, v_exp=None, out=None,
+                 positions=None, axes=None):
     """Append new tokens to a paged cache, rotating q and k on the way.  q [T,Hq,d] (or None),
     k, v [T,Hkv,d], packed; sequence b owns tokens starts[b] .. starts[b+1]-1 (int32 [B+1]; None:
     one token each, T == B), the last of its seq_lens[b] (int32 [B], new tokens included).
@@ -636,7 +668,10 @@ def append_paged(q, k, v, k_pages, v_pages, block_table, seq_lens, inv_freq=None
     v_exp [num_pages, Hkv, page_size] (uint8 or float8_e8m0fnu); block_table int32 [B, max_pages].
     inv_freq, interleaved, factor as for rope (inv_freq None: no rotation).  The pages are written
     in place; returns the rotated q [T,Hq,d] (None without q).  Rows of q's result that no
-    sequence owns are left as they were (a result allocated here: undefined)."""
+    sequence owns are left as they were (a result allocated here: undefined).
+    positions int32 [T]: the positions to rotate by, where they are not those of the tokens in
+    their sequences (the tokens of a drafted tree: see decode_tree); or, with axes (as for rope),
+    int32 [A,T]."""
     index = _gpu(k, "k")
     T, dtype = k.shape[0], k.dtype
     lead = [T]
@@ -677,8 +712,18 @@ def append_paged(q, k, v, k_pages, v_pages, block_table, seq_lens, inv_freq=None
     rot_dim = 0
     if inv_freq is not None:
         rot_dim = 2 * _same(inv_freq, "inv_freq", index, torch.float64).numel()
-    _launch("swiattn_append_paged", index, _addr(q), k.data_ptr(), v.data_ptr(), _addr(starts),
-            seq_lens.data_ptr(), block_table.data_ptr(), _addr(inv_freq), _addr(out),
+    where, more = "swiattn_append_paged", ()
+    if positions is not None or axes is not None:
+        if inv_freq is None or positions is None:
+            raise ValueError("positions turn by inv_freq, and axes are of positions")
+        given = _same(positions, "positions", index, torch.int32).shape
+        if len(given) != (1 if axes is None else 2) or given[-1] != T:
+            raise ValueError(f"positions must be [{T}], or [axes, {T}] with axes, got {list(given)}")
+        where = "swiattn_append_paged_at"
+        more = (positions.data_ptr(), None if axes is None else _axes(axes, rot_dim // 2),
+                1 if axes is None else given[0])
+    _launch(where, index, _addr(q), k.data_ptr(), v.data_ptr(), _addr(starts),
+            seq_lens.data_ptr(), block_table.data_ptr(), *more, _addr(inv_freq), _addr(out),
             k_pages.data_ptr(), v_pages.data_ptr(), ke, ve, T, B, table[1], shape[1],
             shape[0], Hq, Hkv, d, rot_dim, bool(interleaved), factor, qs, ks, vs, _DT[dtype], kind)
     return out

@@ -6,7 +6,8 @@
 //   a' = m (a cos - b sin),   b' = m (b cos + a sin),
 // with (a, b) = (x[f], x[f + r/2]) or, interleaved, (x[2f], x[2f+1]); the
 // dimensions from r on pass through.  The gradient is the transposed map: the
-// same with the sine negated.
+// same with the sine negated.  With several axes (time, height, width) a token
+// has a position on each, and p is the one on the axis of f.
 //
 // The angle: w_f / 2pi is held as a 64-bit binary fraction of a turn F, so
 // p F mod 2^64 is the angle modulo a whole turn without any rounding (a float
@@ -275,13 +276,13 @@ __global__ void __launch_bounds__(kMaxThreads) rotate_kernel(const __grid_consta
         if (kStored) {
             place = place_of(a, t);
             page = place.b < 0 ? -1 : a.block_table[static_cast<int64_t>(place.b) * a.max_pages + (place.pos >> a.page_lg)];
-        } else {
-            place.pos = a.positions ? a.positions[t] : t % a.N;
         }
         if (table_used && f < half) {   // while the page number is on its way
+            int pos = kStored ? place.pos : t % a.N;
+            if (a.positions) pos = a.positions[(a.axes > 1 ? static_cast<int64_t>(a.axis_of[f]) * a.tokens : 0) + t];
             float factor = a.factor;
             const uint64_t fraction = turn_fraction(a.inv_freq[f], factor);
-            const float2 cs = cos_sin(fraction, place.pos, factor);
+            const float2 cs = cos_sin(fraction, pos, factor);
             s_table[j][table_at(f)] = cs.x;
             s_table[j][table_at(f) + 2] = cs.y;
         }

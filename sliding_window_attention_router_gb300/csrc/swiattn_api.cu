@@ -708,9 +708,21 @@ bool token_stride_ok(int64_t stride, int heads, int d, int dtype) {
 bool rot_dim_ok(int rot_dim, int d) { return rot_dim >= 16 && rot_dim <= d && rot_dim % 16 == 0; }
 bool heads_ok(int heads) { return heads > 0 && heads <= (1 << 16); }
 
-int rope_call(const void* q, const void* k, const int32_t* positions, const double* inv_freq,
-              void* q_out, void* k_out, int B, int N, int Hq, int Hkv, int d, int rot_dim,
-              int interleaved, float factor, int64_t q_stride, int64_t k_stride,
+// The axes of rotated positions: `axes` a host array of rot_dim / 2 (nullptr: all 0).
+constexpr int kOneAxis = 1;
+bool set_axes(RotateArgs& a, const uint8_t* axes, int n_axes, int rot_dim) {
+    if (n_axes < 1 || n_axes > 64) return false;
+    a.axes = n_axes;
+    for (int f = 0; axes && f < rot_dim / 2; ++f) {
+        if (axes[f] >= n_axes) return false;
+        a.axis_of[f] = axes[f];
+    }
+    return true;
+}
+
+int rope_call(const void* q, const void* k, const int32_t* positions, const uint8_t* axes, int n_axes,
+              const double* inv_freq, void* q_out, void* k_out, int B, int N, int Hq, int Hkv, int d,
+              int rot_dim, int interleaved, float factor, int64_t q_stride, int64_t k_stride,
               int64_t q_out_stride, int64_t k_out_stride, int dtype, bool backward, void* stream) {
     if (B <= 0 || N <= 0 || (d != 64 && d != 128) || !rot_dim_ok(rot_dim, d)) return SWIATTN_EINVAL;
     if (dtype != SWIATTN_BF16 && dtype != SWIATTN_F32) return SWIATTN_EINVAL;
@@ -730,6 +742,7 @@ int rope_call(const void* q, const void* k, const int32_t* positions, const doub
               (k == k_out && k_stride != k_out_stride)))
         return SWIATTN_EINVAL;
     RotateArgs a = {};
+    if (!set_axes(a, axes, n_axes, rot_dim)) return SWIATTN_EINVAL;
     a.q = q;
     a.k = k;
     a.positions = positions;
@@ -761,8 +774,9 @@ int swiattn_rope(const void* q, const void* k, const int32_t* positions, const d
                  void* q_out, void* k_out, int B, int N, int Hq, int Hkv, int d, int rot_dim,
                  int interleaved, float factor, int64_t q_stride, int64_t k_stride,
                  int64_t q_out_stride, int64_t k_out_stride, int dtype, void* stream) {
-    return rope_call(q, k, positions, inv_freq, q_out, k_out, B, N, Hq, Hkv, d, rot_dim, interleaved,
-                     factor, q_stride, k_stride, q_out_stride, k_out_stride, dtype, false, stream);
+    return rope_call(q, k, positions, nullptr, kOneAxis, inv_freq, q_out, k_out, B, N, Hq, Hkv, d,
+                     rot_dim, interleaved, factor, q_stride, k_stride, q_out_stride, k_out_stride,
+                     dtype, false, stream);
 }
 
 int swiattn_rope_backward(const void* dq_rot, const void* dk_rot, const int32_t* positions,
@@ -770,18 +784,43 @@ int swiattn_rope_backward(const void* dq_rot, const void* dk_rot, const int32_t*
                           int Hkv, int d, int rot_dim, int interleaved, float factor,
                           int64_t q_stride, int64_t k_stride, int64_t q_out_stride,
                           int64_t k_out_stride, int dtype, void* stream) {
-    return rope_call(dq_rot, dk_rot, positions, inv_freq, dq, dk, B, N, Hq, Hkv, d, rot_dim,
-                     interleaved, factor, q_stride, k_stride, q_out_stride, k_out_stride, dtype,
-                     true, stream);
+    return rope_call(dq_rot, dk_rot, positions, nullptr, kOneAxis, inv_freq, dq, dk, B, N, Hq, Hkv, d,
+                     rot_dim, interleaved, factor, q_stride, k_stride, q_out_stride, k_out_stride,
+                     dtype, true, stream);
 }
 
-int swiattn_append_paged(const void* q, const void* k, const void* v, const int32_t* starts,
-                         const int32_t* seq_lens, const int32_t* block_table,
-                         const double* inv_freq, void* q_out, void* k_pages, void* v_pages,
-                         uint8_t* k_exp, uint8_t* v_exp, int T, int B, int max_pages,
-                         int page_size, int num_pages, int Hq, int Hkv, int d, int rot_dim,
-                         int interleaved, float factor, int64_t q_stride, int64_t k_stride,
-                         int64_t v_stride, int dtype, int page_dtype, void* stream) {
+int swiattn_rope_axes(const void* q, const void* k, const int32_t* positions, const uint8_t* axes,
+                      int n_axes, const double* inv_freq, void* q_out, void* k_out, int B, int N,
+                      int Hq, int Hkv, int d, int rot_dim, int interleaved, float factor,
+                      int64_t q_stride, int64_t k_stride, int64_t q_out_stride,
+                      int64_t k_out_stride, int dtype, void* stream) {
+    if (!positions || !axes) return SWIATTN_EINVAL;
+    return rope_call(q, k, positions, axes, n_axes, inv_freq, q_out, k_out, B, N, Hq, Hkv, d, rot_dim,
+                     interleaved, factor, q_stride, k_stride, q_out_stride, k_out_stride, dtype, false,
+                     stream);
+}
+
+int swiattn_rope_axes_backward(const void* dq_rot, const void* dk_rot, const int32_t* positions,
+                               const uint8_t* axes, int n_axes, const double* inv_freq, void* dq,
+                               void* dk, int B, int N, int Hq, int Hkv, int d, int rot_dim,
+                               int interleaved, float factor, int64_t q_stride, int64_t k_stride,
+                               int64_t q_out_stride, int64_t k_out_stride, int dtype,
+                               void* stream) {
+    if (!positions || !axes) return SWIATTN_EINVAL;
+    return rope_call(dq_rot, dk_rot, positions, axes, n_axes, inv_freq, dq, dk, B, N, Hq, Hkv, d,
+                     rot_dim, interleaved, factor, q_stride, k_stride, q_out_stride, k_out_stride,
+                     dtype, true, stream);
+}
+
+namespace {
+
+int append_call(const void* q, const void* k, const void* v, const int32_t* starts,
+                const int32_t* seq_lens, const int32_t* block_table, const int32_t* positions,
+                const uint8_t* axes, int n_axes, const double* inv_freq, void* q_out, void* k_pages,
+                void* v_pages, uint8_t* k_exp, uint8_t* v_exp, int T, int B, int max_pages,
+                int page_size, int num_pages, int Hq, int Hkv, int d, int rot_dim, int interleaved,
+                float factor, int64_t q_stride, int64_t k_stride, int64_t v_stride, int dtype,
+                int page_dtype, void* stream) {
     if (T < 0 || B <= 0 || B > (1 << 30) || !heads_ok(Hkv) || (d != 64 && d != 128)) return SWIATTN_EINVAL;
     if (page_size <= 0 || (page_size & (page_size - 1)) != 0 || max_pages <= 0 || num_pages <= 0 ||
         (int64_t)max_pages * page_size > (1 << 30))
@@ -804,9 +843,11 @@ int swiattn_append_paged(const void* q, const void* k, const void* v, const int3
               !token_stride_ok(q_stride, Hq, d, dtype) ||
               (q == q_out && q_stride != (int64_t)Hq * d)))
         return SWIATTN_EINVAL;
+    RotateArgs a = {};
+    if (!set_axes(a, axes, n_axes, rot_dim)) return SWIATTN_EINVAL;
     DeviceInfo di;
     if (!device_info(di)) return SWIATTN_ECUDA;
-    RotateArgs a = {};
+    a.positions = positions;
     a.q = q;
     a.k = k;
     a.v = v;
@@ -841,6 +882,37 @@ int swiattn_append_paged(const void* q, const void* k, const void* v, const int3
     const cudaError_t e = launch_append(a, dtype, page_dtype, s);
     prof_stop(s);
     return launched(e);
+}
+
+}  // namespace
+
+int swiattn_append_paged(const void* q, const void* k, const void* v, const int32_t* starts,
+                         const int32_t* seq_lens, const int32_t* block_table,
+                         const double* inv_freq, void* q_out, void* k_pages, void* v_pages,
+                         uint8_t* k_exp, uint8_t* v_exp, int T, int B, int max_pages,
+                         int page_size, int num_pages, int Hq, int Hkv, int d, int rot_dim,
+                         int interleaved, float factor, int64_t q_stride, int64_t k_stride,
+                         int64_t v_stride, int dtype, int page_dtype, void* stream) {
+    return append_call(q, k, v, starts, seq_lens, block_table, nullptr, nullptr, kOneAxis, inv_freq,
+                       q_out, k_pages, v_pages, k_exp, v_exp, T, B, max_pages, page_size, num_pages,
+                       Hq, Hkv, d, rot_dim, interleaved, factor, q_stride, k_stride, v_stride, dtype,
+                       page_dtype, stream);
+}
+
+int swiattn_append_paged_at(const void* q, const void* k, const void* v, const int32_t* starts,
+                            const int32_t* seq_lens, const int32_t* block_table,
+                            const int32_t* positions, const uint8_t* axes, int n_axes,
+                            const double* inv_freq, void* q_out, void* k_pages, void* v_pages,
+                            uint8_t* k_exp, uint8_t* v_exp, int T, int B, int max_pages,
+                            int page_size, int num_pages, int Hq, int Hkv, int d, int rot_dim,
+                            int interleaved, float factor, int64_t q_stride, int64_t k_stride,
+                            int64_t v_stride, int dtype, int page_dtype, void* stream) {
+    if (T > 0 && !positions) return SWIATTN_EINVAL;
+    if (rot_dim == 0 || (n_axes > 1 && !axes)) return SWIATTN_EINVAL;
+    return append_call(q, k, v, starts, seq_lens, block_table, positions, axes, n_axes, inv_freq,
+                       q_out, k_pages, v_pages, k_exp, v_exp, T, B, max_pages, page_size, num_pages,
+                       Hq, Hkv, d, rot_dim, interleaved, factor, q_stride, k_stride, v_stride, dtype,
+                       page_dtype, stream);
 }
 
 namespace {

@@ -303,8 +303,12 @@ struct RotateArgs {
     int interleaved;
     float factor;
     int part_slots, span;   // how the work is cut, set by the launcher
-    // rope
-    const int32_t* positions;   // nullptr: token t of sequences of N is at t % N
+    // The angles' positions: [axes, tokens], frequency f on axis axis_of[f] (axes
+    // 1: every frequency on the one there is).  nullptr: token t of sequences of N
+    // is at t % N, or, append, where its slot is.
+    const int32_t* positions;
+    int axes;
+    uint8_t axis_of[64];
     int N;
     // append
     const int32_t* starts;      // [B+1] first token of each sequence; nullptr: one token each

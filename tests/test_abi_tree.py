@@ -1,0 +1,51 @@
+"""Host-side refusals of the rotation with axes, the append at given positions, the tree attention and
+the calls that keep and fork sequences (no GPU): every argument rule of include/swiattn.h, checked
+before anything is launched."""
+import numpy as np
+import pytest
+
+from oracle import kvcache as ref
+from test_abi_cache import BF16, BIG, E4M3, EINVAL, F32, FAKE, ODD, OK, EUNSUPPORTED, lib  # noqa: F401
+
+AXES = bytes([0, 1, 2, 3] * 16)
+
+
+@pytest.mark.parametrize("name", ["swiattn_rope_axes", "swiattn_rope_axes_backward"])
+def test_rope_axes_refusals(lib, name):
+    def call(q=FAKE, k=FAKE, pos=FAKE, axes=AXES, n=4, w=FAKE, qo=BIG, ko=BIG, B=2, N=64, Hq=4, Hkv=2, d=128, rot=128,
+             inter=0, factor=1.0, qs=512, ks=256, qos=512, kos=256, dt=BF16):
+        return getattr(lib, name)(q, k, pos, axes, n, w, qo, ko, B, N, Hq, Hkv, d, rot, inter, factor, qs, ks, qos,
+                                  kos, dt, None)
+    for bad in (dict(pos=None), dict(axes=None), dict(n=0), dict(n=3), dict(n=-1), dict(n=65), dict(axes=bytes(63) + b"\4"),
+                dict(B=0), dict(d=96), dict(rot=24), dict(w=None), dict(q=None), dict(q=ODD), dict(qs=516),
+                dict(factor=float("nan")), dict(dt=E4M3)):
+        assert call(**bad) == EINVAL, bad
+
+
+def test_append_at_refusals(lib):
+    def call(q=FAKE, k=FAKE, v=FAKE, starts=FAKE, sl=FAKE, bt=FAKE, pos=FAKE, axes=AXES, n=4, w=FAKE, qo=BIG, kp=BIG,
+             vps=BIG, ke=BIG, ve=BIG, T=10, B=3, mp=4, ps=16, np_=12, Hq=4, Hkv=2, d=128, rot=128, inter=0, factor=1.0,
+             qs=512, ks=256, vs=256, dt=BF16, pdt=BF16):
+        return lib.swiattn_append_paged_at(q, k, v, starts, sl, bt, pos, axes, n, w, qo, kp, vps, ke, ve, T, B, mp, ps,
+                                           np_, Hq, Hkv, d, rot, inter, factor, qs, ks, vs, dt, pdt, None)
+    for bad in (dict(pos=None), dict(axes=None), dict(n=0), dict(n=3), dict(rot=0), dict(w=None), dict(T=-1), dict(ps=12),
+                dict(k=ODD), dict(pdt=E4M3, ke=None), dict(dt=F32, pdt=BF16)):
+        assert call(**bad) == EINVAL, bad
+    assert call(dt=F32, pdt=E4M3) == EUNSUPPORTED
+    assert call(T=0) == OK
+
+
+def test_reference_rotation_with_axes():
+    """Axes that agree are one rotation; an axis at position 0 leaves its pairs alone."""
+    rng = np.random.default_rng(1)
+    x, w = rng.standard_normal((5, 2, 64)), 100.0 ** -(np.arange(24) / 24)
+    axes, p = np.arange(24) % 3, rng.integers(0, 99, 5)
+    for inter in (False, True):
+        one = ref.rotate(x, p, w, inter, 1.5)
+        np.testing.assert_allclose(ref.rotate_axes(x, [p, p, p], axes, w, inter, 1.5), one, atol=1e-12)
+        got = ref.rotate_axes(x, [p, 0 * p, p], axes, w, inter)
+        first, second = (np.s_[..., 0:48:2], np.s_[..., 1:48:2]) if inter else (np.s_[..., :24], np.s_[..., 24:48])
+        for half in (first, second):
+            np.testing.assert_allclose(got[half][..., axes == 1], x[half][..., axes == 1], atol=1e-12)
+            np.testing.assert_allclose(got[half][..., axes != 1], (ref.rotate(x, p, w, inter))[half][..., axes != 1],
+                                       atol=1e-12)
