@@ -478,6 +478,61 @@ int swiattn_decode_paged_e4m3(const void* q, const void* k_pages, const void* v_
                               int n_anchor, float scale, int dtype, void* workspace,
                               size_t workspace_bytes, void* stream);
 
+/* Keeps the accepted path of each sequence's drafted tree (swiattn_decode_tree)
+ * in a paged cache, for all layers at once: the keys and values of the path's
+ * tokens, from its root to leaf[b], move to the first slots of the tree, in the
+ * path's order, and the sequence's length becomes what it was before the tree plus
+ * the path's tokens.
+ *  - k_pages, v_pages [layers, num_pages, page_size, Hkv, d] of page_dtype
+ *    (SWIATTN_F32, SWIATTN_BF16, or SWIATTN_E4M3 with k_exp, v_exp uint8
+ *    [layers, num_pages, Hkv, page_size], which move along), one block table for
+ *    all layers.
+ *  - seq_lens, starts, parents, T: as swiattn_decode_tree took them.  leaf int32
+ *    [B]: the path's last token, counted from the tree's first; negative: none of
+ *    the tree is kept.  lens_out int32 [B] receives the new lengths; it must not
+ *    overlap seq_lens.  A sequence without drafted tokens keeps its length.
+ *  - Only the path's slots are written; rows behind them stay as they are.
+ *  - A sequence with more than 256 drafted tokens, with fewer tokens than
+ *    drafted ones, with a length or starts outside their range, or with leaf not
+ *    in its tree is left as it is, lens_out[b] = seq_lens[b]; a parent that does
+ *    not come before its token ends the path there; a row whose table entry lies
+ *    outside [0, num_pages) is not moved.  Each is reported: swiattn_get_device_error
+ *    returns SWIATTN_EINVAL.
+ *  - Two sequences must not share the pages that the trees are on.
+ * d in {64, 128}; page_size a power of two with max_pages * page_size <= 2^30;
+ * layers <= 2^14, B <= 2^30 (larger: SWIATTN_EUNSUPPORTED).  No workspace. */
+int swiattn_accept_tree(void* k_pages, void* v_pages, uint8_t* k_exp, uint8_t* v_exp,
+                        const int32_t* block_table, const int32_t* seq_lens, const int32_t* starts,
+                        const int32_t* parents, const int32_t* leaf, int32_t* lens_out, int layers,
+                        int T, int B, int max_pages, int page_size, int num_pages, int Hkv, int d,
+                        int page_dtype, void* stream);
+
+/* Forks sequences of a paged cache, for all layers at once: child c continues
+ * sequence source[c] (samples of one prompt, beams), sharing its full pages and
+ * getting a copy of the part-filled last one.
+ *  - source int32 [C]: the sequence each child continues; negative: an empty
+ *    slot (length 0, table entries 0).
+ *  - new_page int32 [C]: the page that becomes the child's own: it receives the
+ *    rows of the source's part-filled last page and takes its place in the child's
+ *    table; where the source ends with a full page, it becomes the next one, if
+ *    the table has room, with nothing copied.  Negative: the child keeps the
+ *    source's table (one child may go on in the source's own page).
+ *  - table_out int32 [C, max_pages] and lens_out int32 [C] receive the children's
+ *    tables and lengths; they must not overlap block_table and seq_lens.
+ *  - Pools as for swiattn_accept_tree.  No two children may be given one page, nor
+ *    a page that a source ends in other than its own.  Rows of a new page past the
+ *    copied ones stay as they are.
+ *  - A child whose source is not below B, whose source's length is outside
+ *    [0, max_pages * page_size], or whose new_page or source page lies outside the
+ *    pool becomes an empty slot, and swiattn_get_device_error then reports
+ *    SWIATTN_EINVAL.
+ * Sizes as for swiattn_accept_tree; C == 0 is a valid no-op.  No workspace. */
+int swiattn_fork_paged(void* k_pages, void* v_pages, uint8_t* k_exp, uint8_t* v_exp,
+                       const int32_t* block_table, const int32_t* seq_lens, const int32_t* source,
+                       const int32_t* new_page, int32_t* table_out, int32_t* lens_out, int layers,
+                       int B, int C, int max_pages, int page_size, int num_pages, int Hkv, int d,
+                       int page_dtype, void* stream);
+
 /* Synchronises `stream`, then returns and clears the device error word of the
  * current device: SWIATTN_OK, SWIATTN_ETIMEOUT if a bounded device wait
  * expired since the last query, or SWIATTN_ECUDA if the synchronisation itself

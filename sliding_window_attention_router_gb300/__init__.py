@@ -23,6 +23,7 @@ __all__ = [
     "prefill_backward_workspace", "route_backward", "route_backward_workspace", "decode_paged",
     "decode_paged_workspace", "decode_anchored", "decode_anchored_workspace", "rope",
     "rope_backward", "append_paged", "decode_paged_e4m3", "decode_paged_e4m3_workspace",
+    "accept_tree", "fork_paged",
 ]
 
 F32, BF16, E4M3 = 0, 1, 2
@@ -52,6 +53,7 @@ EXPORTS = (
     "swiattn_num_sms", "swiattn_set_wait_limit_ns", "swiattn_rope", "swiattn_rope_backward",
     "swiattn_append_paged", "swiattn_decode_paged_e4m3_workspace", "swiattn_decode_paged_e4m3",
     "swiattn_rope_axes", "swiattn_rope_axes_backward", "swiattn_append_paged_at",
+    "swiattn_accept_tree", "swiattn_fork_paged",
 )
 
 
@@ -121,6 +123,8 @@ def _load() -> ctypes.CDLL:
             lib.swiattn_decode_paged_e4m3_workspace.argtypes = [i32] * 8
             lib.swiattn_decode_paged_e4m3_workspace.restype = sz
             lib.swiattn_decode_paged_e4m3.argtypes = [vp] * 10 + [i32] * 9 + [f32, i32, vp, sz, vp]
+            for name in ("swiattn_accept_tree", "swiattn_fork_paged"):
+                getattr(lib, name).argtypes = [vp] * 10 + [i32] * 9 + [vp]
             lib.swiattn_get_device_error.argtypes = [vp]
             lib.swiattn_status_string.argtypes = [i32]
             lib.swiattn_status_string.restype = ctypes.c_char_p
@@ -135,7 +139,8 @@ def _load() -> ctypes.CDLL:
                          "swiattn_prefill_anchored", "swiattn_route_prefill",
                          "swiattn_prefill_host", "swiattn_rope", "swiattn_rope_backward",
                          "swiattn_append_paged", "swiattn_decode_paged_e4m3", "swiattn_rope_axes",
-                         "swiattn_rope_axes_backward", "swiattn_append_paged_at"):
+                         "swiattn_rope_axes_backward", "swiattn_append_paged_at",
+                         "swiattn_accept_tree", "swiattn_fork_paged"):
                 getattr(lib, name).restype = ctypes.c_int
             _lib = lib
     return _lib
@@ -775,3 +780,99 @@ def decode_paged_e4m3(q, k_pages, v_pages, k_exp, v_exp, block_table, seq_lens, 
             page_size, num_pages, Hq, Hkv, d, W, n_anchor, scale, _DT[q.dtype],
             workspace.data_ptr(), workspace.numel())
     return (out, lse) if want_lse else out
+
+
+_PAGE_TYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float8_e4m3fn: E4M3}
+
+
+def _pools(k_pages, v_pages, k_exp, v_exp, index: int):
+    """Check page pools of one layer [num_pages, page_size, Hkv, d] or of several
+    [layers, num_pages, page_size, Hkv, d]; returns the pointers and (layers, num_pages, page_size,
+    Hkv, d, page type)."""
+    shape, dtype = _same(k_pages, "k_pages", index).shape, k_pages.dtype
+    if _same(v_pages, "v_pages", index, dtype).shape != shape or len(shape) not in (4, 5):
+        raise ValueError("k_pages and v_pages must both be [num_pages, page_size, Hkv, d] or "
+                         "[layers, num_pages, page_size, Hkv, d]")
+    kind = _PAGE_TYPES.get(dtype)
+    if kind is None:
+        raise ValueError(f"pages must be float32, bfloat16 or float8_e4m3fn, got {dtype}")
+    num_pages, page_size, Hkv, d = shape[-4:]
+    ke = ve = None
+    if kind == E4M3:
+        want = (*shape[:-4], num_pages, Hkv, page_size)
+        _exponents(k_exp, "k_exp", index, want)
+        _exponents(v_exp, "v_exp", index, want)
+        ke, ve = k_exp.data_ptr(), v_exp.data_ptr()
+    return ((k_pages.data_ptr(), v_pages.data_ptr(), ke, ve),
+            (shape[0] if len(shape) == 5 else 1, num_pages, page_size, Hkv, d, kind))
+
+
+def _sequences(block_table, seq_lens, index: int):
+    """Check block_table [B, max_pages] and seq_lens [B]; returns (B, max_pages)."""
+    B = _same(seq_lens, "seq_lens", index, torch.int32).numel()
+    table = _same(block_table, "block_table", index, torch.int32).shape
+    if len(table) != 2 or table[0] != B:
+        raise ValueError(f"block_table must be [{B}, max_pages]")
+    return B, table[1]
+
+
+def _trees(starts, parents, B: int, index: int):
+    """Check starts [B + 1] and parents [T] (None: chains)."""
+    if _same(starts, "starts", index, torch.int32).numel() != B + 1:
+        raise ValueError(f"starts must hold {B + 1} values")
+    if parents is not None and _same(parents, "parents", index, torch.int32).dim() != 1:
+        raise ValueError("parents must be [T]")
+
+
+def accept_tree(k_pages, v_pages, block_table, seq_lens, starts, parents, leaf, k_exp=None,
+                v_exp=None, out=None):
+    """Keep the accepted path of each drafted tree, all layers at once: the keys and values of the
+    tokens from the root to leaf[b] (int32 [B], counted from the tree's first token; negative: none)
+    move to the tree's first slots.  k_pages, v_pages [layers, num_pages, page_size, Hkv, d] or one
+    layer's [num_pages, page_size, Hkv, d], float8_e4m3fn with k_exp, v_exp [..., num_pages, Hkv,
+    page_size]; block_table, seq_lens, starts, parents as for decode_tree.  The pages are written in
+    place; returns the new lengths, int32 [B] (out, if given; not seq_lens itself)."""
+    index = _gpu(k_pages, "k_pages")
+    pointers, (layers, num_pages, page_size, Hkv, d, kind) = _pools(k_pages, v_pages, k_exp, v_exp,
+                                                                    index)
+    B, max_pages = _sequences(block_table, seq_lens, index)
+    _trees(starts, parents, B, index)
+    if _same(leaf, "leaf", index, torch.int32).numel() != B:
+        raise ValueError(f"leaf must hold {B} values")
+    if out is None:
+        out = torch.empty_like(seq_lens)
+    elif _same(out, "out", index, torch.int32).numel() != B:
+        raise ValueError(f"out must hold {B} values")
+    T = (1 << 31) - 1 if parents is None else parents.numel()
+    _launch("swiattn_accept_tree", index, *pointers, block_table.data_ptr(), seq_lens.data_ptr(),
+            starts.data_ptr(), _addr(parents), leaf.data_ptr(), out.data_ptr(), layers, T, B,
+            max_pages, page_size, num_pages, Hkv, d, kind)
+    return out
+
+
+def fork_paged(k_pages, v_pages, block_table, seq_lens, source, new_page, k_exp=None, v_exp=None,
+               out=None):
+    """Fork sequences of a paged cache, all layers at once: child c continues sequence source[c]
+    (int32 [C]; negative: an empty slot), shares its full pages, and has the rows of its part-filled
+    last page copied to page new_page[c] (int32 [C]; negative: no page of its own).  Pools as for
+    accept_tree; block_table int32 [B, max_pages], seq_lens int32 [B].  Returns the children's
+    (block_table int32 [C, max_pages], seq_lens int32 [C]) (out, if given)."""
+    index = _gpu(k_pages, "k_pages")
+    pointers, (layers, num_pages, page_size, Hkv, d, kind) = _pools(k_pages, v_pages, k_exp, v_exp,
+                                                                    index)
+    B, max_pages = _sequences(block_table, seq_lens, index)
+    C = _same(source, "source", index, torch.int32).numel()
+    if _same(new_page, "new_page", index, torch.int32).numel() != C:
+        raise ValueError(f"new_page must hold {C} values")
+    if out is None:
+        table = torch.empty((C, max_pages), dtype=torch.int32, device=k_pages.device)
+        lens = torch.empty(C, dtype=torch.int32, device=k_pages.device)
+    else:
+        table, lens = out
+        if _same(table, "out", index, torch.int32).shape != (C, max_pages) or (
+                _same(lens, "out", index, torch.int32).numel() != C):
+            raise ValueError(f"out must be [{C}, {max_pages}] and [{C}]")
+    _launch("swiattn_fork_paged", index, *pointers, block_table.data_ptr(), seq_lens.data_ptr(),
+            source.data_ptr(), new_page.data_ptr(), table.data_ptr(), lens.data_ptr(), layers, B, C,
+            max_pages, page_size, num_pages, Hkv, d, kind)
+    return table, lens

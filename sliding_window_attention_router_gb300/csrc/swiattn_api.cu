@@ -989,4 +989,102 @@ int swiattn_decode_paged_e4m3(const void* q, const void* k_pages, const void* v_
     return launched(launch_decode_e4m3(a, d, di.sms, static_cast<cudaStream_t>(stream)));
 }
 
+namespace {
+
+// Pools and tables of the calls on paged caches of several layers: SWIATTN_OK, or
+// why not.
+int pools_ok(const void* k_pages, const void* v_pages, const uint8_t* k_exp, const uint8_t* v_exp,
+             const int32_t* block_table, const int32_t* seq_lens, int layers, int B, int max_pages,
+             int page_size, int num_pages, int Hkv, int d, int page_dtype) {
+    if (layers <= 0 || B <= 0 || !heads_ok(Hkv) || (d != 64 && d != 128)) return SWIATTN_EINVAL;
+    if (page_size <= 0 || (page_size & (page_size - 1)) != 0 || max_pages <= 0 || num_pages <= 0 ||
+        (int64_t)max_pages * page_size > (1 << 30))
+        return SWIATTN_EINVAL;
+    if (page_dtype != SWIATTN_F32 && page_dtype != SWIATTN_BF16 && page_dtype != SWIATTN_E4M3)
+        return SWIATTN_EINVAL;
+    if (!k_pages || !v_pages || !block_table || !seq_lens || !aligned16(k_pages) || !aligned16(v_pages))
+        return SWIATTN_EINVAL;
+    if (page_dtype == SWIATTN_E4M3 && (!k_exp || !v_exp)) return SWIATTN_EINVAL;
+    if (B > (1 << 30) || layers > (1 << 14)) return SWIATTN_EUNSUPPORTED;
+    return SWIATTN_OK;
+}
+
+PagingArgs paging_args(void* k_pages, void* v_pages, uint8_t* k_exp, uint8_t* v_exp,
+                       const int32_t* block_table, const int32_t* seq_lens, int layers, int B,
+                       int max_pages, int page_size, int num_pages, int Hkv, int d, int page_dtype) {
+    PagingArgs a = {};
+    a.k_pages = k_pages;
+    a.v_pages = v_pages;
+    a.k_exp = page_dtype == SWIATTN_E4M3 ? k_exp : nullptr;
+    a.v_exp = page_dtype == SWIATTN_E4M3 ? v_exp : nullptr;
+    a.block_table = block_table;
+    a.seq_lens = seq_lens;
+    a.layers = layers;
+    a.B = B;
+    a.max_pages = max_pages;
+    while ((1 << a.page_lg) < page_size) ++a.page_lg;
+    a.num_pages = num_pages;
+    a.Hkv = Hkv;
+    a.row_bytes = Hkv * d * (page_dtype == SWIATTN_E4M3 ? 1 : page_dtype == SWIATTN_BF16 ? 2 : 4);
+    return a;
+}
+
+}  // namespace
+
+int swiattn_accept_tree(void* k_pages, void* v_pages, uint8_t* k_exp, uint8_t* v_exp,
+                        const int32_t* block_table, const int32_t* seq_lens, const int32_t* starts,
+                        const int32_t* parents, const int32_t* leaf, int32_t* lens_out, int layers,
+                        int T, int B, int max_pages, int page_size, int num_pages, int Hkv, int d,
+                        int page_dtype, void* stream) {
+    const int ok = pools_ok(k_pages, v_pages, k_exp, v_exp, block_table, seq_lens, layers, B,
+                            max_pages, page_size, num_pages, Hkv, d, page_dtype);
+    if (ok == SWIATTN_EINVAL || T < 0 || !starts || !leaf || !lens_out || lens_out == seq_lens)
+        return SWIATTN_EINVAL;
+    if (ok != SWIATTN_OK) return ok;
+    DeviceInfo di;
+    if (!device_info(di)) return SWIATTN_ECUDA;
+    PagingArgs a = paging_args(k_pages, v_pages, k_exp, v_exp, block_table, seq_lens, layers, B,
+                               max_pages, page_size, num_pages, Hkv, d, page_dtype);
+    a.starts = starts;
+    a.parents = parents;
+    a.leaf = leaf;
+    a.lens_out = lens_out;
+    a.T = T;
+    a.err = di.err;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    prof_start(s);
+    const cudaError_t e = launch_accept(a, s);
+    prof_stop(s);
+    return launched(e);
+}
+
+int swiattn_fork_paged(void* k_pages, void* v_pages, uint8_t* k_exp, uint8_t* v_exp,
+                       const int32_t* block_table, const int32_t* seq_lens, const int32_t* source,
+                       const int32_t* new_page, int32_t* table_out, int32_t* lens_out, int layers,
+                       int B, int C, int max_pages, int page_size, int num_pages, int Hkv, int d,
+                       int page_dtype, void* stream) {
+    const int ok = pools_ok(k_pages, v_pages, k_exp, v_exp, block_table, seq_lens, layers, B,
+                            max_pages, page_size, num_pages, Hkv, d, page_dtype);
+    if (ok == SWIATTN_EINVAL || C < 0) return SWIATTN_EINVAL;
+    if (C == 0) return SWIATTN_OK;
+    if (!source || !new_page || !table_out || !lens_out || table_out == block_table || lens_out == seq_lens)
+        return SWIATTN_EINVAL;
+    if (ok != SWIATTN_OK) return ok;
+    DeviceInfo di;
+    if (!device_info(di)) return SWIATTN_ECUDA;
+    PagingArgs a = paging_args(k_pages, v_pages, k_exp, v_exp, block_table, seq_lens, layers, B,
+                               max_pages, page_size, num_pages, Hkv, d, page_dtype);
+    a.source = source;
+    a.new_page = new_page;
+    a.table_out = table_out;
+    a.lens_out = lens_out;
+    a.C = C;
+    a.err = di.err;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    prof_start(s);
+    const cudaError_t e = launch_fork(a, s);
+    prof_stop(s);
+    return launched(e);
+}
+
 }  // extern "C"

@@ -348,6 +348,32 @@ struct DecodeE4m3Ws {
 DecodeE4m3Ws decode_e4m3_ws_layout(int B, int Hq, int Hkv, int d);
 cudaError_t launch_decode_e4m3(const DecodeE4m3Args& a, int d, int sms, cudaStream_t s);
 
+// ---------------------------- drafted trees, accepted paths and forks ---------
+constexpr int kMaxTree = 256;   // drafted tokens of a sequence
+
+struct PagingArgs {
+    void* k_pages;              // [layers, num_pages, 1 << page_lg] rows of row_bytes
+    void* v_pages;
+    uint8_t* k_exp;             // [layers, num_pages, Hkv, 1 << page_lg]; nullptr: none
+    uint8_t* v_exp;
+    const int32_t* block_table; // [B, max_pages]
+    const int32_t* seq_lens;    // [B]
+    // accept
+    const int32_t* starts;      // [B+1]
+    const int32_t* parents;     // [T], nullptr: each token's is the one before
+    const int32_t* leaf;        // [B]
+    // fork
+    const int32_t* source;      // [C]
+    const int32_t* new_page;    // [C]
+    int32_t* table_out;         // [C, max_pages]
+    int32_t* lens_out;          // [B], fork: [C]
+    unsigned int* err;
+    int T, B, C, layers, max_pages, page_lg, num_pages, Hkv;
+    int row_bytes;              // a token's heads
+};
+cudaError_t launch_accept(const PagingArgs& a, cudaStream_t s);
+cudaError_t launch_fork(const PagingArgs& a, cudaStream_t s);
+
 // Timing hook around the dominant kernel of a call (no-ops unless set).
 void prof_start(cudaStream_t s);
 void prof_stop(cudaStream_t s);

@@ -49,3 +49,28 @@ def test_reference_rotation_with_axes():
             np.testing.assert_allclose(got[half][..., axes == 1], x[half][..., axes == 1], atol=1e-12)
             np.testing.assert_allclose(got[half][..., axes != 1], (ref.rotate(x, p, w, inter))[half][..., axes != 1],
                                        atol=1e-12)
+
+
+def test_accept_refusals(lib):
+    def call(kp=FAKE, vps=BIG, ke=FAKE, ve=FAKE, bt=FAKE, sl=FAKE, st=FAKE, pa=FAKE, leaf=FAKE, out=BIG, layers=2, T=9,
+             B=3, mp=4, ps=16, np_=12, Hkv=2, d=128, pdt=BF16):
+        return lib.swiattn_accept_tree(kp, vps, ke, ve, bt, sl, st, pa, leaf, out, layers, T, B, mp, ps, np_, Hkv, d, pdt, None)
+    for bad in (dict(kp=None), dict(vps=None), dict(kp=ODD), dict(vps=ODD), dict(bt=None), dict(sl=None), dict(st=None),
+                dict(leaf=None), dict(out=None), dict(out=FAKE), dict(layers=0), dict(T=-1), dict(B=0), dict(mp=0), dict(ps=0),
+                dict(ps=24), dict(np_=0), dict(ps=1 << 20, mp=1 << 12), dict(Hkv=0), dict(d=96), dict(pdt=3),
+                dict(pdt=E4M3, ke=None), dict(pdt=E4M3, ve=None)):
+        assert call(**bad) == EINVAL, bad
+    for bad in (dict(layers=(1 << 14) + 1), dict(B=(1 << 30) + 1)):
+        assert call(**bad) == EUNSUPPORTED, bad
+
+
+def test_fork_refusals(lib):
+    def call(kp=FAKE, vps=BIG, ke=FAKE, ve=FAKE, bt=FAKE, sl=FAKE, src=FAKE, new=FAKE, to=BIG, lo=BIG, layers=2, B=3, C=4,
+             mp=4, ps=16, np_=12, Hkv=2, d=128, pdt=BF16):
+        return lib.swiattn_fork_paged(kp, vps, ke, ve, bt, sl, src, new, to, lo, layers, B, C, mp, ps, np_, Hkv, d, pdt, None)
+    for bad in (dict(kp=None), dict(vps=ODD), dict(bt=None), dict(sl=None), dict(src=None), dict(new=None), dict(to=None),
+                dict(lo=None), dict(to=FAKE), dict(lo=FAKE), dict(layers=-1), dict(B=0), dict(C=-1), dict(mp=-3), dict(ps=5),
+                dict(np_=0), dict(Hkv=-1), dict(d=80), dict(pdt=-1), dict(pdt=E4M3, ke=None)):
+        assert call(**bad) == EINVAL, bad
+    assert call(C=0) == OK
+    assert call(layers=1 << 15) == EUNSUPPORTED
