@@ -478,6 +478,55 @@ int swiattn_decode_paged_e4m3(const void* q, const void* k_pages, const void* v_
                               int n_anchor, float scale, int dtype, void* workspace,
                               size_t workspace_bytes, void* stream);
 
+/* Bytes of device workspace swiattn_decode_tree needs for these sizes (0 for
+ * invalid sizes). */
+size_t swiattn_decode_tree_workspace(int T, int B, int Hq, int Hkv, int d, int dtype);
+
+/* Attention of drafted tokens over a paged cache, for verifying several tokens of
+ * each sequence in one step (the pages decode one token a step; their gate and
+ * window are applied here to each drafted token as if it were that one).  The
+ * drafted tokens of a sequence form a tree: each continues the cached tokens or
+ * another drafted one.  Their keys and values are in the cache already
+ * (swiattn_append_paged_at), in the last slots of their sequence.
+ *  - T drafted tokens, packed: sequence b owns tokens [starts[b], starts[b+1])
+ *    (int32 [B+1], non-decreasing, starts[0] >= 0, starts[B] <= T), at most 256,
+ *    the last of its seq_lens[b] tokens (int32 [B]).
+ *  - parents int32 [T]: the token that each one continues, counted from its
+ *    sequence's first drafted one and coming before it; negative: the cached
+ *    tokens.  NULL: each continues the one before it (a chain).
+ *  - A token with x drafted ones before it on its path stands at position
+ *    base + x, base being its sequence's tokens that are not drafted.  It reads
+ *    the cached entries and those of the tokens on its path (itself among them)
+ *    that swiattn_decode_paged's query at that position would: gate[t] != 0 all,
+ *    else those at the last W positions and at the first n_anchor.
+ *  - q, o [T,Hq,d] of `dtype`; lse (nullable) fp32 [T,Hq]; gate uint8 [T]; pages
+ *    of `dtype` (k_exp, v_exp unused, may be NULL) or, with bf16, SWIATTN_E4M3 as
+ *    for swiattn_decode_paged_e4m3.  Rows of tokens that no sequence owns are left
+ *    as they were, and so are those of an empty slot (seq_lens[b] == 0).
+ *  - Whatever entries that a token does not read hold (NaN included) does not
+ *    reach its result; a NaN in one that it reads does.  A token whose result is
+ *    not finite costs more time.
+ *  - A sequence with more than 256 drafted tokens, with fewer tokens than drafted
+ *    ones or with a length outside [0, max_pages * page_size] is passed over, and
+ *    every sequence is where starts are not as above; a parent that does not come
+ *    before its token counts as negative; a table entry outside [0, num_pages) is
+ *    read as page 0.  Each is reported: swiattn_get_device_error returns
+ *    SWIATTN_EINVAL.
+ * d in {64, 128}; Hq / Hkv any whole number up to 128, B <= 65535, Hkv <= 2^16,
+ * T * Hq <= 2^26, num_pages * page_size <= 2^32 (larger: SWIATTN_EUNSUPPORTED);
+ * page_size a power of two, max_pages * page_size <= 2^30; T == 0 is a valid no-op.
+ * Bitwise repeatable; how a sequence's keys are split for the GPU depends on the
+ * whole batch, so the last bits of its result may.
+ * workspace: at least swiattn_decode_tree_workspace(...) bytes, 256-byte aligned,
+ * scratch only; calls that share one must not overlap in time. */
+int swiattn_decode_tree(const void* q, const void* k_pages, const void* v_pages,
+                        const uint8_t* k_exp, const uint8_t* v_exp, const int32_t* block_table,
+                        const int32_t* seq_lens, const int32_t* starts, const int32_t* parents,
+                        const uint8_t* gate, void* o, float* lse, int T, int B, int max_pages,
+                        int page_size, int num_pages, int Hq, int Hkv, int d, int W, int n_anchor,
+                        float scale, int dtype, int page_dtype, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
 /* Keeps the accepted path of each sequence's drafted tree (swiattn_decode_tree)
  * in a paged cache, for all layers at once: the keys and values of the path's
  * tokens, from its root to leaf[b], move to the first slots of the tree, in the

@@ -155,3 +155,54 @@ def rotate_axes(x, positions, axes, inv_freq, interleaved=False, factor=1.0, tra
         mine = np.where(np.asarray(axes) == a, np.asarray(inv_freq, dtype=np.float64), 0.0)
         y = rotate(y, p, mine, interleaved, factor if a == 0 else 1.0, transposed)
     return y
+
+
+def tree_path(parents, t):
+    """The tokens from the root of t's path to t; a parent that is not before its token ends it."""
+    out = [t]
+    while 0 <= parents[t] < t:
+        t = parents[t]
+        out.append(t)
+    return out[::-1]
+
+
+def tree_visible(parents, gates, base, W, S):
+    """[n, base + n] which entries each drafted token reads: the cached ones and its path's at
+    positions that the decode step at its own would read (``visited``)."""
+    n = len(parents)
+    seen = np.zeros((n, base + n), bool)
+    for t in range(n):
+        path = tree_path(parents, t)
+        at = visited(base + len(path), gates[t], W, S)
+        entry = np.concatenate([np.arange(base), base + np.array(path)])   # of each position
+        seen[t, entry[at]] = True
+    return seen
+
+
+def decode_tree(q, k, v, seq_lens, starts, parents, gates, W, S, scale):
+    """Attention of drafted tokens q [T, Hq, d] over values k, v [B, L, Hkv, d].  Returns o, lse and,
+    for tolerances: sum_j p_j |v_j| [T, Hq, d]; max_j scale sum_c |q_c k_jc| [T, Hq]; and the number of
+    entries read [T].  Rows of no sequence are NaN."""
+    T, Hq, d = q.shape
+    G = Hq // k.shape[2]
+    o, absum = np.full((T, Hq, d), np.nan), np.zeros((T, Hq, d))
+    lse, size, count = np.full((T, Hq), np.nan), np.zeros((T, Hq)), np.zeros(T, np.int64)
+    for b in range(len(seq_lens)):
+        first, n = int(starts[b]), int(starts[b + 1] - starts[b])
+        if n == 0 or seq_lens[b] == 0:
+            continue
+        base = int(seq_lens[b]) - n
+        seen = tree_visible(parents[first:first + n], gates[first:first + n], base, W, S)
+        for i in range(n):
+            at = np.flatnonzero(seen[i])
+            count[first + i] = len(at)
+            for h in range(Hq):
+                kk, vv = k[b, at, h // G], v[b, at, h // G]
+                s = scale * (kk @ q[first + i, h])
+                m = s.max()
+                e = np.exp(s - m)
+                p = e / e.sum()
+                lse[first + i, h] = m + np.log(e.sum())
+                o[first + i, h], absum[first + i, h] = p @ vv, p @ np.abs(vv)
+                size[first + i, h] = scale * np.max(np.abs(kk) @ np.abs(q[first + i, h]))
+    return o, lse, absum, size, count

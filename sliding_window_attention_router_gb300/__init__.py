@@ -23,7 +23,7 @@ __all__ = [
     "prefill_backward_workspace", "route_backward", "route_backward_workspace", "decode_paged",
     "decode_paged_workspace", "decode_anchored", "decode_anchored_workspace", "rope",
     "rope_backward", "append_paged", "decode_paged_e4m3", "decode_paged_e4m3_workspace",
-    "accept_tree", "fork_paged",
+    "decode_tree", "decode_tree_workspace", "accept_tree", "fork_paged",
 ]
 
 F32, BF16, E4M3 = 0, 1, 2
@@ -53,7 +53,8 @@ EXPORTS = (
     "swiattn_num_sms", "swiattn_set_wait_limit_ns", "swiattn_rope", "swiattn_rope_backward",
     "swiattn_append_paged", "swiattn_decode_paged_e4m3_workspace", "swiattn_decode_paged_e4m3",
     "swiattn_rope_axes", "swiattn_rope_axes_backward", "swiattn_append_paged_at",
-    "swiattn_accept_tree", "swiattn_fork_paged",
+    "swiattn_accept_tree", "swiattn_fork_paged", "swiattn_decode_tree_workspace",
+    "swiattn_decode_tree",
 )
 
 
@@ -125,6 +126,9 @@ def _load() -> ctypes.CDLL:
             lib.swiattn_decode_paged_e4m3.argtypes = [vp] * 10 + [i32] * 9 + [f32, i32, vp, sz, vp]
             for name in ("swiattn_accept_tree", "swiattn_fork_paged"):
                 getattr(lib, name).argtypes = [vp] * 10 + [i32] * 9 + [vp]
+            lib.swiattn_decode_tree_workspace.argtypes = [i32] * 6
+            lib.swiattn_decode_tree_workspace.restype = sz
+            lib.swiattn_decode_tree.argtypes = ([vp] * 12 + [i32] * 10 + [f32, i32, i32, vp, sz, vp])
             lib.swiattn_get_device_error.argtypes = [vp]
             lib.swiattn_status_string.argtypes = [i32]
             lib.swiattn_status_string.restype = ctypes.c_char_p
@@ -140,7 +144,7 @@ def _load() -> ctypes.CDLL:
                          "swiattn_prefill_host", "swiattn_rope", "swiattn_rope_backward",
                          "swiattn_append_paged", "swiattn_decode_paged_e4m3", "swiattn_rope_axes",
                          "swiattn_rope_axes_backward", "swiattn_append_paged_at",
-                         "swiattn_accept_tree", "swiattn_fork_paged"):
+                         "swiattn_accept_tree", "swiattn_fork_paged", "swiattn_decode_tree"):
                 getattr(lib, name).restype = ctypes.c_int
             _lib = lib
     return _lib
@@ -822,6 +826,53 @@ def _trees(starts, parents, B: int, index: int):
         raise ValueError(f"starts must hold {B + 1} values")
     if parents is not None and _same(parents, "parents", index, torch.int32).dim() != 1:
         raise ValueError("parents must be [T]")
+
+
+def decode_tree_workspace(T, B, Hq, Hkv, d, dtype) -> int:
+    return int(_load().swiattn_decode_tree_workspace(T, B, Hq, Hkv, d, _DT.get(dtype, dtype)))
+
+
+def decode_tree(q, k_pages, v_pages, block_table, seq_lens, starts, parents, gate, W: int,
+                scale: Optional[float] = None, out=None, want_lse=False, workspace=None,
+                n_anchor: int = 0, k_exp=None, v_exp=None):
+    """Attention of drafted tokens over a paged cache, each sequence's forming a tree.
+    q [T,Hq,d], packed; sequence b owns tokens starts[b] .. starts[b+1]-1 (int32 [B+1], at most 256),
+    the last of its seq_lens[b] (int32 [B]); parents int32 [T]: the token each one continues, counted
+    from its sequence's first drafted one, negative: the cached tokens (None: chains); gate uint8 [T].
+    k_pages, v_pages [num_pages, page_size, Hkv, d] of q's type, or float8_e4m3fn with k_exp, v_exp
+    [num_pages, Hkv, page_size] for bf16 q; block_table int32 [B, max_pages].  Returns o [T,Hq,d]
+    (and lse fp32 [T,Hq]); rows that no sequence owns are left as they were (a result allocated
+    here: undefined)."""
+    index = _gpu(q, "q")
+    _same(q, "q", index)
+    if q.dim() != 3:
+        raise ValueError(f"q must be [T, Hq, d], got {list(q.shape)}")
+    T, Hq, d = q.shape
+    dtype = _DT[q.dtype]
+    pointers, (_, num_pages, page_size, Hkv, dk, kind) = _pools(k_pages, v_pages, k_exp, v_exp, index)
+    if k_pages.dim() != 4 or dk != d:
+        raise ValueError("k_pages and v_pages must be [num_pages, page_size, Hkv, d]")
+    B, max_pages = _sequences(block_table, seq_lens, index)
+    _trees(starts, parents, B, index)
+    if (parents is not None and parents.numel() != T) or (
+            _same(gate, "gate", index, torch.uint8).numel() != T):
+        raise ValueError(f"parents and gate must hold {T} values")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty_like(q)
+    elif _same(out, "out", index, q.dtype).shape != q.shape:
+        raise ValueError(f"out must be {list(q.shape)}, got {list(out.shape)}")
+    lse = torch.empty((T, Hq), device=q.device, dtype=torch.float32) if want_lse else None
+    if workspace is None:
+        workspace = _workspace(decode_tree_workspace(T, B, Hq, Hkv, d, dtype), q.device, None)
+    else:
+        _same(workspace, "workspace", index, torch.uint8)
+    _launch("swiattn_decode_tree", index, q.data_ptr(), *pointers, block_table.data_ptr(),
+            seq_lens.data_ptr(), starts.data_ptr(), _addr(parents), gate.data_ptr(), out.data_ptr(),
+            _addr(lse), T, B, max_pages, page_size, num_pages, Hq, Hkv, d, W, n_anchor, scale, dtype,
+            kind, workspace.data_ptr(), workspace.numel())
+    return (out, lse) if want_lse else out
 
 
 def accept_tree(k_pages, v_pages, block_table, seq_lens, starts, parents, leaf, k_exp=None,

@@ -1,0 +1,526 @@
+// Attention of drafted tokens that form a tree, over a paged cache: the plan, the
+// products on CUDA cores, the join, and the choice between these products and the
+// tensor cores' (decode_tree_tc.cu).
+//
+// The mathematics, for a row (token t, query head) and the entries j it reads, in
+// base 2:  s_j = scale log2(e) <q, k_j>,  m = max s_j,  l = sum 2^(s_j - m),
+//   o = sum 2^(s_j - m) v_j / l,   lse = ln 2 (m + log2 l).
+// Parts (m, l, o l) over disjoint sets of entries join by their maxima.
+// Token t at depth x of the tree after `base` cached tokens stands at position
+// base + x.  It reads the cached entries j < base and those of the tokens on its
+// path, itself among them, that a decode step at its position would: with its gate
+// set all of them, else those whose positions are above base + x - W or below the
+// number of anchors.
+
+#include "swiattn.h"
+#include "ptx.cuh"
+#include "tree_plan.cuh"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <math.h>
+#include <algorithm>
+#include <atomic>
+
+namespace swi {
+namespace {
+
+constexpr int kWords = kMaxTree / 32;
+
+// ---- the plan ----------------------------------------------------------------
+// Block b: sequence b's tokens, one a thread.  The paths come by doubling: after r
+// rounds mask[t] holds the 2^r last tokens of t's path, and up[t] the one before
+// them.
+__global__ void __launch_bounds__(kMaxTree) tree_plan_kernel(const __grid_constant__ TreeDecodeArgs a, int keys) {
+    __shared__ uint32_t s_mask[2][kWords][kMaxTree];
+    __shared__ short s_up[2][kMaxTree], s_depth[kMaxTree];
+    __shared__ int s_count[kMaxTree / 32], s_bad;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int b = blockIdx.x, t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    if (t == 0) s_bad = 0;
+    __syncthreads();
+    // Sequences must not overlap: the workspace has room for each token once.
+    bool bad = t == 0 && (a.starts[0] < 0 || a.starts[a.B] > a.T);
+    for (int i = t; i < a.B; i += kMaxTree) bad |= a.starts[i + 1] < a.starts[i];
+    if (bad) s_bad = 1;
+    __syncthreads();
+    bad = s_bad != 0;
+    const int first = a.starts[b], len = a.seq_lens[b];
+    int n = bad ? 0 : a.starts[b + 1] - first;
+    if (n > 0 && len != 0 && (n > kMaxTree || len < n || len > (a.max_pages << a.page_lg))) bad = true;
+    if (bad || len == 0) n = 0;   // an empty slot has no tokens to look at
+    const int base = len - n;
+
+    const bool on = t < n;
+    const bool gate = on && a.gate[first + t] != 0;
+    int up = -1;
+    if (on) {
+        up = a.parents ? a.parents[first + t] : t - 1;
+        if (up >= t) bad = true;
+        if (up >= t || up < 0) up = -1;
+    }
+    if (bad) atomicOr(a.err, kDevErrInput);
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) s_mask[0][w][t] = on && w == warp ? 1u << lane : 0u;
+    s_up[0][t] = static_cast<short>(up);
+    __syncthreads();
+    int cur = 0;
+    for (int reach = 1; reach < n; reach *= 2, cur ^= 1) {
+        const int p = s_up[cur][t];
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) s_mask[cur ^ 1][w][t] = s_mask[cur][w][t] | (p >= 0 ? s_mask[cur][w][p] : 0u);
+        s_up[cur ^ 1][t] = p >= 0 ? s_up[cur][p] : static_cast<short>(-1);
+        __syncthreads();
+    }
+    uint32_t mask[kWords];
+    int depth = -1;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+        mask[w] = s_mask[cur][w][t];
+        depth += __popc(mask[w]);
+    }
+    s_depth[t] = static_cast<short>(depth);
+    // Routed tokens first, each kind in its order.
+    const unsigned routed = __ballot_sync(0xffffffffu, gate);
+    if (lane == 0) s_count[warp] = __popc(routed);
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kMaxTree / 32; ++w) {
+        before += w < warp ? s_count[w] : 0;
+        all += s_count[w];
+    }
+    before += __popc(routed & ((1u << lane) - 1));   // routed tokens before this one
+    if (on) {
+        if (!gate && depth >= a.W) {   // the top of the path has left the window
+            for (int u = 0; u < n; ++u)
+                if (s_depth[u] <= depth - a.W && base + s_depth[u] >= a.n_anchor) mask[u >> 5] &= ~(1u << (u & 31));
+        }
+        a.plan.order[first + (gate ? before : all + t - before)] = t;
+        a.plan.lo[first + t] = gate ? 0 : min(max(0, base + depth - a.W + 1), base);
+        uint4* to = reinterpret_cast<uint4*>(a.plan.mask + static_cast<size_t>(first + t) * kWords);
+        to[0] = make_uint4(mask[0], mask[1], mask[2], mask[3]);
+        to[1] = make_uint4(mask[4], mask[5], mask[6], mask[7]);
+    }
+    if (t == 0) {
+        TreeSeq s = {};
+        if (n > 0) {
+            s.first = first;
+            s.n = n;
+            s.base = base;
+            s.routed = all;
+            s.lo = max(0, base - a.W + 1);
+            s.na = min(a.n_anchor, s.lo);
+            s.far_tiles = (len + keys - 1) / keys;
+            s.near_tiles = min((s.na + keys - 1) / keys, s.lo / keys) + s.far_tiles - s.lo / keys;
+        }
+        a.plan.seqs[b] = s;
+    }
+}
+
+// ---- elements of a page row ---------------------------------------------------
+// Four elements of a row as floats; `up` is an e4m3 row's power of two.
+template <int KIND>
+__device__ __forceinline__ float4 four_of(const void* row, int at, float up) {
+    if constexpr (KIND == SWIATTN_F32) {
+        return reinterpret_cast<const float4*>(row)[at];
+    } else if constexpr (KIND == SWIATTN_BF16) {
+        const uint2 u = reinterpret_cast<const uint2*>(row)[at];
+        const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
+        const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
+        return make_float4(x.x, x.y, y.x, y.y);
+    } else {
+        const uint32_t u = reinterpret_cast<const uint32_t*>(row)[at];
+        const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(u & 0xffff), __NV_E4M3);
+        const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(u >> 16), __NV_E4M3);
+        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+        return make_float4(x.x * up, x.y * up, y.x * up, y.y * up);
+    }
+}
+template <int KIND>
+__host__ __device__ constexpr int bytes_of() { return KIND == SWIATTN_F32 ? 4 : KIND == SWIATTN_BF16 ? 2 : 1; }
+
+// Page of a token (a bad table entry: page 0, reported).
+__device__ __forceinline__ int page_of(const TreeDecodeArgs& a, int b, int tok) {
+    const int p = a.block_table[static_cast<int64_t>(b) * a.max_pages + (tok >> a.page_lg)];
+    if (p >= 0 && p < a.num_pages) return p;
+    atomicOr(a.err, kDevErrInput);
+    return 0;
+}
+
+// Key (0) or value (1) row of token tok for key head h, and its power of two.
+template <int KIND, int D>
+struct Row {
+    const void* at;
+    float up;
+};
+template <int KIND, int D>
+__device__ __forceinline__ Row<KIND, D> row_of(const TreeDecodeArgs& a, int which, int page, int tok, int h) {
+    const int slot = tok & ((1 << a.page_lg) - 1);
+    const int64_t row = ((static_cast<int64_t>(page) << a.page_lg) + slot) * a.Hkv + h;
+    Row<KIND, D> r;
+    r.at = static_cast<const char*>(which ? a.v_pages : a.k_pages) + row * (D * bytes_of<KIND>());
+    r.up = 1.f;
+    if (KIND == SWIATTN_E4M3)
+        r.up = __uint_as_float(static_cast<uint32_t>((which ? a.v_exp : a.k_exp)[((static_cast<int64_t>(page) * a.Hkv + h) << a.page_lg) + slot]) << 23);
+    return r;
+}
+
+// ---- products on CUDA cores ------------------------------------------------------
+// For fp32, exact where the tensor cores are not: 32 rows by 64 keys, a thread 4 x 4
+// scores, then 4 rows by D/16 dimensions.
+constexpr int kR = 32, kK = 64, kSimtThreads = 128;
+template <int D>
+struct SimtShared {
+    float q[kR][D], k[kK][D + 4], v[kK][D], p[kR][kK + 4];
+    uint32_t mask[kR][kWords];
+    int lo[kR];
+    int start_b, start_units;
+    int64_t start_at, start_end, start_before;
+};
+
+template <int KIND, int D>
+__global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_constant__ TreeDecodeArgs a) {
+    extern __shared__ __align__(16) uint8_t raw[];
+    SimtShared<D>& s = *reinterpret_cast<SimtShared<D>*>(raw);
+    constexpr int F = D / 4;      // float4 of a row
+    constexpr int C = D / 64;     // float4 of a thread's output row
+    using T = typename std::conditional<KIND == SWIATTN_F32, float, __nv_bfloat16>::type;   // of q
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, G = a.Hq / a.Hkv;
+    TreeWalk<kR> walk{a};
+    if (tid < 32) {
+        start_walk<kR>(a, walk);
+        if (tid == 0) {
+            s.start_b = walk.b;
+            s.start_units = walk.units;
+            s.start_at = walk.at;
+            s.start_end = walk.end;
+            s.start_before = walk.before;
+        }
+    }
+    __syncthreads();
+    walk.G = G;
+    walk.b = s.start_b;
+    walk.units = s.start_units;
+    walk.at = s.start_at;
+    walk.end = s.start_end;
+    walk.before = s.start_before;
+    const float sl = a.scale_log2;
+
+    TreeWork w;
+    while (walk.next(w)) {
+        const int rows = min(kR, w.s.n * G - w.rt * kR);
+        const int anchors = min(a.n_anchor, w.s.base), len = w.s.base + w.s.n;
+        __syncthreads();   // the last unit's tiles have been read
+        for (int i = tid; i < kR * F; i += kSimtThreads) {
+            const int r = i / F, c = i % F, R = w.rt * kR + r;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < rows) {
+                const int tok = w.s.first + a.plan.order[w.s.first + R / G];
+                x = four_of<KIND == SWIATTN_F32 ? SWIATTN_F32 : SWIATTN_BF16>(
+                    static_cast<const T*>(a.q) + (static_cast<int64_t>(tok) * a.Hq + w.h * G + R % G) * D, c, 1.f);
+            }
+            reinterpret_cast<float4*>(s.q[r])[c] = x;
+        }
+        for (int i = tid; i < kR * kWords; i += kSimtThreads) {
+            const int r = i / kWords, R = w.rt * kR + r;
+            uint32_t m = 0;
+            if (r < rows) {
+                const int tok = w.s.first + a.plan.order[w.s.first + R / G];
+                m = a.plan.mask[static_cast<size_t>(tok) * kWords + i % kWords];
+                if (i % kWords == 0) s.lo[r] = a.plan.lo[tok];
+            }
+            s.mask[r][i % kWords] = m;
+        }
+        float m[4], l[4], acc[4][4 * C];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+#pragma unroll
+            for (int c = 0; c < 4 * C; ++c) acc[i][c] = 0.f;
+        }
+        for (int kt = w.kt0; kt < w.kt1; ++kt) {
+            const int key0 = tile_key<kK>(w.s, w.far, kt);
+            __syncthreads();
+            for (int i = tid; i < kK * F; i += kSimtThreads) {
+                const int r = i / F, c = i % F, tok = key0 + r;
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+                if (tok < len && (w.far || tok >= w.s.lo || tok < w.s.na)) {
+                    const int page = page_of(a, w.b, tok);
+                    const Row<KIND, D> k = row_of<KIND, D>(a, 0, page, tok, w.h), v = row_of<KIND, D>(a, 1, page, tok, w.h);
+                    x = four_of<KIND>(k.at, c, k.up);
+                    y = four_of<KIND>(v.at, c, v.up);
+                }
+                reinterpret_cast<float4*>(s.k[r])[c] = x;
+                reinterpret_cast<float4*>(s.v[r])[c] = y;
+            }
+            __syncthreads();
+            float x[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[i][j] = 0.f;
+#pragma unroll 4
+            for (int c = 0; c < F; ++c) {
+                float4 q[4], k[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) q[i] = reinterpret_cast<const float4*>(s.q[ty * 4 + i])[c];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) k[j] = reinterpret_cast<const float4*>(s.k[tx + 16 * j])[c];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        x[i][j] = fmaf(q[i].x, k[j].x, x[i][j]);
+                        x[i][j] = fmaf(q[i].y, k[j].y, x[i][j]);
+                        x[i][j] = fmaf(q[i].z, k[j].z, x[i][j]);
+                        x[i][j] = fmaf(q[i].w, k[j].w, x[i][j]);
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = ty * 4 + i;
+                float top = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int tok = key0 + tx + 16 * j, u = tok - w.s.base;
+                    const bool seen = r < rows && (u < 0 ? tok >= s.lo[r] || tok < anchors
+                                                         : u < w.s.n && (s.mask[r][u >> 5] >> (u & 31) & 1));
+                    x[i][j] = seen ? x[i][j] * sl : -INFINITY;
+                    top = fmaxf(top, x[i][j]);
+                }
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const float mn = fmaxf(m[i], top), ref = mn == -INFINITY ? 0.f : mn;
+                const float f = exp2f(m[i] - ref);
+                m[i] = mn;
+                l[i] *= f;
+#pragma unroll
+                for (int c = 0; c < 4 * C; ++c) acc[i][c] *= f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float p = exp2f(x[i][j] - ref);
+                    l[i] += p;
+                    s.p[r][tx + 16 * j] = p;
+                }
+            }
+            __syncwarp();   // a row's weights are written and read by one half-warp
+#pragma unroll 2
+            for (int k = 0; k < kK; ++k) {
+                float4 v[C];
+#pragma unroll
+                for (int c = 0; c < C; ++c) v[c] = reinterpret_cast<const float4*>(s.v[k])[tx + 16 * c];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float p = s.p[ty * 4 + i][k];
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        acc[i][4 * c] = fmaf(p, v[c].x, acc[i][4 * c]);
+                        acc[i][4 * c + 1] = fmaf(p, v[c].y, acc[i][4 * c + 1]);
+                        acc[i][4 * c + 2] = fmaf(p, v[c].z, acc[i][4 * c + 2]);
+                        acc[i][4 * c + 3] = fmaf(p, v[c].w, acc[i][4 * c + 3]);
+                    }
+                }
+            }
+            __syncwarp();
+        }
+        float* part = a.plan.part + static_cast<size_t>(w.slot) * kR * (D + 2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = ty * 4 + i;
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+            if (r < rows) {
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    reinterpret_cast<float4*>(part + r * D)[tx + 16 * c] =
+                        make_float4(acc[i][4 * c], acc[i][4 * c + 1], acc[i][4 * c + 2], acc[i][4 * c + 3]);
+                if (tx == 0) reinterpret_cast<float2*>(part + kR * D)[r] = make_float2(m[i], l[i]);
+            }
+        }
+    }
+}
+
+// ---- the join ---------------------------------------------------------------------
+// A warp a row: the parts of its unit, by their maxima, in the CTAs' order.  Every
+// row of a tile multiplies every value row that the tile's walk reads, with weight
+// 0 where the row itself does not read it; where that value is not finite, 0 times
+// it is a NaN that is none of the row's.  So a row that comes out not finite is
+// computed again, key by key over what it does read (slow, and right whatever the
+// reason).
+constexpr int kJoinThreads = 256;
+
+template <int N>
+struct Dims {
+    float x[N];
+};
+
+template <int KIND, int D>
+__device__ void row_again(const TreeDecodeArgs& a, int b, int h, int tok, const TreeSeq& s, const float* q, Dims<D / 32>& o, float& m, float& l) {
+    constexpr int N = D / 32;
+    const int lane = threadIdx.x & 31;
+    m = -INFINITY;
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) o.x[i] = 0.f;
+    const int lo = a.plan.lo[tok], anchors = min(a.n_anchor, lo);
+    const uint32_t* mask = a.plan.mask + static_cast<size_t>(tok) * kWords;
+    for (int j = anchors > 0 ? 0 : lo; j < s.base + s.n; ++j) {
+        if (j == anchors && j < lo) {
+            j = lo - 1;
+            continue;
+        }
+        const int u = j - s.base;
+        if (u >= 0 && !(mask[u >> 5] >> (u & 31) & 1)) continue;
+        const int page = page_of(a, b, j);
+        const Row<KIND, D> k = row_of<KIND, D>(a, 0, page, j, h), v = row_of<KIND, D>(a, 1, page, j, h);
+        // lane's dimensions: N side by side
+        float x = 0.f, vv[N];
+        const float4 kx = four_of<KIND>(k.at, lane * N / 4, k.up), vx = four_of<KIND>(v.at, lane * N / 4, v.up);
+        if (N == 4) {
+            x = q[0] * kx.x + q[1] * kx.y + q[2] * kx.z + q[3] * kx.w;
+            vv[0] = vx.x, vv[1] = vx.y, vv[N - 2] = vx.z, vv[N - 1] = vx.w;
+        } else {
+            x = lane & 1 ? q[0] * kx.z + q[1] * kx.w : q[0] * kx.x + q[1] * kx.y;
+            vv[0] = lane & 1 ? vx.z : vx.x;
+            vv[1] = lane & 1 ? vx.w : vx.y;
+        }
+#pragma unroll
+        for (int w = 16; w > 0; w >>= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
+        x *= a.scale_log2;
+        const float mn = fmaxf(m, x), f = m == -INFINITY ? 0.f : exp2f(m - mn), p = exp2f(x - mn);
+        l = (m == -INFINITY ? 0.f : l * f) + p;
+#pragma unroll
+        for (int i = 0; i < N; ++i) o.x[i] = (m == -INFINITY ? 0.f : o.x[i] * f) + p * vv[i];
+        m = mn;
+    }
+}
+
+template <int KIND, int D, int R>
+__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeDecodeArgs a, int ctas) {
+    constexpr int N = D / 32;
+    using T = typename std::conditional<KIND == SWIATTN_F32, float, __nv_bfloat16>::type;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int b = blockIdx.x, lane = threadIdx.x & 31, G = a.Hq / a.Hkv;
+    const TreeSeq s = a.plan.seqs[b];
+    if (s.n == 0) return;
+    const int far = row_tiles<R>(s.routed, G), all = row_tiles<R>(s.n, G);
+    const int64_t total = a.plan.start[a.B], start = a.plan.start[b], head = seq_tiles<R>(s, G, 1);
+    const int unit = a.plan.unit[b];
+    const int64_t shares = share_count(total, ctas);
+    auto cta_of = [&](int64_t tile) { return static_cast<int>(((tile + 1) * shares - 1) / total); };
+    for (int i = blockIdx.y * (kJoinThreads / 32) + threadIdx.x / 32; i < s.n * a.Hq; i += gridDim.y * (kJoinThreads / 32)) {
+        const int h = i / (s.n * G), row = i % (s.n * G), rt = row / R, r = row % R;
+        const int tok = s.first + a.plan.order[s.first + row / G];
+        const int64_t out = static_cast<int64_t>(tok) * a.Hq + h * G + row % G;
+        const int64_t from = start + h * head + (rt < far ? static_cast<int64_t>(rt) * s.far_tiles : static_cast<int64_t>(far) * s.far_tiles + static_cast<int64_t>(rt - far) * s.near_tiles);
+        const int c0 = cta_of(from), parts = cta_of(from + (rt < far ? s.far_tiles : s.near_tiles) - 1) - c0 + 1;
+        const float* part = a.plan.part + static_cast<size_t>(c0 + unit + h * all + rt) * R * (D + 2);
+        float m = -INFINITY, l = 0.f;
+        Dims<N> o;
+#pragma unroll
+        for (int e = 0; e < N; ++e) o.x[e] = 0.f;
+        for (int p = 0; p < parts; ++p, part += R * (D + 2)) {
+            const float2 st = __ldcg(reinterpret_cast<const float2*>(part + R * D) + r);
+            Dims<N> x;
+            if constexpr (N == 4) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(part + r * D) + lane);
+                x.x[0] = v.x, x.x[1] = v.y, x.x[2] = v.z, x.x[3] = v.w;
+            } else {
+                const float2 v = __ldcg(reinterpret_cast<const float2*>(part + r * D) + lane);
+                x.x[0] = v.x, x.x[1] = v.y;
+            }
+            const float mn = fmaxf(m, st.x), ref = mn == -INFINITY ? 0.f : mn;
+            const float f = exp2f(m - ref), g = exp2f(st.x - ref);
+            l = l * f + st.y * g;
+#pragma unroll
+            for (int e = 0; e < N; ++e) o.x[e] = o.x[e] * f + x.x[e] * g;
+            m = mn;
+        }
+        bool fine = l - l == 0.f && l > 0.f;
+#pragma unroll
+        for (int e = 0; e < N; ++e) fine &= o.x[e] - o.x[e] == 0.f;
+        if (!__all_sync(0xffffffffu, fine)) {
+            float q[N];
+            const T* src = static_cast<const T*>(a.q) + out * D + lane * N;
+#pragma unroll
+            for (int e = 0; e < N; ++e) q[e] = static_cast<float>(src[e]);
+            row_again<KIND, D>(a, b, h, tok, s, q, o, m, l);
+        }
+        const float inv = 1.f / l;
+        T y[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) y[e] = static_cast<T>(o.x[e] * inv);
+        T* to = static_cast<T*>(a.o) + out * D + lane * N;
+#pragma unroll
+        for (int e = 0; e < N; ++e) to[e] = y[e];
+        if (a.lse && lane == 0) a.lse[out] = (m + log2f(l)) * 0.69314718055994531f;
+    }
+}
+
+template <int KIND, int D>
+cudaError_t launch_simt(const TreeDecodeArgs& a, int ctas, cudaStream_t s) {
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_dynamic_smem(tree_simt_kernel<KIND, D>, sizeof(SimtShared<D>), done);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = dependent_launch(ctas, kSimtThreads, s, attr);
+    cfg.dynamicSmemBytes = sizeof(SimtShared<D>);
+    return cudaLaunchKernelEx(&cfg, tree_simt_kernel<KIND, D>, a);
+}
+
+template <int KIND, int D>
+cudaError_t launch_all(const TreeDecodeArgs& a, int sms, cudaStream_t s) {
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = dependent_launch(a.B, kMaxTree, s, attr);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, tree_plan_kernel, a, kK);
+    if (e != cudaSuccess) return e;
+    const int ctas = std::min(2 * sms, kTreeCtas);
+    prof_start(s);
+    e = launch_simt<KIND, D>(a, ctas, s);
+    prof_stop(s);
+    if (e != cudaSuccess) return e;
+    const int most = (std::min(a.T, kMaxTree) * a.Hq + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
+    cfg = dependent_launch(dim3(a.B, std::min(most, std::max(1, 4096 / a.B))), kJoinThreads, s, attr);
+    e = cudaLaunchKernelEx(&cfg, tree_join_kernel<KIND, D, kR>, a, ctas);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int KIND>
+cudaError_t launch_kind(const TreeDecodeArgs& a, int d, int sms, cudaStream_t s) {
+    return d == 128 ? launch_all<KIND, 128>(a, sms, s) : launch_all<KIND, 64>(a, sms, s);
+}
+
+}  // namespace
+
+TreeWs tree_ws_layout(int T, int B, int Hq, int Hkv, int d) {
+    auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+    const size_t t = T, b = B, G = Hq / Hkv;
+    TreeWs L;
+    L.seqs = 0;
+    L.start = up(sizeof(int) * 8 * b);
+    L.unit = up(L.start + sizeof(int64_t) * (b + 1));
+    L.order = up(L.unit + sizeof(int) * (b + 1));
+    L.lo = up(L.order + sizeof(int) * t);
+    L.mask = up(L.lo + sizeof(int) * t);
+    L.part = up(L.mask + sizeof(uint32_t) * kWords * t);
+    // A unit is at least part of a sequence's rows and no part is empty.
+    const size_t units = Hkv * (t * G / kR + std::min(b, t));
+    L.total = up(L.part + (kTreeCtas + units) * kR * (d + 2) * sizeof(float));
+    return L;
+}
+
+cudaError_t launch_decode_tree(const TreeDecodeArgs& a, int d, int page_dtype, int sms, cudaStream_t s) {
+    if (page_dtype == SWIATTN_F32) return launch_kind<SWIATTN_F32>(a, d, sms, s);
+    if (page_dtype == SWIATTN_BF16) return launch_kind<SWIATTN_BF16>(a, d, sms, s);
+    return launch_kind<SWIATTN_E4M3>(a, d, sms, s);
+}
+
+}  // namespace swi

@@ -1031,6 +1031,82 @@ PagingArgs paging_args(void* k_pages, void* v_pages, uint8_t* k_exp, uint8_t* v_
 
 }  // namespace
 
+namespace {
+
+// Sizes of a tree attention: SWIATTN_OK, or why not.
+int decode_tree_sizes_ok(int T, int B, int Hq, int Hkv, int d, int dtype) {
+    if (T < 0 || B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || (d != 64 && d != 128))
+        return SWIATTN_EINVAL;
+    if (dtype != SWIATTN_BF16 && dtype != SWIATTN_F32) return SWIATTN_EINVAL;
+    if (Hq / Hkv > 128 || B > 65535 || (int64_t)T * Hq > (1 << 26) || Hkv > (1 << 16)) return SWIATTN_EUNSUPPORTED;
+    return SWIATTN_OK;
+}
+
+}  // namespace
+
+size_t swiattn_decode_tree_workspace(int T, int B, int Hq, int Hkv, int d, int dtype) {
+    if (decode_tree_sizes_ok(T, B, Hq, Hkv, d, dtype) != SWIATTN_OK) return 0;
+    return tree_ws_layout(T, B, Hq, Hkv, d).total;
+}
+
+int swiattn_decode_tree(const void* q, const void* k_pages, const void* v_pages,
+                        const uint8_t* k_exp, const uint8_t* v_exp, const int32_t* block_table,
+                        const int32_t* seq_lens, const int32_t* starts, const int32_t* parents,
+                        const uint8_t* gate, void* o, float* lse, int T, int B, int max_pages,
+                        int page_size, int num_pages, int Hq, int Hkv, int d, int W, int n_anchor,
+                        float scale, int dtype, int page_dtype, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+    const int ok = decode_tree_sizes_ok(T, B, Hq, Hkv, d, dtype);
+    const int pools = pools_ok(k_pages, v_pages, k_exp, v_exp, block_table, seq_lens, 1, B, max_pages,
+                               page_size, num_pages, Hkv, d, page_dtype);
+    if (ok == SWIATTN_EINVAL || pools == SWIATTN_EINVAL || W <= 0 || n_anchor < 0) return SWIATTN_EINVAL;
+    if (page_dtype != dtype && page_dtype != SWIATTN_E4M3) return SWIATTN_EINVAL;
+    if (!(scale > 0.f) || !(scale - scale == 0.f)) return SWIATTN_EINVAL;
+    if (!starts) return SWIATTN_EINVAL;
+    if (ok != SWIATTN_OK || (page_dtype == SWIATTN_E4M3 && dtype != SWIATTN_BF16)) return SWIATTN_EUNSUPPORTED;
+    if ((int64_t)num_pages * page_size > (int64_t(1) << 32)) return SWIATTN_EUNSUPPORTED;
+    if (T == 0) return SWIATTN_OK;
+    if (!q || !gate || !o || !aligned16(q) || !aligned16(o)) return SWIATTN_EINVAL;
+    const TreeWs L = tree_ws_layout(T, B, Hq, Hkv, d);
+    if (!workspace || !aligned256(workspace) || workspace_bytes < L.total) return SWIATTN_EINVAL;
+    DeviceInfo di;
+    if (!device_info(di)) return SWIATTN_ECUDA;
+    char* ws = static_cast<char*>(workspace);
+    TreeDecodeArgs a;
+    a.q = q;
+    a.k_pages = k_pages;
+    a.v_pages = v_pages;
+    a.k_exp = k_exp;
+    a.v_exp = v_exp;
+    a.block_table = block_table;
+    a.seq_lens = seq_lens;
+    a.starts = starts;
+    a.parents = parents;
+    a.gate = gate;
+    a.o = o;
+    a.lse = lse;
+    a.plan.seqs = reinterpret_cast<TreeSeq*>(ws + L.seqs);
+    a.plan.start = reinterpret_cast<int64_t*>(ws + L.start);
+    a.plan.unit = reinterpret_cast<int*>(ws + L.unit);
+    a.plan.order = reinterpret_cast<int*>(ws + L.order);
+    a.plan.lo = reinterpret_cast<int*>(ws + L.lo);
+    a.plan.mask = reinterpret_cast<uint32_t*>(ws + L.mask);
+    a.plan.part = reinterpret_cast<float*>(ws + L.part);
+    a.err = di.err;
+    a.T = T;
+    a.B = B;
+    a.max_pages = max_pages;
+    a.page_lg = 0;
+    while ((1 << a.page_lg) < page_size) ++a.page_lg;
+    a.num_pages = num_pages;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.W = W;
+    a.n_anchor = n_anchor;
+    a.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+    return launched(launch_decode_tree(a, d, page_dtype, di.sms, static_cast<cudaStream_t>(stream)));
+}
+
 int swiattn_accept_tree(void* k_pages, void* v_pages, uint8_t* k_exp, uint8_t* v_exp,
                         const int32_t* block_table, const int32_t* seq_lens, const int32_t* starts,
                         const int32_t* parents, const int32_t* leaf, int32_t* lens_out, int layers,

@@ -371,6 +371,42 @@ struct PagingArgs {
     int T, B, C, layers, max_pages, page_lg, num_pages, Hkv;
     int row_bytes;              // a token's heads
 };
+// Attention of drafted trees over a paged cache.
+struct TreeSeq;
+struct TreePlan {       // in the workspace, see tree_plan.cuh
+    TreeSeq* seqs;      // [B]
+    int64_t* start;     // [B + 1] key tiles of the units before each sequence's
+    int* unit;          // [B + 1] units before each sequence's
+    int* order;         // [T] at first + i: the tree's token (0 .. n-1) that comes i-th
+    int* lo;            // [T] the first cached key that a token reads (but for anchors)
+    uint32_t* mask;     // [T][kMaxTree / 32] the tree's tokens that a token reads
+    float* part;        // [CTAs + units][a tile's rows][d + 2]
+};
+struct TreeDecodeArgs {
+    const void* q;              // [T, Hq, d], bf16 or, for fp32 pages, fp32
+    const void* k_pages;        // [num_pages, 1 << page_lg, Hkv, d]
+    const void* v_pages;
+    const uint8_t* k_exp;       // e4m3 pages: [num_pages, Hkv, 1 << page_lg]
+    const uint8_t* v_exp;
+    const int32_t* block_table; // [B, max_pages]
+    const int32_t* seq_lens;    // [B]
+    const int32_t* starts;      // [B+1]
+    const int32_t* parents;     // [T], nullptr: each token's is the one before
+    const uint8_t* gate;        // [T]
+    void* o;                    // [T, Hq, d]
+    float* lse;                 // [T, Hq], nullable
+    TreePlan plan;
+    unsigned int* err;
+    int T, B, max_pages, page_lg, num_pages, Hq, Hkv, W, n_anchor;
+    float scale_log2;           // softmax scale times log2(e)
+};
+struct TreeWs {
+    size_t seqs, start, unit, order, lo, mask, part, total;   // byte offsets
+};
+constexpr int kTreeCtas = 2 * 152;   // of a call at most: what fills a GB300
+TreeWs tree_ws_layout(int T, int B, int Hq, int Hkv, int d);
+cudaError_t launch_decode_tree(const TreeDecodeArgs& a, int d, int page_dtype, int sms, cudaStream_t s);
+
 cudaError_t launch_accept(const PagingArgs& a, cudaStream_t s);
 cudaError_t launch_fork(const PagingArgs& a, cudaStream_t s);
 

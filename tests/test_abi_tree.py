@@ -74,3 +74,28 @@ def test_fork_refusals(lib):
         assert call(**bad) == EINVAL, bad
     assert call(C=0) == OK
     assert call(layers=1 << 15) == EUNSUPPORTED
+
+
+def test_decode_tree_refusals_and_workspace(lib):
+    def size(T=20, B=3, Hq=8, Hkv=2, d=128, dt=BF16):
+        return lib.swiattn_decode_tree_workspace(T, B, Hq, Hkv, d, dt)
+    assert size() > 0 and size() % 256 == 0
+    assert size(T=4000) > size() and size(B=200) >= size() and size(dt=F32) > 0
+    for bad in (dict(T=-1), dict(B=0), dict(Hq=7), dict(Hkv=0), dict(d=96), dict(dt=E4M3), dict(Hq=258), dict(B=1 << 16),
+                dict(T=1 << 24, Hq=16)):
+        assert size(**bad) == 0, bad
+
+    def call(q=FAKE, kp=FAKE, vps=FAKE, ke=FAKE, ve=FAKE, bt=FAKE, sl=FAKE, st=FAKE, pa=FAKE, gate=FAKE, o=BIG, T=20, B=3,
+             mp=8, ps=16, np_=30, Hq=8, Hkv=2, d=128, W=64, S=0, scale=0.1, dt=BF16, pdt=BF16, ws=FAKE, nbytes=1 << 40):
+        return lib.swiattn_decode_tree(q, kp, vps, ke, ve, bt, sl, st, pa, gate, o, None, T, B, mp, ps, np_, Hq, Hkv, d, W, S,
+                                       scale, dt, pdt, ws, nbytes, None)
+    for bad in (dict(q=None), dict(kp=None), dict(vps=None), dict(bt=None), dict(sl=None), dict(st=None), dict(gate=None),
+                dict(o=None), dict(q=ODD), dict(o=ODD), dict(kp=ODD), dict(vps=ODD), dict(T=-1), dict(B=0), dict(mp=0),
+                dict(ps=24), dict(np_=0), dict(Hq=9), dict(Hkv=-2), dict(d=32), dict(W=0), dict(S=-1), dict(scale=0.0),
+                dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(dt=E4M3), dict(dt=F32),
+                dict(pdt=F32), dict(pdt=7), dict(pdt=E4M3, ke=None), dict(pdt=E4M3, ve=None), dict(ws=None), dict(ws=ODD),
+                dict(nbytes=size() - 1), dict(ps=1 << 20, mp=1 << 12)):
+        assert call(**bad) == EINVAL, bad
+    for bad in (dict(Hq=258), dict(B=1 << 16), dict(dt=F32, pdt=E4M3), dict(np_=1 << 30)):
+        assert call(**bad) == EUNSUPPORTED, bad
+    assert call(T=0, q=None, o=None, gate=None, ws=None) == OK
