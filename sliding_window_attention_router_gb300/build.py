@@ -22,7 +22,8 @@ LIB = os.path.join(PKG, "libswiattn.so")
 
 SOURCES = ["swiattn_api.cu", "route.cu", "schedule.cu", "attn_prefill.cu", "attn_simt.cu", "decode.cu",
            "bwd_schedule.cu", "attn_bwd.cu", "bwd_simt.cu", "attn_dual.cu", "rope.cu",
-           "decode_e4m3.cu", "paging.cu", "decode_tree.cu"]
+           "decode_e4m3.cu", "paging.cu", "decode_tree.cu",
+           "decode_tree_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "-I", INCLUDE, "-I", CSRC]

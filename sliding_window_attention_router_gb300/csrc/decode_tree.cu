@@ -172,7 +172,7 @@ __device__ __forceinline__ Row<KIND, D> row_of(const TreeDecodeArgs& a, int whic
 // ---- products on CUDA cores ------------------------------------------------------
 // For fp32, exact where the tensor cores are not: 32 rows by 64 keys, a thread 4 x 4
 // scores, then 4 rows by D/16 dimensions.
-constexpr int kR = 32, kK = 64, kSimtThreads = 128;
+constexpr int kR = kTreeRows, kK = kTreeKeys, kSimtThreads = 128;
 template <int D>
 struct SimtShared {
     float q[kR][D], k[kK][D + 4], v[kK][D], p[kR][kK + 4];
@@ -478,18 +478,21 @@ cudaError_t launch_simt(const TreeDecodeArgs& a, int ctas, cudaStream_t s) {
 
 template <int KIND, int D>
 cudaError_t launch_all(const TreeDecodeArgs& a, int sms, cudaStream_t s) {
+    constexpr bool kTc = KIND == SWIATTN_BF16;
+    constexpr int kRows = kTc ? kTreeTcRows : kTreeRows;
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = dependent_launch(a.B, kMaxTree, s, attr);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, tree_plan_kernel, a, kK);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, tree_plan_kernel, a, kTc ? kTreeTcKeys : kTreeKeys);
     if (e != cudaSuccess) return e;
-    const int ctas = std::min(2 * sms, kTreeCtas);
+    const int ctas = kTc ? std::min(sms, kTreeTcCtas) : std::min(2 * sms, kTreeCtas);
     prof_start(s);
-    e = launch_simt<KIND, D>(a, ctas, s);
+    if constexpr (kTc) e = launch_tree_tc(a, D, ctas, s);
+    else e = launch_simt<KIND, D>(a, ctas, s);
     prof_stop(s);
     if (e != cudaSuccess) return e;
     const int most = (std::min(a.T, kMaxTree) * a.Hq + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
     cfg = dependent_launch(dim3(a.B, std::min(most, std::max(1, 4096 / a.B))), kJoinThreads, s, attr);
-    e = cudaLaunchKernelEx(&cfg, tree_join_kernel<KIND, D, kR>, a, ctas);
+    e = cudaLaunchKernelEx(&cfg, tree_join_kernel<KIND, D, kRows>, a, ctas);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -500,7 +503,7 @@ cudaError_t launch_kind(const TreeDecodeArgs& a, int d, int sms, cudaStream_t s)
 
 }  // namespace
 
-TreeWs tree_ws_layout(int T, int B, int Hq, int Hkv, int d) {
+TreeWs tree_ws_layout(int T, int B, int Hq, int Hkv, int d, int dtype) {
     auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
     const size_t t = T, b = B, G = Hq / Hkv;
     TreeWs L;
@@ -511,9 +514,11 @@ TreeWs tree_ws_layout(int T, int B, int Hq, int Hkv, int d) {
     L.lo = up(L.order + sizeof(int) * t);
     L.mask = up(L.lo + sizeof(int) * t);
     L.part = up(L.mask + sizeof(uint32_t) * kWords * t);
-    // A unit is at least part of a sequence's rows and no part is empty.
-    const size_t units = Hkv * (t * G / kR + std::min(b, t));
-    L.total = up(L.part + (kTreeCtas + units) * kR * (d + 2) * sizeof(float));
+    // Units: a key head's row tiles, of which each sequence with tokens has at most
+    // one that is not full.  (What the tensor cores' tiles take is enough for the others.)
+    const size_t rows = dtype == SWIATTN_BF16 ? kTreeTcRows : kTreeRows, ctas = dtype == SWIATTN_BF16 ? kTreeTcCtas : kTreeCtas;
+    const size_t units = Hkv * (t * G / rows + std::min(b, t));
+    L.total = up(L.part + (ctas + units) * rows * (d + 2) * sizeof(float));
     return L;
 }
 

@@ -157,7 +157,8 @@ void swiattn_set_profile_events(void* start, void* stop) {
 
 int swiattn_set_wait_limit_ns(uint64_t ns) {
     if (prefill_set_wait_limit(ns) != cudaSuccess || dual_set_wait_limit(ns) != cudaSuccess ||
-        bwd_set_wait_limit(ns) != cudaSuccess || decode_e4m3_set_wait_limit(ns) != cudaSuccess)
+        bwd_set_wait_limit(ns) != cudaSuccess || decode_e4m3_set_wait_limit(ns) != cudaSuccess ||
+        tree_set_wait_limit(ns) != cudaSuccess)
         return SWIATTN_ECUDA;
     return SWIATTN_OK;
 }
@@ -1046,7 +1047,7 @@ int decode_tree_sizes_ok(int T, int B, int Hq, int Hkv, int d, int dtype) {
 
 size_t swiattn_decode_tree_workspace(int T, int B, int Hq, int Hkv, int d, int dtype) {
     if (decode_tree_sizes_ok(T, B, Hq, Hkv, d, dtype) != SWIATTN_OK) return 0;
-    return tree_ws_layout(T, B, Hq, Hkv, d).total;
+    return tree_ws_layout(T, B, Hq, Hkv, d, dtype).total;
 }
 
 int swiattn_decode_tree(const void* q, const void* k_pages, const void* v_pages,
@@ -1067,7 +1068,7 @@ int swiattn_decode_tree(const void* q, const void* k_pages, const void* v_pages,
     if ((int64_t)num_pages * page_size > (int64_t(1) << 32)) return SWIATTN_EUNSUPPORTED;
     if (T == 0) return SWIATTN_OK;
     if (!q || !gate || !o || !aligned16(q) || !aligned16(o)) return SWIATTN_EINVAL;
-    const TreeWs L = tree_ws_layout(T, B, Hq, Hkv, d);
+    const TreeWs L = tree_ws_layout(T, B, Hq, Hkv, d, dtype);
     if (!workspace || !aligned256(workspace) || workspace_bytes < L.total) return SWIATTN_EINVAL;
     DeviceInfo di;
     if (!device_info(di)) return SWIATTN_ECUDA;

@@ -23,7 +23,7 @@ constexpr uint64_t kDrainLimitNs = 100000000ull;   // 0.1 s, waits while abortin
 
 // Per translation unit setters of the wait limit (current device; 0 restores
 // the default): the routed prefill, the dual-branch forward, the backward,
-// decode over e4m3 pages.
+// decode over e4m3 pages, the tree attention.
 cudaError_t prefill_set_wait_limit(uint64_t ns);
 cudaError_t dual_set_wait_limit(uint64_t ns);
 cudaError_t bwd_set_wait_limit(uint64_t ns);
@@ -403,9 +403,14 @@ struct TreeDecodeArgs {
 struct TreeWs {
     size_t seqs, start, unit, order, lo, mask, part, total;   // byte offsets
 };
-constexpr int kTreeCtas = 2 * 152;   // of a call at most: what fills a GB300
-TreeWs tree_ws_layout(int T, int B, int Hq, int Hkv, int d);
+// CTAs of a call at most (what fills a GB300), rows and keys of a tile: on CUDA
+// cores, and on the tensor cores.
+constexpr int kTreeCtas = 2 * 152, kTreeRows = 32, kTreeKeys = 64;
+constexpr int kTreeTcCtas = 152, kTreeTcRows = 128, kTreeTcKeys = 128;
+TreeWs tree_ws_layout(int T, int B, int Hq, int Hkv, int d, int dtype);
 cudaError_t launch_decode_tree(const TreeDecodeArgs& a, int d, int page_dtype, int sms, cudaStream_t s);
+cudaError_t launch_tree_tc(const TreeDecodeArgs& a, int d, int ctas, cudaStream_t s);
+cudaError_t tree_set_wait_limit(uint64_t ns);
 
 cudaError_t launch_accept(const PagingArgs& a, cudaStream_t s);
 cudaError_t launch_fork(const PagingArgs& a, cudaStream_t s);
