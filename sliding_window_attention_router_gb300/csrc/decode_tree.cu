@@ -423,18 +423,22 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
         const int64_t from = start + h * head + (rt < far ? static_cast<int64_t>(rt) * s.far_tiles : static_cast<int64_t>(far) * s.far_tiles + static_cast<int64_t>(rt - far) * s.near_tiles);
         const int c0 = cta_of(from), parts = cta_of(from + (rt < far ? s.far_tiles : s.near_tiles) - 1) - c0 + 1;
         const float* part = a.plan.part + static_cast<size_t>(c0 + unit + h * all + rt) * R * (D + 2);
+        // Tiles of the tensor cores hold few rows several times over, each a part.
+        const int each = R == kTreeTcRows ? tree_copy_rows(min(R, s.n * G - rt * R)) : R, copies = R / each;
         float m = -INFINITY, l = 0.f;
         Dims<N> o;
 #pragma unroll
         for (int e = 0; e < N; ++e) o.x[e] = 0.f;
-        for (int p = 0; p < parts; ++p, part += R * (D + 2)) {
-            const float2 st = __ldcg(reinterpret_cast<const float2*>(part + R * D) + r);
+        for (int p = 0; p < parts * copies; ++p) {
+            const float* from = part + static_cast<size_t>(p / copies) * R * (D + 2);
+            const int at = r + p % copies * each;
+            const float2 st = __ldcg(reinterpret_cast<const float2*>(from + R * D) + at);
             Dims<N> x;
             if constexpr (N == 4) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(part + r * D) + lane);
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(from + at * D) + lane);
                 x.x[0] = v.x, x.x[1] = v.y, x.x[2] = v.z, x.x[3] = v.w;
             } else {
-                const float2 v = __ldcg(reinterpret_cast<const float2*>(part + r * D) + lane);
+                const float2 v = __ldcg(reinterpret_cast<const float2*>(from + at * D) + lane);
                 x.x[0] = v.x, x.x[1] = v.y;
             }
             const float mn = fmaxf(m, st.x), ref = mn == -INFINITY ? 0.f : mn;

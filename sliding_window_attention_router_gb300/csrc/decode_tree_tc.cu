@@ -12,6 +12,11 @@
 // the first alone, 2^-9 of each, errors would be of the size of that rounding.  The
 // tensor cores have the time.
 //
+// Where a unit has 64 rows or fewer, Q holds them two or four times, and each copy
+// takes the weights of its own half or quarter of every tile's keys, the others
+// being zero to it: all four softmax warps work, each on fewer keys, and the join
+// adds up the copies as it does parts.
+//
 //   warps 0-3   softmax: thread r owns row r, TMEM lane r
 //   warp 4      TMEM and MMA issue (converged, elected issue)
 //   warp 5      Q: gathers a unit's rows
@@ -177,18 +182,18 @@ __device__ bool q_loader(const TreeDecodeArgs& a, const Ctx<D>& c) {
     TreeWork w;
     for (uint32_t u = 0; walk.next(w); ++u) {
         if (!wait_w(&c.bar[c.kQEmpty], (u & 1) ^ 1, c.abort_flag, a.err)) return false;
-        const int rows = min(R, w.s.n * walk.G - w.rt * R);
+        const int rows = min(R, w.s.n * walk.G - w.rt * R), each = tree_copy_rows(rows);
         for (int r0 = 0; r0 < R; r0 += 32) {
-            const int mine = w.rt * R + r0 + lane;
-            int64_t at = 0;   // the lane's row of q
-            if (r0 + lane < rows)
+            const int in = (r0 & (each - 1)) + lane, mine = w.rt * R + in;
+            int64_t at = -1;   // the lane's row of q
+            if (in < rows)
                 at = static_cast<int64_t>(w.s.first + a.plan.order[w.s.first + mine / walk.G]) * a.Hq + w.h * walk.G + mine % walk.G;
 #pragma unroll 4
             for (int i = 0; i < P; ++i) {
                 const int r = i * kPer + lane / P;
                 const int64_t from = __shfl_sync(0xffffffffu, at, r);
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(col + (r0 + r) * 128 + (((piece & 7) ^ (r & 7)) << 4)),
-                             "l"(static_cast<const __nv_bfloat16*>(a.q) + from * D + piece * 8), "r"(r0 + r < rows ? 16u : 0u)
+                             "l"(static_cast<const __nv_bfloat16*>(a.q) + max(from, static_cast<int64_t>(0)) * D + piece * 8), "r"(from >= 0 ? 16u : 0u)
                              : "memory");
             }
         }
@@ -259,111 +264,148 @@ __device__ bool mma_issuer(const TreeDecodeArgs& a, const Ctx<D>& c, uint32_t tm
 __device__ __forceinline__ uint32_t below(int x) { return x <= 0 ? 0u : x >= 32 ? ~0u : (1u << x) - 1; }
 __device__ __forceinline__ uint32_t bits_of(int k0, int from, int to) { return below(to - k0) & ~below(from - k0); }
 
+// What a softmax thread knows of its row.
+struct RowOf {
+    const uint32_t* mask;
+    int lo, base, anchors, n;
+    bool on;
+    float m, l;
+};
+
+// Weights of columns [C0, C0 + N) of the tile at key0, whose scores are in TMEM at
+// ts, written over them with zeros for the other columns.  Returns the factor that
+// the sums so far have to be scaled by.
+template <int N>
+__device__ __forceinline__ float weigh(RowOf& row, uint32_t ts, int c0, int key0, float sl) {
+    uint32_t sr[N];
+#pragma unroll
+    for (int i = 0; i < N; i += 32) tmem_ld32(ts + c0 + i, sr + i);
+    tmem_ld_wait();
+    float* s = reinterpret_cast<float*>(sr);
+    key0 += c0;
+    const bool full = !row.on || (key0 + N <= row.base && (key0 >= row.lo || key0 + N <= row.anchors));
+    if (!__all_sync(0xffffffffu, full)) {
+#pragma unroll
+        for (int i = 0; i < N / 32; ++i) {
+            const int k0 = key0 + 32 * i, at = k0 - row.base;
+            uint32_t bits = bits_of(k0, row.lo, row.base) | bits_of(k0, 0, row.anchors);
+            if (row.on && at > -32 && at < row.n) {   // the tree's tokens at .. at + 31
+                const int word = at >> 5;
+                const uint32_t x = word >= 0 ? row.mask[word] : 0u, y = word + 1 < kWords ? row.mask[word + 1] : 0u;
+                bits |= __funnelshift_r(x, y, at & 31);
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[32 * i + e] = bits >> e & 1 ? s[32 * i + e] : -INFINITY;
+        }
+    }
+    float m8[8];
+#pragma unroll
+    for (int t = 0; t < 8; ++t) m8[t] = s[t];
+#pragma unroll
+    for (int i = 8; i < N; i += 16)
+#pragma unroll
+        for (int t = 0; t < 8; ++t) m8[t] = i + 8 + t < N ? fmax3(m8[t], s[i + t], s[i + 8 + t]) : fmaxf(m8[t], s[i + t]);
+    const float mx = fmaxf(fmax3(m8[0], m8[1], m8[2]), fmax3(fmax3(m8[3], m8[4], m8[5]), m8[6], m8[7]));
+    // The reference of the weights follows the maximum where that is over it by more
+    // than 2^8: weights stay under 2^8, O is rescaled seldom.
+    const float mn = fmaxf(row.m, mx * sl);
+    float f = 1.f;
+    if (mn > row.m + 8.f) {
+        f = ex2_approx(row.m - mn);
+        row.m = mn;
+    }
+    const float ref = row.m == -INFINITY ? 0.f : row.m;
+    const float2 sl2 = make_float2(sl, sl), off = make_float2(-ref, -ref);
+    float2 sum[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) sum[t] = make_float2(0.f, 0.f);
+    constexpr int kAt = N == 128 ? 64 : N, kWide = kAt / 2;   // columns at a time, and those of TMEM they become
+#pragma unroll
+    for (int part = 0; part < N / kAt; ++part) {
+        uint32_t hi[kWide], rest[kWide];
+#pragma unroll
+        for (int i = 0; i < kWide; ++i) {
+            const int at = part * kAt + 2 * i;
+            const float2 x = ffma2(make_float2(s[at], s[at + 1]), sl2, off);
+            const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            sum[i & 3] = fadd2(sum[i & 3], p);
+            hi[i] = pack_bf16x2(p.x, p.y);
+            rest[i] = pack_bf16x2(p.x - __uint_as_float(hi[i] << 16), p.y - __uint_as_float(hi[i] & 0xffff0000u));
+        }
+        const uint32_t to = ts + c0 / 2 + part * kWide;
+        if constexpr (kWide == 32) {
+            tmem_st32(to, hi);
+            tmem_st32(to + K / 2, rest);
+        } else {
+            tmem_st16(to, hi);
+            tmem_st16(to + K / 2, rest);
+        }
+    }
+    if constexpr (N < K) {
+        uint32_t zero[N / 2];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) zero[i] = 0;
+#pragma unroll
+        for (int i = 0; i < K / N; ++i) {
+            if (i * N == c0) continue;
+            if constexpr (N == 64) {
+                tmem_st32(ts + i * 32, zero);
+                tmem_st32(ts + K / 2 + i * 32, zero);
+            } else {
+                tmem_st16(ts + i * 16, zero);
+                tmem_st16(ts + K / 2 + i * 16, zero);
+            }
+        }
+    }
+    const float2 s2 = fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
+    const bool had = row.l > 0.f;
+    row.l = row.l * f + (s2.x + s2.y);
+    return had ? f : 1.f;
+}
+
 template <int D>
 __device__ bool softmax(const TreeDecodeArgs& a, const Ctx<D>& c, uint32_t tmem, int warp) {
     const int lane = threadIdx.x & 31, r = warp * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     const uint32_t to = lanes + kColO;
-    const float sl = a.scale_log2;
     uint32_t tiles = 0, done = 0;
     TreeWalk<R> walk = walk_of(a, *c.start);
     TreeWork w;
     for (uint32_t u = 0; walk.next(w); ++u) {
-        const int rows = min(R, w.s.n * walk.G - w.rt * R);
-        const bool mine = r < rows, any = warp * 32 < rows;   // the warp has rows
-        int lo = 0;
-        const uint32_t* mask = nullptr;
-        if (mine) {
-            const int tok = w.s.first + a.plan.order[w.s.first + (w.rt * R + r) / walk.G];
-            lo = a.plan.lo[tok];
-            mask = a.plan.mask + static_cast<size_t>(tok) * kWords;
+        const int rows = min(R, w.s.n * walk.G - w.rt * R), each = tree_copy_rows(rows);
+        const int in = r & (each - 1), first = (warp * 32) & (each - 1);
+        const bool any = first < rows;   // the warp has rows
+        const int c0 = warp * 32 / each * each;   // its copy's columns, as many as the copy has rows
+        RowOf row{nullptr, 0, w.s.base, min(a.n_anchor, w.s.base), w.s.n, in < rows, -INFINITY, 0.f};
+        if (row.on) {
+            const int tok = w.s.first + a.plan.order[w.s.first + (w.rt * R + in) / walk.G];
+            row.lo = a.plan.lo[tok];
+            row.mask = a.plan.mask + static_cast<size_t>(tok) * kWords;
         }
-        const int base = w.s.base, anchors = min(a.n_anchor, base);
-        float m2 = -INFINITY, l = 0.f;
         for (int kt = w.kt0; kt < w.kt1; ++kt, ++tiles) {
             const int key0 = tile_key<K>(w.s, w.far, kt);
             if (!wait_w(&c.bar[c.kSFull + (tiles & 1)], tiles >> 1 & 1, c.abort_flag, a.err)) return false;
             tc_fence_after();
             if (any) {
                 const uint32_t ts = lanes + (tiles & 1) * K;
-                uint32_t sr[K];
-#pragma unroll
-                for (int i = 0; i < K; i += 32) tmem_ld32(ts + i, sr + i);
-                tmem_ld_wait();
-                float* s = reinterpret_cast<float*>(sr);
-                const bool full = !mine || (key0 + K <= base && (key0 >= lo || key0 + K <= anchors));
-                if (!__all_sync(0xffffffffu, full)) {
-#pragma unroll
-                    for (int i = 0; i < K / 32; ++i) {
-                        const int k0 = key0 + 32 * i, at = k0 - base;
-                        uint32_t bits = bits_of(k0, lo, base) | bits_of(k0, 0, anchors);
-                        if (mine && at > -32 && at < w.s.n) {   // the tree's tokens at .. at + 31
-                            const int word = at >> 5;
-                            const uint32_t x = word >= 0 ? mask[word] : 0u, y = word + 1 < kWords ? mask[word + 1] : 0u;
-                            bits |= __funnelshift_r(x, y, at & 31);
-                        }
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) s[32 * i + e] = bits >> e & 1 ? s[32 * i + e] : -INFINITY;
-                    }
-                }
-                float m8[8];
-#pragma unroll
-                for (int t = 0; t < 8; ++t) m8[t] = s[t];
-#pragma unroll
-                for (int i = 8; i < K; i += 16)
-#pragma unroll
-                    for (int t = 0; t < 8; ++t) m8[t] = i + 8 + t < K ? fmax3(m8[t], s[i + t], s[i + 8 + t]) : fmaxf(m8[t], s[i + t]);
-                const float mx = fmaxf(fmax3(m8[0], m8[1], m8[2]), fmax3(fmax3(m8[3], m8[4], m8[5]), m8[6], m8[7]));
-                // The reference of the weights follows the maximum where that is over it
-                // by more than 2^8: weights stay under 2^8, O is rescaled seldom.
-                const float mn = fmaxf(m2, mx * sl);
-                const bool raise = mn > m2 + 8.f;
-                float f = 1.f;
-                if (raise) {
-                    f = ex2_approx(m2 - mn);
-                    m2 = mn;
-                }
-                const float ref = m2 == -INFINITY ? 0.f : m2;
-                const float2 sl2 = make_float2(sl, sl), off = make_float2(-ref, -ref);
-                float2 sum[4];
-#pragma unroll
-                for (int t = 0; t < 4; ++t) sum[t] = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t hi[K / 4], rest[K / 4];
-#pragma unroll
-                    for (int i = 0; i < K / 4; ++i) {
-                        const int at = half * (K / 2) + 2 * i;
-                        const float2 x = ffma2(make_float2(s[at], s[at + 1]), sl2, off);
-                        const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-                        sum[i & 3] = fadd2(sum[i & 3], p);
-                        hi[i] = pack_bf16x2(p.x, p.y);
-                        rest[i] = pack_bf16x2(p.x - __uint_as_float(hi[i] << 16), p.y - __uint_as_float(hi[i] & 0xffff0000u));
-                    }
-                    tmem_st32(ts + half * (K / 4), hi);
-                    tmem_st32(ts + K / 2 + half * (K / 4), rest);
-                }
-                const float2 s2 = fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
+                const float f = each == 32   ? weigh<32>(row, ts, c0, key0, a.scale_log2)
+                                : each == 64 ? weigh<64>(row, ts, c0, key0, a.scale_log2)
+                                             : weigh<128>(row, ts, 0, key0, a.scale_log2);
                 // O may be rescaled once the last tile's PV has landed; every PV but a
                 // unit's last one arrives at kODone.
-                const bool need = raise && l > 0.f && mine;
-                if (__any_sync(0xffffffffu, need)) {
-                    if (kt > w.kt0) {
-                        if (!wait_w(&c.bar[c.kODone], done & 1, c.abort_flag, a.err)) return false;
-                        tc_fence_after();
-                    }
-                    const float g = need ? f : 1.f;
+                if (__any_sync(0xffffffffu, row.on && f != 1.f)) {
+                    if (!wait_w(&c.bar[c.kODone], done & 1, c.abort_flag, a.err)) return false;
+                    tc_fence_after();
 #pragma unroll
                     for (int i = 0; i < D; i += 32) {
                         uint32_t o[32];
                         tmem_ld32(to + i, o);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int t = 0; t < 32; ++t) o[t] = __float_as_uint(__uint_as_float(o[t]) * g);
+                        for (int t = 0; t < 32; ++t) o[t] = __float_as_uint(__uint_as_float(o[t]) * f);
                         tmem_st32(to + i, o);
                     }
                 }
-                l = l * f + (s2.x + s2.y);
                 tmem_st_wait();
             }
             if (kt > w.kt0) ++done;
@@ -379,12 +421,12 @@ __device__ bool softmax(const TreeDecodeArgs& a, const Ctx<D>& c, uint32_t tmem,
                 uint32_t o[32];
                 tmem_ld32(to + i, o);
                 tmem_ld_wait();
-                if (mine)
+                if (row.on)
 #pragma unroll
                     for (int t = 0; t < 32; t += 4)
                         *reinterpret_cast<uint4*>(part + r * D + i + t) = make_uint4(o[t], o[t + 1], o[t + 2], o[t + 3]);
             }
-            if (mine) reinterpret_cast<float2*>(part + R * D)[r] = make_float2(m2, l);
+            if (row.on) reinterpret_cast<float2*>(part + R * D)[r] = make_float2(row.m, row.l);
         }
         tc_fence_before();
         mbar_arrive(&c.bar[c.kOFree]);

@@ -29,6 +29,10 @@ __device__ __forceinline__ int64_t seq_tiles(const TreeSeq& s, int G, int Hkv) {
     return (static_cast<int64_t>(far) * s.far_tiles + static_cast<int64_t>(all - far) * s.near_tiles) * Hkv;
 }
 
+// Rows of each of the copies in which a tile on the tensor cores holds its rows: 32,
+// 64 or, once, all.
+__device__ __forceinline__ int tree_copy_rows(int rows) { return rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+
 // The CTAs that the key tiles are dealt out to: as many as there are, and no share
 // empty.  CTA c takes [total c / n, total (c + 1) / n).
 __device__ __forceinline__ int64_t share_count(int64_t total, int ctas) { return min(total, static_cast<int64_t>(ctas)); }
