@@ -32,7 +32,7 @@ constexpr int kWords = kMaxTree / 32;
 // Block b: sequence b's tokens, one a thread.  The paths come by doubling: after r
 // rounds mask[t] holds the 2^r last tokens of t's path, and up[t] the one before
 // them.
-__global__ void __launch_bounds__(kMaxTree) tree_plan_kernel(const __grid_constant__ TreeDecodeArgs a, int keys) {
+__global__ void __launch_bounds__(kMaxTree) tree_plan_kernel(const __grid_constant__ TreeDecodeArgs a, int rows, int keys) {
     __shared__ uint32_t s_mask[2][kWords][kMaxTree];
     __shared__ short s_up[2][kMaxTree], s_depth[kMaxTree];
     __shared__ int s_count[kMaxTree / 32], s_bad;
@@ -110,7 +110,8 @@ __global__ void __launch_bounds__(kMaxTree) tree_plan_kernel(const __grid_consta
             s.first = first;
             s.n = n;
             s.base = base;
-            s.routed = all;
+            const int G = a.Hq / a.Hkv;
+            s.far_rows = (n * G > rows || all == 0 ? all : n) * G;
             s.lo = max(0, base - a.W + 1);
             s.na = min(a.n_anchor, s.lo);
             s.far_tiles = (len + keys - 1) / keys;
@@ -178,8 +179,7 @@ struct SimtShared {
     float q[kR][D], k[kK][D + 4], v[kK][D], p[kR][kK + 4];
     uint32_t mask[kR][kWords];
     int lo[kR];
-    int start_b, start_units;
-    int64_t start_at, start_end, start_before;
+    TreeStart start;
 };
 
 template <int KIND, int D>
@@ -192,33 +192,21 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, G = a.Hq / a.Hkv;
-    TreeWalk<kR> walk{a};
     if (tid < 32) {
-        start_walk<kR>(a, walk);
-        if (tid == 0) {
-            s.start_b = walk.b;
-            s.start_units = walk.units;
-            s.start_at = walk.at;
-            s.start_end = walk.end;
-            s.start_before = walk.before;
-        }
+        const TreeStart start = start_walk<kR>(a);
+        if (tid == 0) s.start = start;
     }
     __syncthreads();
-    walk.G = G;
-    walk.b = s.start_b;
-    walk.units = s.start_units;
-    walk.at = s.start_at;
-    walk.end = s.start_end;
-    walk.before = s.start_before;
+    TreeWalk<kR> walk{a, s.start};
     const float sl = a.scale_log2;
 
     TreeWork w;
     while (walk.next(w)) {
-        const int rows = min(kR, w.s.n * G - w.rt * kR);
+        const int rows = w.rows;
         const int anchors = min(a.n_anchor, w.s.base), len = w.s.base + w.s.n;
         __syncthreads();   // the last unit's tiles have been read
         for (int i = tid; i < kR * F; i += kSimtThreads) {
-            const int r = i / F, c = i % F, R = w.rt * kR + r;
+            const int r = i / F, c = i % F, R = w.row0 + r;
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < rows) {
                 const int tok = w.s.first + a.plan.order[w.s.first + R / G];
@@ -228,7 +216,7 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
             reinterpret_cast<float4*>(s.q[r])[c] = x;
         }
         for (int i = tid; i < kR * kWords; i += kSimtThreads) {
-            const int r = i / kWords, R = w.rt * kR + r;
+            const int r = i / kWords, R = w.row0 + r;
             uint32_t m = 0;
             if (r < rows) {
                 const int tok = w.s.first + a.plan.order[w.s.first + R / G];
@@ -330,6 +318,7 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
             }
             __syncwarp();
         }
+        static_assert(kPartRows<kR> == kR, "a part has the tile's rows");
         float* part = a.plan.part + static_cast<size_t>(w.slot) * kR * (D + 2);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -354,7 +343,7 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
 // it is a NaN that is none of the row's.  So a row that comes out not finite is
 // computed again, key by key over what it does read (slow, and right whatever the
 // reason).
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 256, kAtOnce = 8;
 
 template <int N>
 struct Dims {
@@ -411,42 +400,67 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
     const int b = blockIdx.x, lane = threadIdx.x & 31, G = a.Hq / a.Hkv;
     const TreeSeq s = a.plan.seqs[b];
     if (s.n == 0) return;
-    const int far = row_tiles<R>(s.routed, G), all = row_tiles<R>(s.n, G);
-    const int64_t total = a.plan.start[a.B], start = a.plan.start[b], head = seq_tiles<R>(s, G, 1);
-    const int unit = a.plan.unit[b];
+    const int far = far_tiles<R>(s);
+    const int64_t head = a.plan.start[a.B], total = head * a.Hkv, start = a.plan.start[b];   // tiles of a head, of all
+    const int unit = a.plan.unit[b], head_units = a.plan.unit[a.B];
     const int64_t shares = share_count(total, ctas);
     auto cta_of = [&](int64_t tile) { return static_cast<int>(((tile + 1) * shares - 1) / total); };
     for (int i = blockIdx.y * (kJoinThreads / 32) + threadIdx.x / 32; i < s.n * a.Hq; i += gridDim.y * (kJoinThreads / 32)) {
-        const int h = i / (s.n * G), row = i % (s.n * G), rt = row / R, r = row % R;
+        const int h = i / (s.n * G), row = i % (s.n * G), in = row < s.far_rows ? row : row - s.far_rows;   // of its kind
+        const int rt = in / R + (row < s.far_rows ? 0 : far), r = in % R;
         const int tok = s.first + a.plan.order[s.first + row / G];
         const int64_t out = static_cast<int64_t>(tok) * a.Hq + h * G + row % G;
-        const int64_t from = start + h * head + (rt < far ? static_cast<int64_t>(rt) * s.far_tiles : static_cast<int64_t>(far) * s.far_tiles + static_cast<int64_t>(rt - far) * s.near_tiles);
+        const int64_t from = h * head + start + (rt < far ? static_cast<int64_t>(rt) * s.far_tiles : static_cast<int64_t>(far) * s.far_tiles + static_cast<int64_t>(rt - far) * s.near_tiles);
         const int c0 = cta_of(from), parts = cta_of(from + (rt < far ? s.far_tiles : s.near_tiles) - 1) - c0 + 1;
-        const float* part = a.plan.part + static_cast<size_t>(c0 + unit + h * all + rt) * R * (D + 2);
         // Tiles of the tensor cores hold few rows several times over, each a part.
-        const int each = R == kTreeTcRows ? tree_copy_rows(min(R, s.n * G - rt * R)) : R, copies = R / each;
+        constexpr int kPart = kPartRows<R>;
+        const int each = R == kTreeTcRows ? tree_copy_rows(min(R, (row < s.far_rows ? s.far_rows : s.n * G - s.far_rows) - (in - r))) : R, copies = kPart / each, n = parts * copies;
+        const float* part = a.plan.part + static_cast<size_t>(c0 + h * head_units + unit + rt) * kPart * (D + 2);
+        auto row_at = [&](int p) { return r + p % copies * each; };
+        auto part_at = [&](int p) { return part + static_cast<size_t>(p / copies) * kPart * (D + 2); };
+        // Lane i looks up the maximum and the sum of part i of 32; their weights
+        // are then known before the rows come, eight at once.
         float m = -INFINITY, l = 0.f;
         Dims<N> o;
 #pragma unroll
         for (int e = 0; e < N; ++e) o.x[e] = 0.f;
-        for (int p = 0; p < parts * copies; ++p) {
-            const float* from = part + static_cast<size_t>(p / copies) * R * (D + 2);
-            const int at = r + p % copies * each;
-            const float2 st = __ldcg(reinterpret_cast<const float2*>(from + R * D) + at);
-            Dims<N> x;
-            if constexpr (N == 4) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(from + at * D) + lane);
-                x.x[0] = v.x, x.x[1] = v.y, x.x[2] = v.z, x.x[3] = v.w;
-            } else {
-                const float2 v = __ldcg(reinterpret_cast<const float2*>(from + at * D) + lane);
-                x.x[0] = v.x, x.x[1] = v.y;
-            }
-            const float mn = fmaxf(m, st.x), ref = mn == -INFINITY ? 0.f : mn;
-            const float f = exp2f(m - ref), g = exp2f(st.x - ref);
-            l = l * f + st.y * g;
+        for (int p0 = 0; p0 < n; p0 += 32) {
+            float2 st = make_float2(-INFINITY, 0.f);
+            if (p0 + lane < n) st = __ldcg(reinterpret_cast<const float2*>(part_at(p0 + lane) + kPart * D) + row_at(p0 + lane));
+            float mn = fmaxf(m, st.x);
 #pragma unroll
-            for (int e = 0; e < N; ++e) o.x[e] = o.x[e] * f + x.x[e] * g;
+            for (int w = 16; w > 0; w >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, w));
+            const float ref = mn == -INFINITY ? 0.f : mn, f = exp2f(m - ref), mine = exp2f(st.x - ref);
+            float sum = st.y * mine;
+#pragma unroll
+            for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+            l = l * f + sum;
             m = mn;
+#pragma unroll
+            for (int e = 0; e < N; ++e) o.x[e] *= f;
+            for (int q = 0; q < min(32, n - p0); q += kAtOnce) {
+                Dims<N> x[kAtOnce];
+#pragma unroll
+                for (int i = 0; i < kAtOnce; ++i)
+                    if (p0 + q + i < n) {
+                        const float* from = part_at(p0 + q + i) + row_at(p0 + q + i) * D;
+                        if constexpr (N == 4) {
+                            const float4 v = __ldcg(reinterpret_cast<const float4*>(from) + lane);
+                            x[i].x[0] = v.x, x[i].x[1] = v.y, x[i].x[2] = v.z, x[i].x[3] = v.w;
+                        } else {
+                            const float2 v = __ldcg(reinterpret_cast<const float2*>(from) + lane);
+                            x[i].x[0] = v.x, x[i].x[1] = v.y;
+                        }
+                    }
+#pragma unroll
+                for (int i = 0; i < kAtOnce; ++i) {
+                    const float g = __shfl_sync(0xffffffffu, mine, q + i);
+                    if (p0 + q + i < n) {
+#pragma unroll
+                        for (int e = 0; e < N; ++e) o.x[e] = fmaf(x[i].x[e], g, o.x[e]);
+                    }
+                }
+            }
         }
         bool fine = l - l == 0.f && l > 0.f;
 #pragma unroll
@@ -486,7 +500,7 @@ cudaError_t launch_all(const TreeDecodeArgs& a, int sms, cudaStream_t s) {
     constexpr int kRows = kTc ? kTreeTcRows : kTreeRows;
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = dependent_launch(a.B, kMaxTree, s, attr);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, tree_plan_kernel, a, kTc ? kTreeTcKeys : kTreeKeys);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, tree_plan_kernel, a, kRows, kTc ? kTreeTcKeys : kTreeKeys);
     if (e != cudaSuccess) return e;
     const int ctas = kTc ? std::min(sms, kTreeTcCtas) : std::min(2 * sms, kTreeCtas);
     prof_start(s);
@@ -519,10 +533,11 @@ TreeWs tree_ws_layout(int T, int B, int Hq, int Hkv, int d, int dtype) {
     L.mask = up(L.lo + sizeof(int) * t);
     L.part = up(L.mask + sizeof(uint32_t) * kWords * t);
     // Units: a key head's row tiles, of which each sequence with tokens has at most
-    // one that is not full.  (What the tensor cores' tiles take is enough for the others.)
+    // two that are not full.
     const size_t rows = dtype == SWIATTN_BF16 ? kTreeTcRows : kTreeRows, ctas = dtype == SWIATTN_BF16 ? kTreeTcCtas : kTreeCtas;
-    const size_t units = Hkv * (t * G / rows + std::min(b, t));
-    L.total = up(L.part + (ctas + units) * rows * (d + 2) * sizeof(float));
+    const size_t units = Hkv * (t * G / rows + 2 * std::min(b, t));
+    const size_t part_rows = dtype == SWIATTN_BF16 ? kPartRows<kTreeTcRows> : kPartRows<kTreeRows>;
+    L.total = up(L.part + (ctas + units) * part_rows * (d + 2) * sizeof(float));
     return L;
 }
 

@@ -12,18 +12,19 @@
 // the first alone, 2^-9 of each, errors would be of the size of that rounding.  The
 // tensor cores have the time.
 //
-// Where a unit has 64 rows or fewer, Q holds them two or four times, and each copy
-// takes the weights of its own half or quarter of every tile's keys, the others
-// being zero to it: all four softmax warps work, each on fewer keys, and the join
-// adds up the copies as it does parts.
+// A tile's keys are two halves of 64, each with softmax warps, weights and an O of
+// its own: neither waits for the other, and the join adds the two up as it does
+// parts.  Where a unit has 64 rows or fewer, Q holds them two or four times, and each
+// copy takes the weights of its own half or quarter of those keys, the others being
+// zero to it: all eight softmax warps work, each on fewer keys.
 //
-//   warps 0-3   softmax: thread r owns row r, TMEM lane r
-//   warp 4      TMEM and MMA issue (converged, elected issue)
-//   warp 5      Q: gathers a unit's rows
-//   warps 8-11  K and V: a ring of tiles in the order in which they are used (K0,
+//   warps 0-7   softmax: four warps a half; thread r of them owns row r, TMEM lane r
+//   warp 8      TMEM and MMA issue (converged, elected issue)
+//   warp 9      Q: gathers a unit's rows
+//   warps 12-15 K and V: a ring of tiles in the order in which they are used (K0,
 //               K1, V0, K2, V1, ...), 32 rows of each tile a warp
-//   (warps 6, 7 fill up a warpgroup, the unit that registers are moved by)
-// TMEM: S at [0, 128) and [128, 256), O at [256, 256 + d).
+//   (warps 10, 11 fill up a warpgroup, the unit that registers are moved by)
+// TMEM: S at [0, 128) and [128, 256), the halves' O at [256, 256 + d) and from 256 + d.
 
 #include "swiattn.h"
 #include "ptx.cuh"
@@ -32,6 +33,7 @@
 #include <cuda_bf16.h>
 #include <math.h>
 #include <atomic>
+#include <cstring>
 
 namespace swi {
 namespace {
@@ -39,55 +41,41 @@ namespace {
 constexpr int R = kTreeTcRows, K = kTreeTcKeys;
 constexpr int kWords = kMaxTree / 32;
 constexpr int kLoaders = 4;
-constexpr int kThreads = 384;   // 3 warpgroups, launched at 168 registers a thread,
-constexpr uint32_t kRegsSoftmax = 232, kRegsOther = 136;   // of 3 * 168
+constexpr int kThreads = 512;   // 4 warpgroups, launched at 128 registers a thread,
+constexpr uint32_t kRegsSoftmax = 168, kRegsOther = 88;   // of 4 * 128
 constexpr int kHalf = R * 128;   // 128 rows of 64 bf16 columns, 128-byte swizzled
 constexpr uint32_t kTmemCols = 512;
+constexpr int kHalfKeys = K / 2;
 constexpr uint32_t kColO = 256;
 
 template <int D>
 struct Sizes {
     static constexpr int kTile = R * D * 2;            // Q, and a slot of the ring
     static constexpr int kSlots = 6 * 128 / D;
-    static constexpr int kLag = 4 * 128 / D;           // slots between a copy's start and the look whether it has come
-    static constexpr int kBars = 2 * kSlots + 2 + 2 + 2 + 3 + 1;
+    static constexpr int kBars = 2 * kSlots + 2 + 2 + 4 + 3 + 1;
     static constexpr int kOffBar = (1 + kSlots) * kTile;
     static constexpr int kOffMisc = kOffBar + kBars * 8;
     static constexpr int kBytes = kOffMisc + 64 + 1024;   // and room to align
 };
+static_assert(sizeof(TreeStart) + 8 <= 64, "what follows the barriers");
 static_assert(Sizes<128>::kBytes <= 232448 && Sizes<64>::kBytes <= 232448, "shared memory budget");
-
-struct Start {   // where the CTA's share of the work begins
-    int64_t at, end, before;
-    int b, units;
-};
 
 template <int D>
 struct Ctx {
     uint8_t* smem;
     uint64_t* bar;
     volatile int* abort_flag;
-    const Start* start;
+    const TreeStart* start;
     static constexpr int kFull = 0, kEmpty = Sizes<D>::kSlots, kQFull = 2 * Sizes<D>::kSlots, kQEmpty = kQFull + 1,
-                         kSFull = kQEmpty + 1, kPFull = kSFull + 2, kODone = kPFull + 2, kOFull = kODone + 1,
+                         kSFull = kQEmpty + 1, kPFull = kSFull + 2, kODone = kPFull + 4, kOFull = kODone + 1,
                          kOFree = kOFull + 1, kDrain = kOFree + 1;
 };
 
-__device__ __forceinline__ TreeWalk<R> walk_of(const TreeDecodeArgs& a, const Start& s) {
-    TreeWalk<R> w{a};
-    w.at = s.at;
-    w.end = s.end;
-    w.before = s.before;
-    w.b = s.b;
-    w.units = s.units;
-    w.G = a.Hq / a.Hkv;
-    return w;
-}
-
-// As mbar_wait_w, with a first try that does not suspend, so that a lowered limit
-// reaches waits that would end within it.
+// As mbar_wait_w, but that a lowered limit, which polls, reaches waits that would end
+// within it: the try that suspends the warp comes only under limits that do not.
 __device__ __forceinline__ bool wait_w(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned int* err) {
-    if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+    const bool there = mbar_test_wait(bar, parity) || (g_wait_limit_ns >= kPollBelowNs && mbar_try_wait(bar, parity));
+    if (__all_sync(0xffffffffu, there)) return true;
     const bool ok = mbar_wait_on(bar, parity, abort_flag, err);
     return __all_sync(0xffffffffu, ok);
 }
@@ -132,30 +120,64 @@ __device__ __forceinline__ void copy_rows(const TreeDecodeArgs& a, const void* p
     }
 }
 
+// All but the last `left` groups of copies have come.
+__device__ __forceinline__ void copies_but(int left) {
+    switch (left) {
+        case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+        case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+        case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+        case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+        case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+        default: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;   // fewer left than asked for
+    }
+}
+
+// A warp fills its 32 rows of every slot: by TMA, which announces itself, where a
+// page holds `box` of them (16 or 32) and all are read; else by copies of its own
+// threads, which it announces, in their order, when it has no slot to fill.
 template <int D>
-__device__ bool loader(const TreeDecodeArgs& a, const Ctx<D>& c, int w32) {
-    constexpr int S = Sizes<D>::kSlots, kLag = Sizes<D>::kLag;
+__device__ bool loader(const TreeDecodeArgs& a, const Ctx<D>& c, const CUtensorMap* maps, int box, int w32, uint32_t& g) {
+    constexpr int S = Sizes<D>::kSlots;
     const int lane = threadIdx.x & 31;
     const uint32_t ring = smem_u32(c.smem) + Sizes<D>::kTile + w32 * 32 * 128;
-    uint32_t g = 0;   // slots filled (or, at the end, passed)
-    // Starts slot g's copies; then slot g - kLag's have come, and are announced.
-    auto fill = [&](const void* pages, const Rows* rows, int h) -> bool {
-        if (rows) {
-            const uint32_t slot = g % S;
-            if (!wait_w(&c.bar[c.kEmpty + slot], (g / S & 1) ^ 1, c.abort_flag, a.err)) return false;
-            copy_rows<D>(a, pages, *rows, h, ring + slot * Sizes<D>::kTile);
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
-        if (g >= kLag) {
-            fence_proxy_async_smem();
+    uint32_t own[2] = {0, 0};        // those of them with copies not announced: their slots, 4 bits each, the first lowest
+    int owned = 0;
+    auto announce = [&]() {
+        copies_but(owned - 1);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c.bar[c.kFull + (own[0] & 15)]);
+        own[0] = own[0] >> 4 | own[1] << 28;
+        own[1] >>= 4;
+        --owned;
+    };
+    auto fill = [&](int which, const Rows& rows, int h) -> bool {
+        const uint32_t slot = g % S, dst = ring + slot * Sizes<D>::kTile, parity = (g / S & 1) ^ 1;
+        uint64_t* empty = &c.bar[c.kEmpty + slot];
+        while (owned && !__all_sync(0xffffffffu, mbar_test_wait(empty, parity))) announce();
+        if (!wait_w(empty, parity, c.abort_flag, a.err)) return false;
+        if (box && rows.read == 0xffffffffu) {
+            uint64_t* full = &c.bar[c.kFull + slot];
+            if (lane == 0) mbar_arrive_expect_tx(full, 32 * D * 2);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&c.bar[c.kFull + (g - kLag) % S]);
+            for (int r = 0; r < 32; r += box) {
+                const int row = __shfl_sync(0xffffffffu, rows.row, r);
+                if (lane == 0)
+#pragma unroll
+                    for (int half = 0; half < D / 64; ++half)
+                        tma_load_4d_at(dst + half * kHalf + r * 128, maps + which, full, half * 64, h, row, 0);
+            }
+        } else {
+            copy_rows<D>(a, which ? a.v_pages : a.k_pages, rows, h, dst);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            if (owned < 8) own[0] |= slot << (4 * owned);
+            else own[1] |= slot << (4 * (owned - 8));
+            ++owned;
         }
         ++g;
         return true;
     };
-    TreeWalk<R> walk = walk_of(a, *c.start);
+    TreeWalk<R> walk{a, *c.start};
     TreeWork w;
     while (walk.next(w)) {
         Rows next = rows_of(a, w, w.kt0, w32 * 32), now = next;
@@ -163,31 +185,40 @@ __device__ bool loader(const TreeDecodeArgs& a, const Ctx<D>& c, int w32) {
             const Rows last = now;
             now = next;
             if (kt + 1 < w.kt1) next = rows_of(a, w, kt + 1, w32 * 32);   // the page numbers are on their way during the copies
-            if (kt < w.kt1 && !fill(a.k_pages, &now, w.h)) return false;
-            if (kt > w.kt0 && !fill(a.v_pages, &last, w.h)) return false;
+            if (kt < w.kt1 && !fill(0, now, w.h)) return false;
+            if (kt > w.kt0 && !fill(1, last, w.h)) return false;
         }
     }
-#pragma unroll 1
-    for (int i = 0; i < kLag; ++i) fill(nullptr, nullptr, 0);
+    while (owned) announce();
     return true;
+}
+
+// The copies in flight of a call that gave up.
+template <int D>
+__device__ void drain(const Ctx<D>& c, uint32_t filled) {
+    constexpr int S = Sizes<D>::kSlots;
+    for (uint32_t back = 1; back <= S && back <= filled; ++back) {
+        const uint32_t g = filled - back;
+        mbar_drain(&c.bar[c.kFull + g % S], g / S & 1);
+    }
 }
 
 // ---- Q ---------------------------------------------------------------------------------
 template <int D>
 __device__ bool q_loader(const TreeDecodeArgs& a, const Ctx<D>& c) {
     constexpr int P = D / 8, kPer = 32 / P;
-    const int lane = threadIdx.x & 31, piece = lane % P;
+    const int lane = threadIdx.x & 31, piece = lane % P, G = a.Hq / a.Hkv;
     const uint32_t col = smem_u32(c.smem) + (piece >> 3) * kHalf;
-    TreeWalk<R> walk = walk_of(a, *c.start);
+    TreeWalk<R> walk{a, *c.start};
     TreeWork w;
     for (uint32_t u = 0; walk.next(w); ++u) {
         if (!wait_w(&c.bar[c.kQEmpty], (u & 1) ^ 1, c.abort_flag, a.err)) return false;
-        const int rows = min(R, w.s.n * walk.G - w.rt * R), each = tree_copy_rows(rows);
+        const int rows = w.rows, each = tree_copy_rows(rows);
         for (int r0 = 0; r0 < R; r0 += 32) {
-            const int in = (r0 & (each - 1)) + lane, mine = w.rt * R + in;
+            const int in = (r0 & (each - 1)) + lane, mine = w.row0 + in;
             int64_t at = -1;   // the lane's row of q
             if (in < rows)
-                at = static_cast<int64_t>(w.s.first + a.plan.order[w.s.first + mine / walk.G]) * a.Hq + w.h * walk.G + mine % walk.G;
+                at = static_cast<int64_t>(w.s.first + a.plan.order[w.s.first + mine / G]) * a.Hq + w.h * G + mine % G;
 #pragma unroll 4
             for (int i = 0; i < P; ++i) {
                 const int r = i * kPer + lane / P;
@@ -218,7 +249,7 @@ __device__ bool mma_issuer(const TreeDecodeArgs& a, const Ctx<D>& c, uint32_t tm
     const uint64_t v0 = sdesc_sw128(smem_u32(c.smem) + Sizes<D>::kTile, kHalf, 1024);
     uint32_t g = 0, tiles = 0, u = 0;
     auto full = [&]() { return wait_w(&c.bar[c.kFull + g % S], g / S & 1, c.abort_flag, a.err); };
-    TreeWalk<R> walk = walk_of(a, *c.start);
+    TreeWalk<R> walk{a, *c.start};
     TreeWork w;
     for (; walk.next(w); ++u) {
         const int n = w.kt1 - w.kt0;
@@ -241,15 +272,19 @@ __device__ bool mma_issuer(const TreeDecodeArgs& a, const Ctx<D>& c, uint32_t tm
             }
             if (j > 0) {
                 const uint32_t t = tiles - (j < n ? 2 : 1);   // tile j - 1
-                if (!wait_w(&c.bar[c.kPFull + (t & 1)], t >> 1 & 1, c.abort_flag, a.err)) return false;
                 if (j == 1 && !wait_w(&c.bar[c.kOFree], (u & 1) ^ 1, c.abort_flag, a.err)) return false;
                 if (!full()) return false;
-                tc_fence_after();
                 const uint64_t v = v0 + (g % S) * (Sizes<D>::kTile >> 4);
 #pragma unroll
-                for (int i = 0; i < 2 * K / 16; ++i)   // the nearest bf16, then what they leave
-                    umma_bf16_ts_w(tmem + kColO, tmem + (t & 1) * K + i * 8, v + ((i % (K / 16)) * 16 * 128 >> 4), kIdescO,
-                                   j == 1 && i == 0 ? 0u : 1u);
+                for (int half = 0; half < 2; ++half) {
+                    if (!wait_w(&c.bar[c.kPFull + (t & 1) * 2 + half], t >> 1 & 1, c.abort_flag, a.err)) return false;
+                    tc_fence_after();
+#pragma unroll
+                    for (int i = 0; i < 2 * kHalfKeys / 16; ++i)   // the nearest bf16, then what they leave
+                        umma_bf16_ts_w(tmem + kColO + half * D, tmem + (t & 1) * K + half * kHalfKeys + i * 8,
+                                       v + ((half * kHalfKeys + i % (kHalfKeys / 16) * 16) * 128 >> 4), kIdescO,
+                                       j == 1 && i == 0 ? 0u : 1u);
+                }
                 umma_commit_w(&c.bar[c.kEmpty + g % S]);
                 umma_commit_w(&c.bar[j == n ? c.kOFull : c.kODone]);
                 ++g;
@@ -272,22 +307,40 @@ struct RowOf {
     float m, l;
 };
 
-// Weights of columns [C0, C0 + N) of the tile at key0, whose scores are in TMEM at
-// ts, written over them with zeros for the other columns.  Returns the factor that
-// the sums so far have to be scaled by.
+// Columns of TMEM to and from registers.
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t* x) {
+    if constexpr (N == 64) {
+        tmem_ld32(at, x);
+        tmem_ld32(at + 32, x + 32);
+    } else if constexpr (N == 32) {
+        tmem_ld32(at, x);
+    } else {
+        tmem_ld16(at, x);
+    }
+}
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t* x) {
+    if constexpr (N == 32) tmem_st32(at, x);
+    else if constexpr (N == 16) tmem_st16(at, x);
+    else tmem_st8(at, x);
+}
+
+// Weights of N columns from c0 of the half tile whose first key is key0 and whose
+// scores are in TMEM at ts, written over them with zeros for the other columns.
+// Returns the factor that the sums so far have to be scaled by.
 template <int N>
 __device__ __forceinline__ float weigh(RowOf& row, uint32_t ts, int c0, int key0, float sl) {
     uint32_t sr[N];
-#pragma unroll
-    for (int i = 0; i < N; i += 32) tmem_ld32(ts + c0 + i, sr + i);
+    tmem_ld<N>(ts + c0, sr);
     tmem_ld_wait();
     float* s = reinterpret_cast<float*>(sr);
     key0 += c0;
     const bool full = !row.on || (key0 + N <= row.base && (key0 >= row.lo || key0 + N <= row.anchors));
     if (!__all_sync(0xffffffffu, full)) {
 #pragma unroll
-        for (int i = 0; i < N / 32; ++i) {
-            const int k0 = key0 + 32 * i, at = k0 - row.base;
+        for (int i = 0; i < N; i += 32) {
+            const int k0 = key0 + i, at = k0 - row.base;
             uint32_t bits = bits_of(k0, row.lo, row.base) | bits_of(k0, 0, row.anchors);
             if (row.on && at > -32 && at < row.n) {   // the tree's tokens at .. at + 31
                 const int word = at >> 5;
@@ -295,17 +348,17 @@ __device__ __forceinline__ float weigh(RowOf& row, uint32_t ts, int c0, int key0
                 bits |= __funnelshift_r(x, y, at & 31);
             }
 #pragma unroll
-            for (int e = 0; e < 32; ++e) s[32 * i + e] = bits >> e & 1 ? s[32 * i + e] : -INFINITY;
+            for (int e = 0; e < (N < 32 ? N : 32); ++e) s[i + e] = bits >> e & 1 ? s[i + e] : -INFINITY;
         }
     }
-    float m8[8];
+    float m4[4];
 #pragma unroll
-    for (int t = 0; t < 8; ++t) m8[t] = s[t];
+    for (int t = 0; t < 4; ++t) m4[t] = fmaxf(s[t], s[4 + t]);
 #pragma unroll
-    for (int i = 8; i < N; i += 16)
+    for (int i = 8; i < N; i += 8)
 #pragma unroll
-        for (int t = 0; t < 8; ++t) m8[t] = i + 8 + t < N ? fmax3(m8[t], s[i + t], s[i + 8 + t]) : fmaxf(m8[t], s[i + t]);
-    const float mx = fmaxf(fmax3(m8[0], m8[1], m8[2]), fmax3(fmax3(m8[3], m8[4], m8[5]), m8[6], m8[7]));
+        for (int t = 0; t < 4; ++t) m4[t] = fmax3(m4[t], s[i + t], s[i + 4 + t]);
+    const float mx = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
     // The reference of the weights follows the maximum where that is over it by more
     // than 2^8: weights stay under 2^8, O is rescaled seldom.
     const float mn = fmaxf(row.m, mx * sl);
@@ -319,42 +372,26 @@ __device__ __forceinline__ float weigh(RowOf& row, uint32_t ts, int c0, int key0
     float2 sum[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) sum[t] = make_float2(0.f, 0.f);
-    constexpr int kAt = N == 128 ? 64 : N, kWide = kAt / 2;   // columns at a time, and those of TMEM they become
+    uint32_t hi[N / 2], rest[N / 2];
 #pragma unroll
-    for (int part = 0; part < N / kAt; ++part) {
-        uint32_t hi[kWide], rest[kWide];
-#pragma unroll
-        for (int i = 0; i < kWide; ++i) {
-            const int at = part * kAt + 2 * i;
-            const float2 x = ffma2(make_float2(s[at], s[at + 1]), sl2, off);
-            const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-            sum[i & 3] = fadd2(sum[i & 3], p);
-            hi[i] = pack_bf16x2(p.x, p.y);
-            rest[i] = pack_bf16x2(p.x - __uint_as_float(hi[i] << 16), p.y - __uint_as_float(hi[i] & 0xffff0000u));
-        }
-        const uint32_t to = ts + c0 / 2 + part * kWide;
-        if constexpr (kWide == 32) {
-            tmem_st32(to, hi);
-            tmem_st32(to + K / 2, rest);
-        } else {
-            tmem_st16(to, hi);
-            tmem_st16(to + K / 2, rest);
-        }
+    for (int i = 0; i < N / 2; ++i) {
+        const float2 x = ffma2(make_float2(s[2 * i], s[2 * i + 1]), sl2, off);
+        const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+        sum[i & 3] = fadd2(sum[i & 3], p);
+        hi[i] = pack_bf16x2(p.x, p.y);
+        rest[i] = pack_bf16x2(p.x - __uint_as_float(hi[i] << 16), p.y - __uint_as_float(hi[i] & 0xffff0000u));
     }
-    if constexpr (N < K) {
+    tmem_st<N / 2>(ts + c0 / 2, hi);
+    tmem_st<N / 2>(ts + kHalfKeys / 2 + c0 / 2, rest);
+    if constexpr (N < kHalfKeys) {
         uint32_t zero[N / 2];
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) zero[i] = 0;
 #pragma unroll
-        for (int i = 0; i < K / N; ++i) {
-            if (i * N == c0) continue;
-            if constexpr (N == 64) {
-                tmem_st32(ts + i * 32, zero);
-                tmem_st32(ts + K / 2 + i * 32, zero);
-            } else {
-                tmem_st16(ts + i * 16, zero);
-                tmem_st16(ts + K / 2 + i * 16, zero);
-            }
+        for (int i = 0; i < kHalfKeys; i += N) {
+            if (i == c0) continue;
+            tmem_st<N / 2>(ts + i / 2, zero);
+            tmem_st<N / 2>(ts + kHalfKeys / 2 + i / 2, zero);
         }
     }
     const float2 s2 = fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
@@ -364,33 +401,33 @@ __device__ __forceinline__ float weigh(RowOf& row, uint32_t ts, int c0, int key0
 }
 
 template <int D>
-__device__ bool softmax(const TreeDecodeArgs& a, const Ctx<D>& c, uint32_t tmem, int warp) {
-    const int lane = threadIdx.x & 31, r = warp * 32 + lane;
+__device__ bool softmax(const TreeDecodeArgs& a, const Ctx<D>& c, uint32_t tmem, int half, int warp) {
+    const int lane = threadIdx.x & 31, r = warp * 32 + lane, G = a.Hq / a.Hkv;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    const uint32_t to = lanes + kColO;
+    const uint32_t to = lanes + kColO + half * D;
     uint32_t tiles = 0, done = 0;
-    TreeWalk<R> walk = walk_of(a, *c.start);
+    TreeWalk<R> walk{a, *c.start};
     TreeWork w;
     for (uint32_t u = 0; walk.next(w); ++u) {
-        const int rows = min(R, w.s.n * walk.G - w.rt * R), each = tree_copy_rows(rows);
+        const int rows = w.rows, each = tree_copy_rows(rows);
         const int in = r & (each - 1), first = (warp * 32) & (each - 1);
         const bool any = first < rows;   // the warp has rows
-        const int c0 = warp * 32 / each * each;   // its copy's columns, as many as the copy has rows
+        const int c0 = warp * 32 / each * (each / 2);   // its copy's columns, half as many as the copy has rows
         RowOf row{nullptr, 0, w.s.base, min(a.n_anchor, w.s.base), w.s.n, in < rows, -INFINITY, 0.f};
         if (row.on) {
-            const int tok = w.s.first + a.plan.order[w.s.first + (w.rt * R + in) / walk.G];
+            const int tok = w.s.first + a.plan.order[w.s.first + (w.row0 + in) / G];
             row.lo = a.plan.lo[tok];
             row.mask = a.plan.mask + static_cast<size_t>(tok) * kWords;
         }
         for (int kt = w.kt0; kt < w.kt1; ++kt, ++tiles) {
-            const int key0 = tile_key<K>(w.s, w.far, kt);
+            const int key0 = tile_key<K>(w.s, w.far, kt) + half * kHalfKeys;
             if (!wait_w(&c.bar[c.kSFull + (tiles & 1)], tiles >> 1 & 1, c.abort_flag, a.err)) return false;
             tc_fence_after();
             if (any) {
-                const uint32_t ts = lanes + (tiles & 1) * K;
-                const float f = each == 32   ? weigh<32>(row, ts, c0, key0, a.scale_log2)
-                                : each == 64 ? weigh<64>(row, ts, c0, key0, a.scale_log2)
-                                             : weigh<128>(row, ts, 0, key0, a.scale_log2);
+                const uint32_t ts = lanes + (tiles & 1) * K + half * kHalfKeys;
+                const float f = each == 32   ? weigh<16>(row, ts, c0, key0, a.scale_log2)
+                                : each == 64 ? weigh<32>(row, ts, c0, key0, a.scale_log2)
+                                             : weigh<64>(row, ts, 0, key0, a.scale_log2);
                 // O may be rescaled once the last tile's PV has landed; every PV but a
                 // unit's last one arrives at kODone.
                 if (__any_sync(0xffffffffu, row.on && f != 1.f)) {
@@ -410,12 +447,12 @@ __device__ bool softmax(const TreeDecodeArgs& a, const Ctx<D>& c, uint32_t tmem,
             }
             if (kt > w.kt0) ++done;
             tc_fence_before();
-            mbar_arrive(&c.bar[c.kPFull + (tiles & 1)]);
+            mbar_arrive(&c.bar[c.kPFull + (tiles & 1) * 2 + half]);
         }
         if (!wait_w(&c.bar[c.kOFull], u & 1, c.abort_flag, a.err)) return false;
         tc_fence_after();
         if (any) {
-            float* part = a.plan.part + static_cast<size_t>(w.slot) * R * (D + 2);
+            float* part = a.plan.part + static_cast<size_t>(w.slot) * 2 * R * (D + 2) + half * R * D;
 #pragma unroll
             for (int i = 0; i < D; i += 32) {
                 uint32_t o[32];
@@ -426,7 +463,7 @@ __device__ bool softmax(const TreeDecodeArgs& a, const Ctx<D>& c, uint32_t tmem,
                     for (int t = 0; t < 32; t += 4)
                         *reinterpret_cast<uint4*>(part + r * D + i + t) = make_uint4(o[t], o[t + 1], o[t + 2], o[t + 3]);
             }
-            if (row.on) reinterpret_cast<float2*>(part + R * D)[r] = make_float2(row.m, row.l);
+            if (row.on) reinterpret_cast<float2*>(part + (2 - half) * R * D)[half * R + r] = make_float2(row.m, row.l);
         }
         tc_fence_before();
         mbar_arrive(&c.bar[c.kOFree]);
@@ -434,17 +471,21 @@ __device__ bool softmax(const TreeDecodeArgs& a, const Ctx<D>& c, uint32_t tmem,
     return true;
 }
 
+struct TreeMaps {
+    CUtensorMap of[2];   // K's pages, V's
+};
+
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_constant__ TreeDecodeArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_constant__ TreeDecodeArgs a, const __grid_constant__ TreeMaps maps, int box) {
     extern __shared__ uint8_t raw[];
     using Z = Sizes<D>;
     Ctx<D> c;
     c.smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
     c.bar = reinterpret_cast<uint64_t*>(c.smem + Z::kOffBar);
-    Start* start = reinterpret_cast<Start*>(c.smem + Z::kOffMisc);
+    TreeStart* start = reinterpret_cast<TreeStart*>(c.smem + Z::kOffMisc);
     c.start = start;
-    c.abort_flag = reinterpret_cast<volatile int*>(c.smem + Z::kOffMisc + 40);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(c.smem + Z::kOffMisc + 44);
+    c.abort_flag = reinterpret_cast<volatile int*>(c.smem + Z::kOffMisc + sizeof(TreeStart));
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(c.smem + Z::kOffMisc + sizeof(TreeStart) + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < Z::kSlots; ++i) {
@@ -453,52 +494,50 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         }
         mbar_init(&c.bar[c.kQFull], 1);
         mbar_init(&c.bar[c.kQEmpty], 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&c.bar[c.kSFull + i], 1);
-            mbar_init(&c.bar[c.kPFull + i], R);
-        }
+        for (int i = 0; i < 2; ++i) mbar_init(&c.bar[c.kSFull + i], 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&c.bar[c.kPFull + i], R);
         mbar_init(&c.bar[c.kODone], 1);
         mbar_init(&c.bar[c.kOFull], 1);
-        mbar_init(&c.bar[c.kOFree], R);
+        mbar_init(&c.bar[c.kOFree], 2 * R);
         mbar_init(&c.bar[c.kDrain], 1);
         *c.abort_flag = 0;
         fence_barrier_init();
     }
-    if (warp == 4) {
+    if (warp == 8) {
         tmem_alloc(tmem_slot, kTmemCols);
         tmem_relinquish();
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");   // for the plan
     if (warp == 0) {
-        TreeWalk<R> walk{a};
-        start_walk<R>(a, walk);
-        if (lane == 0) *start = Start{walk.at, walk.end, walk.before, walk.b, walk.units};
+        const TreeStart begin = start_walk<R>(a);
+        if (lane == 0) *start = begin;
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    if (warp < 4) {
+    if (warp < 8) {
         warpgroup_reg_inc<kRegsSoftmax>();
-        softmax<D>(a, c, tmem, warp);
+        softmax<D>(a, c, tmem, warp >> 2, warp & 3);
     } else {
         warpgroup_reg_dec<kRegsOther>();
-        if (warp == 4) {
+        if (warp == 8) {
             mma_issuer<D>(a, c, tmem);
             umma_commit_w(&c.bar[c.kDrain]);   // all that was issued
             mbar_drain(&c.bar[c.kDrain], 0);
-        } else if (warp == 5) {
+        } else if (warp == 9) {
             q_loader<D>(a, c);
-        } else if (warp >= 8) {
-            loader<D>(a, c, warp - 8);
+        } else if (warp >= 12) {
+            uint32_t filled = 0;
+            if (!loader<D>(a, c, maps.of, box, warp - 12, filled)) drain<D>(c, filled);
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 4) {
+    if (warp == 8) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
@@ -512,7 +551,16 @@ cudaError_t launch(const TreeDecodeArgs& a, int ctas, cudaStream_t s) {
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = dependent_launch(ctas, kThreads, s, attr);
     cfg.dynamicSmemBytes = Sizes<D>::kBytes;
-    return cudaLaunchKernelEx(&cfg, tree_tc_kernel<D>, a);
+    // Rows that follow one another in the pool, for a warp's copies; none in pages of
+    // fewer tokens, or where a row's number does not fit a coordinate.
+    const int64_t rows = static_cast<int64_t>(a.num_pages) << a.page_lg;
+    const int box = a.page_lg < 4 || rows >= (int64_t(1) << 31) ? 0 : a.page_lg == 4 ? 16 : 32;
+    TreeMaps maps;
+    std::memset(&maps, 0, sizeof(maps));
+    if (box && (!make_tmap_4d_bf16(&maps.of[0], a.k_pages, D, a.Hkv, rows, 1, 64, box) ||
+                !make_tmap_4d_bf16(&maps.of[1], a.v_pages, D, a.Hkv, rows, 1, 64, box)))
+        return cudaErrorInvalidValue;
+    return cudaLaunchKernelEx(&cfg, tree_tc_kernel<D>, a, maps, box);
 }
 
 }  // namespace

@@ -375,12 +375,12 @@ struct PagingArgs {
 struct TreeSeq;
 struct TreePlan {       // in the workspace, see tree_plan.cuh
     TreeSeq* seqs;      // [B]
-    int64_t* start;     // [B + 1] key tiles of the units before each sequence's
-    int* unit;          // [B + 1] units before each sequence's
+    int64_t* start;     // [B + 1] of one head: key tiles of the units before each sequence's, and all
+    int* unit;          // [B + 1] of one head: units before each sequence's, and all
     int* order;         // [T] at first + i: the tree's token (0 .. n-1) that comes i-th
     int* lo;            // [T] the first cached key that a token reads (but for anchors)
     uint32_t* mask;     // [T][kMaxTree / 32] the tree's tokens that a token reads
-    float* part;        // [CTAs + units][a tile's rows][d + 2]
+    float* part;        // [CTAs + units]: sums [kPartRows][d], then (m, l) [kPartRows]
 };
 struct TreeDecodeArgs {
     const void* q;              // [T, Hq, d], bf16 or, for fp32 pages, fp32

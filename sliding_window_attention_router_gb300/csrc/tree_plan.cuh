@@ -3,11 +3,16 @@
 //
 // A sequence's n drafted tokens times the G query heads of a key head are rows,
 // the routed tokens' first; rows are cut into tiles of R, keys into tiles of K from
-// the cache's start.  A row tile that holds a routed token walks all key tiles, one
-// without walks those of the anchors and of the window.  A unit is the walk of one
+// the cache's start.  A row tile of routed tokens walks all key tiles, one of others
+// those of the anchors and of the window; where all rows fit one tile, that walks all
+// key tiles if any token is routed.  A unit is the walk of one
 // row tile of one key head of one sequence; the units' key tiles, laid end to end,
 // are dealt out to the CTAs in equal shares, whatever units they belong to.  So a
 // unit is a run of consecutive CTAs' parts, one of each; the join adds them up.
+// All of a head's units come before the next head's: CTAs a head's number of shares
+// apart then read the same tokens at the same time, whose heads lie side by side in
+// memory (16 sequences of 32K with 16 key heads: 622 us; a sequence's heads one
+// after another, 676).
 #pragma once
 
 #include "swiattn_internal.h"
@@ -15,19 +20,29 @@
 namespace swi {
 
 struct TreeSeq {
-    int first, n, base, routed;   // packed tokens [first, first + n), cached ones before them, routed among the n
+    int first, n, base;           // packed tokens [first, first + n), cached ones before them
+    int far_rows;                 // rows of the tiles that walk all key tiles
     int lo, na;                   // a window token reads none of [na, lo)
     int far_tiles, near_tiles;    // key tiles of a row tile with routed tokens, and of one without
 };
 static_assert(sizeof(TreeSeq) == 32, "TreeSeq is read as two int4");
 
+// Row tiles of one key head: the far ones, then the others.
 template <int R>
-__device__ __forceinline__ int row_tiles(int tokens, int G) { return (tokens * G + R - 1) / R; }
+__device__ __forceinline__ int far_tiles(const TreeSeq& s) { return (s.far_rows + R - 1) / R; }
 template <int R>
-__device__ __forceinline__ int64_t seq_tiles(const TreeSeq& s, int G, int Hkv) {
-    const int far = row_tiles<R>(s.routed, G), all = row_tiles<R>(s.n, G);
-    return (static_cast<int64_t>(far) * s.far_tiles + static_cast<int64_t>(all - far) * s.near_tiles) * Hkv;
+__device__ __forceinline__ int row_tiles(const TreeSeq& s, int G) { return far_tiles<R>(s) + (s.n * G - s.far_rows + R - 1) / R; }
+// Key tiles of all its units of one head.
+template <int R>
+__device__ __forceinline__ int64_t seq_tiles(const TreeSeq& s, int G) {
+    const int far = far_tiles<R>(s), all = row_tiles<R>(s, G);
+    return static_cast<int64_t>(far) * s.far_tiles + static_cast<int64_t>(all - far) * s.near_tiles;
 }
+
+// Rows that the parts of a tile are laid out for: on the tensor cores two halves of
+// the keys have one each.
+template <int R>
+constexpr int kPartRows = R == kTreeTcRows ? 2 * R : R;
 
 // Rows of each of the copies in which a tile on the tensor cores holds its rows: 32,
 // 64 or, once, all.
@@ -48,47 +63,61 @@ __device__ __forceinline__ int tile_key(const TreeSeq& s, bool far, int kt) {
 // One unit's share of a CTA: key tiles [kt0, kt1) of the walk.
 struct TreeWork {
     TreeSeq s;
-    int b, h, rt, slot;
+    int b, h, slot;
+    int row0, rows;   // rows [row0, row0 + rows) of the head's, row i being token order[i / G], head i % G
     int kt0, kt1;
     bool far;
+};
+
+// Where a CTA's share of the work begins, and what it needs to walk it.
+struct TreeStart {
+    int64_t at, end;      // key tiles [at, end) of all
+    int64_t head_tiles;   // of one head
+    int64_t before;       // of the head, before sequence b
+    int h, b;
+    int head_units, units;   // units of one head, and of the head before sequence b
 };
 
 // A CTA's share of the work, unit by unit.
 template <int R>
 struct TreeWalk {
     const TreeDecodeArgs& a;
-    int64_t at, end;      // key tiles [at, end) of all
-    int64_t before;       // those of the sequences before b
-    int b, units;         // units before sequence b's
-    int G;
-    // `first`: the sequence that the share begins in, and what lies before it.
+    TreeStart s;
     __device__ __forceinline__ bool next(TreeWork& w) {
-        if (at >= end) return false;
-        int64_t tiles;
-        for (;;) {   // ends: `end` is no further than all sequences' tiles
-            const int4* p = reinterpret_cast<const int4*>(a.plan.seqs + b);
+        if (s.at >= s.end) return false;
+        const int G = a.Hq / a.Hkv;
+        int64_t in = s.at - s.h * s.head_tiles;
+        if (in >= s.head_tiles) {   // the next head
+            ++s.h;
+            s.b = s.units = 0;
+            s.before = 0;
+            in -= s.head_tiles;
+        }
+        for (;;) {   // ends: the head has more than `in` tiles
+            const int4* p = reinterpret_cast<const int4*>(a.plan.seqs + s.b);
             const int4 x = p[0], y = p[1];
             w.s = TreeSeq{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-            tiles = seq_tiles<R>(w.s, G, a.Hkv);
-            if (at < before + tiles || b + 1 >= a.B) break;
-            before += tiles;
-            units += row_tiles<R>(w.s.n, G) * a.Hkv;
-            ++b;
+            const int64_t tiles = seq_tiles<R>(w.s, G);
+            if (in < s.before + tiles || s.b + 1 >= a.B) break;
+            s.before += tiles;
+            s.units += row_tiles<R>(w.s, G);
+            ++s.b;
         }
-        const int far = row_tiles<R>(w.s.routed, G), all = row_tiles<R>(w.s.n, G);
-        const int64_t head = tiles / a.Hkv, in = at - before;   // of one head
-        w.h = static_cast<int>(in / head);
-        int64_t rest = in - w.h * head;
+        const int far = far_tiles<R>(w.s);
+        int64_t rest = in - s.before;
         const int64_t far_all = static_cast<int64_t>(far) * w.s.far_tiles;
         w.far = rest < far_all;
         const int len = w.far ? w.s.far_tiles : w.s.near_tiles;
         if (!w.far) rest -= far_all;
-        w.rt = static_cast<int>(rest / len) + (w.far ? 0 : far);
-        w.kt0 = static_cast<int>(rest % len);
-        w.kt1 = static_cast<int>(min(static_cast<int64_t>(len), w.kt0 + end - at));
-        w.b = b;
-        w.slot = blockIdx.x + units + w.h * all + w.rt;
-        at += w.kt1 - w.kt0;
+        const int tile = static_cast<int>(rest / len);   // of its kind
+        w.row0 = tile * R + (w.far ? 0 : w.s.far_rows);
+        w.rows = min(R, (w.far ? w.s.far_rows : w.s.n * G) - w.row0);
+        w.kt0 = static_cast<int>(rest - static_cast<int64_t>(tile) * len);
+        w.kt1 = static_cast<int>(min(static_cast<int64_t>(len), w.kt0 + s.end - s.at));
+        w.b = s.b;
+        w.h = s.h;
+        w.slot = blockIdx.x + s.h * s.head_units + s.units + tile + (w.far ? 0 : far);
+        s.at += w.kt1 - w.kt0;
         return true;
     }
 };
@@ -96,29 +125,32 @@ struct TreeWalk {
 // The walk of this CTA, by one warp over all sequences; CTA 0 leaves their
 // running sums for the join.
 template <int R>
-__device__ __forceinline__ void start_walk(const TreeDecodeArgs& a, TreeWalk<R>& w) {
+__device__ __forceinline__ TreeStart start_walk(const TreeDecodeArgs& a) {
     const int lane = threadIdx.x & 31, G = a.Hq / a.Hkv;
     int64_t total = 0;
-    for (int i = lane; i < a.B; i += 32) total += seq_tiles<R>(a.plan.seqs[i], G, a.Hkv);
+    for (int i = lane; i < a.B; i += 32) total += seq_tiles<R>(a.plan.seqs[i], G);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    w.G = G;
-    const int64_t ctas = share_count(total, gridDim.x), c = blockIdx.x;
-    w.at = c < ctas ? total * c / ctas : 0;
-    w.end = c < ctas ? total * (c + 1) / ctas : 0;
+    TreeStart w;
+    w.head_tiles = total;
+    const int64_t all = total * a.Hkv, ctas = share_count(all, gridDim.x), c = blockIdx.x;
+    w.at = c < ctas ? all * c / ctas : 0;
+    w.end = c < ctas ? all * (c + 1) / ctas : 0;
+    w.h = total > 0 ? static_cast<int>(w.at / total) : 0;
     w.before = 0;
     w.b = w.units = 0;
+    const int64_t in = w.at - w.h * total;
     int64_t before = 0;
     int units = 0;
     bool found = false;
-    for (int from = 0; from < a.B && (blockIdx.x == 0 || !found); from += 32) {
+    for (int from = 0; from < a.B; from += 32) {
         const int i = from + lane;
         int64_t mine = 0;
         int u = 0;
         if (i < a.B) {
             const TreeSeq s = a.plan.seqs[i];
-            mine = seq_tiles<R>(s, G, a.Hkv);
-            u = row_tiles<R>(s.n, G) * a.Hkv;
+            mine = seq_tiles<R>(s, G);
+            u = row_tiles<R>(s, G);
         }
         int64_t sum = mine;
         int usum = u;
@@ -135,7 +167,7 @@ __device__ __forceinline__ void start_walk(const TreeDecodeArgs& a, TreeWalk<R>&
             a.plan.start[i] = before + sum - mine;
             a.plan.unit[i] = units + usum - u;
         }
-        const unsigned hit = __ballot_sync(0xffffffffu, before + sum > w.at);
+        const unsigned hit = __ballot_sync(0xffffffffu, before + sum > in);
         if (hit && !found) {
             const int who = __ffs(hit) - 1;
             w.b = from + who;
@@ -146,10 +178,12 @@ __device__ __forceinline__ void start_walk(const TreeDecodeArgs& a, TreeWalk<R>&
         before += __shfl_sync(0xffffffffu, sum, 31);
         units += __shfl_sync(0xffffffffu, usum, 31);
     }
+    w.head_units = units;
     if (blockIdx.x == 0 && lane == 0) {
         a.plan.start[a.B] = total;
         a.plan.unit[a.B] = units;
     }
+    return w;
 }
 
 }  // namespace swi
