@@ -182,13 +182,13 @@ struct SimtShared {
     TreeStart start;
 };
 
-template <int KIND, int D>
+template <int D>
 __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_constant__ TreeDecodeArgs a) {
     extern __shared__ __align__(16) uint8_t raw[];
     SimtShared<D>& s = *reinterpret_cast<SimtShared<D>*>(raw);
     constexpr int F = D / 4;      // float4 of a row
     constexpr int C = D / 64;     // float4 of a thread's output row
-    using T = typename std::conditional<KIND == SWIATTN_F32, float, __nv_bfloat16>::type;   // of q
+    constexpr int KIND = SWIATTN_F32;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, G = a.Hq / a.Hkv;
@@ -210,8 +210,7 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < rows) {
                 const int tok = w.s.first + a.plan.order[w.s.first + R / G];
-                x = four_of<KIND == SWIATTN_F32 ? SWIATTN_F32 : SWIATTN_BF16>(
-                    static_cast<const T*>(a.q) + (static_cast<int64_t>(tok) * a.Hq + w.h * G + R % G) * D, c, 1.f);
+                x = four_of<KIND>(static_cast<const float*>(a.q) + (static_cast<int64_t>(tok) * a.Hq + w.h * G + R % G) * D, c, 1.f);
             }
             reinterpret_cast<float4*>(s.q[r])[c] = x;
         }
@@ -328,7 +327,7 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
             if (r < rows) {
 #pragma unroll
                 for (int c = 0; c < C; ++c)
-                    reinterpret_cast<float4*>(part + r * D)[tx + 16 * c] =
+                    reinterpret_cast<float4*>(part)[(tx + 16 * c) * kR + r] =
                         make_float4(acc[i][4 * c], acc[i][4 * c + 1], acc[i][4 * c + 2], acc[i][4 * c + 3]);
                 if (tx == 0) reinterpret_cast<float2*>(part + kR * D)[r] = make_float2(m[i], l[i]);
             }
@@ -337,13 +336,19 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
 }
 
 // ---- the join ---------------------------------------------------------------------
-// A warp a row: the parts of its unit, by their maxima, in the CTAs' order.  Every
-// row of a tile multiplies every value row that the tile's walk reads, with weight
-// 0 where the row itself does not read it; where that value is not finite, 0 times
-// it is a NaN that is none of the row's.  So a row that comes out not finite is
+// A block 32 rows of a row tile at a time, lane r row r, warp w the (w % 8)-th eighth of
+// the dimensions and, by w / 8, every other part of the rows' unit; where there are
+// 16 rows or 8, two or four lanes share a row's parts.  Parts join by their maxima,
+// in an order that the numbers of rows and parts decide.  They lie four dimensions of
+// all rows together, then the next four, so that lanes read (and the threads that own
+// a row write) neighbouring 16 bytes.
+//
+// Every row of a tile multiplies every value row that the tile's walk reads, with
+// weight 0 where the row itself does not read it; where that value is not finite, 0
+// times it is a NaN that is none of the row's.  So a row that comes out not finite is
 // computed again, key by key over what it does read (slow, and right whatever the
 // reason).
-constexpr int kJoinThreads = 256, kAtOnce = 8;
+constexpr int kJoinThreads = 512;
 
 template <int N>
 struct Dims {
@@ -351,7 +356,7 @@ struct Dims {
 };
 
 template <int KIND, int D>
-__device__ void row_again(const TreeDecodeArgs& a, int b, int h, int tok, const TreeSeq& s, const float* q, Dims<D / 32>& o, float& m, float& l) {
+__device__ __noinline__ void row_again(const TreeDecodeArgs& a, int b, int h, int tok, const TreeSeq& s, const float* q, Dims<D / 32>& o, float& m, float& l) {
     constexpr int N = D / 32;
     const int lane = threadIdx.x & 31;
     m = -INFINITY;
@@ -391,112 +396,185 @@ __device__ void row_again(const TreeDecodeArgs& a, int b, int h, int tok, const 
     }
 }
 
+__device__ __forceinline__ void add(float4& o, const float4& x, float w) {
+    o = make_float4(fmaf(x.x, w, o.x), fmaf(x.y, w, o.y), fmaf(x.z, w, o.z), fmaf(x.w, w, o.w));
+}
+
 template <int KIND, int D, int R>
-__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeDecodeArgs a, int ctas) {
-    constexpr int N = D / 32;
+__global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(const __grid_constant__ TreeDecodeArgs a, int ctas) {
+    constexpr int N = D / 32, kAcross = 8, kGroups = D / 4 / kAcross;   // warps across the dimensions; fours of a warp
+    constexpr int kWarps = kJoinThreads / 32, kDown = kWarps / kAcross;
+    static_assert(kDown == 2, "the two halves of the warps");
+    constexpr int kAtOnce = 8 / kGroups;   // parts on their way: 32 registers
+    constexpr int kPart = kPartRows<R>;
     using T = typename std::conditional<KIND == SWIATTN_F32, float, __nv_bfloat16>::type;
+    __shared__ float s_o[32][D + 4];
+    __shared__ float2 s_stats[32];   // of the second warps
+    __shared__ float s_lse[32];
+    __shared__ unsigned s_bad[2];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int b = blockIdx.x, lane = threadIdx.x & 31, G = a.Hq / a.Hkv;
+    const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x / 32, G = a.Hq / a.Hkv;
+    const int across = warp % kAcross, down = warp / kAcross;
     const TreeSeq s = a.plan.seqs[b];
     if (s.n == 0) return;
-    const int far = far_tiles<R>(s);
+    const int far = far_tiles<R>(s), near_rows = s.n * G - s.far_rows;
     const int64_t head = a.plan.start[a.B], total = head * a.Hkv, start = a.plan.start[b];   // tiles of a head, of all
     const int unit = a.plan.unit[b], head_units = a.plan.unit[a.B];
-    const int64_t shares = share_count(total, ctas);
+    const int64_t shares = share_count(total, ctas), share = total / ctas;
     auto cta_of = [&](int64_t tile) { return static_cast<int>(((tile + 1) * shares - 1) / total); };
-    for (int i = blockIdx.y * (kJoinThreads / 32) + threadIdx.x / 32; i < s.n * a.Hq; i += gridDim.y * (kJoinThreads / 32)) {
-        const int h = i / (s.n * G), row = i % (s.n * G), in = row < s.far_rows ? row : row - s.far_rows;   // of its kind
-        const int rt = in / R + (row < s.far_rows ? 0 : far), r = in % R;
+    const int far_chunks = (s.far_rows + 31) / 32, chunks = far_chunks + (near_rows + 31) / 32;
+    if (threadIdx.x < 2) s_bad[threadIdx.x] = 0;
+    __syncthreads();
+    int turn = 0;
+    for (int i = blockIdx.y; i < chunks * a.Hkv; i += gridDim.y, turn ^= 1) {
+        const int h = i / chunks, chunk = i - h * chunks;
+        const bool is_far = chunk < far_chunks;
+        const int in = (is_far ? chunk : chunk - far_chunks) * 32, rows = is_far ? s.far_rows : near_rows;   // of its kind
+        const int here = min(32, rows - in), lanes = here <= 8 ? 8 : here <= 16 ? 16 : 32, at_row = lane & (lanes - 1);
+        const int rt = in / R, r = in % R + at_row;
+        const bool on = at_row < here;
+        const int row = on ? in + at_row + (is_far ? 0 : s.far_rows) : 0;
         const int tok = s.first + a.plan.order[s.first + row / G];
         const int64_t out = static_cast<int64_t>(tok) * a.Hq + h * G + row % G;
-        const int64_t from = h * head + start + (rt < far ? static_cast<int64_t>(rt) * s.far_tiles : static_cast<int64_t>(far) * s.far_tiles + static_cast<int64_t>(rt - far) * s.near_tiles);
-        const int c0 = cta_of(from), parts = cta_of(from + (rt < far ? s.far_tiles : s.near_tiles) - 1) - c0 + 1;
+        const int len = is_far ? s.far_tiles : s.near_tiles;
+        const int64_t from = h * head + start + static_cast<int64_t>(rt) * len + (is_far ? 0 : static_cast<int64_t>(far) * s.far_tiles);
+        const int c0 = cta_of(from);
         // Tiles of the tensor cores hold few rows several times over, each a part.
-        constexpr int kPart = kPartRows<R>;
-        const int each = R == kTreeTcRows ? tree_copy_rows(min(R, (row < s.far_rows ? s.far_rows : s.n * G - s.far_rows) - (in - r))) : R, copies = kPart / each, n = parts * copies;
-        const float* part = a.plan.part + static_cast<size_t>(c0 + h * head_units + unit + rt) * kPart * (D + 2);
-        auto row_at = [&](int p) { return r + p % copies * each; };
-        auto part_at = [&](int p) { return part + static_cast<size_t>(p / copies) * kPart * (D + 2); };
-        // Lane i looks up the maximum and the sum of part i of 32; their weights
-        // are then known before the rows come, eight at once.
+        const int each = R == kTreeTcRows ? tree_copy_rows(min(R, rows - rt * R), share) : R, copies = kPart / each;
+        const int n = (cta_of(from + len - 1) - c0 + 1) * copies;
+        const float* part = a.plan.part + static_cast<size_t>(c0 + h * head_units + unit + rt + (is_far ? 0 : far)) * kPart * (D + 2);
         float m = -INFINITY, l = 0.f;
-        Dims<N> o;
+        float4 o[kGroups];
 #pragma unroll
-        for (int e = 0; e < N; ++e) o.x[e] = 0.f;
-        for (int p0 = 0; p0 < n; p0 += 32) {
-            float2 st = make_float2(-INFINITY, 0.f);
-            if (p0 + lane < n) st = __ldcg(reinterpret_cast<const float2*>(part_at(p0 + lane) + kPart * D) + row_at(p0 + lane));
-            float mn = fmaxf(m, st.x);
+        for (int g = 0; g < kGroups; ++g) o[g] = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int step = kDown * (32 / lanes);   // this lane's parts: the first, and how far apart
+        for (int p0 = down * (32 / lanes) + lane / lanes; p0 < n; p0 += kAtOnce * step) {
+            float2 st[kAtOnce];
+            float4 x[kAtOnce][kGroups];
 #pragma unroll
-            for (int w = 16; w > 0; w >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, w));
-            const float ref = mn == -INFINITY ? 0.f : mn, f = exp2f(m - ref), mine = exp2f(st.x - ref);
-            float sum = st.y * mine;
+            for (int p = 0; p < kAtOnce; ++p) {
+                st[p] = make_float2(-INFINITY, 0.f);
+                const int q = p0 + p * step;
+                if (on && q < n) {
+                    const float* at = part + static_cast<size_t>(q / copies) * kPart * (D + 2);
+                    const int in_part = r + q % copies * each;
+                    st[p] = __ldcg(reinterpret_cast<const float2*>(at + kPart * D) + in_part);
 #pragma unroll
-            for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-            l = l * f + sum;
-            m = mn;
-#pragma unroll
-            for (int e = 0; e < N; ++e) o.x[e] *= f;
-            for (int q = 0; q < min(32, n - p0); q += kAtOnce) {
-                Dims<N> x[kAtOnce];
-#pragma unroll
-                for (int i = 0; i < kAtOnce; ++i)
-                    if (p0 + q + i < n) {
-                        const float* from = part_at(p0 + q + i) + row_at(p0 + q + i) * D;
-                        if constexpr (N == 4) {
-                            const float4 v = __ldcg(reinterpret_cast<const float4*>(from) + lane);
-                            x[i].x[0] = v.x, x[i].x[1] = v.y, x[i].x[2] = v.z, x[i].x[3] = v.w;
-                        } else {
-                            const float2 v = __ldcg(reinterpret_cast<const float2*>(from) + lane);
-                            x[i].x[0] = v.x, x[i].x[1] = v.y;
-                        }
-                    }
-#pragma unroll
-                for (int i = 0; i < kAtOnce; ++i) {
-                    const float g = __shfl_sync(0xffffffffu, mine, q + i);
-                    if (p0 + q + i < n) {
-#pragma unroll
-                        for (int e = 0; e < N; ++e) o.x[e] = fmaf(x[i].x[e], g, o.x[e]);
-                    }
+                    for (int g = 0; g < kGroups; ++g)
+                        x[p][g] = __ldcg(reinterpret_cast<const float4*>(at) + (across * kGroups + g) * kPart + in_part);
                 }
             }
+            float mn = m;
+#pragma unroll
+            for (int p = 0; p < kAtOnce; ++p) mn = fmaxf(mn, st[p].x);
+            const float ref = mn == -INFINITY ? 0.f : mn, f = exp2f(m - ref);
+            l *= f;
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) o[g] = make_float4(o[g].x * f, o[g].y * f, o[g].z * f, o[g].w * f);
+#pragma unroll
+            for (int p = 0; p < kAtOnce; ++p)
+                if (on && p0 + p * step < n) {
+                    const float w = exp2f(st[p].x - ref);
+                    l = fmaf(st[p].y, w, l);
+#pragma unroll
+                    for (int g = 0; g < kGroups; ++g) add(o[g], x[p][g], w);
+                }
+            m = mn;
         }
-        bool fine = l - l == 0.f && l > 0.f;
+        // The row's other lanes, then its other warps.
+        auto join = [&](float m2, float l2, auto other) {
+            const float mn = fmaxf(m, m2), ref = mn == -INFINITY ? 0.f : mn, f = exp2f(m - ref), w = exp2f(m2 - ref);
+            l = l * f + l2 * w;
 #pragma unroll
-        for (int e = 0; e < N; ++e) fine &= o.x[e] - o.x[e] == 0.f;
-        if (!__all_sync(0xffffffffu, fine)) {
-            float q[N];
-            const T* src = static_cast<const T*>(a.q) + out * D + lane * N;
+            for (int g = 0; g < kGroups; ++g) {
+                const float4 x = other(g);
+                o[g] = make_float4(o[g].x * f, o[g].y * f, o[g].z * f, o[g].w * f);
+                add(o[g], x, w);
+            }
+            m = mn;
+        };
+        for (int w = lanes; w < 32; w *= 2)
+            join(__shfl_xor_sync(0xffffffffu, m, w), __shfl_xor_sync(0xffffffffu, l, w), [&](int g) {
+                return make_float4(__shfl_xor_sync(0xffffffffu, o[g].x, w), __shfl_xor_sync(0xffffffffu, o[g].y, w),
+                                   __shfl_xor_sync(0xffffffffu, o[g].z, w), __shfl_xor_sync(0xffffffffu, o[g].w, w));
+            });
+        if (down == 1) {
 #pragma unroll
-            for (int e = 0; e < N; ++e) q[e] = static_cast<float>(src[e]);
-            row_again<KIND, D>(a, b, h, tok, s, q, o, m, l);
+            for (int g = 0; g < kGroups; ++g) *reinterpret_cast<float4*>(&s_o[lane][(across * kGroups + g) * 4]) = o[g];
+            if (across == 0) s_stats[lane] = make_float2(m, l);
         }
-        const float inv = 1.f / l;
-        T y[N];
+        __syncthreads();
+        if (down == 0) {
+            const float2 st = s_stats[lane];
+            join(st.x, st.y, [&](int g) { return *reinterpret_cast<const float4*>(&s_o[lane][(across * kGroups + g) * 4]); });
+        }
+        bool fine = true;
+        if (down == 0) {
+            const float inv = 1.f / l;
+            fine = l - l == 0.f && l > 0.f;
 #pragma unroll
-        for (int e = 0; e < N; ++e) y[e] = static_cast<T>(o.x[e] * inv);
-        T* to = static_cast<T*>(a.o) + out * D + lane * N;
+            for (int g = 0; g < kGroups; ++g) {
+                o[g] = make_float4(o[g].x * inv, o[g].y * inv, o[g].z * inv, o[g].w * inv);
+                fine &= (o[g].x - o[g].x == 0.f) & (o[g].y - o[g].y == 0.f) & (o[g].z - o[g].z == 0.f) & (o[g].w - o[g].w == 0.f);
+                *reinterpret_cast<float4*>(&s_o[lane][(across * kGroups + g) * 4]) = o[g];
+            }
+            if (across == 0) s_lse[lane] = (m + log2f(l)) * 0.69314718055994531f;
+        }
+        const unsigned odd = __ballot_sync(0xffffffffu, lane < here && !fine);
+        if (odd && lane == 0) atomicOr(&s_bad[turn], odd);
+        if (threadIdx.x == 0) s_bad[turn ^ 1] = 0;
+        __syncthreads();
+        const unsigned bad = s_bad[turn];
+        // A warp's rows: two, lanes side by side along the dimensions.
 #pragma unroll
-        for (int e = 0; e < N; ++e) to[e] = y[e];
-        if (a.lse && lane == 0) a.lse[out] = (m + log2f(l)) * 0.69314718055994531f;
+        for (int k = 0; k < 32 / kWarps; ++k) {
+            const int at = warp * (32 / kWarps) + k;
+            const int64_t to = __shfl_sync(0xffffffffu, out, at & (lanes - 1));
+            if (at >= here) break;
+            float y[N];
+#pragma unroll
+            for (int e = 0; e < N; ++e) y[e] = s_o[at][lane * N + e];
+            float lse = s_lse[at];
+            if (bad >> at & 1) {
+                Dims<N> again;
+                float q[N], am, al;
+                const T* src = static_cast<const T*>(a.q) + to * D + lane * N;
+#pragma unroll
+                for (int e = 0; e < N; ++e) q[e] = static_cast<float>(src[e]);
+                row_again<KIND, D>(a, b, h, static_cast<int>(to / a.Hq), s, q, again, am, al);
+                lse = (am + log2f(al)) * 0.69314718055994531f;
+#pragma unroll
+                for (int e = 0; e < N; ++e) y[e] = again.x[e] / al;
+            }
+            T* dst = static_cast<T*>(a.o) + to * D + lane * N;
+            if constexpr (KIND == SWIATTN_F32) {
+                if constexpr (N == 4) *reinterpret_cast<float4*>(dst) = make_float4(y[0], y[1], y[2], y[3]);
+                else *reinterpret_cast<float2*>(dst) = make_float2(y[0], y[1]);
+            } else {
+                if constexpr (N == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+                else *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(y[0], y[1]);
+            }
+            if (a.lse && lane == 0) a.lse[to] = lse;
+        }
+        __syncthreads();   // s_o is written again
     }
 }
 
-template <int KIND, int D>
+template <int D>
 cudaError_t launch_simt(const TreeDecodeArgs& a, int ctas, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_dynamic_smem(tree_simt_kernel<KIND, D>, sizeof(SimtShared<D>), done);
+    const cudaError_t e = allow_dynamic_smem(tree_simt_kernel<D>, sizeof(SimtShared<D>), done);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = dependent_launch(ctas, kSimtThreads, s, attr);
     cfg.dynamicSmemBytes = sizeof(SimtShared<D>);
-    return cudaLaunchKernelEx(&cfg, tree_simt_kernel<KIND, D>, a);
+    return cudaLaunchKernelEx(&cfg, tree_simt_kernel<D>, a);
 }
 
 template <int KIND, int D>
 cudaError_t launch_all(const TreeDecodeArgs& a, int sms, cudaStream_t s) {
-    constexpr bool kTc = KIND == SWIATTN_BF16;
+    constexpr bool kTc = KIND != SWIATTN_F32;
     constexpr int kRows = kTc ? kTreeTcRows : kTreeRows;
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = dependent_launch(a.B, kMaxTree, s, attr);
@@ -504,12 +582,13 @@ cudaError_t launch_all(const TreeDecodeArgs& a, int sms, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const int ctas = kTc ? std::min(sms, kTreeTcCtas) : std::min(2 * sms, kTreeCtas);
     prof_start(s);
-    if constexpr (kTc) e = launch_tree_tc(a, D, ctas, s);
-    else e = launch_simt<KIND, D>(a, ctas, s);
+    if constexpr (kTc) e = launch_tree_tc(a, D, KIND == SWIATTN_E4M3, ctas, s);
+    else e = launch_simt<D>(a, ctas, s);
     prof_stop(s);
     if (e != cudaSuccess) return e;
-    const int most = (std::min(a.T, kMaxTree) * a.Hq + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
-    cfg = dependent_launch(dim3(a.B, std::min(most, std::max(1, 4096 / a.B))), kJoinThreads, s, attr);
+    // About the chunks of a sequence of mean size (blocks without one cost time too).
+    const int64_t mean = (static_cast<int64_t>(a.T) * (a.Hq / a.Hkv) / a.B / 32 + 1) * a.Hkv;
+    cfg = dependent_launch(dim3(a.B, static_cast<unsigned>(std::min<int64_t>(mean, std::max(1, 8192 / a.B)))), kJoinThreads, s, attr);
     e = cudaLaunchKernelEx(&cfg, tree_join_kernel<KIND, D, kRows>, a, ctas);
     return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -22,7 +22,8 @@
 //   warp 8      TMEM and MMA issue (converged, elected issue)
 //   warp 9      Q: gathers a unit's rows
 //   warps 12-15 K and V: a ring of tiles in the order in which they are used (K0,
-//               K1, V0, K2, V1, ...), 32 rows of each tile a warp
+//               K1, V0, K2, V1, ...), 32 rows of each tile a warp; e4m3 pages come
+//               through a ring of their own and are converted on the way
 //   (warps 10, 11 fill up a warpgroup, the unit that registers are moved by)
 // TMEM: S at [0, 128) and [128, 256), the halves' O at [256, 256 + d) and from 256 + d.
 
@@ -48,25 +49,31 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kHalfKeys = K / 2;
 constexpr uint32_t kColO = 256;
 
-template <int D>
+template <int D, bool E4M3>
 struct Sizes {
-    static constexpr int kTile = R * D * 2;            // Q, and a slot of the ring
-    static constexpr int kSlots = 6 * 128 / D;
+    static constexpr int kTile = R * D * 2;                    // Q, and a slot of the ring
+    static constexpr int kSlots = (E4M3 ? 3 : 6) * 128 / D;
+    static constexpr int kRaw = E4M3 ? 6 * 128 / D : 0;        // tiles as they are in the pages
     static constexpr int kBars = 2 * kSlots + 2 + 2 + 4 + 3 + 1;
-    static constexpr int kOffBar = (1 + kSlots) * kTile;
+    static constexpr int kOffRaw = (1 + kSlots) * kTile;
+    static constexpr int kOffExp = kOffRaw + kRaw * (R * D);   // and their rows' exponent bytes
+    static constexpr int kOffBar = kOffExp + kRaw * R;
     static constexpr int kOffMisc = kOffBar + kBars * 8;
-    static constexpr int kBytes = kOffMisc + 64 + 1024;   // and room to align
+    static constexpr int kBytes = kOffMisc + 80 + 1024;        // and room to align
 };
-static_assert(sizeof(TreeStart) + 8 <= 64, "what follows the barriers");
-static_assert(Sizes<128>::kBytes <= 232448 && Sizes<64>::kBytes <= 232448, "shared memory budget");
+static_assert(sizeof(TreeStart) + 8 <= 80, "what follows the barriers");
+template <int D, bool E4M3>
+constexpr bool kFits = Sizes<D, E4M3>::kBytes <= 232448;
+static_assert(kFits<128, false> && kFits<64, false> && kFits<128, true> && kFits<64, true>, "shared memory budget");
 
-template <int D>
+template <int D, bool E4M3>
 struct Ctx {
+    using Z = Sizes<D, E4M3>;
     uint8_t* smem;
     uint64_t* bar;
     volatile int* abort_flag;
     const TreeStart* start;
-    static constexpr int kFull = 0, kEmpty = Sizes<D>::kSlots, kQFull = 2 * Sizes<D>::kSlots, kQEmpty = kQFull + 1,
+    static constexpr int kFull = 0, kEmpty = Z::kSlots, kQFull = 2 * Z::kSlots, kQEmpty = kQFull + 1,
                          kSFull = kQEmpty + 1, kPFull = kSFull + 2, kODone = kPFull + 4, kOFull = kODone + 1,
                          kOFree = kOFull + 1, kDrain = kOFree + 1;
 };
@@ -87,21 +94,70 @@ __device__ __forceinline__ bool wait_w(uint64_t* bar, uint32_t parity, volatile 
 struct Rows {
     uint32_t row;     // lane's
     uint32_t read;    // the warp's, a bit a row
+    uint32_t exps;    // e4m3: lane's, of the key row and, 8 bits up, of the value row
 };
+template <bool E4M3>
 __device__ __forceinline__ Rows rows_of(const TreeDecodeArgs& a, const TreeWork& w, int kt, int row32) {
     const int tok = tile_key<K>(w.s, w.far, kt) + row32 + (threadIdx.x & 31);
     const bool on = tok < w.s.base + w.s.n && (w.far || tok >= w.s.lo || tok < w.s.na);
     Rows r;
     r.row = 0;
+    r.exps = 127 | 127 << 8;
     if (on) {
         const int p = a.block_table[static_cast<int64_t>(w.b) * a.max_pages + (tok >> a.page_lg)];
         const bool in = p >= 0 && p < a.num_pages;
         if (!in) atomicOr(a.err, kDevErrInput);
-        r.row = (static_cast<uint32_t>(in ? p : 0) << a.page_lg) + (tok & ((1 << a.page_lg) - 1));
+        const int page = in ? p : 0, slot = tok & ((1 << a.page_lg) - 1);
+        r.row = (static_cast<uint32_t>(page) << a.page_lg) + slot;
+        if (E4M3) {
+            const int64_t at = ((static_cast<int64_t>(page) * a.Hkv + w.h) << a.page_lg) + slot;
+            r.exps = a.k_exp[at] | a.v_exp[at] << 8;
+        }
     }
     r.read = __ballot_sync(0xffffffffu, on);
     return r;
 }
+
+// The tiles of the ring in their order, one by one; the next key tile's page numbers
+// are looked up while the last one's rows are copied.
+template <bool E4M3>
+struct SlotWalk {
+    const TreeDecodeArgs& a;
+    TreeWalk<R> walk;
+    int row32;
+    TreeWork w;
+    int kt = 0, which = 2;   // K (0) of key tile kt or V (1) of the one before it comes next, or (2) a new unit
+    Rows before, now, ahead;
+    // Whether there is a next one: K (0) or V (1), its rows and their head in w.h.
+    __device__ __forceinline__ bool next(int& kind, Rows& rows) {
+        for (;;) {
+            if (which == 2) {
+                if (!walk.next(w)) return false;
+                kt = w.kt0;
+                which = 0;
+                now = ahead = rows_of<E4M3>(a, w, kt, row32);
+                if (kt + 1 < w.kt1) ahead = rows_of<E4M3>(a, w, kt + 1, row32);
+            }
+            if (which == 0) {
+                which = 1;
+                if (kt < w.kt1) {
+                    kind = 0;
+                    rows = now;
+                    return true;
+                }
+            }
+            const bool v = kt > w.kt0;
+            kind = 1;
+            rows = before;
+            before = now;
+            now = ahead;
+            ++kt;
+            which = kt > w.kt1 ? 2 : 0;
+            if (kt + 1 < w.kt1) ahead = rows_of<E4M3>(a, w, kt + 1, row32);
+            if (v) return true;
+        }
+    }
+};
 
 template <int D>
 __device__ __forceinline__ void copy_rows(const TreeDecodeArgs& a, const void* pages, const Rows& rows, int h, uint32_t dst) {
@@ -134,27 +190,35 @@ __device__ __forceinline__ void copies_but(int left) {
 
 // A warp fills its 32 rows of every slot: by TMA, which announces itself, where a
 // page holds `box` of them (16 or 32) and all are read; else by copies of its own
-// threads, which it announces, in their order, when it has no slot to fill.
+// threads, which it announces, in their order, three slots later or when it has no
+// slot to fill.
 template <int D>
-__device__ bool loader(const TreeDecodeArgs& a, const Ctx<D>& c, const CUtensorMap* maps, int box, int w32, uint32_t& g) {
-    constexpr int S = Sizes<D>::kSlots;
+__device__ bool loader(const TreeDecodeArgs& a, const Ctx<D, false>& c, const CUtensorMap* maps, int box, int w32, uint32_t& g) {
+    using Z = Sizes<D, false>;
+    constexpr int S = Z::kSlots;
     const int lane = threadIdx.x & 31;
-    const uint32_t ring = smem_u32(c.smem) + Sizes<D>::kTile + w32 * 32 * 128;
-    uint32_t own[2] = {0, 0};        // those of them with copies not announced: their slots, 4 bits each, the first lowest
-    int owned = 0;
-    auto announce = [&]() {
-        copies_but(owned - 1);
+    const uint32_t ring = smem_u32(c.smem) + Z::kTile + w32 * 32 * 128;
+    uint32_t first = 0;              // of the slots with copies not announced, which follow one another
+    uint32_t own = 0;                // bit i: slot first + i is one of them
+    auto announce = [&]() {          // slot `first`
+        copies_but(__popc(own) - 1);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&c.bar[c.kFull + (own[0] & 15)]);
-        own[0] = own[0] >> 4 | own[1] << 28;
-        own[1] >>= 4;
-        --owned;
+        if (lane == 0) mbar_arrive(&c.bar[c.kFull + first % S]);
+        own >>= 1;
+        ++first;
+        if (own) {
+            const int skip = __ffs(own) - 1;
+            own >>= skip;
+            first += skip;
+        }
     };
-    auto fill = [&](int which, const Rows& rows, int h) -> bool {
-        const uint32_t slot = g % S, dst = ring + slot * Sizes<D>::kTile, parity = (g / S & 1) ^ 1;
+    SlotWalk<false> slots{a, TreeWalk<R>{a, *c.start}, w32 * 32};
+    Rows rows;
+    for (int which; slots.next(which, rows); ++g) {
+        const uint32_t slot = g % S, dst = ring + slot * Z::kTile, parity = (g / S & 1) ^ 1;
         uint64_t* empty = &c.bar[c.kEmpty + slot];
-        while (owned && !__all_sync(0xffffffffu, mbar_test_wait(empty, parity))) announce();
+        while (own && (g - first >= 3 || !__all_sync(0xffffffffu, mbar_test_wait(empty, parity)))) announce();
         if (!wait_w(empty, parity, c.abort_flag, a.err)) return false;
         if (box && rows.read == 0xffffffffu) {
             uint64_t* full = &c.bar[c.kFull + slot];
@@ -165,38 +229,121 @@ __device__ bool loader(const TreeDecodeArgs& a, const Ctx<D>& c, const CUtensorM
                 if (lane == 0)
 #pragma unroll
                     for (int half = 0; half < D / 64; ++half)
-                        tma_load_4d_at(dst + half * kHalf + r * 128, maps + which, full, half * 64, h, row, 0);
+                        tma_load_4d_at(dst + half * kHalf + r * 128, maps + which, full, half * 64, slots.w.h, row, 0);
             }
         } else {
-            copy_rows<D>(a, which ? a.v_pages : a.k_pages, rows, h, dst);
+            copy_rows<D>(a, which ? a.v_pages : a.k_pages, rows, slots.w.h, dst);
             asm volatile("cp.async.commit_group;" ::: "memory");
-            if (owned < 8) own[0] |= slot << (4 * owned);
-            else own[1] |= slot << (4 * (owned - 8));
-            ++owned;
-        }
-        ++g;
-        return true;
-    };
-    TreeWalk<R> walk{a, *c.start};
-    TreeWork w;
-    while (walk.next(w)) {
-        Rows next = rows_of(a, w, w.kt0, w32 * 32), now = next;
-        for (int kt = w.kt0; kt <= w.kt1; ++kt) {
-            const Rows last = now;
-            now = next;
-            if (kt + 1 < w.kt1) next = rows_of(a, w, kt + 1, w32 * 32);   // the page numbers are on their way during the copies
-            if (kt < w.kt1 && !fill(0, now, w.h)) return false;
-            if (kt > w.kt0 && !fill(1, last, w.h)) return false;
+            if (!own) first = g;
+            own |= 1u << (g - first);
         }
     }
-    while (owned) announce();
+    while (own) announce();
+    return true;
+}
+
+// Four e4m3 bytes as bf16 over 2^120: bytes 0 and 2 in lo, 1 and 3 in hi (the sign, then
+// exponent and mantissa where a bf16 has its lowest ones).  0x7f comes out as 480.
+__device__ __forceinline__ void bf16_of(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    hi = (w & 0x80008000u) | (w >> 4 & 0x07f007f0u);
+    lo = (w << 8 & 0x80008000u) | (w << 4 & 0x07f007f0u);
+}
+__device__ __forceinline__ uint32_t times(uint32_t x, uint32_t y) {   // two bf16
+    uint32_t z;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(z) : "r"(x), "r"(y));
+    return z;
+}
+
+// 16 e4m3 bytes of a row with exponent byte `e`, as 16 bf16 whose every four are in the
+// order 0 2 1 3 (Q's elements are laid out alike, and so come O's).  Exact where a
+// bf16 reaches: powers of two from 2^-133 to below 2^128.
+__device__ __forceinline__ void row_piece(const uint4& raw, uint32_t e, uint32_t* x) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    // 2^(e - 127 + 120), a second factor where that is over 2^127
+    const uint32_t up = min(e + 120, 254u), scale = up << 7 | up << 23;
+    uint32_t nan = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        bf16_of(w[i], x[2 * i], x[2 * i + 1]);
+        x[2 * i] = times(x[2 * i], scale);
+        x[2 * i + 1] = times(x[2 * i + 1], scale);
+        nan |= (w[i] & 0x7f7f7f7fu) + 0x01010101u;
+    }
+    if (e > 134) {
+        const uint32_t more = (e - 134 + 127) << 7 | (e - 134 + 127) << 23;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = times(x[i], more);
+    }
+    if (nan & 0x80808080u) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t is = (w[i] & 0x7f7f7f7fu) + 0x01010101u & 0x80808080u;   // bit 7 of the bytes that are
+            x[2 * i] |= (is & 0x80u ? 0x7fffu : 0u) | (is & 0x800000u ? 0x7fff0000u : 0u);
+            x[2 * i + 1] |= (is & 0x8000u ? 0x7fffu : 0u) | (is & 0x80000000u ? 0x7fff0000u : 0u);
+        }
+    }
+}
+
+// The same for e4m3 pages: a thread copies pieces of 16 bytes into a ring of its own,
+// kRaw - 1 tiles ahead, and once they have come writes them as bf16 to the slot.
+template <int D>
+__device__ bool converter(const TreeDecodeArgs& a, const Ctx<D, true>& c, int w32) {
+    using Z = Sizes<D, true>;
+    constexpr int S = Z::kSlots, P = D / 16, kPer = 32 / P;   // pieces of a row; rows at a time
+    const int lane = threadIdx.x & 31, piece = lane % P, line = lane / P;
+    const uint32_t raw = smem_u32(c.smem) + Z::kOffRaw + w32 * 32 * D + lane * 16;
+    uint8_t* exps = c.smem + Z::kOffExp + w32 * 32;
+    // A piece becomes two of its row's 16-byte pieces; lanes of the second 64 columns
+    // begin with the second, so that eight lanes write to all banks.
+    const uint32_t col = smem_u32(c.smem) + Z::kTile + w32 * 32 * 128 + (piece >> 2) * kHalf;
+    const int first = 2 * (piece & 3) + (piece >> 2), second = first ^ 1;
+    const size_t step = static_cast<size_t>(a.Hkv) * D;
+    const uint32_t total = static_cast<uint32_t>(2 * (c.start->end - c.start->at));
+    SlotWalk<true> slots{a, TreeWalk<R>{a, *c.start}, w32 * 32};
+    Rows rows;
+    for (uint32_t g = 0; g < total + Z::kRaw - 1; ++g) {
+        int which;
+        if (g < total && slots.next(which, rows)) {
+            const uint32_t slot = g % Z::kRaw;
+            const char* src = static_cast<const char*>(which ? a.v_pages : a.k_pages) + static_cast<size_t>(slots.w.h) * D + piece * 16;
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const int r = i * kPer + line;
+                const uint32_t row = __shfl_sync(0xffffffffu, rows.row, r);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(raw + slot * (R * D) + i * 512), "l"(src + row * step),
+                             "r"(rows.read >> r & 1 ? 16u : 0u)
+                             : "memory");
+            }
+            exps[slot * R + lane] = static_cast<uint8_t>(rows.exps >> (8 * which));
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (g < Z::kRaw - 1) continue;
+        const uint32_t t = g - (Z::kRaw - 1), slot = t % S, from = t % Z::kRaw;
+        asm volatile("cp.async.wait_group %0;" ::"n"(Z::kRaw - 1) : "memory");
+        if (!wait_w(&c.bar[c.kEmpty + slot], (t / S & 1) ^ 1, c.abort_flag, a.err)) return false;
+        __syncwarp();   // the exponents are other lanes'
+        const uint32_t dst = col + slot * Z::kTile;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int r = i * kPer + line;
+            uint32_t x[8];
+            row_piece(ld_shared_v4(raw + from * (R * D) + i * 512), exps[from * R + r], x);
+            const uint32_t to = dst + r * 128;
+            const bool swap = first & 1;
+            st_shared_v4(to + ((first ^ (r & 7)) << 4), swap ? x[4] : x[0], swap ? x[5] : x[1], swap ? x[6] : x[2], swap ? x[7] : x[3]);
+            st_shared_v4(to + ((second ^ (r & 7)) << 4), swap ? x[0] : x[4], swap ? x[1] : x[5], swap ? x[2] : x[6], swap ? x[3] : x[7]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();   // and the ring's tile and exponents have been read
+        if (lane == 0) mbar_arrive(&c.bar[c.kFull + slot]);
+    }
     return true;
 }
 
 // The copies in flight of a call that gave up.
 template <int D>
-__device__ void drain(const Ctx<D>& c, uint32_t filled) {
-    constexpr int S = Sizes<D>::kSlots;
+__device__ void drain(const Ctx<D, false>& c, uint32_t filled) {
+    constexpr int S = Sizes<D, false>::kSlots;
     for (uint32_t back = 1; back <= S && back <= filled; ++back) {
         const uint32_t g = filled - back;
         mbar_drain(&c.bar[c.kFull + g % S], g / S & 1);
@@ -204,8 +351,8 @@ __device__ void drain(const Ctx<D>& c, uint32_t filled) {
 }
 
 // ---- Q ---------------------------------------------------------------------------------
-template <int D>
-__device__ bool q_loader(const TreeDecodeArgs& a, const Ctx<D>& c) {
+template <int D, bool E4M3>
+__device__ bool q_loader(const TreeDecodeArgs& a, const Ctx<D, E4M3>& c) {
     constexpr int P = D / 8, kPer = 32 / P;
     const int lane = threadIdx.x & 31, piece = lane % P, G = a.Hq / a.Hkv;
     const uint32_t col = smem_u32(c.smem) + (piece >> 3) * kHalf;
@@ -213,7 +360,7 @@ __device__ bool q_loader(const TreeDecodeArgs& a, const Ctx<D>& c) {
     TreeWork w;
     for (uint32_t u = 0; walk.next(w); ++u) {
         if (!wait_w(&c.bar[c.kQEmpty], (u & 1) ^ 1, c.abort_flag, a.err)) return false;
-        const int rows = w.rows, each = tree_copy_rows(rows);
+        const int rows = w.rows, each = tree_copy_rows(rows, walk.s.share);
         for (int r0 = 0; r0 < R; r0 += 32) {
             const int in = (r0 & (each - 1)) + lane, mine = w.row0 + in;
             int64_t at = -1;   // the lane's row of q
@@ -223,12 +370,19 @@ __device__ bool q_loader(const TreeDecodeArgs& a, const Ctx<D>& c) {
             for (int i = 0; i < P; ++i) {
                 const int r = i * kPer + lane / P;
                 const int64_t from = __shfl_sync(0xffffffffu, at, r);
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(col + (r0 + r) * 128 + (((piece & 7) ^ (r & 7)) << 4)),
-                             "l"(static_cast<const __nv_bfloat16*>(a.q) + max(from, static_cast<int64_t>(0)) * D + piece * 8), "r"(from >= 0 ? 16u : 0u)
-                             : "memory");
+                const uint32_t to = col + (r0 + r) * 128 + (((piece & 7) ^ (r & 7)) << 4);
+                const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + max(from, static_cast<int64_t>(0)) * D + piece * 8;
+                if constexpr (E4M3) {   // every four elements in the order that the pages' come in
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (from >= 0) x = *reinterpret_cast<const uint4*>(src);
+                    st_shared_v4(to, __byte_perm(x.x, x.y, 0x5410), __byte_perm(x.x, x.y, 0x7632), __byte_perm(x.z, x.w, 0x5410),
+                                 __byte_perm(x.z, x.w, 0x7632));
+                } else {
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(from >= 0 ? 16u : 0u) : "memory");
+                }
             }
         }
-        asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+        if (!E4M3) asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&c.bar[c.kQFull]);
@@ -240,13 +394,14 @@ __device__ bool q_loader(const TreeDecodeArgs& a, const Ctx<D>& c) {
 // Step j of a unit: S of tile j, then, its weights being there, O += P V of tile j - 1.
 // A tile's S buffer is written again two tiles on, by this thread after the PV that
 // read it.
-template <int D>
-__device__ bool mma_issuer(const TreeDecodeArgs& a, const Ctx<D>& c, uint32_t tmem) {
-    constexpr int S = Sizes<D>::kSlots;
+template <int D, bool E4M3>
+__device__ bool mma_issuer(const TreeDecodeArgs& a, const Ctx<D, E4M3>& c, uint32_t tmem) {
+    using Z = Sizes<D, E4M3>;
+    constexpr int S = Z::kSlots;
     constexpr uint32_t kIdescS = idesc_bf16_f32(R, K, false, false), kIdescO = idesc_bf16_f32(R, D, false, true);
     const uint64_t q = sdesc_sw128(smem_u32(c.smem), 16, 1024);
-    const uint64_t k0 = sdesc_sw128(smem_u32(c.smem) + Sizes<D>::kTile, 16, 1024);
-    const uint64_t v0 = sdesc_sw128(smem_u32(c.smem) + Sizes<D>::kTile, kHalf, 1024);
+    const uint64_t k0 = sdesc_sw128(smem_u32(c.smem) + Z::kTile, 16, 1024);
+    const uint64_t v0 = sdesc_sw128(smem_u32(c.smem) + Z::kTile, kHalf, 1024);
     uint32_t g = 0, tiles = 0, u = 0;
     auto full = [&]() { return wait_w(&c.bar[c.kFull + g % S], g / S & 1, c.abort_flag, a.err); };
     TreeWalk<R> walk{a, *c.start};
@@ -258,7 +413,7 @@ __device__ bool mma_issuer(const TreeDecodeArgs& a, const Ctx<D>& c, uint32_t tm
             if (j < n) {
                 if (!full()) return false;
                 tc_fence_after();
-                const uint64_t k = k0 + (g % S) * (Sizes<D>::kTile >> 4);
+                const uint64_t k = k0 + (g % S) * (Z::kTile >> 4);
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
                     const uint64_t off = ((i >> 2) * kHalf + (i & 3) * 32) >> 4;
@@ -274,7 +429,7 @@ __device__ bool mma_issuer(const TreeDecodeArgs& a, const Ctx<D>& c, uint32_t tm
                 const uint32_t t = tiles - (j < n ? 2 : 1);   // tile j - 1
                 if (j == 1 && !wait_w(&c.bar[c.kOFree], (u & 1) ^ 1, c.abort_flag, a.err)) return false;
                 if (!full()) return false;
-                const uint64_t v = v0 + (g % S) * (Sizes<D>::kTile >> 4);
+                const uint64_t v = v0 + (g % S) * (Z::kTile >> 4);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     if (!wait_w(&c.bar[c.kPFull + (t & 1) * 2 + half], t >> 1 & 1, c.abort_flag, a.err)) return false;
@@ -400,8 +555,8 @@ __device__ __forceinline__ float weigh(RowOf& row, uint32_t ts, int c0, int key0
     return had ? f : 1.f;
 }
 
-template <int D>
-__device__ bool softmax(const TreeDecodeArgs& a, const Ctx<D>& c, uint32_t tmem, int half, int warp) {
+template <int D, bool E4M3>
+__device__ bool softmax(const TreeDecodeArgs& a, const Ctx<D, E4M3>& c, uint32_t tmem, int half, int warp) {
     const int lane = threadIdx.x & 31, r = warp * 32 + lane, G = a.Hq / a.Hkv;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     const uint32_t to = lanes + kColO + half * D;
@@ -409,7 +564,7 @@ __device__ bool softmax(const TreeDecodeArgs& a, const Ctx<D>& c, uint32_t tmem,
     TreeWalk<R> walk{a, *c.start};
     TreeWork w;
     for (uint32_t u = 0; walk.next(w); ++u) {
-        const int rows = w.rows, each = tree_copy_rows(rows);
+        const int rows = w.rows, each = tree_copy_rows(rows, walk.s.share);
         const int in = r & (each - 1), first = (warp * 32) & (each - 1);
         const bool any = first < rows;   // the warp has rows
         const int c0 = warp * 32 / each * (each / 2);   // its copy's columns, half as many as the copy has rows
@@ -452,7 +607,10 @@ __device__ bool softmax(const TreeDecodeArgs& a, const Ctx<D>& c, uint32_t tmem,
         if (!wait_w(&c.bar[c.kOFull], u & 1, c.abort_flag, a.err)) return false;
         tc_fence_after();
         if (any) {
-            float* part = a.plan.part + static_cast<size_t>(w.slot) * 2 * R * (D + 2) + half * R * D;
+            // Parts lie four dimensions of all rows together: lanes write side by side
+            // (row by row, 128 rows took 8 to 10 thousand cycles).
+            float* part = a.plan.part + static_cast<size_t>(w.slot) * kPartRows<R> * (D + 2);
+            const int at = half * R + r;
 #pragma unroll
             for (int i = 0; i < D; i += 32) {
                 uint32_t o[32];
@@ -461,9 +619,10 @@ __device__ bool softmax(const TreeDecodeArgs& a, const Ctx<D>& c, uint32_t tmem,
                 if (row.on)
 #pragma unroll
                     for (int t = 0; t < 32; t += 4)
-                        *reinterpret_cast<uint4*>(part + r * D + i + t) = make_uint4(o[t], o[t + 1], o[t + 2], o[t + 3]);
+                        reinterpret_cast<uint4*>(part)[(i + t) / 4 * kPartRows<R> + at] =
+                            E4M3 ? make_uint4(o[t], o[t + 2], o[t + 1], o[t + 3]) : make_uint4(o[t], o[t + 1], o[t + 2], o[t + 3]);
             }
-            if (row.on) reinterpret_cast<float2*>(part + (2 - half) * R * D)[half * R + r] = make_float2(row.m, row.l);
+            if (row.on) reinterpret_cast<float2*>(part + kPartRows<R> * D)[at] = make_float2(row.m, row.l);
         }
         tc_fence_before();
         mbar_arrive(&c.bar[c.kOFree]);
@@ -475,11 +634,11 @@ struct TreeMaps {
     CUtensorMap of[2];   // K's pages, V's
 };
 
-template <int D>
+template <int D, bool E4M3>
 __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_constant__ TreeDecodeArgs a, const __grid_constant__ TreeMaps maps, int box) {
     extern __shared__ uint8_t raw[];
-    using Z = Sizes<D>;
-    Ctx<D> c;
+    using Z = Sizes<D, E4M3>;
+    Ctx<D, E4M3> c;
     c.smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
     c.bar = reinterpret_cast<uint64_t*>(c.smem + Z::kOffBar);
     TreeStart* start = reinterpret_cast<TreeStart*>(c.smem + Z::kOffMisc);
@@ -519,18 +678,22 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     const uint32_t tmem = *tmem_slot;
     if (warp < 8) {
         warpgroup_reg_inc<kRegsSoftmax>();
-        softmax<D>(a, c, tmem, warp >> 2, warp & 3);
+        softmax<D, E4M3>(a, c, tmem, warp >> 2, warp & 3);
     } else {
         warpgroup_reg_dec<kRegsOther>();
         if (warp == 8) {
-            mma_issuer<D>(a, c, tmem);
+            mma_issuer<D, E4M3>(a, c, tmem);
             umma_commit_w(&c.bar[c.kDrain]);   // all that was issued
             mbar_drain(&c.bar[c.kDrain], 0);
         } else if (warp == 9) {
-            q_loader<D>(a, c);
+            q_loader<D, E4M3>(a, c);
         } else if (warp >= 12) {
-            uint32_t filled = 0;
-            if (!loader<D>(a, c, maps.of, box, warp - 12, filled)) drain<D>(c, filled);
+            if constexpr (E4M3) {
+                converter<D>(a, c, warp - 12);
+            } else {
+                uint32_t filled = 0;
+                if (!loader<D>(a, c, maps.of, box, warp - 12, filled)) drain<D>(c, filled);
+            }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     }
@@ -543,30 +706,32 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     }
 }
 
-template <int D>
+template <int D, bool E4M3>
 cudaError_t launch(const TreeDecodeArgs& a, int ctas, cudaStream_t s) {
+    using Z = Sizes<D, E4M3>;
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_dynamic_smem(tree_tc_kernel<D>, Sizes<D>::kBytes, done);
+    const cudaError_t e = allow_dynamic_smem(tree_tc_kernel<D, E4M3>, Z::kBytes, done);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = dependent_launch(ctas, kThreads, s, attr);
-    cfg.dynamicSmemBytes = Sizes<D>::kBytes;
+    cfg.dynamicSmemBytes = Z::kBytes;
     // Rows that follow one another in the pool, for a warp's copies; none in pages of
     // fewer tokens, or where a row's number does not fit a coordinate.
     const int64_t rows = static_cast<int64_t>(a.num_pages) << a.page_lg;
-    const int box = a.page_lg < 4 || rows >= (int64_t(1) << 31) ? 0 : a.page_lg == 4 ? 16 : 32;
+    const int box = E4M3 || a.page_lg < 4 || rows >= (int64_t(1) << 31) ? 0 : a.page_lg == 4 ? 16 : 32;
     TreeMaps maps;
     std::memset(&maps, 0, sizeof(maps));
     if (box && (!make_tmap_4d_bf16(&maps.of[0], a.k_pages, D, a.Hkv, rows, 1, 64, box) ||
                 !make_tmap_4d_bf16(&maps.of[1], a.v_pages, D, a.Hkv, rows, 1, 64, box)))
         return cudaErrorInvalidValue;
-    return cudaLaunchKernelEx(&cfg, tree_tc_kernel<D>, a, maps, box);
+    return cudaLaunchKernelEx(&cfg, tree_tc_kernel<D, E4M3>, a, maps, box);
 }
 
 }  // namespace
 
-cudaError_t launch_tree_tc(const TreeDecodeArgs& a, int d, int ctas, cudaStream_t s) {
-    return d == 128 ? launch<128>(a, ctas, s) : launch<64>(a, ctas, s);
+cudaError_t launch_tree_tc(const TreeDecodeArgs& a, int d, bool e4m3, int ctas, cudaStream_t s) {
+    if (e4m3) return d == 128 ? launch<128, true>(a, ctas, s) : launch<64, true>(a, ctas, s);
+    return d == 128 ? launch<128, false>(a, ctas, s) : launch<64, false>(a, ctas, s);
 }
 
 cudaError_t tree_set_wait_limit(uint64_t ns) { return set_wait_limit_of_unit(ns); }

@@ -380,7 +380,7 @@ struct TreePlan {       // in the workspace, see tree_plan.cuh
     int* order;         // [T] at first + i: the tree's token (0 .. n-1) that comes i-th
     int* lo;            // [T] the first cached key that a token reads (but for anchors)
     uint32_t* mask;     // [T][kMaxTree / 32] the tree's tokens that a token reads
-    float* part;        // [CTAs + units]: sums [kPartRows][d], then (m, l) [kPartRows]
+    float* part;        // [CTAs + units]: sums [d / 4][kPartRows][4], then (m, l) [kPartRows]
 };
 struct TreeDecodeArgs {
     const void* q;              // [T, Hq, d], bf16 or, for fp32 pages, fp32
@@ -409,7 +409,7 @@ constexpr int kTreeCtas = 2 * 152, kTreeRows = 32, kTreeKeys = 64;
 constexpr int kTreeTcCtas = 152, kTreeTcRows = 128, kTreeTcKeys = 128;
 TreeWs tree_ws_layout(int T, int B, int Hq, int Hkv, int d, int dtype);
 cudaError_t launch_decode_tree(const TreeDecodeArgs& a, int d, int page_dtype, int sms, cudaStream_t s);
-cudaError_t launch_tree_tc(const TreeDecodeArgs& a, int d, int ctas, cudaStream_t s);
+cudaError_t launch_tree_tc(const TreeDecodeArgs& a, int d, bool e4m3, int ctas, cudaStream_t s);
 cudaError_t tree_set_wait_limit(uint64_t ns);
 
 cudaError_t launch_accept(const PagingArgs& a, cudaStream_t s);
