@@ -22,9 +22,10 @@
 //   warp 8      TMEM and MMA issue (converged, elected issue)
 //   warp 9      Q: gathers a unit's rows
 //   warps 12-15 K and V: a ring of tiles in the order in which they are used (K0,
-//               K1, V0, K2, V1, ...), 32 rows of each tile a warp; e4m3 pages come
-//               through a ring of their own and are converted on the way
+//               K1, V0, K2, V1, ...), 32 rows of each tile a warp
 //   (warps 10, 11 fill up a warpgroup, the unit that registers are moved by)
+// e4m3 pages come through a ring of their own: warp 10 has them copied, warps 12-15
+// write K, warps 16-19 V as bf16 to the ring that the products read.
 // TMEM: S at [0, 128) and [128, 256), the halves' O at [256, 256 + d) and from 256 + d.
 
 #include "swiattn.h"
@@ -33,6 +34,7 @@
 
 #include <cuda_bf16.h>
 #include <math.h>
+#include <algorithm>
 #include <atomic>
 #include <cstring>
 
@@ -42,8 +44,14 @@ namespace {
 constexpr int R = kTreeTcRows, K = kTreeTcKeys;
 constexpr int kWords = kMaxTree / 32;
 constexpr int kLoaders = 4;
-constexpr int kThreads = 512;   // 4 warpgroups, launched at 128 registers a thread,
-constexpr uint32_t kRegsSoftmax = 168, kRegsOther = 88;   // of 4 * 128
+// 4 warpgroups, launched at 128 registers a thread, or 5 at 96: of these the two that
+// do the softmax take their share, 2 * 168 + 2 * 88 = 4 * 128, 2 * 144 + 3 * 64 = 5 * 96.
+template <bool E4M3>
+constexpr int kThreads = E4M3 ? 640 : 512;
+template <bool E4M3>
+constexpr uint32_t kRegsSoftmax = E4M3 ? 144 : 168;
+template <bool E4M3>
+constexpr uint32_t kRegsOther = E4M3 ? 64 : 88;
 constexpr int kHalf = R * 128;   // 128 rows of 64 bf16 columns, 128-byte swizzled
 constexpr uint32_t kTmemCols = 512;
 constexpr int kHalfKeys = K / 2;
@@ -54,10 +62,11 @@ struct Sizes {
     static constexpr int kTile = R * D * 2;                    // Q, and a slot of the ring
     static constexpr int kSlots = (E4M3 ? 3 : 6) * 128 / D;
     static constexpr int kRaw = E4M3 ? 6 * 128 / D : 0;        // tiles as they are in the pages
-    static constexpr int kBars = 2 * kSlots + 2 + 2 + 4 + 3 + 1;
+    static constexpr int kBars = 2 * kSlots + 2 + 2 + 4 + 3 + 1 + 2 * kRaw;
     static constexpr int kOffRaw = (1 + kSlots) * kTile;
-    static constexpr int kOffExp = kOffRaw + kRaw * (R * D);   // and their rows' exponent bytes
-    static constexpr int kOffBar = kOffExp + kRaw * R;
+    static constexpr int kOffExp = kOffRaw + kRaw * (R * D);   // their rows' exponent bytes,
+    static constexpr int kOffRead = kOffExp + kRaw * R;        // and, a bit a row, which are read
+    static constexpr int kOffBar = kOffRead + kRaw * (R / 8);
     static constexpr int kOffMisc = kOffBar + kBars * 8;
     static constexpr int kBytes = kOffMisc + 80 + 1024;        // and room to align
 };
@@ -75,7 +84,8 @@ struct Ctx {
     const TreeStart* start;
     static constexpr int kFull = 0, kEmpty = Z::kSlots, kQFull = 2 * Z::kSlots, kQEmpty = kQFull + 1,
                          kSFull = kQEmpty + 1, kPFull = kSFull + 2, kODone = kPFull + 4, kOFull = kODone + 1,
-                         kOFree = kOFull + 1, kDrain = kOFree + 1;
+                         kOFree = kOFull + 1, kDrain = kOFree + 1,
+                         kRawFull = kDrain + 1, kRawEmpty = kRawFull + Z::kRaw;
 };
 
 // As mbar_wait_w, but that a lowered limit, which polls, reaches waits that would end
@@ -94,25 +104,17 @@ __device__ __forceinline__ bool wait_w(uint64_t* bar, uint32_t parity, volatile 
 struct Rows {
     uint32_t row;     // lane's
     uint32_t read;    // the warp's, a bit a row
-    uint32_t exps;    // e4m3: lane's, of the key row and, 8 bits up, of the value row
 };
-template <bool E4M3>
 __device__ __forceinline__ Rows rows_of(const TreeDecodeArgs& a, const TreeWork& w, int kt, int row32) {
     const int tok = tile_key<K>(w.s, w.far, kt) + row32 + (threadIdx.x & 31);
     const bool on = tok < w.s.base + w.s.n && (w.far || tok >= w.s.lo || tok < w.s.na);
     Rows r;
     r.row = 0;
-    r.exps = 127 | 127 << 8;
     if (on) {
         const int p = a.block_table[static_cast<int64_t>(w.b) * a.max_pages + (tok >> a.page_lg)];
         const bool in = p >= 0 && p < a.num_pages;
         if (!in) atomicOr(a.err, kDevErrInput);
-        const int page = in ? p : 0, slot = tok & ((1 << a.page_lg) - 1);
-        r.row = (static_cast<uint32_t>(page) << a.page_lg) + slot;
-        if (E4M3) {
-            const int64_t at = ((static_cast<int64_t>(page) * a.Hkv + w.h) << a.page_lg) + slot;
-            r.exps = a.k_exp[at] | a.v_exp[at] << 8;
-        }
+        r.row = (static_cast<uint32_t>(in ? p : 0) << a.page_lg) + (tok & ((1 << a.page_lg) - 1));
     }
     r.read = __ballot_sync(0xffffffffu, on);
     return r;
@@ -120,7 +122,6 @@ __device__ __forceinline__ Rows rows_of(const TreeDecodeArgs& a, const TreeWork&
 
 // The tiles of the ring in their order, one by one; the next key tile's page numbers
 // are looked up while the last one's rows are copied.
-template <bool E4M3>
 struct SlotWalk {
     const TreeDecodeArgs& a;
     TreeWalk<R> walk;
@@ -135,8 +136,8 @@ struct SlotWalk {
                 if (!walk.next(w)) return false;
                 kt = w.kt0;
                 which = 0;
-                now = ahead = rows_of<E4M3>(a, w, kt, row32);
-                if (kt + 1 < w.kt1) ahead = rows_of<E4M3>(a, w, kt + 1, row32);
+                now = ahead = rows_of(a, w, kt, row32);
+                if (kt + 1 < w.kt1) ahead = rows_of(a, w, kt + 1, row32);
             }
             if (which == 0) {
                 which = 1;
@@ -153,7 +154,7 @@ struct SlotWalk {
             now = ahead;
             ++kt;
             which = kt > w.kt1 ? 2 : 0;
-            if (kt + 1 < w.kt1) ahead = rows_of<E4M3>(a, w, kt + 1, row32);
+            if (kt + 1 < w.kt1) ahead = rows_of(a, w, kt + 1, row32);
             if (v) return true;
         }
     }
@@ -213,7 +214,7 @@ __device__ bool loader(const TreeDecodeArgs& a, const Ctx<D, false>& c, const CU
             first += skip;
         }
     };
-    SlotWalk<false> slots{a, TreeWalk<R>{a, *c.start}, w32 * 32};
+    SlotWalk slots{a, TreeWalk<R>{a, *c.start}, w32 * 32};
     Rows rows;
     for (int which; slots.next(which, rows); ++g) {
         const uint32_t slot = g % S, dst = ring + slot * Z::kTile, parity = (g / S & 1) ^ 1;
@@ -242,7 +243,8 @@ __device__ bool loader(const TreeDecodeArgs& a, const Ctx<D, false>& c, const CU
     return true;
 }
 
-// Four e4m3 bytes as bf16 over 2^120: bytes 0 and 2 in lo, 1 and 3 in hi (the sign, then
+// e4m3 to bf16, exact where a bf16 reaches: powers of two from 2^-133 to below 2^128.
+// Four bytes over 2^120: bytes 0 and 2 in lo, 1 and 3 in hi (the sign, then
 // exponent and mantissa where a bf16 has its lowest ones).  0x7f comes out as 480.
 __device__ __forceinline__ void bf16_of(uint32_t w, uint32_t& lo, uint32_t& hi) {
     hi = (w & 0x80008000u) | (w >> 4 & 0x07f007f0u);
@@ -254,99 +256,211 @@ __device__ __forceinline__ uint32_t times(uint32_t x, uint32_t y) {   // two bf1
     return z;
 }
 
-// 16 e4m3 bytes of a row with exponent byte `e`, as 16 bf16 whose every four are in the
-// order 0 2 1 3 (Q's elements are laid out alike, and so come O's).  Exact where a
-// bf16 reaches: powers of two from 2^-133 to below 2^128.
-__device__ __forceinline__ void row_piece(const uint4& raw, uint32_t e, uint32_t* x) {
+// Bit 7 of every byte that is a NaN (0x7f or 0xff), and other bits.
+__device__ __forceinline__ uint32_t nans_of(uint32_t w) { return (w & 0x7f7f7f7fu) + 0x01010101u; }
+
+// 16 e4m3 bytes of a row, times `scale` (two bf16), as 16 bf16 whose every four are in
+// the order 0 2 1 3 (Q's elements are laid out alike, and so come O's).
+__device__ __forceinline__ void row_piece(const uint4& raw, uint32_t scale, uint32_t* x) {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-    // 2^(e - 127 + 120), a second factor where that is over 2^127
-    const uint32_t up = min(e + 120, 254u), scale = up << 7 | up << 23;
-    uint32_t nan = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         bf16_of(w[i], x[2 * i], x[2 * i + 1]);
         x[2 * i] = times(x[2 * i], scale);
         x[2 * i + 1] = times(x[2 * i + 1], scale);
-        nan |= (w[i] & 0x7f7f7f7fu) + 0x01010101u;
-    }
-    if (e > 134) {
-        const uint32_t more = (e - 134 + 127) << 7 | (e - 134 + 127) << 23;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = times(x[i], more);
-    }
-    if (nan & 0x80808080u) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t is = (w[i] & 0x7f7f7f7fu) + 0x01010101u & 0x80808080u;   // bit 7 of the bytes that are
-            x[2 * i] |= (is & 0x80u ? 0x7fffu : 0u) | (is & 0x800000u ? 0x7fff0000u : 0u);
-            x[2 * i + 1] |= (is & 0x8000u ? 0x7fffu : 0u) | (is & 0x80000000u ? 0x7fff0000u : 0u);
-        }
     }
 }
 
-// The same for e4m3 pages: a thread copies pieces of 16 bytes into a ring of its own,
-// kRaw - 1 tiles ahead, and once they have come writes them as bf16 to the slot.
+// What row_piece leaves out: exponent bytes over 134, whose power of two takes a second
+// factor, and NaN.
+__device__ __noinline__ void row_piece_rest(const uint4& raw, uint32_t e, uint32_t* x) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    const uint32_t more = e > 134 ? e - 134 + 127 : 127;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = times(x[2 * i], more << 7 | more << 23);
+        x[2 * i + 1] = times(x[2 * i + 1], more << 7 | more << 23);
+        const uint32_t is = nans_of(w[i]);
+        x[2 * i] |= (is & 0x80u ? 0x7fffu : 0u) | (is & 0x800000u ? 0x7fff0000u : 0u);
+        x[2 * i + 1] |= (is & 0x8000u ? 0x7fffu : 0u) | (is & 0x80000000u ? 0x7fff0000u : 0u);
+    }
+}
+
+// The ring of tiles as they are in e4m3 pages: rows of D bytes, their 16-byte pieces
+// swizzled as a tile copy of that width leaves them.
 template <int D>
-__device__ bool converter(const TreeDecodeArgs& a, const Ctx<D, true>& c, int w32) {
+__device__ __forceinline__ int raw_piece(int row, int piece) {
+    return row * D + ((D == 128 ? piece ^ (row & 7) : piece ^ ((row >> 1) & 3)) << 4);
+}
+
+// Fills it, one warp, tile by tile: by TMA and bulk copies `box` rows at a time where a
+// page holds 16 rows or more, else row by row.  Boxes of which no row is read are left
+// as they were.
+template <int D>
+__device__ bool raw_loader(const TreeDecodeArgs& a, const Ctx<D, true>& c, const CUtensorMap* maps, int box, uint32_t& g) {
+    using Z = Sizes<D, true>;
+    const int lane = threadIdx.x & 31;
+    const uint32_t ring = smem_u32(c.smem) + Z::kOffRaw;
+    uint8_t* exps = c.smem + Z::kOffExp;
+    uint32_t* read = reinterpret_cast<uint32_t*>(c.smem + Z::kOffRead);
+    const int mask = (1 << a.page_lg) - 1;
+    TreeWalk<R> walk{a, *c.start};
+    TreeWork w;
+    while (walk.next(w)) {
+        const int len = w.s.base + w.s.n, n = w.kt1 - w.kt0;
+        // Page of a token of the tile, or -1 where it is not read.
+        auto page_of = [&](int tok, bool on) {
+            int p = -1;
+            if (on) {
+                p = a.block_table[static_cast<int64_t>(w.b) * a.max_pages + (tok >> a.page_lg)];
+                if (p < 0 || p >= a.num_pages) {
+                    p = 0;
+                    atomicOr(a.err, kDevErrInput);
+                }
+            }
+            return p;
+        };
+        auto is_read = [&](int tok) { return tok < len && (w.far || tok >= w.s.lo || tok < w.s.na); };
+        // Lane i looks up the page of box i of key tile kt.
+        auto box_page = [&](int kt) {
+            const int tok = tile_key<K>(w.s, w.far, kt) + lane * box;
+            bool on = false;   // any of its rows
+            if (kt < w.kt1 && lane * box < K) on = tok < len && (w.far || tok + box > w.s.lo || tok < w.s.na);
+            return page_of(min(tok, len - 1), on);
+        };
+        int before = -1, now = box ? box_page(w.kt0) : 0, ahead = -1;
+        for (int j = 0; j <= n; ++j) {
+            if (box) ahead = box_page(w.kt0 + j + 1);
+#pragma unroll 1
+            for (int which = 0; which < 2; ++which) {
+                if (which == 0 ? j == n : j == 0) continue;
+                const int key0 = tile_key<K>(w.s, w.far, w.kt0 + j - which), slot = g % Z::kRaw;
+                const uint32_t dst = ring + slot * (R * D);
+                uint64_t* full = &c.bar[c.kRawFull + slot];
+                if (!wait_w(&c.bar[c.kRawEmpty + slot], (g / Z::kRaw & 1) ^ 1, c.abort_flag, a.err)) return false;
+#pragma unroll
+                for (int i = 0; i < R / 32; ++i) {
+                    const uint32_t bits = __ballot_sync(0xffffffffu, is_read(key0 + i * 32 + lane));
+                    if (lane == 0) read[slot * (R / 32) + i] = bits;
+                }
+                const uint8_t* from = which ? a.v_exp : a.k_exp;
+                if (box) {
+                    const int page = which ? before : now;
+                    const unsigned boxes = __ballot_sync(0xffffffffu, page >= 0);
+                    if (lane == 0) mbar_arrive_expect_tx(full, __popc(boxes) * box * (D + 1));
+                    __syncwarp();
+                    if (page >= 0) {
+                        const int slot_at = (key0 + lane * box) & mask;
+                        tma_load_3d(dst + lane * box * D, maps + which, full, w.h * D, slot_at, page);
+                        bulk_load(smem_u32(exps + slot * R) + lane * box, from + (((static_cast<int64_t>(page) * a.Hkv + w.h) << a.page_lg) + slot_at), box, full);
+                    }
+                } else {
+                    const uint8_t* pages = static_cast<const uint8_t*>(which ? a.v_pages : a.k_pages);
+#pragma unroll 1
+                    for (int r = lane; r < R; r += 32) {
+                        const int tok = key0 + r;
+                        const int page = page_of(tok, is_read(tok));
+                        if (page < 0) continue;
+                        const int64_t row = ((static_cast<int64_t>(page) << a.page_lg) + (tok & mask)) * a.Hkv + w.h;
+                        exps[slot * R + r] = from[((static_cast<int64_t>(page) * a.Hkv + w.h) << a.page_lg) + (tok & mask)];
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i)
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + raw_piece<D>(r, i)), "l"(pages + row * D + i * 16) : "memory");
+                    }
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(full)) : "memory");
+                    mbar_arrive(full);
+                }
+                ++g;
+            }
+            before = now;
+            now = ahead;
+        }
+    }
+    return true;
+}
+
+// From that ring to the products': four warps K's tiles, four V's, 32 rows a warp.
+template <int D>
+__device__ bool converter(const TreeDecodeArgs& a, const Ctx<D, true>& c, int which, int w32) {
     using Z = Sizes<D, true>;
     constexpr int S = Z::kSlots, P = D / 16, kPer = 32 / P;   // pieces of a row; rows at a time
     const int lane = threadIdx.x & 31, piece = lane % P, line = lane / P;
-    const uint32_t raw = smem_u32(c.smem) + Z::kOffRaw + w32 * 32 * D + lane * 16;
-    uint8_t* exps = c.smem + Z::kOffExp + w32 * 32;
+    const uint32_t ring = smem_u32(c.smem) + Z::kOffRaw;
+    const uint8_t* exps = c.smem + Z::kOffExp + w32 * 32;
+    const uint32_t* read = reinterpret_cast<const uint32_t*>(c.smem + Z::kOffRead) + w32;
     // A piece becomes two of its row's 16-byte pieces; lanes of the second 64 columns
     // begin with the second, so that eight lanes write to all banks.
     const uint32_t col = smem_u32(c.smem) + Z::kTile + w32 * 32 * 128 + (piece >> 2) * kHalf;
-    const int first = 2 * (piece & 3) + (piece >> 2), second = first ^ 1;
-    const size_t step = static_cast<size_t>(a.Hkv) * D;
-    const uint32_t total = static_cast<uint32_t>(2 * (c.start->end - c.start->at));
-    SlotWalk<true> slots{a, TreeWalk<R>{a, *c.start}, w32 * 32};
-    Rows rows;
-    for (uint32_t g = 0; g < total + Z::kRaw - 1; ++g) {
-        int which;
-        if (g < total && slots.next(which, rows)) {
-            const uint32_t slot = g % Z::kRaw;
-            const char* src = static_cast<const char*>(which ? a.v_pages : a.k_pages) + static_cast<size_t>(slots.w.h) * D + piece * 16;
+    const int odd = piece >> 2, first = 2 * (piece & 3) + odd, second = first ^ 1;
+    uint32_t g0 = 0;   // slots of the units before
+    TreeWalk<R> walk{a, *c.start};
+    TreeWork w;
+    while (walk.next(w)) {
+        const int n = w.kt1 - w.kt0;
+        for (int j = 0; j < n; ++j) {
+            const uint32_t g = g0 + (which ? (j < n - 1 ? 2 * j + 2 : 2 * j + 1) : j ? 2 * j - 1 : 0);
+            const uint32_t slot = g % S, from = g % Z::kRaw;
+            if (!wait_w(&c.bar[c.kRawFull + from], g / Z::kRaw & 1, c.abort_flag, a.err)) return false;
+            if (!wait_w(&c.bar[c.kEmpty + slot], (g / S & 1) ^ 1, c.abort_flag, a.err)) return false;
+            const uint32_t bits = read[from * (R / 32)], dst = col + slot * Z::kTile, raw = ring + from * (R * D);
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const int r = i * kPer + line;
-                const uint32_t row = __shfl_sync(0xffffffffu, rows.row, r);
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(raw + slot * (R * D) + i * 512), "l"(src + row * step),
-                             "r"(rows.read >> r & 1 ? 16u : 0u)
-                             : "memory");
+            for (int i0 = 0; i0 < P; i0 += 4) {   // four at a time, loads first
+                uint2 lo[4], hi[4];
+                uint32_t e[4];
+                uint32_t nan = 0, large = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = (i0 + i) * kPer + line;
+                    const uint32_t at = raw + raw_piece<D>(w32 * 32 + r, piece);
+                    lo[i] = ld_shared_v2(at + odd * 8);
+                    hi[i] = ld_shared_v2(at + (odd ^ 1) * 8);
+                    e[i] = exps[from * R + r];
+                }
+                if (bits != 0xffffffffu) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (!(bits >> ((i0 + i) * kPer + line) & 1)) {
+                            lo[i] = hi[i] = make_uint2(0, 0);
+                            e[i] = 127;
+                        }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    nan |= nans_of(lo[i].x) | nans_of(lo[i].y) | nans_of(hi[i].x) | nans_of(hi[i].y);
+                    large = max(large, e[i]);
+                }
+                const bool rest = large > 134 || (nan & 0x80808080u);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = (i0 + i) * kPer + line;
+                    const uint4 bytes = make_uint4(lo[i].x, lo[i].y, hi[i].x, hi[i].y);
+                    const uint32_t up = min(e[i] + 120, 254u);   // 2^(e - 127 + 120)
+                    uint32_t x[8];
+                    row_piece(bytes, up << 7 | up << 23, x);
+                    if (rest) row_piece_rest(bytes, e[i], x);
+                    const uint32_t to = dst + r * 128;
+                    st_shared_v4(to + ((first ^ (r & 7)) << 4), x[0], x[1], x[2], x[3]);
+                    st_shared_v4(to + ((second ^ (r & 7)) << 4), x[4], x[5], x[6], x[7]);
+                }
             }
-            exps[slot * R + lane] = static_cast<uint8_t>(rows.exps >> (8 * which));
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&c.bar[c.kFull + slot]);
+                mbar_arrive(&c.bar[c.kRawEmpty + from]);
+            }
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        if (g < Z::kRaw - 1) continue;
-        const uint32_t t = g - (Z::kRaw - 1), slot = t % S, from = t % Z::kRaw;
-        asm volatile("cp.async.wait_group %0;" ::"n"(Z::kRaw - 1) : "memory");
-        if (!wait_w(&c.bar[c.kEmpty + slot], (t / S & 1) ^ 1, c.abort_flag, a.err)) return false;
-        __syncwarp();   // the exponents are other lanes'
-        const uint32_t dst = col + slot * Z::kTile;
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const int r = i * kPer + line;
-            uint32_t x[8];
-            row_piece(ld_shared_v4(raw + from * (R * D) + i * 512), exps[from * R + r], x);
-            const uint32_t to = dst + r * 128;
-            const bool swap = first & 1;
-            st_shared_v4(to + ((first ^ (r & 7)) << 4), swap ? x[4] : x[0], swap ? x[5] : x[1], swap ? x[6] : x[2], swap ? x[7] : x[3]);
-            st_shared_v4(to + ((second ^ (r & 7)) << 4), swap ? x[0] : x[4], swap ? x[1] : x[5], swap ? x[2] : x[6], swap ? x[3] : x[7]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();   // and the ring's tile and exponents have been read
-        if (lane == 0) mbar_arrive(&c.bar[c.kFull + slot]);
+        g0 += 2 * n;
     }
     return true;
 }
 
 // The copies in flight of a call that gave up.
-template <int D>
-__device__ void drain(const Ctx<D, false>& c, uint32_t filled) {
-    constexpr int S = Sizes<D, false>::kSlots;
+template <int S>
+__device__ void drain(uint64_t* full, uint32_t filled) {
     for (uint32_t back = 1; back <= S && back <= filled; ++back) {
         const uint32_t g = filled - back;
-        mbar_drain(&c.bar[c.kFull + g % S], g / S & 1);
+        mbar_drain(&full[g % S], g / S & 1);
     }
 }
 
@@ -635,7 +749,7 @@ struct TreeMaps {
 };
 
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_constant__ TreeDecodeArgs a, const __grid_constant__ TreeMaps maps, int box) {
+__global__ void __launch_bounds__(kThreads<E4M3>, 1) tree_tc_kernel(const __grid_constant__ TreeDecodeArgs a, const __grid_constant__ TreeMaps maps, int box) {
     extern __shared__ uint8_t raw[];
     using Z = Sizes<D, E4M3>;
     Ctx<D, E4M3> c;
@@ -659,6 +773,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         mbar_init(&c.bar[c.kOFull], 1);
         mbar_init(&c.bar[c.kOFree], 2 * R);
         mbar_init(&c.bar[c.kDrain], 1);
+        for (int i = 0; i < Z::kRaw; ++i) {
+            mbar_init(&c.bar[c.kRawFull + i], box ? 1 : 64);
+            mbar_init(&c.bar[c.kRawEmpty + i], kLoaders);
+        }
         *c.abort_flag = 0;
         fence_barrier_init();
     }
@@ -677,10 +795,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     if (warp < 8) {
-        warpgroup_reg_inc<kRegsSoftmax>();
+        warpgroup_reg_inc<kRegsSoftmax<E4M3>>();
         softmax<D, E4M3>(a, c, tmem, warp >> 2, warp & 3);
     } else {
-        warpgroup_reg_dec<kRegsOther>();
+        warpgroup_reg_dec<kRegsOther<E4M3>>();
         if (warp == 8) {
             mma_issuer<D, E4M3>(a, c, tmem);
             umma_commit_w(&c.bar[c.kDrain]);   // all that was issued
@@ -689,10 +807,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
             q_loader<D, E4M3>(a, c);
         } else if (warp >= 12) {
             if constexpr (E4M3) {
-                converter<D>(a, c, warp - 12);
+                converter<D>(a, c, (warp - 12) / kLoaders, (warp - 12) % kLoaders);
             } else {
                 uint32_t filled = 0;
-                if (!loader<D>(a, c, maps.of, box, warp - 12, filled)) drain<D>(c, filled);
+                if (!loader<D>(a, c, maps.of, box, warp - 12, filled)) drain<Z::kSlots>(&c.bar[c.kFull], filled);
+            }
+        } else if (E4M3 && warp == 10) {
+            if constexpr (E4M3) {
+                uint32_t filled = 0;
+                if (!raw_loader<D>(a, c, maps.of, box, filled)) drain<Z::kRaw>(&c.bar[c.kRawFull], filled);
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -713,17 +836,21 @@ cudaError_t launch(const TreeDecodeArgs& a, int ctas, cudaStream_t s) {
     const cudaError_t e = allow_dynamic_smem(tree_tc_kernel<D, E4M3>, Z::kBytes, done);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t cfg = dependent_launch(ctas, kThreads, s, attr);
+    cudaLaunchConfig_t cfg = dependent_launch(ctas, kThreads<E4M3>, s, attr);
     cfg.dynamicSmemBytes = Z::kBytes;
-    // Rows that follow one another in the pool, for a warp's copies; none in pages of
-    // fewer tokens, or where a row's number does not fit a coordinate.
+    // Rows that a copy takes, by what pages hold; none in pages of fewer than 16, or
+    // (bf16) where a row's number in the pool does not fit a coordinate.
     const int64_t rows = static_cast<int64_t>(a.num_pages) << a.page_lg;
-    const int box = E4M3 || a.page_lg < 4 || rows >= (int64_t(1) << 31) ? 0 : a.page_lg == 4 ? 16 : 32;
+    int box = a.page_lg < 4 || (!E4M3 && rows >= (int64_t(1) << 31)) ? 0 : std::min(1 << a.page_lg, E4M3 ? K : 32);
     TreeMaps maps;
     std::memset(&maps, 0, sizeof(maps));
-    if (box && (!make_tmap_4d_bf16(&maps.of[0], a.k_pages, D, a.Hkv, rows, 1, 64, box) ||
-                !make_tmap_4d_bf16(&maps.of[1], a.v_pages, D, a.Hkv, rows, 1, 64, box)))
-        return cudaErrorInvalidValue;
+    if (box) {
+        const void* pages[2] = {a.k_pages, a.v_pages};
+        for (int i = 0; i < 2; ++i)
+            if (!(E4M3 ? make_tmap_pages_u8(&maps.of[i], pages[i], static_cast<uint64_t>(a.Hkv) * D, 1ull << a.page_lg, a.num_pages, D, box)
+                       : make_tmap_4d_bf16(&maps.of[i], pages[i], D, a.Hkv, rows, 1, 64, box)))
+                return cudaErrorInvalidValue;
+    }
     return cudaLaunchKernelEx(&cfg, tree_tc_kernel<D, E4M3>, a, maps, box);
 }
 

@@ -1062,6 +1062,7 @@ int swiattn_decode_tree(const void* q, const void* k_pages, const void* v_pages,
                                page_size, num_pages, Hkv, d, page_dtype);
     if (ok == SWIATTN_EINVAL || pools == SWIATTN_EINVAL || W <= 0 || n_anchor < 0) return SWIATTN_EINVAL;
     if (page_dtype != dtype && page_dtype != SWIATTN_E4M3) return SWIATTN_EINVAL;
+    if (page_dtype == SWIATTN_E4M3 && (!aligned16(k_exp) || !aligned16(v_exp))) return SWIATTN_EINVAL;
     if (!(scale > 0.f) || !(scale - scale == 0.f)) return SWIATTN_EINVAL;
     if (!starts) return SWIATTN_EINVAL;
     if (ok != SWIATTN_OK || (page_dtype == SWIATTN_E4M3 && dtype != SWIATTN_BF16)) return SWIATTN_EUNSUPPORTED;

@@ -93,7 +93,8 @@ def test_decode_tree_refusals_and_workspace(lib):
                 dict(o=None), dict(q=ODD), dict(o=ODD), dict(kp=ODD), dict(vps=ODD), dict(T=-1), dict(B=0), dict(mp=0),
                 dict(ps=24), dict(np_=0), dict(Hq=9), dict(Hkv=-2), dict(d=32), dict(W=0), dict(S=-1), dict(scale=0.0),
                 dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(dt=E4M3), dict(dt=F32),
-                dict(pdt=F32), dict(pdt=7), dict(pdt=E4M3, ke=None), dict(pdt=E4M3, ve=None), dict(ws=None), dict(ws=ODD),
+                dict(pdt=F32), dict(pdt=7), dict(pdt=E4M3, ke=None), dict(pdt=E4M3, ve=None), dict(pdt=E4M3, ke=ODD),
+                dict(pdt=E4M3, ve=ODD), dict(ws=None), dict(ws=ODD),
                 dict(nbytes=size() - 1), dict(ps=1 << 20, mp=1 << 12)):
         assert call(**bad) == EINVAL, bad
     for bad in (dict(Hq=258), dict(B=1 << 16), dict(dt=F32, pdt=E4M3), dict(np_=1 << 30)):
