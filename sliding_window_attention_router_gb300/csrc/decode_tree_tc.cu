@@ -271,18 +271,16 @@ __device__ __forceinline__ void row_piece(const uint4& raw, uint32_t scale, uint
     }
 }
 
-// What row_piece leaves out: exponent bytes over 134, whose power of two takes a second
-// factor, and NaN.
-__device__ __noinline__ void row_piece_rest(const uint4& raw, uint32_t e, uint32_t* x) {
+// For any exponent byte: over 134 its power of two takes a second factor; and NaN.
+__device__ __forceinline__ void row_piece_rest(const uint4& raw, uint32_t e, uint32_t* x) {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
     const uint32_t more = e > 134 ? e - 134 + 127 : 127;
+    row_piece(raw, min(e + 120, 254u) * 0x00800080u, x);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        x[2 * i] = times(x[2 * i], more << 7 | more << 23);
-        x[2 * i + 1] = times(x[2 * i + 1], more << 7 | more << 23);
         const uint32_t is = nans_of(w[i]);
-        x[2 * i] |= (is & 0x80u ? 0x7fffu : 0u) | (is & 0x800000u ? 0x7fff0000u : 0u);
-        x[2 * i + 1] |= (is & 0x8000u ? 0x7fffu : 0u) | (is & 0x80000000u ? 0x7fff0000u : 0u);
+        x[2 * i] = times(x[2 * i], more * 0x00800080u) | (is & 0x80u ? 0x7fffu : 0u) | (is & 0x800000u ? 0x7fff0000u : 0u);
+        x[2 * i + 1] = times(x[2 * i + 1], more * 0x00800080u) | (is & 0x8000u ? 0x7fffu : 0u) | (is & 0x80000000u ? 0x7fff0000u : 0u);
     }
 }
 
@@ -403,44 +401,41 @@ __device__ bool converter(const TreeDecodeArgs& a, const Ctx<D, true>& c, int wh
             if (!wait_w(&c.bar[c.kRawFull + from], g / Z::kRaw & 1, c.abort_flag, a.err)) return false;
             if (!wait_w(&c.bar[c.kEmpty + slot], (g / S & 1) ^ 1, c.abort_flag, a.err)) return false;
             const uint32_t bits = read[from * (R / 32)], dst = col + slot * Z::kTile, raw = ring + from * (R * D);
-#pragma unroll
+            uint32_t nan = 0, large = 0;
+#pragma unroll 1
             for (int i0 = 0; i0 < P; i0 += 4) {   // four at a time, loads first
-                uint2 lo[4], hi[4];
+                uint4 bytes[4];
                 uint32_t e[4];
-                uint32_t nan = 0, large = 0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int r = (i0 + i) * kPer + line;
-                    const uint32_t at = raw + raw_piece<D>(w32 * 32 + r, piece);
-                    lo[i] = ld_shared_v2(at + odd * 8);
-                    hi[i] = ld_shared_v2(at + (odd ^ 1) * 8);
+                    bytes[i] = ld_shared_v4(raw + raw_piece<D>(w32 * 32 + r, piece));
                     e[i] = exps[from * R + r];
                 }
-                if (bits != 0xffffffffu) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (!(bits >> ((i0 + i) * kPer + line) & 1)) {
-                            lo[i] = hi[i] = make_uint2(0, 0);
-                            e[i] = 127;
-                        }
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    nan |= nans_of(lo[i].x) | nans_of(lo[i].y) | nans_of(hi[i].x) | nans_of(hi[i].y);
-                    large = max(large, e[i]);
-                }
-                const bool rest = large > 134 || (nan & 0x80808080u);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int r = (i0 + i) * kPer + line;
-                    const uint4 bytes = make_uint4(lo[i].x, lo[i].y, hi[i].x, hi[i].y);
-                    const uint32_t up = min(e[i] + 120, 254u);   // 2^(e - 127 + 120)
+                    nan |= nans_of(bytes[i].x) | nans_of(bytes[i].y) | nans_of(bytes[i].z) | nans_of(bytes[i].w);
+                    large = max(large, e[i]);
+                    const uint4 turned = odd ? make_uint4(bytes[i].z, bytes[i].w, bytes[i].x, bytes[i].y) : bytes[i];
                     uint32_t x[8];
-                    row_piece(bytes, up << 7 | up << 23, x);
-                    if (rest) row_piece_rest(bytes, e[i], x);
-                    const uint32_t to = dst + r * 128;
-                    st_shared_v4(to + ((first ^ (r & 7)) << 4), x[0], x[1], x[2], x[3]);
-                    st_shared_v4(to + ((second ^ (r & 7)) << 4), x[4], x[5], x[6], x[7]);
+                    row_piece(turned, (e[i] + 120) * 0x00800080u, x);   // 2^(e - 127 + 120)
+                    st_shared_v4(dst + r * 128 + ((first ^ (r & 7)) << 4), x[0], x[1], x[2], x[3]);
+                    st_shared_v4(dst + r * 128 + ((second ^ (r & 7)) << 4), x[4], x[5], x[6], x[7]);
+                }
+            }
+            if (bits != 0xffffffffu || large > 134 || (nan & 0x80808080u)) {
+                // Once more, with what that leaves out.
+#pragma unroll 1
+                for (int i = 0; i < P; ++i) {
+                    const int r = i * kPer + line;
+                    const bool on = bits >> r & 1;
+                    uint4 bytes = ld_shared_v4(raw + raw_piece<D>(w32 * 32 + r, piece));
+                    if (!on) bytes = make_uint4(0, 0, 0, 0);
+                    uint32_t x[8];
+                    row_piece_rest(bytes, on ? exps[from * R + r] : 127u, x);
+                    st_shared_v4(dst + r * 128 + (((first & ~1) ^ (r & 7)) << 4), x[0], x[1], x[2], x[3]);
+                    st_shared_v4(dst + r * 128 + (((first | 1) ^ (r & 7)) << 4), x[4], x[5], x[6], x[7]);
                 }
             }
             fence_proxy_async_smem();
@@ -641,17 +636,21 @@ __device__ __forceinline__ float weigh(RowOf& row, uint32_t ts, int c0, int key0
     float2 sum[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) sum[t] = make_float2(0.f, 0.f);
-    uint32_t hi[N / 2], rest[N / 2];
+    constexpr int kAt = N < 32 ? N : 32;   // columns at a time
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-        const float2 x = ffma2(make_float2(s[2 * i], s[2 * i + 1]), sl2, off);
-        const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-        sum[i & 3] = fadd2(sum[i & 3], p);
-        hi[i] = pack_bf16x2(p.x, p.y);
-        rest[i] = pack_bf16x2(p.x - __uint_as_float(hi[i] << 16), p.y - __uint_as_float(hi[i] & 0xffff0000u));
+    for (int at = 0; at < N; at += kAt) {
+        uint32_t hi[kAt / 2], rest[kAt / 2];
+#pragma unroll
+        for (int i = 0; i < kAt / 2; ++i) {
+            const float2 x = ffma2(make_float2(s[at + 2 * i], s[at + 2 * i + 1]), sl2, off);
+            const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            sum[i & 3] = fadd2(sum[i & 3], p);
+            hi[i] = pack_bf16x2(p.x, p.y);
+            rest[i] = pack_bf16x2(p.x - __uint_as_float(hi[i] << 16), p.y - __uint_as_float(hi[i] & 0xffff0000u));
+        }
+        tmem_st<kAt / 2>(ts + (c0 + at) / 2, hi);
+        tmem_st<kAt / 2>(ts + kHalfKeys / 2 + (c0 + at) / 2, rest);
     }
-    tmem_st<N / 2>(ts + c0 / 2, hi);
-    tmem_st<N / 2>(ts + kHalfKeys / 2 + c0 / 2, rest);
     if constexpr (N < kHalfKeys) {
         uint32_t zero[N / 2];
 #pragma unroll
