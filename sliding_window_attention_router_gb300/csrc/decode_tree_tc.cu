@@ -377,19 +377,22 @@ __device__ bool raw_loader(const TreeDecodeArgs& a, const Ctx<D, true>& c, const
     return true;
 }
 
-// From that ring to the products': four warps K's tiles, four V's, 32 rows a warp.
+// From that ring to the products': four warps K's tiles, four V's, 32 rows a warp.  The
+// conversion is bound by the integer pipe (a warp's instruction takes it two cycles),
+// so its addresses are constants: a lane has one row a of every eight and one of four
+// pieces of half a row.  Eight lanes hold rows a and a ^ 5, whose pieces differ in
+// their banks both in the pages' layout and, two for one, in the products'.
 template <int D>
 __device__ bool converter(const TreeDecodeArgs& a, const Ctx<D, true>& c, int which, int w32) {
     using Z = Sizes<D, true>;
-    constexpr int S = Z::kSlots, P = D / 16, kPer = 32 / P;   // pieces of a row; rows at a time
-    const int lane = threadIdx.x & 31, piece = lane % P, line = lane / P;
-    const uint32_t ring = smem_u32(c.smem) + Z::kOffRaw;
-    const uint8_t* exps = c.smem + Z::kOffExp + w32 * 32;
+    constexpr int S = Z::kSlots, kHalves = D / 64;
+    const int lane = threadIdx.x & 31, quarter = lane & 3, row = (lane >> 3) ^ (lane & 4 ? 5 : 0);
+    const uint32_t raw0 = smem_u32(c.smem) + Z::kOffRaw + raw_piece<D>(w32 * 32 + row, quarter);
+    const uint32_t raw1 = smem_u32(c.smem) + Z::kOffRaw + raw_piece<D>(w32 * 32 + row, quarter + (D == 128 ? 4 : 0));
+    const uint32_t to = smem_u32(c.smem) + Z::kTile + (w32 * 32 + row) * 128;
+    const uint32_t to0 = to + ((2 * quarter ^ row) << 4), to1 = to + (((2 * quarter + 1) ^ row) << 4);
+    const uint8_t* exps = c.smem + Z::kOffExp + w32 * 32 + row;
     const uint32_t* read = reinterpret_cast<const uint32_t*>(c.smem + Z::kOffRead) + w32;
-    // A piece becomes two of its row's 16-byte pieces; lanes of the second 64 columns
-    // begin with the second, so that eight lanes write to all banks.
-    const uint32_t col = smem_u32(c.smem) + Z::kTile + w32 * 32 * 128 + (piece >> 2) * kHalf;
-    const int odd = piece >> 2, first = 2 * (piece & 3) + odd, second = first ^ 1;
     uint32_t g0 = 0;   // slots of the units before
     TreeWalk<R> walk{a, *c.start};
     TreeWork w;
@@ -400,42 +403,39 @@ __device__ bool converter(const TreeDecodeArgs& a, const Ctx<D, true>& c, int wh
             const uint32_t slot = g % S, from = g % Z::kRaw;
             if (!wait_w(&c.bar[c.kRawFull + from], g / Z::kRaw & 1, c.abort_flag, a.err)) return false;
             if (!wait_w(&c.bar[c.kEmpty + slot], (g / S & 1) ^ 1, c.abort_flag, a.err)) return false;
-            const uint32_t bits = read[from * (R / 32)], dst = col + slot * Z::kTile, raw = ring + from * (R * D);
+            const uint32_t bits = read[from * (R / 32)], in = from * (R * D), out = slot * Z::kTile;
             uint32_t nan = 0, large = 0;
-#pragma unroll 1
-            for (int i0 = 0; i0 < P; i0 += 4) {   // four at a time, loads first
-                uint4 bytes[4];
+#pragma unroll
+            for (int half = 0; half < kHalves; ++half) {
+                uint4 x4[4];   // four rows, eight apart: loads first
                 uint32_t e[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int r = (i0 + i) * kPer + line;
-                    bytes[i] = ld_shared_v4(raw + raw_piece<D>(w32 * 32 + r, piece));
-                    e[i] = exps[from * R + r];
+                    x4[i] = ld_shared_v4((half ? raw1 : raw0) + in + i * (8 * D));
+                    e[i] = exps[from * R + i * 8];
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int r = (i0 + i) * kPer + line;
-                    nan |= nans_of(bytes[i].x) | nans_of(bytes[i].y) | nans_of(bytes[i].z) | nans_of(bytes[i].w);
+                    nan |= nans_of(x4[i].x) | nans_of(x4[i].y) | nans_of(x4[i].z) | nans_of(x4[i].w);
                     large = max(large, e[i]);
-                    const uint4 turned = odd ? make_uint4(bytes[i].z, bytes[i].w, bytes[i].x, bytes[i].y) : bytes[i];
                     uint32_t x[8];
-                    row_piece(turned, (e[i] + 120) * 0x00800080u, x);   // 2^(e - 127 + 120)
-                    st_shared_v4(dst + r * 128 + ((first ^ (r & 7)) << 4), x[0], x[1], x[2], x[3]);
-                    st_shared_v4(dst + r * 128 + ((second ^ (r & 7)) << 4), x[4], x[5], x[6], x[7]);
+                    row_piece(x4[i], (e[i] + 120) * 0x00800080u, x);   // 2^(e - 127 + 120)
+                    st_shared_v4(to0 + out + half * kHalf + i * 1024, x[0], x[1], x[2], x[3]);
+                    st_shared_v4(to1 + out + half * kHalf + i * 1024, x[4], x[5], x[6], x[7]);
                 }
             }
             if (bits != 0xffffffffu || large > 134 || (nan & 0x80808080u)) {
                 // Once more, with what that leaves out.
 #pragma unroll 1
-                for (int i = 0; i < P; ++i) {
-                    const int r = i * kPer + line;
-                    const bool on = bits >> r & 1;
-                    uint4 bytes = ld_shared_v4(raw + raw_piece<D>(w32 * 32 + r, piece));
+                for (int i = 0; i < 4 * kHalves; ++i) {
+                    const int half = i >> 2, at = i & 3;
+                    const bool on = bits >> (row + at * 8) & 1;
+                    uint4 bytes = ld_shared_v4((half ? raw1 : raw0) + in + at * (8 * D));
                     if (!on) bytes = make_uint4(0, 0, 0, 0);
                     uint32_t x[8];
-                    row_piece_rest(bytes, on ? exps[from * R + r] : 127u, x);
-                    st_shared_v4(dst + r * 128 + (((first & ~1) ^ (r & 7)) << 4), x[0], x[1], x[2], x[3]);
-                    st_shared_v4(dst + r * 128 + (((first | 1) ^ (r & 7)) << 4), x[4], x[5], x[6], x[7]);
+                    row_piece_rest(bytes, on ? exps[from * R + at * 8] : 127u, x);
+                    st_shared_v4(to0 + out + half * kHalf + at * 1024, x[0], x[1], x[2], x[3]);
+                    st_shared_v4(to1 + out + half * kHalf + at * 1024, x[4], x[5], x[6], x[7]);
                 }
             }
             fence_proxy_async_smem();
