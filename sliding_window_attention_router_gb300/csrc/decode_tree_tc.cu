@@ -405,23 +405,24 @@ __device__ bool converter(const TreeDecodeArgs& a, const Ctx<D, true>& c, int wh
             if (!wait_w(&c.bar[c.kEmpty + slot], (g / S & 1) ^ 1, c.abort_flag, a.err)) return false;
             const uint32_t bits = read[from * (R / 32)], in = from * (R * D), out = slot * Z::kTile;
             uint32_t nan = 0, large = 0;
+#pragma unroll 1
+            for (int i = 0; i < 2 * kHalves; ++i) {   // two rows, eight apart: loads first
+                const uint32_t from_row = in + (i & 1) * (16 * D), to_row = out + (i >> 1) * kHalf + (i & 1) * 2048;
+                uint4 x4[2];
+                uint32_t e[2];
 #pragma unroll
-            for (int half = 0; half < kHalves; ++half) {
-                uint4 x4[4];   // four rows, eight apart: loads first
-                uint32_t e[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x4[i] = ld_shared_v4((half ? raw1 : raw0) + in + i * (8 * D));
-                    e[i] = exps[from * R + i * 8];
+                for (int k = 0; k < 2; ++k) {
+                    x4[k] = ld_shared_v4((i >> 1 ? raw1 : raw0) + from_row + k * (8 * D));
+                    e[k] = exps[from * R + (i & 1) * 16 + k * 8];
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    nan |= nans_of(x4[i].x) | nans_of(x4[i].y) | nans_of(x4[i].z) | nans_of(x4[i].w);
-                    large = max(large, e[i]);
+                for (int k = 0; k < 2; ++k) {
+                    nan |= nans_of(x4[k].x) | nans_of(x4[k].y) | nans_of(x4[k].z) | nans_of(x4[k].w);
+                    large = max(large, e[k]);
                     uint32_t x[8];
-                    row_piece(x4[i], (e[i] + 120) * 0x00800080u, x);   // 2^(e - 127 + 120)
-                    st_shared_v4(to0 + out + half * kHalf + i * 1024, x[0], x[1], x[2], x[3]);
-                    st_shared_v4(to1 + out + half * kHalf + i * 1024, x[4], x[5], x[6], x[7]);
+                    row_piece(x4[k], (e[k] + 120) * 0x00800080u, x);   // 2^(e - 127 + 120)
+                    st_shared_v4(to0 + to_row + k * 1024, x[0], x[1], x[2], x[3]);
+                    st_shared_v4(to1 + to_row + k * 1024, x[4], x[5], x[6], x[7]);
                 }
             }
             if (bits != 0xffffffffu || large > 134 || (nan & 0x80808080u)) {
@@ -481,17 +482,20 @@ __device__ bool q_loader(const TreeDecodeArgs& a, const Ctx<D, E4M3>& c) {
                 const int64_t from = __shfl_sync(0xffffffffu, at, r);
                 const uint32_t to = col + (r0 + r) * 128 + (((piece & 7) ^ (r & 7)) << 4);
                 const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + max(from, static_cast<int64_t>(0)) * D + piece * 8;
-                if constexpr (E4M3) {   // every four elements in the order that the pages' come in
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (from >= 0) x = *reinterpret_cast<const uint4*>(src);
-                    st_shared_v4(to, __byte_perm(x.x, x.y, 0x5410), __byte_perm(x.x, x.y, 0x7632), __byte_perm(x.z, x.w, 0x5410),
-                                 __byte_perm(x.z, x.w, 0x7632));
-                } else {
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(from >= 0 ? 16u : 0u) : "memory");
-                }
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(from >= 0 ? 16u : 0u) : "memory");
             }
         }
-        if (!E4M3) asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+        asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+        if (E4M3) {   // every four elements in the order that the pages' come in; each lane its own copies
+#pragma unroll 4
+            for (int i = 0; i < R / kPer; ++i) {
+                const int r = i * kPer + lane / P;
+                const uint32_t at = col + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
+                const uint4 x = ld_shared_v4(at);
+                st_shared_v4(at, __byte_perm(x.x, x.y, 0x5410), __byte_perm(x.x, x.y, 0x7632), __byte_perm(x.z, x.w, 0x5410),
+                             __byte_perm(x.z, x.w, 0x7632));
+            }
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&c.bar[c.kQFull]);
