@@ -53,6 +53,13 @@ constexpr uint32_t kRegsSoftmax = E4M3 ? 144 : 168;
 template <bool E4M3>
 constexpr uint32_t kRegsOther = E4M3 ? 64 : 88;
 constexpr int kHalf = R * 128;   // 128 rows of 64 bf16 columns, 128-byte swizzled
+// Powers of two that the compiler does not know: shifts that it would do on the integer
+// pipe become products on another (e4m3 pages: POWFIG).
+struct Powers {
+    uint32_t p0, p4, p8, p16, p28;
+};
+constexpr Powers kPowers = {1u, 1u << 4, 1u << 8, 1u << 16, 1u << 28};
+
 constexpr uint32_t kTmemCols = 512;
 constexpr int kHalfKeys = K / 2;
 constexpr uint32_t kColO = 256;
@@ -82,6 +89,7 @@ struct Ctx {
     uint64_t* bar;
     volatile int* abort_flag;
     const TreeStart* start;
+    Powers by;
     static constexpr int kFull = 0, kEmpty = Z::kSlots, kQFull = 2 * Z::kSlots, kQEmpty = kQFull + 1,
                          kSFull = kQEmpty + 1, kPFull = kSFull + 2, kODone = kPFull + 4, kOFull = kODone + 1,
                          kOFree = kOFull + 1, kDrain = kOFree + 1,
@@ -244,43 +252,43 @@ __device__ bool loader(const TreeDecodeArgs& a, const Ctx<D, false>& c, const CU
 }
 
 // e4m3 to bf16, exact where a bf16 reaches: powers of two from 2^-133 to below 2^128.
-// Four bytes over 2^120: bytes 0 and 2 in lo, 1 and 3 in hi (the sign, then
-// exponent and mantissa where a bf16 has its lowest ones).  0x7f comes out as 480.
-__device__ __forceinline__ void bf16_of(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    hi = (w & 0x80008000u) | (w >> 4 & 0x07f007f0u);
-    lo = (w << 8 & 0x80008000u) | (w << 4 & 0x07f007f0u);
-}
 __device__ __forceinline__ uint32_t times(uint32_t x, uint32_t y) {   // two bf16
     uint32_t z;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(z) : "r"(x), "r"(y));
     return z;
 }
 
-// Bit 7 of every byte that is a NaN (0x7f or 0xff), and other bits.
-__device__ __forceinline__ uint32_t nans_of(uint32_t w) { return (w & 0x7f7f7f7fu) + 0x01010101u; }
-
 // 16 e4m3 bytes of a row, times `scale` (two bf16), as 16 bf16 whose every four are in
-// the order 0 2 1 3 (Q's elements are laid out alike, and so come O's).
-__device__ __forceinline__ void row_piece(const uint4& raw, uint32_t scale, uint32_t* x) {
+// the order 0 2 1 3 (Q's elements are laid out alike, and so come O's).  A byte's sign
+// goes to a bf16's, its exponent and mantissa to the lowest bits of theirs: that is the
+// value over 2^120.  Bit 11 of a half of `nan` is set where one of them is a NaN, which
+// comes out as 480.
+__device__ __forceinline__ void row_piece(const uint4& raw, uint32_t scale, const Powers& by, uint32_t* x, uint32_t& nan) {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        bf16_of(w[i], x[2 * i], x[2 * i + 1]);
-        x[2 * i] = times(x[2 * i], scale);
-        x[2 * i + 1] = times(x[2 * i + 1], scale);
+        const uint32_t lo = (w[i] * by.p8 & 0x80008000u) | (w[i] * by.p4 & 0x07f007f0u);
+        const uint32_t hi = (w[i] & 0x80008000u) | (__umulhi(w[i], by.p28) & 0x07f007f0u);
+        nan |= (lo * by.p0 + 0x00100010u) | (hi * by.p0 + 0x00100010u);
+        x[2 * i] = times(lo, scale);
+        x[2 * i + 1] = times(hi, scale);
     }
 }
 
 // For any exponent byte: over 134 its power of two takes a second factor; and NaN.
-__device__ __forceinline__ void row_piece_rest(const uint4& raw, uint32_t e, uint32_t* x) {
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+__device__ __forceinline__ void row_piece_rest(const uint4& raw, uint32_t e, const Powers& by, uint32_t* x) {
     const uint32_t more = e > 134 ? e - 134 + 127 : 127;
-    row_piece(raw, min(e + 120, 254u) * 0x00800080u, x);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t is = nans_of(w[i]);
-        x[2 * i] = times(x[2 * i], more * 0x00800080u) | (is & 0x80u ? 0x7fffu : 0u) | (is & 0x800000u ? 0x7fff0000u : 0u);
-        x[2 * i + 1] = times(x[2 * i + 1], more * 0x00800080u) | (is & 0x8000u ? 0x7fffu : 0u) | (is & 0x80000000u ? 0x7fff0000u : 0u);
+        const uint4 one = make_uint4(i == 0 ? raw.x : i == 1 ? raw.y : i == 2 ? raw.z : raw.w, 0, 0, 0);
+        uint32_t y[8], nan = 0;
+        row_piece(one, min(e + 120, 254u) * 0x00800080u, by, y, nan);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t both = k ? one.x >> 8 : one.x;   // bytes 0 and 2, or 1 and 3
+            x[2 * i + k] = times(y[k], more * 0x00800080u) | ((both & 0x7fu) == 0x7fu ? 0x7fffu : 0u) |
+                           ((both & 0x7f0000u) == 0x7f0000u ? 0x7fff0000u : 0u);
+        }
     }
 }
 
@@ -417,15 +425,14 @@ __device__ bool converter(const TreeDecodeArgs& a, const Ctx<D, true>& c, int wh
                 }
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    nan |= nans_of(x4[k].x) | nans_of(x4[k].y) | nans_of(x4[k].z) | nans_of(x4[k].w);
                     large = max(large, e[k]);
                     uint32_t x[8];
-                    row_piece(x4[k], (e[k] + 120) * 0x00800080u, x);   // 2^(e - 127 + 120)
+                    row_piece(x4[k], (e[k] + 120) * 0x00800080u, c.by, x, nan);   // 2^(e - 127 + 120)
                     st_shared_v4(to0 + to_row + k * 1024, x[0], x[1], x[2], x[3]);
                     st_shared_v4(to1 + to_row + k * 1024, x[4], x[5], x[6], x[7]);
                 }
             }
-            if (bits != 0xffffffffu || large > 134 || (nan & 0x80808080u)) {
+            if (bits != 0xffffffffu || large > 134 || (nan & 0x08000800u)) {
                 // Once more, with what that leaves out.
 #pragma unroll 1
                 for (int i = 0; i < 4 * kHalves; ++i) {
@@ -434,7 +441,7 @@ __device__ bool converter(const TreeDecodeArgs& a, const Ctx<D, true>& c, int wh
                     uint4 bytes = ld_shared_v4((half ? raw1 : raw0) + in + at * (8 * D));
                     if (!on) bytes = make_uint4(0, 0, 0, 0);
                     uint32_t x[8];
-                    row_piece_rest(bytes, on ? exps[from * R + at * 8] : 127u, x);
+                    row_piece_rest(bytes, on ? exps[from * R + at * 8] : 127u, c.by, x);
                     st_shared_v4(to0 + out + half * kHalf + at * 1024, x[0], x[1], x[2], x[3]);
                     st_shared_v4(to1 + out + half * kHalf + at * 1024, x[4], x[5], x[6], x[7]);
                 }
@@ -598,7 +605,7 @@ __device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t* x) {
 // scores are in TMEM at ts, written over them with zeros for the other columns.
 // Returns the factor that the sums so far have to be scaled by.
 template <int N>
-__device__ __forceinline__ float weigh(RowOf& row, uint32_t ts, int c0, int key0, float sl) {
+__device__ __forceinline__ float weigh(RowOf& row, uint32_t ts, int c0, int key0, float sl, const Powers& by) {
     uint32_t sr[N];
     tmem_ld<N>(ts + c0, sr);
     tmem_ld_wait();
@@ -650,7 +657,7 @@ __device__ __forceinline__ float weigh(RowOf& row, uint32_t ts, int c0, int key0
             const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
             sum[i & 3] = fadd2(sum[i & 3], p);
             hi[i] = pack_bf16x2(p.x, p.y);
-            rest[i] = pack_bf16x2(p.x - __uint_as_float(hi[i] << 16), p.y - __uint_as_float(hi[i] & 0xffff0000u));
+            rest[i] = pack_bf16x2(p.x - __uint_as_float(hi[i] * by.p16), p.y - __uint_as_float(hi[i] & 0xffff0000u));
         }
         tmem_st<kAt / 2>(ts + (c0 + at) / 2, hi);
         tmem_st<kAt / 2>(ts + kHalfKeys / 2 + (c0 + at) / 2, rest);
@@ -697,9 +704,9 @@ __device__ bool softmax(const TreeDecodeArgs& a, const Ctx<D, E4M3>& c, uint32_t
             tc_fence_after();
             if (any) {
                 const uint32_t ts = lanes + (tiles & 1) * K + half * kHalfKeys;
-                const float f = each == 32   ? weigh<16>(row, ts, c0, key0, a.scale_log2)
-                                : each == 64 ? weigh<32>(row, ts, c0, key0, a.scale_log2)
-                                             : weigh<64>(row, ts, 0, key0, a.scale_log2);
+                const float f = each == 32   ? weigh<16>(row, ts, c0, key0, a.scale_log2, c.by)
+                                : each == 64 ? weigh<32>(row, ts, c0, key0, a.scale_log2, c.by)
+                                             : weigh<64>(row, ts, 0, key0, a.scale_log2, c.by);
                 // O may be rescaled once the last tile's PV has landed; every PV but a
                 // unit's last one arrives at kODone.
                 if (__any_sync(0xffffffffu, row.on && f != 1.f)) {
@@ -752,7 +759,8 @@ struct TreeMaps {
 };
 
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(kThreads<E4M3>, 1) tree_tc_kernel(const __grid_constant__ TreeDecodeArgs a, const __grid_constant__ TreeMaps maps, int box) {
+__global__ void __launch_bounds__(kThreads<E4M3>, 1) tree_tc_kernel(const __grid_constant__ TreeDecodeArgs a, const __grid_constant__ TreeMaps maps, int box,
+                   const __grid_constant__ Powers by) {
     extern __shared__ uint8_t raw[];
     using Z = Sizes<D, E4M3>;
     Ctx<D, E4M3> c;
@@ -760,6 +768,7 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) tree_tc_kernel(const __grid
     c.bar = reinterpret_cast<uint64_t*>(c.smem + Z::kOffBar);
     TreeStart* start = reinterpret_cast<TreeStart*>(c.smem + Z::kOffMisc);
     c.start = start;
+    c.by = by;
     c.abort_flag = reinterpret_cast<volatile int*>(c.smem + Z::kOffMisc + sizeof(TreeStart));
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(c.smem + Z::kOffMisc + sizeof(TreeStart) + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -854,7 +863,7 @@ cudaError_t launch(const TreeDecodeArgs& a, int ctas, cudaStream_t s) {
                        : make_tmap_4d_bf16(&maps.of[i], pages[i], D, a.Hkv, rows, 1, 64, box)))
                 return cudaErrorInvalidValue;
     }
-    return cudaLaunchKernelEx(&cfg, tree_tc_kernel<D, E4M3>, a, maps, box);
+    return cudaLaunchKernelEx(&cfg, tree_tc_kernel<D, E4M3>, a, maps, box, kPowers);
 }
 
 }  // namespace
