@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(const __grid
     const int far = far_tiles<R>(s), near_rows = s.n * G - s.far_rows;
     const int64_t head = a.plan.start[a.B], total = head * a.Hkv, start = a.plan.start[b];   // tiles of a head, of all
     const int unit = a.plan.unit[b], head_units = a.plan.unit[a.B];
-    const int64_t shares = share_count(total, ctas), share = total / ctas;
+    const int64_t shares = share_count(total, ctas);
     auto cta_of = [&](int64_t tile) { return static_cast<int>(((tile + 1) * shares - 1) / total); };
     const int far_chunks = (s.far_rows + 31) / 32, chunks = far_chunks + (near_rows + 31) / 32;
     if (threadIdx.x < 2) s_bad[threadIdx.x] = 0;
@@ -440,9 +440,8 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(const __grid
         const int len = is_far ? s.far_tiles : s.near_tiles;
         const int64_t from = h * head + start + static_cast<int64_t>(rt) * len + (is_far ? 0 : static_cast<int64_t>(far) * s.far_tiles);
         const int c0 = cta_of(from);
-        // Tiles of the tensor cores hold few rows several times over, each a part.
-        const int each = R == kTreeTcRows ? tree_copy_rows(min(R, rows - rt * R), share) : R, copies = kPart / each;
-        const int n = (cta_of(from + len - 1) - c0 + 1) * copies;
+        constexpr int kOf = kPart / R;   // parts of a CTA
+        const int n = (cta_of(from + len - 1) - c0 + 1) * kOf;
         const float* part = a.plan.part + static_cast<size_t>(c0 + h * head_units + unit + rt + (is_far ? 0 : far)) * kPart * (D + 2);
         float m = -INFINITY, l = 0.f;
         float4 o[kGroups];
@@ -457,8 +456,8 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(const __grid
                 st[p] = make_float2(-INFINITY, 0.f);
                 const int q = p0 + p * step;
                 if (on && q < n) {
-                    const float* at = part + static_cast<size_t>(q / copies) * kPart * (D + 2);
-                    const int in_part = r + q % copies * each;
+                    const float* at = part + static_cast<size_t>(q / kOf) * kPart * (D + 2);
+                    const int in_part = r + q % kOf * R;
                     st[p] = __ldcg(reinterpret_cast<const float2*>(at + kPart * D) + in_part);
 #pragma unroll
                     for (int g = 0; g < kGroups; ++g)

@@ -14,9 +14,9 @@
 //
 // A tile's keys are two halves of 64, each with softmax warps, weights and an O of
 // its own: neither waits for the other, and the join adds the two up as it does
-// parts.  Where a unit has 64 rows or fewer, Q holds them two or four times, and each
-// copy takes the weights of its own half or quarter of those keys, the others being
-// zero to it: all eight softmax warps work, each on fewer keys.
+// parts.  (Q with few rows held two or four times, each copy with a part of the keys,
+// so that all softmax warps work on fewer: 8 x 32K, 32 rows, 137 us, without 110; the
+// join of the copies and the longer code cost more than they saved.)
 //
 //   warps 0-7   softmax: four warps a half; thread r of them owns row r, TMEM lane r
 //   warp 8      TMEM and MMA issue (converged, elected issue)
@@ -24,8 +24,8 @@
 //   warps 12-15 K and V: a ring of tiles in the order in which they are used (K0,
 //               K1, V0, K2, V1, ...), 32 rows of each tile a warp
 //   (warps 10, 11 fill up a warpgroup, the unit that registers are moved by)
-// e4m3 pages come through a ring of their own: warp 10 has them copied, warps 12-15
-// write K, warps 16-19 V as bf16 to the ring that the products read.
+// e4m3 pages come through a ring of their own: warps 10 and 11 have K and V copied,
+// warps 12-19 write them as bf16 to the ring that the products read.
 // TMEM: S at [0, 128) and [128, 256), the halves' O at [256, 256 + d) and from 256 + d.
 
 #include "swiattn.h"
@@ -43,7 +43,7 @@ namespace {
 
 constexpr int R = kTreeTcRows, K = kTreeTcKeys;
 constexpr int kWords = kMaxTree / 32;
-constexpr int kLoaders = 4;
+constexpr int kLoaders = 4;   // warps that fill a slot
 // 4 warpgroups, launched at 128 registers a thread, or 5 at 96: of these the two that
 // do the softmax take their share, 2 * 168 + 2 * 88 = 4 * 128, 2 * 144 + 3 * 64 = 5 * 96.
 template <bool E4M3>
@@ -53,13 +53,6 @@ constexpr uint32_t kRegsSoftmax = E4M3 ? 144 : 168;
 template <bool E4M3>
 constexpr uint32_t kRegsOther = E4M3 ? 64 : 88;
 constexpr int kHalf = R * 128;   // 128 rows of 64 bf16 columns, 128-byte swizzled
-// Powers of two that the compiler does not know: shifts that it would do on the integer
-// pipe become products on another (e4m3 pages: POWFIG).
-struct Powers {
-    uint32_t p0, p4, p8, p16, p28;
-};
-constexpr Powers kPowers = {1u, 1u << 4, 1u << 8, 1u << 16, 1u << 28};
-
 constexpr uint32_t kTmemCols = 512;
 constexpr int kHalfKeys = K / 2;
 constexpr uint32_t kColO = 256;
@@ -67,8 +60,12 @@ constexpr uint32_t kColO = 256;
 template <int D, bool E4M3>
 struct Sizes {
     static constexpr int kTile = R * D * 2;                    // Q, and a slot of the ring
-    static constexpr int kSlots = (E4M3 ? 3 : 6) * 128 / D;
-    static constexpr int kRaw = E4M3 ? 6 * 128 / D : 0;        // tiles as they are in the pages
+    static constexpr int kSlots = (E4M3 ? 4 : 6) * 128 / D;
+    static constexpr int kRaw = E4M3 ? 4 * 128 / D : 0;        // tiles as they are in the pages
+    // e4m3: the first half of either ring for K, the second for V.  They are filled by
+    // different warps, and a wait by parity is sound only for one that waited for every
+    // use of the slot before.
+    [[maybe_unused]] static constexpr int kOwn = kSlots / 2, kOwnRaw = kRaw / 2;
     static constexpr int kBars = 2 * kSlots + 2 + 2 + 4 + 3 + 1 + 2 * kRaw;
     static constexpr int kOffRaw = (1 + kSlots) * kTile;
     static constexpr int kOffExp = kOffRaw + kRaw * (R * D);   // their rows' exponent bytes,
@@ -89,7 +86,6 @@ struct Ctx {
     uint64_t* bar;
     volatile int* abort_flag;
     const TreeStart* start;
-    Powers by;
     static constexpr int kFull = 0, kEmpty = Z::kSlots, kQFull = 2 * Z::kSlots, kQEmpty = kQFull + 1,
                          kSFull = kQEmpty + 1, kPFull = kSFull + 2, kODone = kPFull + 4, kOFull = kODone + 1,
                          kOFree = kOFull + 1, kDrain = kOFree + 1,
@@ -263,26 +259,26 @@ __device__ __forceinline__ uint32_t times(uint32_t x, uint32_t y) {   // two bf1
 // goes to a bf16's, its exponent and mantissa to the lowest bits of theirs: that is the
 // value over 2^120.  Bit 11 of a half of `nan` is set where one of them is a NaN, which
 // comes out as 480.
-__device__ __forceinline__ void row_piece(const uint4& raw, uint32_t scale, const Powers& by, uint32_t* x, uint32_t& nan) {
+__device__ __forceinline__ void row_piece(const uint4& raw, uint32_t scale, uint32_t* x, uint32_t& nan) {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = (w[i] * by.p8 & 0x80008000u) | (w[i] * by.p4 & 0x07f007f0u);
-        const uint32_t hi = (w[i] & 0x80008000u) | (__umulhi(w[i], by.p28) & 0x07f007f0u);
-        nan |= (lo * by.p0 + 0x00100010u) | (hi * by.p0 + 0x00100010u);
+        const uint32_t lo = (w[i] << 8 & 0x80008000u) | (w[i] << 4 & 0x07f007f0u);
+        const uint32_t hi = (w[i] & 0x80008000u) | (w[i] >> 4 & 0x07f007f0u);
+        nan |= (lo + 0x00100010u) | (hi + 0x00100010u);
         x[2 * i] = times(lo, scale);
         x[2 * i + 1] = times(hi, scale);
     }
 }
 
 // For any exponent byte: over 134 its power of two takes a second factor; and NaN.
-__device__ __forceinline__ void row_piece_rest(const uint4& raw, uint32_t e, const Powers& by, uint32_t* x) {
+__device__ __forceinline__ void row_piece_rest(const uint4& raw, uint32_t e, uint32_t* x) {
     const uint32_t more = e > 134 ? e - 134 + 127 : 127;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint4 one = make_uint4(i == 0 ? raw.x : i == 1 ? raw.y : i == 2 ? raw.z : raw.w, 0, 0, 0);
         uint32_t y[8], nan = 0;
-        row_piece(one, min(e + 120, 254u) * 0x00800080u, by, y, nan);
+        row_piece(one, min(e + 120, 254u) * 0x00800080u, y, nan);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const uint32_t both = k ? one.x >> 8 : one.x;   // bytes 0 and 2, or 1 and 3
@@ -299,17 +295,20 @@ __device__ __forceinline__ int raw_piece(int row, int piece) {
     return row * D + ((D == 128 ? piece ^ (row & 7) : piece ^ ((row >> 1) & 3)) << 4);
 }
 
-// Fills it, one warp, tile by tile: by TMA and bulk copies `box` rows at a time where a
-// page holds 16 rows or more, else row by row.  Boxes of which no row is read are left
-// as they were.
+// Fills it, one warp K's tiles and one V's: by TMA and bulk copies `box` rows at a time
+// where a page holds 16 rows or more, else row by row.  Boxes of which no row is read
+// are left as they were.
 template <int D>
-__device__ bool raw_loader(const TreeDecodeArgs& a, const Ctx<D, true>& c, const CUtensorMap* maps, int box, uint32_t& g) {
+__device__ bool raw_loader(const TreeDecodeArgs& a, const Ctx<D, true>& c, const CUtensorMap* map, int box, int which,
+                           uint32_t& filled) {
     using Z = Sizes<D, true>;
     const int lane = threadIdx.x & 31;
     const uint32_t ring = smem_u32(c.smem) + Z::kOffRaw;
     uint8_t* exps = c.smem + Z::kOffExp;
     uint32_t* read = reinterpret_cast<uint32_t*>(c.smem + Z::kOffRead);
+    const uint8_t* from = which ? a.v_exp : a.k_exp;
     const int mask = (1 << a.page_lg) - 1;
+    uint32_t t = 0;   // tiles filled
     TreeWalk<R> walk{a, *c.start};
     TreeWork w;
     while (walk.next(w)) {
@@ -334,52 +333,49 @@ __device__ bool raw_loader(const TreeDecodeArgs& a, const Ctx<D, true>& c, const
             if (kt < w.kt1 && lane * box < K) on = tok < len && (w.far || tok + box > w.s.lo || tok < w.s.na);
             return page_of(min(tok, len - 1), on);
         };
-        int before = -1, now = box ? box_page(w.kt0) : 0, ahead = -1;
-        for (int j = 0; j <= n; ++j) {
-            if (box) ahead = box_page(w.kt0 + j + 1);
-#pragma unroll 1
-            for (int which = 0; which < 2; ++which) {
-                if (which == 0 ? j == n : j == 0) continue;
-                const int key0 = tile_key<K>(w.s, w.far, w.kt0 + j - which), slot = g % Z::kRaw;
-                const uint32_t dst = ring + slot * (R * D);
-                uint64_t* full = &c.bar[c.kRawFull + slot];
-                if (!wait_w(&c.bar[c.kRawEmpty + slot], (g / Z::kRaw & 1) ^ 1, c.abort_flag, a.err)) return false;
-#pragma unroll
+        int page = box ? box_page(w.kt0) : 0;
+        for (int j = 0; j < n; ++j) {
+            const int ahead = box ? box_page(w.kt0 + j + 1) : 0;
+            const uint32_t slot = which * Z::kOwnRaw + t % Z::kOwnRaw, dst = ring + slot * (R * D);
+            const int key0 = tile_key<K>(w.s, w.far, w.kt0 + j);
+            uint64_t* full = &c.bar[c.kRawFull + slot];
+            if (!wait_w(&c.bar[c.kRawEmpty + slot], (t / Z::kOwnRaw & 1) ^ 1, c.abort_flag, a.err)) return false;
+            uint32_t bits = 0xffffffffu;   // lane i: of rows 32 i .. 32 i + 31
+            if (!(key0 + K <= len && (w.far || key0 >= w.s.lo || key0 + K <= w.s.na))) {
                 for (int i = 0; i < R / 32; ++i) {
-                    const uint32_t bits = __ballot_sync(0xffffffffu, is_read(key0 + i * 32 + lane));
-                    if (lane == 0) read[slot * (R / 32) + i] = bits;
+                    const uint32_t x = __ballot_sync(0xffffffffu, is_read(key0 + i * 32 + lane));
+                    if (lane == i) bits = x;
                 }
-                const uint8_t* from = which ? a.v_exp : a.k_exp;
-                if (box) {
-                    const int page = which ? before : now;
-                    const unsigned boxes = __ballot_sync(0xffffffffu, page >= 0);
-                    if (lane == 0) mbar_arrive_expect_tx(full, __popc(boxes) * box * (D + 1));
-                    __syncwarp();
-                    if (page >= 0) {
-                        const int slot_at = (key0 + lane * box) & mask;
-                        tma_load_3d(dst + lane * box * D, maps + which, full, w.h * D, slot_at, page);
-                        bulk_load(smem_u32(exps + slot * R) + lane * box, from + (((static_cast<int64_t>(page) * a.Hkv + w.h) << a.page_lg) + slot_at), box, full);
-                    }
-                } else {
-                    const uint8_t* pages = static_cast<const uint8_t*>(which ? a.v_pages : a.k_pages);
-#pragma unroll 1
-                    for (int r = lane; r < R; r += 32) {
-                        const int tok = key0 + r;
-                        const int page = page_of(tok, is_read(tok));
-                        if (page < 0) continue;
-                        const int64_t row = ((static_cast<int64_t>(page) << a.page_lg) + (tok & mask)) * a.Hkv + w.h;
-                        exps[slot * R + r] = from[((static_cast<int64_t>(page) * a.Hkv + w.h) << a.page_lg) + (tok & mask)];
-#pragma unroll
-                        for (int i = 0; i < D / 16; ++i)
-                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + raw_piece<D>(r, i)), "l"(pages + row * D + i * 16) : "memory");
-                    }
-                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(full)) : "memory");
-                    mbar_arrive(full);
-                }
-                ++g;
             }
-            before = now;
-            now = ahead;
+            if (lane < R / 32) read[slot * (R / 32) + lane] = bits;
+            __syncwarp();
+            if (box) {
+                const unsigned boxes = __ballot_sync(0xffffffffu, page >= 0);
+                if (lane == 0) mbar_arrive_expect_tx(full, __popc(boxes) * box * (D + 1));
+                __syncwarp();
+                if (page >= 0) {
+                    const int at = (key0 + lane * box) & mask;
+                    tma_load_3d(dst + lane * box * D, map, full, w.h * D, at, page);
+                    bulk_load(smem_u32(exps + slot * R) + lane * box, from + (((static_cast<int64_t>(page) * a.Hkv + w.h) << a.page_lg) + at), box, full);
+                }
+            } else {
+                const uint8_t* pages = static_cast<const uint8_t*>(which ? a.v_pages : a.k_pages);
+#pragma unroll 1
+                for (int r = lane; r < R; r += 32) {
+                    const int tok = key0 + r;
+                    const int p = page_of(tok, is_read(tok));
+                    if (p < 0) continue;
+                    const int64_t row = ((static_cast<int64_t>(p) << a.page_lg) + (tok & mask)) * a.Hkv + w.h;
+                    exps[slot * R + r] = from[((static_cast<int64_t>(p) * a.Hkv + w.h) << a.page_lg) + (tok & mask)];
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + raw_piece<D>(r, i)), "l"(pages + row * D + i * 16) : "memory");
+                }
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(full)) : "memory");
+                mbar_arrive(full);
+            }
+            page = ahead;
+            filled = ++t;
         }
     }
     return true;
@@ -393,7 +389,7 @@ __device__ bool raw_loader(const TreeDecodeArgs& a, const Ctx<D, true>& c, const
 template <int D>
 __device__ bool converter(const TreeDecodeArgs& a, const Ctx<D, true>& c, int which, int w32) {
     using Z = Sizes<D, true>;
-    constexpr int S = Z::kSlots, kHalves = D / 64;
+    constexpr int kHalves = D / 64;
     const int lane = threadIdx.x & 31, quarter = lane & 3, row = (lane >> 3) ^ (lane & 4 ? 5 : 0);
     const uint32_t raw0 = smem_u32(c.smem) + Z::kOffRaw + raw_piece<D>(w32 * 32 + row, quarter);
     const uint32_t raw1 = smem_u32(c.smem) + Z::kOffRaw + raw_piece<D>(w32 * 32 + row, quarter + (D == 128 ? 4 : 0));
@@ -401,59 +397,52 @@ __device__ bool converter(const TreeDecodeArgs& a, const Ctx<D, true>& c, int wh
     const uint32_t to0 = to + ((2 * quarter ^ row) << 4), to1 = to + (((2 * quarter + 1) ^ row) << 4);
     const uint8_t* exps = c.smem + Z::kOffExp + w32 * 32 + row;
     const uint32_t* read = reinterpret_cast<const uint32_t*>(c.smem + Z::kOffRead) + w32;
-    uint32_t g0 = 0;   // slots of the units before
-    TreeWalk<R> walk{a, *c.start};
-    TreeWork w;
-    while (walk.next(w)) {
-        const int n = w.kt1 - w.kt0;
-        for (int j = 0; j < n; ++j) {
-            const uint32_t g = g0 + (which ? (j < n - 1 ? 2 * j + 2 : 2 * j + 1) : j ? 2 * j - 1 : 0);
-            const uint32_t slot = g % S, from = g % Z::kRaw;
-            if (!wait_w(&c.bar[c.kRawFull + from], g / Z::kRaw & 1, c.abort_flag, a.err)) return false;
-            if (!wait_w(&c.bar[c.kEmpty + slot], (g / S & 1) ^ 1, c.abort_flag, a.err)) return false;
-            const uint32_t bits = read[from * (R / 32)], in = from * (R * D), out = slot * Z::kTile;
-            uint32_t nan = 0, large = 0;
+    const uint32_t tiles = static_cast<uint32_t>(c.start->end - c.start->at);
+    for (uint32_t t = 0; t < tiles; ++t) {
+        const uint32_t slot = which * Z::kOwn + t % Z::kOwn, from = which * Z::kOwnRaw + t % Z::kOwnRaw;
+        if (!wait_w(&c.bar[c.kRawFull + from], t / Z::kOwnRaw & 1, c.abort_flag, a.err)) return false;
+        if (!wait_w(&c.bar[c.kEmpty + slot], (t / Z::kOwn & 1) ^ 1, c.abort_flag, a.err)) return false;
+        const uint32_t bits = read[from * (R / 32)], in = from * (R * D), out = slot * Z::kTile;
+        uint32_t nan = 0, large = 0;
 #pragma unroll 1
-            for (int i = 0; i < 2 * kHalves; ++i) {   // two rows, eight apart: loads first
-                const uint32_t from_row = in + (i & 1) * (16 * D), to_row = out + (i >> 1) * kHalf + (i & 1) * 2048;
-                uint4 x4[2];
-                uint32_t e[2];
+        for (int i = 0; i < 2 * kHalves; ++i) {   // two rows, eight apart: loads first
+            const uint32_t from_row = in + (i & 1) * (16 * D), to_row = out + (i >> 1) * kHalf + (i & 1) * 2048;
+            uint4 x4[2];
+            uint32_t e[2];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    x4[k] = ld_shared_v4((i >> 1 ? raw1 : raw0) + from_row + k * (8 * D));
-                    e[k] = exps[from * R + (i & 1) * 16 + k * 8];
-                }
+            for (int k = 0; k < 2; ++k) {
+                x4[k] = ld_shared_v4((i >> 1 ? raw1 : raw0) + from_row + k * (8 * D));
+                e[k] = exps[from * R + (i & 1) * 16 + k * 8];
+            }
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    large = max(large, e[k]);
-                    uint32_t x[8];
-                    row_piece(x4[k], (e[k] + 120) * 0x00800080u, c.by, x, nan);   // 2^(e - 127 + 120)
-                    st_shared_v4(to0 + to_row + k * 1024, x[0], x[1], x[2], x[3]);
-                    st_shared_v4(to1 + to_row + k * 1024, x[4], x[5], x[6], x[7]);
-                }
-            }
-            if (bits != 0xffffffffu || large > 134 || (nan & 0x08000800u)) {
-                // Once more, with what that leaves out.
-#pragma unroll 1
-                for (int i = 0; i < 4 * kHalves; ++i) {
-                    const int half = i >> 2, at = i & 3;
-                    const bool on = bits >> (row + at * 8) & 1;
-                    uint4 bytes = ld_shared_v4((half ? raw1 : raw0) + in + at * (8 * D));
-                    if (!on) bytes = make_uint4(0, 0, 0, 0);
-                    uint32_t x[8];
-                    row_piece_rest(bytes, on ? exps[from * R + at * 8] : 127u, c.by, x);
-                    st_shared_v4(to0 + out + half * kHalf + at * 1024, x[0], x[1], x[2], x[3]);
-                    st_shared_v4(to1 + out + half * kHalf + at * 1024, x[4], x[5], x[6], x[7]);
-                }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&c.bar[c.kFull + slot]);
-                mbar_arrive(&c.bar[c.kRawEmpty + from]);
+            for (int k = 0; k < 2; ++k) {
+                large = max(large, e[k]);
+                uint32_t x[8];
+                row_piece(x4[k], (e[k] + 120) * 0x00800080u, x, nan);   // 2^(e - 127 + 120)
+                st_shared_v4(to0 + to_row + k * 1024, x[0], x[1], x[2], x[3]);
+                st_shared_v4(to1 + to_row + k * 1024, x[4], x[5], x[6], x[7]);
             }
         }
-        g0 += 2 * n;
+        if (bits != 0xffffffffu || large > 134 || (nan & 0x08000800u)) {
+            // Once more, with what that leaves out.
+#pragma unroll 1
+            for (int i = 0; i < 4 * kHalves; ++i) {
+                const int half = i >> 2, at = i & 3;
+                const bool on = bits >> (row + at * 8) & 1;
+                uint4 bytes = ld_shared_v4((half ? raw1 : raw0) + in + at * (8 * D));
+                if (!on) bytes = make_uint4(0, 0, 0, 0);
+                uint32_t x[8];
+                row_piece_rest(bytes, on ? exps[from * R + at * 8] : 127u, x);
+                st_shared_v4(to0 + out + half * kHalf + at * 1024, x[0], x[1], x[2], x[3]);
+                st_shared_v4(to1 + out + half * kHalf + at * 1024, x[4], x[5], x[6], x[7]);
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(&c.bar[c.kFull + slot]);
+            mbar_arrive(&c.bar[c.kRawEmpty + from]);
+        }
     }
     return true;
 }
@@ -477,11 +466,10 @@ __device__ bool q_loader(const TreeDecodeArgs& a, const Ctx<D, E4M3>& c) {
     TreeWork w;
     for (uint32_t u = 0; walk.next(w); ++u) {
         if (!wait_w(&c.bar[c.kQEmpty], (u & 1) ^ 1, c.abort_flag, a.err)) return false;
-        const int rows = w.rows, each = tree_copy_rows(rows, walk.s.share);
         for (int r0 = 0; r0 < R; r0 += 32) {
-            const int in = (r0 & (each - 1)) + lane, mine = w.row0 + in;
+            const int in = r0 + lane, mine = w.row0 + in;
             int64_t at = -1;   // the lane's row of q
-            if (in < rows)
+            if (in < w.rows)
                 at = static_cast<int64_t>(w.s.first + a.plan.order[w.s.first + mine / G]) * a.Hq + w.h * G + mine % G;
 #pragma unroll 4
             for (int i = 0; i < P; ++i) {
@@ -523,7 +511,12 @@ __device__ bool mma_issuer(const TreeDecodeArgs& a, const Ctx<D, E4M3>& c, uint3
     const uint64_t k0 = sdesc_sw128(smem_u32(c.smem) + Z::kTile, 16, 1024);
     const uint64_t v0 = sdesc_sw128(smem_u32(c.smem) + Z::kTile, kHalf, 1024);
     uint32_t g = 0, tiles = 0, u = 0;
-    auto full = [&]() { return wait_w(&c.bar[c.kFull + g % S], g / S & 1, c.abort_flag, a.err); };
+    // K (0) or V (1) of the CTA's t-th key tile: its slot, once it is full.
+    uint32_t slot;
+    auto full = [&](int which, uint32_t t) {
+        slot = E4M3 ? which * Z::kOwn + t % Z::kOwn : g % S;
+        return wait_w(&c.bar[c.kFull + slot], (E4M3 ? t / Z::kOwn : g / S) & 1, c.abort_flag, a.err);
+    };
     TreeWalk<R> walk{a, *c.start};
     TreeWork w;
     for (; walk.next(w); ++u) {
@@ -531,16 +524,16 @@ __device__ bool mma_issuer(const TreeDecodeArgs& a, const Ctx<D, E4M3>& c, uint3
         if (!wait_w(&c.bar[c.kQFull], u & 1, c.abort_flag, a.err)) return false;
         for (int j = 0; j <= n; ++j) {
             if (j < n) {
-                if (!full()) return false;
+                if (!full(0, tiles)) return false;
                 tc_fence_after();
-                const uint64_t k = k0 + (g % S) * (Z::kTile >> 4);
+                const uint64_t k = k0 + slot * (Z::kTile >> 4);
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
                     const uint64_t off = ((i >> 2) * kHalf + (i & 3) * 32) >> 4;
                     umma_bf16_w(tmem + (tiles & 1) * K, q + off, k + off, kIdescS, i > 0 ? 1u : 0u);
                 }
                 umma_commit_w(&c.bar[c.kSFull + (tiles & 1)]);
-                umma_commit_w(&c.bar[c.kEmpty + g % S]);
+                umma_commit_w(&c.bar[c.kEmpty + slot]);
                 if (j == n - 1) umma_commit_w(&c.bar[c.kQEmpty]);
                 ++g;
                 ++tiles;
@@ -548,8 +541,8 @@ __device__ bool mma_issuer(const TreeDecodeArgs& a, const Ctx<D, E4M3>& c, uint3
             if (j > 0) {
                 const uint32_t t = tiles - (j < n ? 2 : 1);   // tile j - 1
                 if (j == 1 && !wait_w(&c.bar[c.kOFree], (u & 1) ^ 1, c.abort_flag, a.err)) return false;
-                if (!full()) return false;
-                const uint64_t v = v0 + (g % S) * (Z::kTile >> 4);
+                if (!full(1, t)) return false;
+                const uint64_t v = v0 + slot * (Z::kTile >> 4);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     if (!wait_w(&c.bar[c.kPFull + (t & 1) * 2 + half], t >> 1 & 1, c.abort_flag, a.err)) return false;
@@ -560,7 +553,7 @@ __device__ bool mma_issuer(const TreeDecodeArgs& a, const Ctx<D, E4M3>& c, uint3
                                        v + ((half * kHalfKeys + i % (kHalfKeys / 16) * 16) * 128 >> 4), kIdescO,
                                        j == 1 && i == 0 ? 0u : 1u);
                 }
-                umma_commit_w(&c.bar[c.kEmpty + g % S]);
+                umma_commit_w(&c.bar[c.kEmpty + slot]);
                 umma_commit_w(&c.bar[j == n ? c.kOFull : c.kODone]);
                 ++g;
             }
@@ -582,35 +575,16 @@ struct RowOf {
     float m, l;
 };
 
-// Columns of TMEM to and from registers.
-template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t* x) {
-    if constexpr (N == 64) {
-        tmem_ld32(at, x);
-        tmem_ld32(at + 32, x + 32);
-    } else if constexpr (N == 32) {
-        tmem_ld32(at, x);
-    } else {
-        tmem_ld16(at, x);
-    }
-}
-template <int N>
-__device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t* x) {
-    if constexpr (N == 32) tmem_st32(at, x);
-    else if constexpr (N == 16) tmem_st16(at, x);
-    else tmem_st8(at, x);
-}
-
-// Weights of N columns from c0 of the half tile whose first key is key0 and whose
-// scores are in TMEM at ts, written over them with zeros for the other columns.
-// Returns the factor that the sums so far have to be scaled by.
-template <int N>
-__device__ __forceinline__ float weigh(RowOf& row, uint32_t ts, int c0, int key0, float sl, const Powers& by) {
+// Weights of the half tile whose first key is key0 and whose scores are in TMEM at ts,
+// written over them: the nearest bf16 of every two keys to a column, then what they
+// leave.  Returns the factor that the sums so far have to be scaled by.
+__device__ __forceinline__ float weigh(RowOf& row, uint32_t ts, int key0, float sl) {
+    constexpr int N = kHalfKeys;
     uint32_t sr[N];
-    tmem_ld<N>(ts + c0, sr);
+    tmem_ld32(ts, sr);
+    tmem_ld32(ts + 32, sr + 32);
     tmem_ld_wait();
     float* s = reinterpret_cast<float*>(sr);
-    key0 += c0;
     const bool full = !row.on || (key0 + N <= row.base && (key0 >= row.lo || key0 + N <= row.anchors));
     if (!__all_sync(0xffffffffu, full)) {
 #pragma unroll
@@ -623,7 +597,7 @@ __device__ __forceinline__ float weigh(RowOf& row, uint32_t ts, int c0, int key0
                 bits |= __funnelshift_r(x, y, at & 31);
             }
 #pragma unroll
-            for (int e = 0; e < (N < 32 ? N : 32); ++e) s[i + e] = bits >> e & 1 ? s[i + e] : -INFINITY;
+            for (int e = 0; e < 32; ++e) s[i + e] = bits >> e & 1 ? s[i + e] : -INFINITY;
         }
     }
     float m4[4];
@@ -647,31 +621,19 @@ __device__ __forceinline__ float weigh(RowOf& row, uint32_t ts, int c0, int key0
     float2 sum[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) sum[t] = make_float2(0.f, 0.f);
-    constexpr int kAt = N < 32 ? N : 32;   // columns at a time
 #pragma unroll
-    for (int at = 0; at < N; at += kAt) {
-        uint32_t hi[kAt / 2], rest[kAt / 2];
+    for (int at = 0; at < N; at += 32) {
+        uint32_t hi[16], rest[16];
 #pragma unroll
-        for (int i = 0; i < kAt / 2; ++i) {
+        for (int i = 0; i < 16; ++i) {
             const float2 x = ffma2(make_float2(s[at + 2 * i], s[at + 2 * i + 1]), sl2, off);
             const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
             sum[i & 3] = fadd2(sum[i & 3], p);
             hi[i] = pack_bf16x2(p.x, p.y);
-            rest[i] = pack_bf16x2(p.x - __uint_as_float(hi[i] * by.p16), p.y - __uint_as_float(hi[i] & 0xffff0000u));
+            rest[i] = pack_bf16x2(p.x - __uint_as_float(hi[i] << 16), p.y - __uint_as_float(hi[i] & 0xffff0000u));
         }
-        tmem_st<kAt / 2>(ts + (c0 + at) / 2, hi);
-        tmem_st<kAt / 2>(ts + kHalfKeys / 2 + (c0 + at) / 2, rest);
-    }
-    if constexpr (N < kHalfKeys) {
-        uint32_t zero[N / 2];
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) zero[i] = 0;
-#pragma unroll
-        for (int i = 0; i < kHalfKeys; i += N) {
-            if (i == c0) continue;
-            tmem_st<N / 2>(ts + i / 2, zero);
-            tmem_st<N / 2>(ts + kHalfKeys / 2 + i / 2, zero);
-        }
+        tmem_st16(ts + at / 2, hi);
+        tmem_st16(ts + N / 2 + at / 2, rest);
     }
     const float2 s2 = fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
     const bool had = row.l > 0.f;
@@ -688,13 +650,10 @@ __device__ bool softmax(const TreeDecodeArgs& a, const Ctx<D, E4M3>& c, uint32_t
     TreeWalk<R> walk{a, *c.start};
     TreeWork w;
     for (uint32_t u = 0; walk.next(w); ++u) {
-        const int rows = w.rows, each = tree_copy_rows(rows, walk.s.share);
-        const int in = r & (each - 1), first = (warp * 32) & (each - 1);
-        const bool any = first < rows;   // the warp has rows
-        const int c0 = warp * 32 / each * (each / 2);   // its copy's columns, half as many as the copy has rows
-        RowOf row{nullptr, 0, w.s.base, min(a.n_anchor, w.s.base), w.s.n, in < rows, -INFINITY, 0.f};
+        const bool any = warp * 32 < w.rows;   // the warp has rows
+        RowOf row{nullptr, 0, w.s.base, min(a.n_anchor, w.s.base), w.s.n, r < w.rows, -INFINITY, 0.f};
         if (row.on) {
-            const int tok = w.s.first + a.plan.order[w.s.first + (w.row0 + in) / G];
+            const int tok = w.s.first + a.plan.order[w.s.first + (w.row0 + r) / G];
             row.lo = a.plan.lo[tok];
             row.mask = a.plan.mask + static_cast<size_t>(tok) * kWords;
         }
@@ -704,9 +663,7 @@ __device__ bool softmax(const TreeDecodeArgs& a, const Ctx<D, E4M3>& c, uint32_t
             tc_fence_after();
             if (any) {
                 const uint32_t ts = lanes + (tiles & 1) * K + half * kHalfKeys;
-                const float f = each == 32   ? weigh<16>(row, ts, c0, key0, a.scale_log2, c.by)
-                                : each == 64 ? weigh<32>(row, ts, c0, key0, a.scale_log2, c.by)
-                                             : weigh<64>(row, ts, 0, key0, a.scale_log2, c.by);
+                const float f = weigh(row, ts, key0, a.scale_log2);
                 // O may be rescaled once the last tile's PV has landed; every PV but a
                 // unit's last one arrives at kODone.
                 if (__any_sync(0xffffffffu, row.on && f != 1.f)) {
@@ -759,8 +716,7 @@ struct TreeMaps {
 };
 
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(kThreads<E4M3>, 1) tree_tc_kernel(const __grid_constant__ TreeDecodeArgs a, const __grid_constant__ TreeMaps maps, int box,
-                   const __grid_constant__ Powers by) {
+__global__ void __launch_bounds__(kThreads<E4M3>, 1) tree_tc_kernel(const __grid_constant__ TreeDecodeArgs a, const __grid_constant__ TreeMaps maps, int box) {
     extern __shared__ uint8_t raw[];
     using Z = Sizes<D, E4M3>;
     Ctx<D, E4M3> c;
@@ -768,7 +724,6 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) tree_tc_kernel(const __grid
     c.bar = reinterpret_cast<uint64_t*>(c.smem + Z::kOffBar);
     TreeStart* start = reinterpret_cast<TreeStart*>(c.smem + Z::kOffMisc);
     c.start = start;
-    c.by = by;
     c.abort_flag = reinterpret_cast<volatile int*>(c.smem + Z::kOffMisc + sizeof(TreeStart));
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(c.smem + Z::kOffMisc + sizeof(TreeStart) + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -824,11 +779,10 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) tree_tc_kernel(const __grid
                 uint32_t filled = 0;
                 if (!loader<D>(a, c, maps.of, box, warp - 12, filled)) drain<Z::kSlots>(&c.bar[c.kFull], filled);
             }
-        } else if (E4M3 && warp == 10) {
-            if constexpr (E4M3) {
-                uint32_t filled = 0;
-                if (!raw_loader<D>(a, c, maps.of, box, filled)) drain<Z::kRaw>(&c.bar[c.kRawFull], filled);
-            }
+        } else if constexpr (E4M3) {
+            uint32_t filled = 0;
+            if (!raw_loader<D>(a, c, &maps.of[warp - 10], box, warp - 10, filled))
+                drain<Z::kOwnRaw>(&c.bar[c.kRawFull + (warp - 10) * Z::kOwnRaw], filled);
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     }
@@ -863,7 +817,7 @@ cudaError_t launch(const TreeDecodeArgs& a, int ctas, cudaStream_t s) {
                        : make_tmap_4d_bf16(&maps.of[i], pages[i], D, a.Hkv, rows, 1, 64, box)))
                 return cudaErrorInvalidValue;
     }
-    return cudaLaunchKernelEx(&cfg, tree_tc_kernel<D, E4M3>, a, maps, box, kPowers);
+    return cudaLaunchKernelEx(&cfg, tree_tc_kernel<D, E4M3>, a, maps, box);
 }
 
 }  // namespace

@@ -44,11 +44,6 @@ __device__ __forceinline__ int64_t seq_tiles(const TreeSeq& s, int G) {
 template <int R>
 constexpr int kPartRows = R == kTreeTcRows ? 2 * R : R;
 
-// Rows of each of the copies in which a tile on the tensor cores holds its rows: 32,
-// 64 or, once, all; all where shares are so short that the join of the copies costs
-// more than they save (one sequence of 777 tokens: 21.7 us, in copies 26.2).
-__device__ __forceinline__ int tree_copy_rows(int rows, int64_t share) { return share <= 2 ? 128 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
-
 // The CTAs that the key tiles are dealt out to: as many as there are, and no share
 // empty.  CTA c takes [total c / n, total (c + 1) / n).
 __device__ __forceinline__ int64_t share_count(int64_t total, int ctas) { return min(total, static_cast<int64_t>(ctas)); }
@@ -77,7 +72,6 @@ struct TreeStart {
     int64_t before;       // of the head, before sequence b
     int h, b;
     int head_units, units;   // units of one head, and of the head before sequence b
-    int64_t share;        // key tiles of a CTA, rounded down
 };
 
 // A CTA's share of the work, unit by unit.
@@ -139,7 +133,6 @@ __device__ __forceinline__ TreeStart start_walk(const TreeDecodeArgs& a) {
     w.at = c < ctas ? all * c / ctas : 0;
     w.end = c < ctas ? all * (c + 1) / ctas : 0;
     w.h = total > 0 ? static_cast<int>(w.at / total) : 0;
-    w.share = all / gridDim.x;
     w.before = 0;
     w.b = w.units = 0;
     const int64_t in = w.at - w.h * total;
