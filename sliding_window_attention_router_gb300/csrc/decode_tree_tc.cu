@@ -60,14 +60,19 @@ constexpr uint32_t kColO = 256;
 template <int D, bool E4M3>
 struct Sizes {
     static constexpr int kTile = R * D * 2;                    // Q, and a slot of the ring
-    static constexpr int kSlots = (E4M3 ? 4 : 6) * 128 / D;
+    // Q's tiles: two, so that a unit's comes while the one before is worked on, where
+    // there is room (33 ragged trees, D 64: QFIG).
+    static constexpr int kQ = E4M3 && D == 128 ? 1 : 2;
+    static constexpr int kSlots = E4M3 ? 4 * 128 / D : 6 * 128 / D - (kQ - 1);
     static constexpr int kRaw = E4M3 ? 4 * 128 / D : 0;        // tiles as they are in the pages
     // e4m3: the first half of either ring for K, the second for V.  They are filled by
     // different warps, and a wait by parity is sound only for one that waited for every
     // use of the slot before.
-    [[maybe_unused]] static constexpr int kOwn = kSlots / 2, kOwnRaw = kRaw / 2;
-    static constexpr int kBars = 2 * kSlots + 2 + 2 + 4 + 3 + 1 + 2 * kRaw;
-    static constexpr int kOffRaw = (1 + kSlots) * kTile;
+    static constexpr int kOwn = kSlots / 2;
+    [[maybe_unused]] static constexpr int kOwnRaw = kRaw / 2;
+    static constexpr int kBars = 2 * kSlots + 2 * kQ + 2 + 4 + 3 + 1 + 2 * kRaw;
+    static constexpr int kOffRing = kQ * kTile;
+    static constexpr int kOffRaw = kOffRing + kSlots * kTile;
     static constexpr int kOffExp = kOffRaw + kRaw * (R * D);   // their rows' exponent bytes,
     static constexpr int kOffRead = kOffExp + kRaw * R;        // and, a bit a row, which are read
     static constexpr int kOffBar = kOffRead + kRaw * (R / 8);
@@ -86,8 +91,8 @@ struct Ctx {
     uint64_t* bar;
     volatile int* abort_flag;
     const TreeStart* start;
-    static constexpr int kFull = 0, kEmpty = Z::kSlots, kQFull = 2 * Z::kSlots, kQEmpty = kQFull + 1,
-                         kSFull = kQEmpty + 1, kPFull = kSFull + 2, kODone = kPFull + 4, kOFull = kODone + 1,
+    static constexpr int kFull = 0, kEmpty = Z::kSlots, kQFull = 2 * Z::kSlots, kQEmpty = kQFull + Z::kQ,
+                         kSFull = kQEmpty + Z::kQ, kPFull = kSFull + 2, kODone = kPFull + 4, kOFull = kODone + 1,
                          kOFree = kOFull + 1, kDrain = kOFree + 1,
                          kRawFull = kDrain + 1, kRawEmpty = kRawFull + Z::kRaw;
 };
@@ -202,7 +207,7 @@ __device__ bool loader(const TreeDecodeArgs& a, const Ctx<D, false>& c, const CU
     using Z = Sizes<D, false>;
     constexpr int S = Z::kSlots;
     const int lane = threadIdx.x & 31;
-    const uint32_t ring = smem_u32(c.smem) + Z::kTile + w32 * 32 * 128;
+    const uint32_t ring = smem_u32(c.smem) + Z::kOffRing + w32 * 32 * 128;
     uint32_t first = 0;              // of the slots with copies not announced, which follow one another
     uint32_t own = 0;                // bit i: slot first + i is one of them
     auto announce = [&]() {          // slot `first`
@@ -393,7 +398,7 @@ __device__ bool converter(const TreeDecodeArgs& a, const Ctx<D, true>& c, int wh
     const int lane = threadIdx.x & 31, quarter = lane & 3, row = (lane >> 3) ^ (lane & 4 ? 5 : 0);
     const uint32_t raw0 = smem_u32(c.smem) + Z::kOffRaw + raw_piece<D>(w32 * 32 + row, quarter);
     const uint32_t raw1 = smem_u32(c.smem) + Z::kOffRaw + raw_piece<D>(w32 * 32 + row, quarter + (D == 128 ? 4 : 0));
-    const uint32_t to = smem_u32(c.smem) + Z::kTile + (w32 * 32 + row) * 128;
+    const uint32_t to = smem_u32(c.smem) + Z::kOffRing + (w32 * 32 + row) * 128;
     const uint32_t to0 = to + ((2 * quarter ^ row) << 4), to1 = to + (((2 * quarter + 1) ^ row) << 4);
     const uint8_t* exps = c.smem + Z::kOffExp + w32 * 32 + row;
     const uint32_t* read = reinterpret_cast<const uint32_t*>(c.smem + Z::kOffRead) + w32;
@@ -459,13 +464,15 @@ __device__ void drain(uint64_t* full, uint32_t filled) {
 // ---- Q ---------------------------------------------------------------------------------
 template <int D, bool E4M3>
 __device__ bool q_loader(const TreeDecodeArgs& a, const Ctx<D, E4M3>& c) {
+    using Z = Sizes<D, E4M3>;
     constexpr int P = D / 8, kPer = 32 / P;
     const int lane = threadIdx.x & 31, piece = lane % P, G = a.Hq / a.Hkv;
-    const uint32_t col = smem_u32(c.smem) + (piece >> 3) * kHalf;
+    const uint32_t col0 = smem_u32(c.smem) + (piece >> 3) * kHalf;
     TreeWalk<R> walk{a, *c.start};
     TreeWork w;
     for (uint32_t u = 0; walk.next(w); ++u) {
-        if (!wait_w(&c.bar[c.kQEmpty], (u & 1) ^ 1, c.abort_flag, a.err)) return false;
+        const uint32_t buf = u % Z::kQ, col = col0 + buf * Z::kTile;
+        if (!wait_w(&c.bar[c.kQEmpty + buf], (u / Z::kQ & 1) ^ 1, c.abort_flag, a.err)) return false;
         for (int r0 = 0; r0 < R; r0 += 32) {
             const int in = r0 + lane, mine = w.row0 + in;
             int64_t at = -1;   // the lane's row of q
@@ -493,7 +500,7 @@ __device__ bool q_loader(const TreeDecodeArgs& a, const Ctx<D, E4M3>& c) {
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&c.bar[c.kQFull]);
+        if (lane == 0) mbar_arrive(&c.bar[c.kQFull + buf]);
     }
     return true;
 }
@@ -507,9 +514,9 @@ __device__ bool mma_issuer(const TreeDecodeArgs& a, const Ctx<D, E4M3>& c, uint3
     using Z = Sizes<D, E4M3>;
     constexpr int S = Z::kSlots;
     constexpr uint32_t kIdescS = idesc_bf16_f32(R, K, false, false), kIdescO = idesc_bf16_f32(R, D, false, true);
-    const uint64_t q = sdesc_sw128(smem_u32(c.smem), 16, 1024);
-    const uint64_t k0 = sdesc_sw128(smem_u32(c.smem) + Z::kTile, 16, 1024);
-    const uint64_t v0 = sdesc_sw128(smem_u32(c.smem) + Z::kTile, kHalf, 1024);
+    const uint64_t q0 = sdesc_sw128(smem_u32(c.smem), 16, 1024);
+    const uint64_t k0 = sdesc_sw128(smem_u32(c.smem) + Z::kOffRing, 16, 1024);
+    const uint64_t v0 = sdesc_sw128(smem_u32(c.smem) + Z::kOffRing, kHalf, 1024);
     uint32_t g = 0, tiles = 0, u = 0;
     // K (0) or V (1) of the CTA's t-th key tile: its slot, once it is full.
     uint32_t slot;
@@ -521,7 +528,9 @@ __device__ bool mma_issuer(const TreeDecodeArgs& a, const Ctx<D, E4M3>& c, uint3
     TreeWork w;
     for (; walk.next(w); ++u) {
         const int n = w.kt1 - w.kt0;
-        if (!wait_w(&c.bar[c.kQFull], u & 1, c.abort_flag, a.err)) return false;
+        const uint32_t buf = u % Z::kQ;
+        const uint64_t q = q0 + buf * (Z::kTile >> 4);
+        if (!wait_w(&c.bar[c.kQFull + buf], u / Z::kQ & 1, c.abort_flag, a.err)) return false;
         for (int j = 0; j <= n; ++j) {
             if (j < n) {
                 if (!full(0, tiles)) return false;
@@ -534,7 +543,7 @@ __device__ bool mma_issuer(const TreeDecodeArgs& a, const Ctx<D, E4M3>& c, uint3
                 }
                 umma_commit_w(&c.bar[c.kSFull + (tiles & 1)]);
                 umma_commit_w(&c.bar[c.kEmpty + slot]);
-                if (j == n - 1) umma_commit_w(&c.bar[c.kQEmpty]);
+                if (j == n - 1) umma_commit_w(&c.bar[c.kQEmpty + buf]);
                 ++g;
                 ++tiles;
             }
@@ -648,12 +657,17 @@ __device__ bool softmax(const TreeDecodeArgs& a, const Ctx<D, E4M3>& c, uint32_t
     const uint32_t to = lanes + kColO + half * D;
     uint32_t tiles = 0, done = 0;
     TreeWalk<R> walk{a, *c.start};
-    TreeWork w;
-    for (uint32_t u = 0; walk.next(w); ++u) {
+    TreeWork w, next;
+    // The place of this thread's row of a unit among the packed tokens, -1: none.
+    auto token_of = [&](const TreeWork& w) { return r < w.rows ? w.s.first + a.plan.order[w.s.first + (w.row0 + r) / G] : -1; };
+    bool more = walk.next(next);
+    int next_tok = more ? token_of(next) : -1;
+    for (uint32_t u = 0; more; ++u) {
+        w = next;
+        const int tok = next_tok;
         const bool any = warp * 32 < w.rows;   // the warp has rows
-        RowOf row{nullptr, 0, w.s.base, min(a.n_anchor, w.s.base), w.s.n, r < w.rows, -INFINITY, 0.f};
+        RowOf row{nullptr, 0, w.s.base, min(a.n_anchor, w.s.base), w.s.n, tok >= 0, -INFINITY, 0.f};
         if (row.on) {
-            const int tok = w.s.first + a.plan.order[w.s.first + (w.row0 + r) / G];
             row.lo = a.plan.lo[tok];
             row.mask = a.plan.mask + static_cast<size_t>(tok) * kWords;
         }
@@ -683,8 +697,12 @@ __device__ bool softmax(const TreeDecodeArgs& a, const Ctx<D, E4M3>& c, uint32_t
             }
             if (kt > w.kt0) ++done;
             tc_fence_before();
-            mbar_arrive(&c.bar[c.kPFull + (tiles & 1) * 2 + half]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c.bar[c.kPFull + (tiles & 1) * 2 + half]);
         }
+        // The next unit, looked up while the last product runs.
+        more = walk.next(next);
+        next_tok = more ? token_of(next) : -1;
         if (!wait_w(&c.bar[c.kOFull], u & 1, c.abort_flag, a.err)) return false;
         tc_fence_after();
         if (any) {
@@ -706,7 +724,8 @@ __device__ bool softmax(const TreeDecodeArgs& a, const Ctx<D, E4M3>& c, uint32_t
             if (row.on) reinterpret_cast<float2*>(part + kPartRows<R> * D)[at] = make_float2(row.m, row.l);
         }
         tc_fence_before();
-        mbar_arrive(&c.bar[c.kOFree]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c.bar[c.kOFree]);
     }
     return true;
 }
@@ -732,13 +751,12 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) tree_tc_kernel(const __grid
             mbar_init(&c.bar[c.kFull + i], kLoaders);
             mbar_init(&c.bar[c.kEmpty + i], 1);
         }
-        mbar_init(&c.bar[c.kQFull], 1);
-        mbar_init(&c.bar[c.kQEmpty], 1);
+        for (int i = 0; i < 2 * Z::kQ; ++i) mbar_init(&c.bar[c.kQFull + i], 1);   // and kQEmpty
         for (int i = 0; i < 2; ++i) mbar_init(&c.bar[c.kSFull + i], 1);
-        for (int i = 0; i < 4; ++i) mbar_init(&c.bar[c.kPFull + i], R);
+        for (int i = 0; i < 4; ++i) mbar_init(&c.bar[c.kPFull + i], 4);   // warps
         mbar_init(&c.bar[c.kODone], 1);
         mbar_init(&c.bar[c.kOFull], 1);
-        mbar_init(&c.bar[c.kOFree], 2 * R);
+        mbar_init(&c.bar[c.kOFree], 8);
         mbar_init(&c.bar[c.kDrain], 1);
         for (int i = 0; i < Z::kRaw; ++i) {
             mbar_init(&c.bar[c.kRawFull + i], box ? 1 : 64);

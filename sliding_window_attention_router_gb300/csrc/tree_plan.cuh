@@ -124,7 +124,13 @@ template <int R>
 __device__ __forceinline__ TreeStart start_walk(const TreeDecodeArgs& a) {
     const int lane = threadIdx.x & 31, G = a.Hq / a.Hkv;
     int64_t total = 0;
-    for (int i = lane; i < a.B; i += 32) total += seq_tiles<R>(a.plan.seqs[i], G);
+    TreeSeq mine_seq = {};   // of up to 32 sequences: looked up once
+    if (a.B <= 32) {
+        if (lane < a.B) mine_seq = a.plan.seqs[lane];
+        total = seq_tiles<R>(mine_seq, G);
+    } else {
+        for (int i = lane; i < a.B; i += 32) total += seq_tiles<R>(a.plan.seqs[i], G);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     TreeStart w;
@@ -144,7 +150,7 @@ __device__ __forceinline__ TreeStart start_walk(const TreeDecodeArgs& a) {
         int64_t mine = 0;
         int u = 0;
         if (i < a.B) {
-            const TreeSeq s = a.plan.seqs[i];
+            const TreeSeq s = a.B <= 32 ? mine_seq : a.plan.seqs[i];
             mine = seq_tiles<R>(s, G);
             u = row_tiles<R>(s, G);
         }
