@@ -584,30 +584,47 @@ struct RowOf {
     float m, l;
 };
 
-// Weights of the half tile whose first key is key0 and whose scores are in TMEM at ts,
-// written over them: the nearest bf16 of every two keys to a column, then what they
-// leave.  Returns the factor that the sums so far have to be scaled by.
-__device__ __forceinline__ float weigh(RowOf& row, uint32_t ts, int key0, float sl) {
+// Which of a half tile's keys, from key0 on, the row reads, a bit a key; whether any
+// row of the warp leaves one out.
+struct Reads {
+    uint32_t bits[kHalfKeys / 32];
+    bool some;
+};
+__device__ __forceinline__ Reads reads_of(const RowOf& row, int key0) {
+    Reads x;
+    x.bits[0] = x.bits[1] = 0xffffffffu;
+    const bool full = !row.on || (key0 + kHalfKeys <= row.base && (key0 >= row.lo || key0 + kHalfKeys <= row.anchors));
+    x.some = !__all_sync(0xffffffffu, full);
+    if (x.some) {
+        const int at = key0 - row.base, word = at >> 5;   // the tree's tokens at ...
+        uint32_t w[3] = {0, 0, 0};
+        if (row.on && at > -kHalfKeys && at < row.n) {
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                if (word + i >= 0 && word + i < kWords) w[i] = row.mask[word + i];
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int k0 = key0 + 32 * i;
+            x.bits[i] = bits_of(k0, row.lo, row.base) | bits_of(k0, 0, row.anchors) | __funnelshift_r(w[i], w[i + 1], at & 31);
+        }
+    }
+    return x;
+}
+
+// Weights of a half tile whose scores are in TMEM at ts, written over them: the nearest
+// bf16 of every two keys to a column, then what they leave.  Returns the factor that
+// the sums so far have to be scaled by.
+__device__ __forceinline__ float weigh(RowOf& row, const Reads& reads, uint32_t ts, float sl) {
     constexpr int N = kHalfKeys;
     uint32_t sr[N];
     tmem_ld32(ts, sr);
     tmem_ld32(ts + 32, sr + 32);
     tmem_ld_wait();
     float* s = reinterpret_cast<float*>(sr);
-    const bool full = !row.on || (key0 + N <= row.base && (key0 >= row.lo || key0 + N <= row.anchors));
-    if (!__all_sync(0xffffffffu, full)) {
+    if (reads.some) {
 #pragma unroll
-        for (int i = 0; i < N; i += 32) {
-            const int k0 = key0 + i, at = k0 - row.base;
-            uint32_t bits = bits_of(k0, row.lo, row.base) | bits_of(k0, 0, row.anchors);
-            if (row.on && at > -32 && at < row.n) {   // the tree's tokens at .. at + 31
-                const int word = at >> 5;
-                const uint32_t x = word >= 0 ? row.mask[word] : 0u, y = word + 1 < kWords ? row.mask[word + 1] : 0u;
-                bits |= __funnelshift_r(x, y, at & 31);
-            }
-#pragma unroll
-            for (int e = 0; e < 32; ++e) s[i + e] = bits >> e & 1 ? s[i + e] : -INFINITY;
-        }
+        for (int i = 0; i < N; ++i) s[i] = reads.bits[i / 32] >> (i % 32) & 1 ? s[i] : -INFINITY;
     }
     float m4[4];
 #pragma unroll
@@ -673,11 +690,12 @@ __device__ bool softmax(const TreeDecodeArgs& a, const Ctx<D, E4M3>& c, uint32_t
         }
         for (int kt = w.kt0; kt < w.kt1; ++kt, ++tiles) {
             const int key0 = tile_key<K>(w.s, w.far, kt) + half * kHalfKeys;
+            const Reads reads = reads_of(row, key0);   // while the scores are on their way
             if (!wait_w(&c.bar[c.kSFull + (tiles & 1)], tiles >> 1 & 1, c.abort_flag, a.err)) return false;
             tc_fence_after();
             if (any) {
                 const uint32_t ts = lanes + (tiles & 1) * K + half * kHalfKeys;
-                const float f = weigh(row, ts, key0, a.scale_log2);
+                const float f = weigh(row, reads, ts, a.scale_log2);
                 // O may be rescaled once the last tile's PV has landed; every PV but a
                 // unit's last one arrives at kODone.
                 if (__any_sync(0xffffffffu, row.on && f != 1.f)) {
