@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
 
 // ---- the join ---------------------------------------------------------------------
 // A block 32 rows of a row tile at a time, lane r row r, warp w the (w % 8)-th eighth of
-// the dimensions and, by w / 8, every other part of the rows' unit; where there are
+// the dimensions and, of 16 warps, every other part of the rows' unit; where there are
 // 16 rows or 8, two or four lanes share a row's parts.  Parts join by their maxima,
 // in an order that the numbers of rows and parts decide.  They lie four dimensions of
 // all rows together, then the next four, so that lanes read (and the threads that own
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
 // times it is a NaN that is none of the row's.  So a row that comes out not finite is
 // computed again, key by key over what it does read (slow, and right whatever the
 // reason).
-constexpr int kJoinThreads = 512;
+constexpr int kJoinThreads = 512;   // at most, or half of them
 
 template <int N>
 struct Dims {
@@ -403,8 +403,7 @@ __device__ __forceinline__ void add(float4& o, const float4& x, float w) {
 template <int KIND, int D, int R>
 __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(const __grid_constant__ TreeDecodeArgs a, int ctas) {
     constexpr int N = D / 32, kAcross = 8, kGroups = D / 4 / kAcross;   // warps across the dimensions; fours of a warp
-    constexpr int kWarps = kJoinThreads / 32, kDown = kWarps / kAcross;
-    static_assert(kDown == 2, "the two halves of the warps");
+    const int warps = blockDim.x / 32, downs = warps / kAcross;   // 8 or 16; 1 or 2
     constexpr int kAtOnce = 8 / kGroups;   // parts on their way: 32 registers
     constexpr int kPart = kPartRows<R>;
     using T = typename std::conditional<KIND == SWIATTN_F32, float, __nv_bfloat16>::type;
@@ -447,7 +446,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(const __grid
         float4 o[kGroups];
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) o[g] = make_float4(0.f, 0.f, 0.f, 0.f);
-        const int step = kDown * (32 / lanes);   // this lane's parts: the first, and how far apart
+        const int step = downs * (32 / lanes);   // this lane's parts: the first, and how far apart
         for (int p0 = down * (32 / lanes) + lane / lanes; p0 < n; p0 += kAtOnce * step) {
             float2 st[kAtOnce];
             float4 x[kAtOnce][kGroups];
@@ -498,15 +497,17 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(const __grid
                 return make_float4(__shfl_xor_sync(0xffffffffu, o[g].x, w), __shfl_xor_sync(0xffffffffu, o[g].y, w),
                                    __shfl_xor_sync(0xffffffffu, o[g].z, w), __shfl_xor_sync(0xffffffffu, o[g].w, w));
             });
-        if (down == 1) {
+        if (downs == 2) {
+            if (down == 1) {
 #pragma unroll
-            for (int g = 0; g < kGroups; ++g) *reinterpret_cast<float4*>(&s_o[lane][(across * kGroups + g) * 4]) = o[g];
-            if (across == 0) s_stats[lane] = make_float2(m, l);
-        }
-        __syncthreads();
-        if (down == 0) {
-            const float2 st = s_stats[lane];
-            join(st.x, st.y, [&](int g) { return *reinterpret_cast<const float4*>(&s_o[lane][(across * kGroups + g) * 4]); });
+                for (int g = 0; g < kGroups; ++g) *reinterpret_cast<float4*>(&s_o[lane][(across * kGroups + g) * 4]) = o[g];
+                if (across == 0) s_stats[lane] = make_float2(m, l);
+            }
+            __syncthreads();
+            if (down == 0) {
+                const float2 st = s_stats[lane];
+                join(st.x, st.y, [&](int g) { return *reinterpret_cast<const float4*>(&s_o[lane][(across * kGroups + g) * 4]); });
+            }
         }
         bool fine = true;
         if (down == 0) {
@@ -525,12 +526,9 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(const __grid
         if (threadIdx.x == 0) s_bad[turn ^ 1] = 0;
         __syncthreads();
         const unsigned bad = s_bad[turn];
-        // A warp's rows: two, lanes side by side along the dimensions.
-#pragma unroll
-        for (int k = 0; k < 32 / kWarps; ++k) {
-            const int at = warp * (32 / kWarps) + k;
+        // A warp's rows, lanes side by side along the dimensions.
+        for (int at = warp; at < here; at += warps) {
             const int64_t to = __shfl_sync(0xffffffffu, out, at & (lanes - 1));
-            if (at >= here) break;
             float y[N];
 #pragma unroll
             for (int e = 0; e < N; ++e) y[e] = s_o[at][lane * N + e];
@@ -587,7 +585,11 @@ cudaError_t launch_all(const TreeDecodeArgs& a, int sms, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     // About the chunks of a sequence of mean size (blocks without one cost time too).
     const int64_t mean = (static_cast<int64_t>(a.T) * (a.Hq / a.Hkv) / a.B / 32 + 1) * a.Hkv;
-    cfg = dependent_launch(dim3(a.B, static_cast<unsigned>(std::min<int64_t>(mean, std::max(1, 8192 / a.B)))), kJoinThreads, s, attr);
+    // Many chunks want many blocks at once, few their parts read by more warps (33
+    // ragged trees, 1400 chunks: 100 us, by 512 threads each 114; 8 x 32K with 64 rows,
+    // 64 chunks: 110 us by 256 threads, 103 by 512).
+    const bool many = mean * a.B > 4 * sms;
+    cfg = dependent_launch(dim3(a.B, static_cast<unsigned>(std::min<int64_t>(mean, std::max(1, 8192 / a.B)))), many ? kJoinThreads / 2 : kJoinThreads, s, attr);
     e = cudaLaunchKernelEx(&cfg, tree_join_kernel<KIND, D, kRows>, a, ctas);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
