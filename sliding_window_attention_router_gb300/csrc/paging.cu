@@ -128,14 +128,17 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const __grid_constant_
 }
 
 // ---- forks -------------------------------------------------------------------
-// Block (c, y): child c, and of its copies the pool y % (2 layers), every
-// gridDim.y / (2 layers)-th piece of the page.  Children come first in the grid,
-// so that those of one source read its page while the L2 holds it.
+// Blocks (c, y): child c, and of the pieces of its copies (of all layers' keys and
+// values) every gridDim.y-th from y on.  Children come first in the grid, so that those
+// of one source read its page while the L2 holds it; a block takes many pieces, as
+// each begins with three reads that wait for one another, but not so many that a child
+// with little to copy leaves the others waiting (64 children of four prompts, 22 layers,
+// 317 MB: 52 us, 6.1 TB/s; a piece a block 67, blocks for 8 a SM 65, for 16, 32 and 128 57,
+// 53 and 59).
 __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ PagingArgs a) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int c = blockIdx.x, units = 2 * a.layers, unit = blockIdx.y % units;
-    const int piece = blockIdx.y / units, pieces = gridDim.y / units;
+    const int c = blockIdx.x;
     const int b = a.source[c];
     int32_t* table_out = a.table_out + static_cast<int64_t>(c) * a.max_pages;
     int len = 0, to = -1;
@@ -165,25 +168,30 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ 
     if (empty || rest == 0 || to < 0) return;
 
     const int64_t pool = static_cast<int64_t>(a.num_pages) << a.page_lg;   // rows of a layer
-    char* rows = static_cast<char*>(unit & 1 ? a.v_pages : a.k_pages) + (unit >> 1) * pool * a.row_bytes;
-    const uint4* src = reinterpret_cast<const uint4*>(rows + (static_cast<int64_t>(from) << a.page_lg) * a.row_bytes);
-    uint4* dst = reinterpret_cast<uint4*>(rows + (static_cast<int64_t>(to) << a.page_lg) * a.row_bytes);
-    const int64_t n = static_cast<int64_t>(rest) * (a.row_bytes / 16);
-    for (int64_t i0 = static_cast<int64_t>(piece) * (kThreads * kAtOnce) + threadIdx.x; i0 < n; i0 += static_cast<int64_t>(pieces) * (kThreads * kAtOnce)) {
+    const int64_t n = static_cast<int64_t>(rest) * (a.row_bytes / 16);     // 16-byte columns of a copy
+    const int64_t pieces = (n + kThreads * kAtOnce - 1) / (kThreads * kAtOnce), units = 2 * a.layers;
+    const int64_t src_at = (static_cast<int64_t>(from) << a.page_lg) * a.row_bytes, dst_at = (static_cast<int64_t>(to) << a.page_lg) * a.row_bytes;
+    for (int64_t p = blockIdx.y; p < units * pieces; p += gridDim.y) {
+        const int64_t unit = p / pieces, i0 = (p - unit * pieces) * (kThreads * kAtOnce) + threadIdx.x;
+        char* rows = static_cast<char*>(unit & 1 ? a.v_pages : a.k_pages) + (unit >> 1) * pool * a.row_bytes;
+        const uint4* src = reinterpret_cast<const uint4*>(rows + src_at);
+        uint4* dst = reinterpret_cast<uint4*>(rows + dst_at);
         uint4 x[kAtOnce];
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i)
             if (i0 + i * kThreads < n) x[i] = src[i0 + i * kThreads];
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i)
-            if (i0 + i * kThreads < n) dst[i0 + i * kThreads] = x[i];
+            if (i0 + i * kThreads < n) __stcs(dst + i0 + i * kThreads, x[i]);
     }
-    if (a.k_exp && piece == pieces - 1) {
-        uint8_t* exps = (unit & 1 ? a.v_exp : a.k_exp) + (unit >> 1) * pool * a.Hkv;
+    if (a.k_exp) {
         const int64_t s = (static_cast<int64_t>(from) * a.Hkv) << a.page_lg, d = (static_cast<int64_t>(to) * a.Hkv) << a.page_lg;
         const int bytes = a.Hkv << a.page_lg;
-        for (int i = threadIdx.x; i < bytes; i += kThreads)
-            if ((i & ((1 << a.page_lg) - 1)) < rest) exps[d + i] = exps[s + i];
+        for (int64_t unit = blockIdx.y; unit < units; unit += gridDim.y) {
+            uint8_t* exps = (unit & 1 ? a.v_exp : a.k_exp) + (unit >> 1) * pool * a.Hkv;
+            for (int i = threadIdx.x; i < bytes; i += kThreads)
+                if ((i & ((1 << a.page_lg) - 1)) < rest) exps[d + i] = exps[s + i];
+        }
     }
 }
 
@@ -199,12 +207,13 @@ cudaError_t launch_accept(const PagingArgs& a, cudaStream_t s) {
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-cudaError_t launch_fork(const PagingArgs& a, cudaStream_t s) {
-    const int64_t page_chunks = (static_cast<int64_t>(a.row_bytes / 16) << a.page_lg) / (kThreads * kAtOnce) + 1;
-    const int64_t most = std::max<int64_t>(1, 65535 / (2 * a.layers));   // of the grid's second dimension
-    const int pieces = static_cast<int>(std::min<int64_t>({page_chunks, most, 64}));
+cudaError_t launch_fork(const PagingArgs& a, int sms, cudaStream_t s) {
+    // Eight times as many blocks as run at once, and no more than there can be pieces.
+    const int64_t pieces = (static_cast<int64_t>(a.row_bytes / 16) << a.page_lg) / (kThreads * kAtOnce) + 1;
+    const int64_t most = std::min<int64_t>(2 * a.layers * pieces, 65535);
+    const int64_t y = std::max<int64_t>(1, std::min<int64_t>(most, (64 * sms + a.C - 1) / a.C));
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = dependent_launch(dim3(a.C, 2 * a.layers * pieces), kThreads, s, attr);
+    const cudaLaunchConfig_t cfg = dependent_launch(dim3(a.C, static_cast<unsigned>(y)), kThreads, s, attr);
     const cudaError_t e = cudaLaunchKernelEx(&cfg, fork_kernel, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -1160,7 +1160,7 @@ int swiattn_fork_paged(void* k_pages, void* v_pages, uint8_t* k_exp, uint8_t* v_
     a.err = di.err;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     prof_start(s);
-    const cudaError_t e = launch_fork(a, s);
+    const cudaError_t e = launch_fork(a, di.sms, s);
     prof_stop(s);
     return launched(e);
 }

@@ -413,7 +413,7 @@ cudaError_t launch_tree_tc(const TreeDecodeArgs& a, int d, bool e4m3, int ctas, 
 cudaError_t tree_set_wait_limit(uint64_t ns);
 
 cudaError_t launch_accept(const PagingArgs& a, cudaStream_t s);
-cudaError_t launch_fork(const PagingArgs& a, cudaStream_t s);
+cudaError_t launch_fork(const PagingArgs& a, int sms, cudaStream_t s);
 
 // Timing hook around the dominant kernel of a call (no-ops unless set).
 void prof_start(cudaStream_t s);
