@@ -226,7 +226,10 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
     a = y;
 }
 
-template <typename T, int MODE, int D>
+// GIVEN: positions on several axes, or an append's tokens with positions of their own
+// (a kernel apart, as its registers cost the others: e4m3 append of 32K tokens 122 us
+// would be 125).
+template <typename T, int MODE, int D, bool GIVEN>
 __global__ void __launch_bounds__(kMaxThreads) rotate_kernel(const __grid_constant__ RotateArgs a) {
     constexpr bool kStored = MODE >= kAppend;   // k and v go to pages
     constexpr bool kBackward = MODE == kRopeBackward;
@@ -271,6 +274,12 @@ __global__ void __launch_bounds__(kMaxThreads) rotate_kernel(const __grid_consta
     for (int x = threadIdx.x / 32; x < tokens * pieces; x += blockDim.x / 32) {
         const int j = pieces == 2 ? x >> 1 : x, f = (pieces == 2 ? (x & 1) * 32 : 0) + (threadIdx.x & 31);
         const int t = t0 + j;
+        // Its position on the frequency's axis: on its way while the place is looked up
+        // (after that, 15K tokens to e4m3 pages took 75 us in place of 72; rotation alone
+        // has nothing to look up, and no register to spare).
+        auto given = [&]() { return a.positions[(a.axes > 1 ? static_cast<int64_t>(a.axis_of[f]) * a.tokens : 0) + t]; };
+        int early = 0;
+        if (GIVEN && kStored && table_used && f < half) early = given();
         Place place = {0, 0};
         int page = 0;
         if (kStored) {
@@ -278,8 +287,7 @@ __global__ void __launch_bounds__(kMaxThreads) rotate_kernel(const __grid_consta
             page = place.b < 0 ? -1 : a.block_table[static_cast<int64_t>(place.b) * a.max_pages + (place.pos >> a.page_lg)];
         }
         if (table_used && f < half) {   // while the page number is on its way
-            int pos = kStored ? place.pos : t % a.N;
-            if (a.positions) pos = a.positions[(a.axes > 1 ? static_cast<int64_t>(a.axis_of[f]) * a.tokens : 0) + t];
+            const int pos = GIVEN ? (kStored ? early : given()) : kStored ? place.pos : a.positions ? a.positions[t] : t % a.N;
             float factor = a.factor;
             const uint64_t fraction = turn_fraction(a.inv_freq[f], factor);
             const float2 cs = cos_sin(fraction, pos, factor);
@@ -365,8 +373,8 @@ __global__ void __launch_bounds__(kMaxThreads) rotate_kernel(const __grid_consta
 // and at most 128 slots (16 + 16 + 16 heads: bf16 append 126 us, in two parts 130,
 // whole 161, as then only two blocks fit an SM; 16 + 4 heads: whole 27 us, in two
 // parts 29).
-template <typename T, int MODE, int D>
-cudaError_t launch(RotateArgs a, cudaStream_t s) {
+template <typename T, int MODE, int D, bool GIVEN>
+cudaError_t launch_as(RotateArgs a, cudaStream_t s) {
     constexpr int U = kAtOnce<T, MODE>, lph = D / 16;
     const int heads = a.Hq + (MODE >= kAppend ? 2 : 1) * a.Hkv;
     const int parts = heads * lph <= kMaxThreads ? 1 : (heads * lph + 127) / 128;
@@ -376,13 +384,19 @@ cudaError_t launch(RotateArgs a, cudaStream_t s) {
     const dim3 grid((a.tokens - 1) / (U * a.span) + 1, parts);
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t cfg = dependent_launch(grid, threads, s, attr);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, rotate_kernel<T, MODE, D>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, rotate_kernel<T, MODE, D, GIVEN>, a);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <typename T, int MODE, int D>
+cudaError_t launch_d(const RotateArgs& a, cudaStream_t s) {
+    const bool given = a.rot > 0 && a.positions && (MODE >= kAppend || a.axes > 1);
+    return given ? launch_as<T, MODE, D, true>(a, s) : launch_as<T, MODE, D, false>(a, s);
 }
 
 template <typename T, int MODE>
 cudaError_t launch(const RotateArgs& a, cudaStream_t s) {
-    return a.d == 128 ? launch<T, MODE, 128>(a, s) : launch<T, MODE, 64>(a, s);
+    return a.d == 128 ? launch_d<T, MODE, 128>(a, s) : launch_d<T, MODE, 64>(a, s);
 }
 
 }  // namespace
