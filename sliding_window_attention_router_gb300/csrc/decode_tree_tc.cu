@@ -537,10 +537,8 @@ __device__ bool mma_issuer(const TreeDecodeArgs& a, const Ctx<D, E4M3>& c, uint3
                 tc_fence_after();
                 const uint64_t k = k0 + slot * (Z::kTile >> 4);
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    const uint64_t off = ((i >> 2) * kHalf + (i & 3) * 32) >> 4;
-                    umma_bf16_w(tmem + (tiles & 1) * K, q + off, k + off, kIdescS, i > 0 ? 1u : 0u);
-                }
+                for (int i = 0; i < D / 64; ++i)
+                    umma_bf16_x4_w(tmem + (tiles & 1) * K, q + i * (kHalf >> 4), k + i * (kHalf >> 4), 2, kIdescS, i > 0 ? 1u : 0u);
                 umma_commit_w(&c.bar[c.kSFull + (tiles & 1)]);
                 umma_commit_w(&c.bar[c.kEmpty + slot]);
                 if (j == n - 1) umma_commit_w(&c.bar[c.kQEmpty + buf]);
@@ -556,11 +554,11 @@ __device__ bool mma_issuer(const TreeDecodeArgs& a, const Ctx<D, E4M3>& c, uint3
                 for (int half = 0; half < 2; ++half) {
                     if (!wait_w(&c.bar[c.kPFull + (t & 1) * 2 + half], t >> 1 & 1, c.abort_flag, a.err)) return false;
                     tc_fence_after();
+                    static_assert(kHalfKeys == 64, "four steps");
 #pragma unroll
-                    for (int i = 0; i < 2 * kHalfKeys / 16; ++i)   // the nearest bf16, then what they leave
-                        umma_bf16_ts_w(tmem + kColO + half * D, tmem + (t & 1) * K + half * kHalfKeys + i * 8,
-                                       v + ((half * kHalfKeys + i % (kHalfKeys / 16) * 16) * 128 >> 4), kIdescO,
-                                       j == 1 && i == 0 ? 0u : 1u);
+                    for (int i = 0; i < 2; ++i)   // the nearest bf16, then what they leave
+                        umma_bf16_ts_x4_w(tmem + kColO + half * D, tmem + (t & 1) * K + half * kHalfKeys + i * 32,
+                                          v + (half * kHalfKeys * 128 >> 4), 16 * 128 >> 4, kIdescO, j == 1 && i == 0 ? 0u : 1u);
                 }
                 umma_commit_w(&c.bar[c.kEmpty + slot]);
                 umma_commit_w(&c.bar[j == n ? c.kOFull : c.kODone]);
