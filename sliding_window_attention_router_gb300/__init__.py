@@ -2,7 +2,8 @@
 
 Every function here marshals arguments to the C ABI declared in
 ``include/swiattn.h`` (same names, without the ``swiattn_`` prefix) and
-returns; all computation runs in the library's CUDA kernels.  PyTorch only
+returns, some through the compiled module ``_binding`` next to it; all
+computation runs in the library's CUDA kernels.  PyTorch only
 provides device memory and the current stream.  There is no fallback: if the
 shared library is missing, the first call raises.
 """
@@ -534,33 +535,6 @@ def _same(t, name: str, index: int, dtype=None):
     raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
 
 
-def _tokens(t, name: str, lead, index: int, dtype):
-    """Check q/k/v of one call, lead + [heads, d] on device `index` with packed heads and one
-    distance between tokens (a view of a fused projection is fine); returns (heads, d, that
-    distance in elements)."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != index:
-        raise ValueError(f"{name} must be a tensor on cuda:{index}")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    *rows, heads, d = t.shape
-    if rows != lead:
-        raise ValueError(f"{name} must be {lead} + [heads, d], got {list(t.shape)}")
-    if t.is_contiguous():
-        return heads, d, heads * d
-    *strides, head_step, last = t.stride()
-    if last != 1 or (heads > 1 and head_step != d):
-        raise ValueError(f"{name}: heads and their elements must be contiguous")
-    step, count = heads * d, 1
-    for size, stride in zip(reversed(rows), reversed(strides)):
-        if size > 1:   # dimensions of size 1 may have any stride
-            if count == 1:
-                step = stride
-            elif stride != count * step:
-                raise ValueError(f"{name}: tokens must be evenly spaced")
-            count *= size
-    return heads, d, step
-
-
 def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -577,62 +551,31 @@ def _launch(where: str, index: int, *args):
         raise SwiAttnError(status, where)
 
 
-def _axes(axes, half: int) -> bytes:
-    """The axis of each of `half` frequencies, as the library takes them."""
-    if isinstance(axes, torch.Tensor):
-        axes = axes.tolist()
-    axes = bytes(axes)   # refuses what is no whole number of 0 to 255
-    if len(axes) != half:
-        raise ValueError(f"axes must hold {half} values, one for each frequency, got {len(axes)}")
-    return axes
+_compiled = None
 
 
-def _rope(where, q, k, inv_freq, positions, axes, interleaved, factor, out):
-    some = q if q is not None else k
-    index = _gpu(some, "q and k")
-    if some.dim() != 4:
-        raise ValueError(f"q and k must be [B, N, heads, d], got {list(some.shape)}")
-    B, N, _, d = some.shape
-    lead, dtype = [B, N], some.dtype
-    kind = _DT[dtype]
-    results, sizes = [], []
-    for name, t, o in (("q", q, out and out[0]), ("k", k, out and out[1])):
-        if t is None:
-            if o is not None:
-                raise ValueError(f"out for {name}, which is None")
-            results.append(None)
-            sizes.append((0, 0, 0))
-            continue
-        heads, dt, step = _tokens(t, name, lead, index, dtype)
-        if dt != d:
-            raise ValueError("q and k must have one head size")
-        if o is None:
-            o, out_step = torch.empty(t.shape, dtype=dtype, device=t.device), heads * d
-        else:
-            oh, od, out_step = _tokens(o, f"out for {name}", lead, index, dtype)
-            if oh != heads or od != d:
-                raise ValueError(f"out for {name} must be {list(t.shape)}, got {list(o.shape)}")
-        results.append(o)
-        sizes.append((heads, step, out_step))
-    _same(inv_freq, "inv_freq", index, torch.float64)
-    (Hq, qs, qos), (Hkv, ks, kos) = sizes
-    more = ()
-    if axes is not None:
-        if positions is None:
-            raise ValueError("axes without positions")
-        shape = _same(positions, "positions", index, torch.int32).shape
-        if len(shape) != 3 or shape[1] != B or shape[2] != N:
-            raise ValueError(f"positions must be [axes, {B}, {N}], got {list(shape)}")
-        where = where.replace("rope", "rope_axes")
-        more = (_axes(axes, inv_freq.numel()), shape[0])
-    elif positions is not None and (
-            _same(positions, "positions", index, torch.int32).numel() != B * N):
-        raise ValueError(f"positions must be [{B}, {N}]")
-    if some.numel():
-        _launch(where, index, _addr(q), _addr(k), _addr(positions), *more, inv_freq.data_ptr(),
-                _addr(results[0]), _addr(results[1]), B, N, Hq, Hkv, d, 2 * inv_freq.numel(),
-                bool(interleaved), factor, qs, ks, qos, kos, kind)
-    return results[0], results[1]
+def _calls():
+    """The compiled part of this binding (csrc/binding.cpp), which checks and makes the calls below."""
+    global _compiled
+    if _compiled is None:
+        lib = _load()
+        from . import _binding
+        _binding.bind({name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+                       for name in EXPORTS}, SwiAttnError)
+        _compiled = _binding
+    return _compiled
+
+
+def _axes(axes) -> bytes:
+    """The axis of each frequency, as the library takes them."""
+    axes = axes.tolist() if isinstance(axes, torch.Tensor) else list(axes)
+    return bytes(axes)   # refuses what is no whole number of 0 to 255
+
+
+def _rope(backward, q, k, inv_freq, positions, axes, interleaved, factor, out):
+    q_out, k_out = out or (None, None)
+    return (_compiled or _calls()).rope(backward, q, k, inv_freq, positions, interleaved, factor,
+                                        q_out, k_out, axes if axes is None else _axes(axes))
 
 
 def rope(q, k, inv_freq, positions=None, interleaved: bool = False, factor: float = 1.0, out=None,
@@ -645,14 +588,13 @@ def rope(q, k, inv_freq, positions=None, interleaved: bool = False, factor: floa
     which may be (q, k) themselves (in place).
     axes: with positions int32 [A,B,N] on A axes (time, height, width), the axis that each
     frequency turns by, a sequence of rot_dim/2 whole numbers below A."""
-    return _rope("swiattn_rope", q, k, inv_freq, positions, axes, interleaved, factor, out)
+    return _rope(False, q, k, inv_freq, positions, axes, interleaved, factor, out)
 
 
 def rope_backward(dq_rot, dk_rot, inv_freq, positions=None, interleaved: bool = False,
                   factor: float = 1.0, out=None, axes=None):
     """Gradient of rope: (dq, dk) from the gradients of its outputs.  Arguments as for rope."""
-    return _rope("swiattn_rope_backward", dq_rot, dk_rot, inv_freq, positions, axes, interleaved,
-                 factor, out)
+    return _rope(True, dq_rot, dk_rot, inv_freq, positions, axes, interleaved, factor, out)
 
 
 _EXPONENTS = (torch.uint8, torch.float8_e8m0fnu)
@@ -681,61 +623,9 @@ def append_paged(q, k, v, k_pages, v_pages, block_table, seq_lens, inv_freq=None
     positions int32 [T]: the positions to rotate by, where they are not those of the tokens in
     their sequences (the tokens of a drafted tree: see decode_tree); or, with axes (as for rope),
     int32 [A,T]."""
-    index = _gpu(k, "k")
-    T, dtype = k.shape[0], k.dtype
-    lead = [T]
-    Hkv, d, ks = _tokens(k, "k", lead, index, dtype)
-    vh, vd, vs = _tokens(v, "v", lead, index, dtype)
-    if vh != Hkv or vd != d:
-        raise ValueError("k and v must have one shape")
-    Hq, qs = 0, 0
-    if q is not None:
-        Hq, qd, qs = _tokens(q, "q", lead, index, dtype)
-        if qd != d:
-            raise ValueError("q and k must have one head size")
-        if out is None:
-            out = torch.empty(q.shape, dtype=dtype, device=q.device)
-        elif _same(out, "out", index, dtype).shape != q.shape:
-            raise ValueError(f"out must be {list(q.shape)}, got {list(out.shape)}")
-    elif out is not None:
-        raise ValueError("out without q")
-    page_dtype = _same(k_pages, "k_pages", index).dtype
-    _same(v_pages, "v_pages", index, page_dtype)
-    shape = k_pages.shape
-    if len(shape) != 4 or shape[2] != Hkv or shape[3] != d or v_pages.shape != shape:
-        raise ValueError("k_pages and v_pages must be [num_pages, page_size, Hkv, d]")
-    if page_dtype is torch.float8_e4m3fn:
-        _exponents(k_exp, "k_exp", index, (shape[0], Hkv, shape[1]))
-        _exponents(v_exp, "v_exp", index, (shape[0], Hkv, shape[1]))
-        kind, ke, ve = E4M3, k_exp.data_ptr(), v_exp.data_ptr()
-    elif page_dtype is dtype:
-        kind, ke, ve = _DT[dtype], None, None
-    else:
-        raise ValueError(f"pages must be {dtype} or float8_e4m3fn, got {page_dtype}")
-    B = _same(seq_lens, "seq_lens", index, torch.int32).numel()
-    table = _same(block_table, "block_table", index, torch.int32).shape
-    if len(table) != 2 or table[0] != B:
-        raise ValueError(f"block_table must be [{B}, max_pages]")
-    if starts is not None and _same(starts, "starts", index, torch.int32).numel() != B + 1:
-        raise ValueError(f"starts must hold {B + 1} values")
-    rot_dim = 0
-    if inv_freq is not None:
-        rot_dim = 2 * _same(inv_freq, "inv_freq", index, torch.float64).numel()
-    where, more = "swiattn_append_paged", ()
-    if positions is not None or axes is not None:
-        if inv_freq is None or positions is None:
-            raise ValueError("positions turn by inv_freq, and axes are of positions")
-        given = _same(positions, "positions", index, torch.int32).shape
-        if len(given) != (1 if axes is None else 2) or given[-1] != T:
-            raise ValueError(f"positions must be [{T}], or [axes, {T}] with axes, got {list(given)}")
-        where = "swiattn_append_paged_at"
-        more = (positions.data_ptr(), None if axes is None else _axes(axes, rot_dim // 2),
-                1 if axes is None else given[0])
-    _launch(where, index, _addr(q), k.data_ptr(), v.data_ptr(), _addr(starts),
-            seq_lens.data_ptr(), block_table.data_ptr(), *more, _addr(inv_freq), _addr(out),
-            k_pages.data_ptr(), v_pages.data_ptr(), ke, ve, T, B, table[1], shape[1],
-            shape[0], Hq, Hkv, d, rot_dim, bool(interleaved), factor, qs, ks, vs, _DT[dtype], kind)
-    return out
+    return (_compiled or _calls()).append_paged(
+        q, k, v, k_pages, v_pages, block_table, seq_lens, inv_freq, starts, interleaved, factor, k_exp,
+        v_exp, out, positions, axes if axes is None else _axes(axes))
 
 
 def decode_paged_e4m3_workspace(B, max_pages, page_size, Hq, Hkv, d, W, n_anchor=0) -> int:
@@ -786,48 +676,6 @@ def decode_paged_e4m3(q, k_pages, v_pages, k_exp, v_exp, block_table, seq_lens, 
     return (out, lse) if want_lse else out
 
 
-_PAGE_TYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float8_e4m3fn: E4M3}
-
-
-def _pools(k_pages, v_pages, k_exp, v_exp, index: int):
-    """Check page pools of one layer [num_pages, page_size, Hkv, d] or of several
-    [layers, num_pages, page_size, Hkv, d]; returns the pointers and (layers, num_pages, page_size,
-    Hkv, d, page type)."""
-    shape, dtype = _same(k_pages, "k_pages", index).shape, k_pages.dtype
-    if _same(v_pages, "v_pages", index, dtype).shape != shape or len(shape) not in (4, 5):
-        raise ValueError("k_pages and v_pages must both be [num_pages, page_size, Hkv, d] or "
-                         "[layers, num_pages, page_size, Hkv, d]")
-    kind = _PAGE_TYPES.get(dtype)
-    if kind is None:
-        raise ValueError(f"pages must be float32, bfloat16 or float8_e4m3fn, got {dtype}")
-    num_pages, page_size, Hkv, d = shape[-4:]
-    ke = ve = None
-    if kind == E4M3:
-        want = (*shape[:-4], num_pages, Hkv, page_size)
-        _exponents(k_exp, "k_exp", index, want)
-        _exponents(v_exp, "v_exp", index, want)
-        ke, ve = k_exp.data_ptr(), v_exp.data_ptr()
-    return ((k_pages.data_ptr(), v_pages.data_ptr(), ke, ve),
-            (shape[0] if len(shape) == 5 else 1, num_pages, page_size, Hkv, d, kind))
-
-
-def _sequences(block_table, seq_lens, index: int):
-    """Check block_table [B, max_pages] and seq_lens [B]; returns (B, max_pages)."""
-    B = _same(seq_lens, "seq_lens", index, torch.int32).numel()
-    table = _same(block_table, "block_table", index, torch.int32).shape
-    if len(table) != 2 or table[0] != B:
-        raise ValueError(f"block_table must be [{B}, max_pages]")
-    return B, table[1]
-
-
-def _trees(starts, parents, B: int, index: int):
-    """Check starts [B + 1] and parents [T] (None: chains)."""
-    if _same(starts, "starts", index, torch.int32).numel() != B + 1:
-        raise ValueError(f"starts must hold {B + 1} values")
-    if parents is not None and _same(parents, "parents", index, torch.int32).dim() != 1:
-        raise ValueError("parents must be [T]")
-
-
 def decode_tree_workspace(T, B, Hq, Hkv, d, dtype) -> int:
     return int(_load().swiattn_decode_tree_workspace(T, B, Hq, Hkv, d, _DT.get(dtype, dtype)))
 
@@ -843,36 +691,9 @@ def decode_tree(q, k_pages, v_pages, block_table, seq_lens, starts, parents, gat
     [num_pages, Hkv, page_size] for bf16 q; block_table int32 [B, max_pages].  Returns o [T,Hq,d]
     (and lse fp32 [T,Hq]); rows that no sequence owns are left as they were (a result allocated
     here: undefined)."""
-    index = _gpu(q, "q")
-    _same(q, "q", index)
-    if q.dim() != 3:
-        raise ValueError(f"q must be [T, Hq, d], got {list(q.shape)}")
-    T, Hq, d = q.shape
-    dtype = _DT[q.dtype]
-    pointers, (_, num_pages, page_size, Hkv, dk, kind) = _pools(k_pages, v_pages, k_exp, v_exp, index)
-    if k_pages.dim() != 4 or dk != d:
-        raise ValueError("k_pages and v_pages must be [num_pages, page_size, Hkv, d]")
-    B, max_pages = _sequences(block_table, seq_lens, index)
-    _trees(starts, parents, B, index)
-    if (parents is not None and parents.numel() != T) or (
-            _same(gate, "gate", index, torch.uint8).numel() != T):
-        raise ValueError(f"parents and gate must hold {T} values")
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    if out is None:
-        out = torch.empty_like(q)
-    elif _same(out, "out", index, q.dtype).shape != q.shape:
-        raise ValueError(f"out must be {list(q.shape)}, got {list(out.shape)}")
-    lse = torch.empty((T, Hq), device=q.device, dtype=torch.float32) if want_lse else None
-    if workspace is None:
-        workspace = _workspace(decode_tree_workspace(T, B, Hq, Hkv, d, dtype), q.device, None)
-    else:
-        _same(workspace, "workspace", index, torch.uint8)
-    _launch("swiattn_decode_tree", index, q.data_ptr(), *pointers, block_table.data_ptr(),
-            seq_lens.data_ptr(), starts.data_ptr(), _addr(parents), gate.data_ptr(), out.data_ptr(),
-            _addr(lse), T, B, max_pages, page_size, num_pages, Hq, Hkv, d, W, n_anchor, scale, dtype,
-            kind, workspace.data_ptr(), workspace.numel())
-    return (out, lse) if want_lse else out
+    return (_compiled or _calls()).decode_tree(
+        q, k_pages, v_pages, block_table, seq_lens, starts, parents, gate, W, scale, out, want_lse,
+        workspace, n_anchor, k_exp, v_exp)
 
 
 def accept_tree(k_pages, v_pages, block_table, seq_lens, starts, parents, leaf, k_exp=None,
@@ -883,22 +704,8 @@ def accept_tree(k_pages, v_pages, block_table, seq_lens, starts, parents, leaf, 
     layer's [num_pages, page_size, Hkv, d], float8_e4m3fn with k_exp, v_exp [..., num_pages, Hkv,
     page_size]; block_table, seq_lens, starts, parents as for decode_tree.  The pages are written in
     place; returns the new lengths, int32 [B] (out, if given; not seq_lens itself)."""
-    index = _gpu(k_pages, "k_pages")
-    pointers, (layers, num_pages, page_size, Hkv, d, kind) = _pools(k_pages, v_pages, k_exp, v_exp,
-                                                                    index)
-    B, max_pages = _sequences(block_table, seq_lens, index)
-    _trees(starts, parents, B, index)
-    if _same(leaf, "leaf", index, torch.int32).numel() != B:
-        raise ValueError(f"leaf must hold {B} values")
-    if out is None:
-        out = torch.empty_like(seq_lens)
-    elif _same(out, "out", index, torch.int32).numel() != B:
-        raise ValueError(f"out must hold {B} values")
-    T = (1 << 31) - 1 if parents is None else parents.numel()
-    _launch("swiattn_accept_tree", index, *pointers, block_table.data_ptr(), seq_lens.data_ptr(),
-            starts.data_ptr(), _addr(parents), leaf.data_ptr(), out.data_ptr(), layers, T, B,
-            max_pages, page_size, num_pages, Hkv, d, kind)
-    return out
+    return (_compiled or _calls()).accept_tree(k_pages, v_pages, block_table, seq_lens, starts, parents,
+                                               leaf, k_exp, v_exp, out)
 
 
 def fork_paged(k_pages, v_pages, block_table, seq_lens, source, new_page, k_exp=None, v_exp=None,
@@ -908,22 +715,6 @@ def fork_paged(k_pages, v_pages, block_table, seq_lens, source, new_page, k_exp=
     last page copied to page new_page[c] (int32 [C]; negative: no page of its own).  Pools as for
     accept_tree; block_table int32 [B, max_pages], seq_lens int32 [B].  Returns the children's
     (block_table int32 [C, max_pages], seq_lens int32 [C]) (out, if given)."""
-    index = _gpu(k_pages, "k_pages")
-    pointers, (layers, num_pages, page_size, Hkv, d, kind) = _pools(k_pages, v_pages, k_exp, v_exp,
-                                                                    index)
-    B, max_pages = _sequences(block_table, seq_lens, index)
-    C = _same(source, "source", index, torch.int32).numel()
-    if _same(new_page, "new_page", index, torch.int32).numel() != C:
-        raise ValueError(f"new_page must hold {C} values")
-    if out is None:
-        table = torch.empty((C, max_pages), dtype=torch.int32, device=k_pages.device)
-        lens = torch.empty(C, dtype=torch.int32, device=k_pages.device)
-    else:
-        table, lens = out
-        if _same(table, "out", index, torch.int32).shape != (C, max_pages) or (
-                _same(lens, "out", index, torch.int32).numel() != C):
-            raise ValueError(f"out must be [{C}, {max_pages}] and [{C}]")
-    _launch("swiattn_fork_paged", index, *pointers, block_table.data_ptr(), seq_lens.data_ptr(),
-            source.data_ptr(), new_page.data_ptr(), table.data_ptr(), lens.data_ptr(), layers, B, C,
-            max_pages, page_size, num_pages, Hkv, d, kind)
-    return table, lens
+    table, lens = out or (None, None)
+    return (_compiled or _calls()).fork_paged(k_pages, v_pages, block_table, seq_lens, source, new_page,
+                                              k_exp, v_exp, table, lens)
