@@ -513,8 +513,9 @@ size_t swiattn_decode_tree_workspace(int T, int B, int Hq, int Hkv, int d, int d
  *    before its token counts as negative; a table entry outside [0, num_pages) is
  *    read as page 0.  Each is reported: swiattn_get_device_error returns
  *    SWIATTN_EINVAL.
+ *  - o must not overlap q.  scale times log2 e has to be a finite fp32.
  * d in {64, 128}; Hq / Hkv any whole number up to 128, B <= 65535, Hkv <= 2^16,
- * T * Hq <= 2^26, num_pages * page_size <= 2^32 (larger: SWIATTN_EUNSUPPORTED);
+ * T * Hq <= 2^26, num_pages * page_size <= 2^31 (larger: SWIATTN_EUNSUPPORTED);
  * page_size a power of two, max_pages * page_size <= 2^30; T == 0 is a valid no-op.
  * Bitwise repeatable; how a sequence's keys are split for the GPU depends on the
  * whole batch, so the last bits of its result may.
@@ -540,7 +541,8 @@ int swiattn_decode_tree(const void* q, const void* k_pages, const void* v_pages,
  *  - seq_lens, starts, parents, T: as swiattn_decode_tree took them.  leaf int32
  *    [B]: the path's last token, counted from the tree's first; negative: none of
  *    the tree is kept.  lens_out int32 [B] receives the new lengths; it must not
- *    overlap seq_lens.  A sequence without drafted tokens keeps its length.
+ *    overlap an input.  A sequence without drafted tokens keeps its length, and so does an
+ *    empty slot (seq_lens[b] == 0), whatever its starts and leaf.
  *  - Only the path's slots are written; rows behind them stay as they are.
  *  - A sequence with more than 256 drafted tokens, with fewer tokens than
  *    drafted ones, with a length or starts outside their range, or with leaf not
@@ -568,7 +570,7 @@ int swiattn_accept_tree(void* k_pages, void* v_pages, uint8_t* k_exp, uint8_t* v
  *    the table has room, with nothing copied.  Negative: the child keeps the
  *    source's table (one child may go on in the source's own page).
  *  - table_out int32 [C, max_pages] and lens_out int32 [C] receive the children's
- *    tables and lengths; they must not overlap block_table and seq_lens.
+ *    tables and lengths; they must not overlap each other or an input.
  *  - Pools as for swiattn_accept_tree.  No two children may be given one page, nor
  *    a page that a source ends in other than its own.  Rows of a new page past the
  *    copied ones stay as they are.
@@ -596,10 +598,11 @@ const char* swiattn_status_string(int status);
 
 /* Timing hook.  When both are non-NULL, every later swiattn_prefill,
  * swiattn_decode, swiattn_dual_branch, swiattn_prefill_backward, swiattn_route,
- * swiattn_route_backward, swiattn_rope(_backward), swiattn_append_paged and
- * swiattn_decode_paged_e4m3 call records `start` (a cudaEvent_t passed as
+ * swiattn_route_backward, swiattn_rope(_backward), swiattn_rope_axes(_backward),
+ * swiattn_append_paged(_at), swiattn_decode_paged_e4m3 and swiattn_decode_tree call
+ * records `start` (a cudaEvent_t passed as
  * void*) on its stream immediately before launching its dominant kernel (the
- * attention kernel, the decode split kernel, the backward's two attention
+ * attention kernel, the decode split kernel, the tree attention's product kernel, the backward's two attention
  * kernels, dK/dV then dQ, the router GEMV, or the router backward's three
  * kernels) and `stop` immediately after it, so cudaEventElapsedTime gives that
  * kernel's device time alone.  Passing NULL, NULL turns the hook off.  Process-wide setting;
@@ -612,7 +615,7 @@ int swiattn_num_sms(void);
 
 /* Failure-detection aid with no counterpart in the paper: sets, on the
  * current device, how long a device-side wait of the tensor-core kernels
- * (routed prefill, dual branch, backward) and of the decode over e4m3 pages
+ * (routed prefill, dual branch, backward, tree attention) and of the decode over e4m3 pages
  * (of 16 tokens and more) may last before the kernel gives up,
  * records SWIATTN_ETIMEOUT for swiattn_get_device_error and returns early
  * without computing the rest of its work; ns = 0 restores the default of 2 s.

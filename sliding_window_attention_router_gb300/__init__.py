@@ -703,7 +703,7 @@ def accept_tree(k_pages, v_pages, block_table, seq_lens, starts, parents, leaf, 
     move to the tree's first slots.  k_pages, v_pages [layers, num_pages, page_size, Hkv, d] or one
     layer's [num_pages, page_size, Hkv, d], float8_e4m3fn with k_exp, v_exp [..., num_pages, Hkv,
     page_size]; block_table, seq_lens, starts, parents as for decode_tree.  The pages are written in
-    place; returns the new lengths, int32 [B] (out, if given; not seq_lens itself)."""
+    place; returns the new lengths, int32 [B] (out, if given; not one of the inputs)."""
     return (_compiled or _calls()).accept_tree(k_pages, v_pages, block_table, seq_lens, starts, parents,
                                                leaf, k_exp, v_exp, out)
 

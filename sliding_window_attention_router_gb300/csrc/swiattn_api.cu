@@ -1030,9 +1030,11 @@ PagingArgs paging_args(void* k_pages, void* v_pages, uint8_t* k_exp, uint8_t* v_
     return a;
 }
 
-}  // namespace
-
-namespace {
+// Whether two buffers share bytes (one that is not given shares none).
+bool overlap(const void* p, int64_t p_bytes, const void* q, int64_t q_bytes) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return p && q && a < b + q_bytes && b < a + p_bytes;
+}
 
 // Sizes of a tree attention: SWIATTN_OK, or why not.
 int decode_tree_sizes_ok(int T, int B, int Hq, int Hkv, int d, int dtype) {
@@ -1063,12 +1065,16 @@ int swiattn_decode_tree(const void* q, const void* k_pages, const void* v_pages,
     if (ok == SWIATTN_EINVAL || pools == SWIATTN_EINVAL || W <= 0 || n_anchor < 0) return SWIATTN_EINVAL;
     if (page_dtype != dtype && page_dtype != SWIATTN_E4M3) return SWIATTN_EINVAL;
     if (page_dtype == SWIATTN_E4M3 && (!aligned16(k_exp) || !aligned16(v_exp))) return SWIATTN_EINVAL;
-    if (!(scale > 0.f) || !(scale - scale == 0.f)) return SWIATTN_EINVAL;
+    const float scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+    if (!(scale > 0.f) || !(scale_log2 - scale_log2 == 0.f)) return SWIATTN_EINVAL;
     if (!starts) return SWIATTN_EINVAL;
     if (ok != SWIATTN_OK || (page_dtype == SWIATTN_E4M3 && dtype != SWIATTN_BF16)) return SWIATTN_EUNSUPPORTED;
-    if ((int64_t)num_pages * page_size > (int64_t(1) << 32)) return SWIATTN_EUNSUPPORTED;
+    // A row of the pool is a coordinate of the tile copies, which is signed.
+    if ((int64_t)num_pages * page_size > (int64_t(1) << 31)) return SWIATTN_EUNSUPPORTED;
     if (T == 0) return SWIATTN_OK;
     if (!q || !gate || !o || !aligned16(q) || !aligned16(o)) return SWIATTN_EINVAL;
+    const int64_t bytes = (int64_t)T * Hq * d * (dtype == SWIATTN_F32 ? 4 : 2);
+    if (overlap(q, bytes, o, bytes)) return SWIATTN_EINVAL;
     const TreeWs L = tree_ws_layout(T, B, Hq, Hkv, d, dtype);
     if (!workspace || !aligned256(workspace) || workspace_bytes < L.total) return SWIATTN_EINVAL;
     DeviceInfo di;
@@ -1105,7 +1111,7 @@ int swiattn_decode_tree(const void* q, const void* k_pages, const void* v_pages,
     a.Hkv = Hkv;
     a.W = W;
     a.n_anchor = n_anchor;
-    a.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+    a.scale_log2 = scale_log2;
     return launched(launch_decode_tree(a, d, page_dtype, di.sms, static_cast<cudaStream_t>(stream)));
 }
 
@@ -1119,6 +1125,10 @@ int swiattn_accept_tree(void* k_pages, void* v_pages, uint8_t* k_exp, uint8_t* v
     if (ok == SWIATTN_EINVAL || T < 0 || !starts || !leaf || !lens_out || lens_out == seq_lens)
         return SWIATTN_EINVAL;
     if (ok != SWIATTN_OK) return ok;
+    const int64_t n = 4 * (int64_t)B;   // several blocks read what one of them would have overwritten
+    if (overlap(lens_out, n, seq_lens, n) || overlap(lens_out, n, leaf, n) || overlap(lens_out, n, starts, n + 4) ||
+        overlap(lens_out, n, block_table, n * max_pages))
+        return SWIATTN_EINVAL;
     DeviceInfo di;
     if (!device_info(di)) return SWIATTN_ECUDA;
     PagingArgs a = paging_args(k_pages, v_pages, k_exp, v_exp, block_table, seq_lens, layers, B,
@@ -1148,6 +1158,13 @@ int swiattn_fork_paged(void* k_pages, void* v_pages, uint8_t* k_exp, uint8_t* v_
     if (!source || !new_page || !table_out || !lens_out || table_out == block_table || lens_out == seq_lens)
         return SWIATTN_EINVAL;
     if (ok != SWIATTN_OK) return ok;
+    const int64_t n = 4 * (int64_t)C, m = 4 * (int64_t)B;
+    const struct { void* p; int64_t bytes; } outs[2] = {{table_out, n * max_pages}, {lens_out, n}};
+    for (const auto& x : outs)
+        if (overlap(x.p, x.bytes, seq_lens, m) || overlap(x.p, x.bytes, block_table, m * max_pages) ||
+            overlap(x.p, x.bytes, source, n) || overlap(x.p, x.bytes, new_page, n))
+            return SWIATTN_EINVAL;
+    if (overlap(table_out, n * max_pages, lens_out, n)) return SWIATTN_EINVAL;
     DeviceInfo di;
     if (!device_info(di)) return SWIATTN_ECUDA;
     PagingArgs a = paging_args(k_pages, v_pages, k_exp, v_exp, block_table, seq_lens, layers, B,

@@ -100,3 +100,29 @@ def test_decode_tree_refusals_and_workspace(lib):
     for bad in (dict(Hq=258), dict(B=1 << 16), dict(dt=F32, pdt=E4M3), dict(np_=1 << 30)):
         assert call(**bad) == EUNSUPPORTED, bad
     assert call(T=0, q=None, o=None, gate=None, ws=None) == OK
+
+
+def test_outputs_that_overlap_inputs_are_refused(lib):
+    """Several blocks read what one of them writes over; apart by no more than a byte's width is apart."""
+    at = 1 << 20
+
+    def accept(bt=0x10000, sl=0x20000, st=0x30000, leaf=0x40000, out=at, B=3, mp=4):
+        return lib.swiattn_accept_tree(FAKE, BIG, None, None, bt, sl, st, None, leaf, out, 1, 9, B, mp, 16, 12, 2, 128, BF16, None)
+    for bad in (dict(leaf=at), dict(leaf=at + 8), dict(leaf=at - 8), dict(sl=at + 8), dict(sl=at - 8), dict(st=at - 12),
+                dict(st=at + 8), dict(bt=at - 44), dict(bt=at + 8)):
+        assert accept(**bad) == EINVAL, bad
+
+    def fork(bt=0x10000, sl=0x20000, src=0x30000, new=0x40000, to=at, lo=2 * at, B=3, C=4, mp=4):
+        return lib.swiattn_fork_paged(FAKE, BIG, None, None, bt, sl, src, new, to, lo, 1, B, C, mp, 16, 12, 2, 128, BF16, None)
+    for out, size in ((at, 64), (2 * at, 16)):
+        for bad in (dict(bt=out + size - 4), dict(bt=out - 44), dict(sl=out - 8), dict(sl=out + size - 4), dict(src=out),
+                    dict(src=out - 12), dict(new=out + size - 4), dict(new=out - 12)):
+            assert fork(**bad) == EINVAL, bad
+    assert fork(lo=at + 60) == EINVAL and fork(lo=at - 12) == EINVAL
+
+    def tree(q=at, o=2 * at, scale=0.1, T=2, np_=30):
+        return lib.swiattn_decode_tree(q, FAKE, BIG, None, None, FAKE, FAKE, FAKE, FAKE, FAKE, o, None, T, 1, 8, 16, np_, 4, 2,
+                                       128, 64, 0, scale, BF16, BF16, FAKE, 1 << 40, None)
+    for bad in (dict(o=at), dict(o=at + 2032), dict(o=at - 2032), dict(scale=3e38)):
+        assert tree(**bad) == EINVAL, bad
+    assert tree(np_=(1 << 27) + 1) == EUNSUPPORTED
