@@ -2,10 +2,16 @@
 // (drafted tokens times the query heads of a key head) by 128 keys at a time.
 //
 // Per key tile: S = Q K^T into TMEM, softmax weights P written back over S as two
-// bf16 each, O += P V with P from TMEM.  What bounds it is the cache's bytes: a tile
-// of 128 keys is 64 KiB (bf16, d = 128), 1466 ns of an SM's share of the copy
+// bf16 each, O += P V with P from TMEM.  What bounds it over bf16 pages is the cache's
+// bytes: a tile of 128 keys is 64 KiB (d = 128), 1466 ns of an SM's share of the copy
 // bandwidth, against 1536 tensor cycles (0.8 us) and about as many of the softmax,
-// overlapped: S of the next tile is computed while the weights of this one are.
+// overlapped: S of the next tile is computed while the weights of this one are.  16
+// sequences of 32K, 16 key heads of one row tile, 4.03 GB: 605 us, 98 % of the copy
+// rate.  33 ragged trees (d = 64, tens of units a CTA, of one to five key tiles): 95 us,
+// 19 %, a unit's chain of Q, S, weights and O, of which two are on their way at once.
+// Over e4m3 pages it is bound by instructions: 8 sequences of 32K with 4 key heads of
+// 128 rows, 273 MB: 139 us (29 %); a tile's bytes would take 733 ns, its conversion and
+// its softmax, on the same four schedulers, are about 2600 cycles each.
 //
 // The weights go in as two bf16, the nearest and what it leaves, right to 2^-17 of
 // each: the products of fp32 weights to less than the result's own rounding.  With
@@ -61,7 +67,7 @@ template <int D, bool E4M3>
 struct Sizes {
     static constexpr int kTile = R * D * 2;                    // Q, and a slot of the ring
     // Q's tiles: two, so that a unit's comes while the one before is worked on, where
-    // there is room (33 ragged trees, D 64: QFIG).
+    // there is room (33 ragged trees, D 64: 120 us with one, 118 with two).
     static constexpr int kQ = E4M3 && D == 128 ? 1 : 2;
     static constexpr int kSlots = E4M3 ? 4 * 128 / D : 6 * 128 / D - (kQ - 1);
     static constexpr int kRaw = E4M3 ? 4 * 128 / D : 0;        // tiles as they are in the pages
@@ -104,6 +110,49 @@ __device__ __forceinline__ bool wait_w(uint64_t* bar, uint32_t parity, volatile 
     if (__all_sync(0xffffffffu, there)) return true;
     const bool ok = mbar_wait_on(bar, parity, abort_flag, err);
     return __all_sync(0xffffffffu, ok);
+}
+
+// As tma_load_4d, by shared-memory address.
+__device__ __forceinline__ void tma_load_4d_at(uint32_t smem_dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1,
+                                               int c2, int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// Four steps of 16 along K by one election: D (+)= A B with A and B in shared memory,
+// `step` (a descriptor's units, bytes / 16) apart.  `accumulate` is the first step's.
+__device__ __forceinline__ void umma_bf16_x4_w(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t step,
+                                               uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred e, p;\n\t.reg .b64 a1, a2, a3, b1, b2, b3, s;\n\t"
+        "cvt.u64.u32 s, %5;\n\tadd.s64 a1, %1, s;\n\tadd.s64 b1, %2, s;\n\tadd.s64 a2, a1, s;\n\tadd.s64 b2, b1, s;\n\t"
+        "add.s64 a3, a2, s;\n\tadd.s64 b3, b2, s;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, 1;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, 1;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, 1;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(step)
+        : "memory");
+}
+
+// The same with A in TMEM, 8 columns a step.
+__device__ __forceinline__ void umma_bf16_ts_x4_w(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t step,
+                                                  uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred e, p;\n\t.reg .b64 b1, b2, b3, s;\n\t.reg .b32 a1, a2, a3;\n\t"
+        "cvt.u64.u32 s, %5;\n\tadd.s64 b1, %2, s;\n\tadd.s64 b2, b1, s;\n\tadd.s64 b3, b2, s;\n\t"
+        "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, 1;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, 1;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, 1;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(step)
+        : "memory");
 }
 
 // ---- K and V -----------------------------------------------------------------------
@@ -387,8 +436,9 @@ __device__ bool raw_loader(const TreeDecodeArgs& a, const Ctx<D, true>& c, const
 }
 
 // From that ring to the products': four warps K's tiles, four V's, 32 rows a warp.  The
-// conversion is bound by the integer pipe (a warp's instruction takes it two cycles),
-// so its addresses are constants: a lane has one row a of every eight and one of four
+// conversion is bound by the instructions that it issues (the SM's own rate, shared with
+// the softmax: shifts written as products, which another pipe runs, changed nothing), so
+// its addresses are constants: a lane has one row a of every eight and one of four
 // pieces of half a row.  Eight lanes hold rows a and a ^ 5, whose pieces differ in
 // their banks both in the pages' layout and, two for one, in the products'.
 template <int D>
