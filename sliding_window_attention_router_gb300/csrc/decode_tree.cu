@@ -418,10 +418,10 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(const __grid
     const TreeSeq s = a.plan.seqs[b];
     if (s.n == 0) return;
     const int far = far_tiles<R>(s), near_rows = s.n * G - s.far_rows;
-    const int64_t head = a.plan.start[a.B], total = head * a.Hkv, start = a.plan.start[b];   // tiles of a head, of all
-    const int unit = a.plan.unit[b], head_units = a.plan.unit[a.B];
+    const int64_t head = a.plan.start[a.B], total = head * a.Hkv, start = a.plan.start[b];   // work of a head, of all
+    const int unit = a.plan.unit[b], head_units = a.plan.unit[a.B], cost = a.plan.cost[0];
     const int64_t shares = share_count(total, ctas);
-    auto cta_of = [&](int64_t tile) { return static_cast<int>(((tile + 1) * shares - 1) / total); };
+    auto cta_of = [&](int64_t at) { return static_cast<int>(((at + 1) * shares - 1) / total); };
     const int far_chunks = (s.far_rows + 31) / 32, chunks = far_chunks + (near_rows + 31) / 32;
     if (threadIdx.x < 2) s_bad[threadIdx.x] = 0;
     __syncthreads();
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(const __grid
         const int tok = s.first + a.plan.order[s.first + row / G];
         const int64_t out = static_cast<int64_t>(tok) * a.Hq + h * G + row % G;
         const int len = is_far ? s.far_tiles : s.near_tiles;
-        const int64_t from = h * head + start + static_cast<int64_t>(rt) * len + (is_far ? 0 : static_cast<int64_t>(far) * s.far_tiles);
+        const int64_t from = h * head + start + cost + static_cast<int64_t>(rt) * (len + cost) + (is_far ? 0 : static_cast<int64_t>(far) * (s.far_tiles + cost));   // its first key tile
         const int c0 = cta_of(from);
         constexpr int kOf = kPart / R;   // parts of a CTA
         const int n = (cta_of(from + len - 1) - c0 + 1) * kOf;
@@ -608,7 +608,8 @@ TreeWs tree_ws_layout(int T, int B, int Hq, int Hkv, int d, int dtype) {
     L.seqs = 0;
     L.start = up(sizeof(int) * 8 * b);
     L.unit = up(L.start + sizeof(int64_t) * (b + 1));
-    L.order = up(L.unit + sizeof(int) * (b + 1));
+    L.cost = L.unit + sizeof(int) * (b + 1);
+    L.order = up(L.cost + sizeof(int));
     L.lo = up(L.order + sizeof(int) * t);
     L.mask = up(L.lo + sizeof(int) * t);
     L.part = up(L.mask + sizeof(uint32_t) * kWords * t);

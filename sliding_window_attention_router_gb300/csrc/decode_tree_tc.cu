@@ -7,8 +7,8 @@
 // bandwidth, against 1536 tensor cycles (0.8 us) and about as many of the softmax,
 // overlapped: S of the next tile is computed while the weights of this one are.  16
 // sequences of 32K, 16 key heads of one row tile, 4.03 GB: 605 us, 98 % of the copy
-// rate.  33 ragged trees (d = 64, tens of units a CTA, of one to five key tiles): 95 us,
-// 19 %, a unit's chain of Q, S, weights and O, of which two are on their way at once.
+// rate.  33 ragged trees (d = 64, tens of units a CTA, of one to five key tiles): 90 us,
+// 20 %, a unit's chain of Q, S, weights and O, of which two are on their way at once.
 // Over e4m3 pages it is bound by instructions: 8 sequences of 32K with 4 key heads of
 // 128 rows, 273 MB: 139 us (29 %); a tile's bytes would take 733 ns, its conversion and
 // its softmax, on the same four schedulers, are about 2600 cycles each.
@@ -452,8 +452,14 @@ __device__ bool converter(const TreeDecodeArgs& a, const Ctx<D, true>& c, int wh
     const uint32_t to0 = to + ((2 * quarter ^ row) << 4), to1 = to + (((2 * quarter + 1) ^ row) << 4);
     const uint8_t* exps = c.smem + Z::kOffExp + w32 * 32 + row;
     const uint32_t* read = reinterpret_cast<const uint32_t*>(c.smem + Z::kOffRead) + w32;
-    const uint32_t tiles = static_cast<uint32_t>(c.start->end - c.start->at);
-    for (uint32_t t = 0; t < tiles; ++t) {
+    TreeWalk<R> walk{a, *c.start};
+    uint32_t left = 0;   // of the unit's tiles
+    for (uint32_t t = 0;; ++t, --left) {
+        if (left == 0) {
+            TreeWork w;
+            if (!walk.next(w)) return true;
+            left = w.kt1 - w.kt0;
+        }
         const uint32_t slot = which * Z::kOwn + t % Z::kOwn, from = which * Z::kOwnRaw + t % Z::kOwnRaw;
         if (!wait_w(&c.bar[c.kRawFull + from], t / Z::kOwnRaw & 1, c.abort_flag, a.err)) return false;
         if (!wait_w(&c.bar[c.kEmpty + slot], (t / Z::kOwn & 1) ^ 1, c.abort_flag, a.err)) return false;
@@ -499,7 +505,6 @@ __device__ bool converter(const TreeDecodeArgs& a, const Ctx<D, true>& c, int wh
             mbar_arrive(&c.bar[c.kRawEmpty + from]);
         }
     }
-    return true;
 }
 
 // The copies in flight of a call that gave up.

@@ -1096,6 +1096,7 @@ int swiattn_decode_tree(const void* q, const void* k_pages, const void* v_pages,
     a.plan.seqs = reinterpret_cast<TreeSeq*>(ws + L.seqs);
     a.plan.start = reinterpret_cast<int64_t*>(ws + L.start);
     a.plan.unit = reinterpret_cast<int*>(ws + L.unit);
+    a.plan.cost = reinterpret_cast<int*>(ws + L.cost);
     a.plan.order = reinterpret_cast<int*>(ws + L.order);
     a.plan.lo = reinterpret_cast<int*>(ws + L.lo);
     a.plan.mask = reinterpret_cast<uint32_t*>(ws + L.mask);

@@ -375,8 +375,9 @@ struct PagingArgs {
 struct TreeSeq;
 struct TreePlan {       // in the workspace, see tree_plan.cuh
     TreeSeq* seqs;      // [B]
-    int64_t* start;     // [B + 1] of one head: key tiles of the units before each sequence's, and all
+    int64_t* start;     // [B + 1] of one head: key tiles and costs of the units before each sequence's, and of all
     int* unit;          // [B + 1] of one head: units before each sequence's, and all
+    int* cost;          // [1] of a unit
     int* order;         // [T] at first + i: the tree's token (0 .. n-1) that comes i-th
     int* lo;            // [T] the first cached key that a token reads (but for anchors)
     uint32_t* mask;     // [T][kMaxTree / 32] the tree's tokens that a token reads
@@ -401,7 +402,7 @@ struct TreeDecodeArgs {
     float scale_log2;           // softmax scale times log2(e)
 };
 struct TreeWs {
-    size_t seqs, start, unit, order, lo, mask, part, total;   // byte offsets
+    size_t seqs, start, unit, cost, order, lo, mask, part, total;   // byte offsets
 };
 // CTAs of a call at most (what fills a GB300), rows and keys of a tile: on CUDA
 // cores, and on the tensor cores.

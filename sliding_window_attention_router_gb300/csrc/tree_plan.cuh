@@ -6,9 +6,9 @@
 // the cache's start.  A row tile of routed tokens walks all key tiles, one of others
 // those of the anchors and of the window; where all rows fit one tile, that walks all
 // key tiles if any token is routed.  A unit is the walk of one
-// row tile of one key head of one sequence; the units' key tiles, laid end to end,
-// are dealt out to the CTAs in equal shares, whatever units they belong to.  So a
-// unit is a run of consecutive CTAs' parts, one of each; the join adds them up.
+// row tile of one key head of one sequence; the units' key tiles, laid end to end (with
+// what a unit costs beside), are dealt out to the CTAs in equal shares, whatever units
+// they belong to.  So a unit is a run of consecutive CTAs' parts, one of each; the join adds them up.
 // All of a head's units come before the next head's: CTAs a head's number of shares
 // apart then read the same tokens at the same time, whose heads lie side by side in
 // memory (16 sequences of 32K with 16 key heads: 622 us; a sequence's heads one
@@ -44,8 +44,16 @@ __device__ __forceinline__ int64_t seq_tiles(const TreeSeq& s, int G) {
 template <int R>
 constexpr int kPartRows = R == kTreeTcRows ? 2 * R : R;
 
-// The CTAs that the key tiles are dealt out to: as many as there are, and no share
-// empty.  CTA c takes [total c / n, total (c + 1) / n).
+// What a unit costs a CTA beside its key tiles (its rows, its first scores, its part
+// written out), in key tiles: it counts in the shares as so many before its first,
+// unless there are CTAs enough for a tile each.  On the tensor cores two (33 ragged
+// trees: 90 us, without 97, with three 92; 7 x 8K, 255 drafts, 16/2 heads: 103, 119, 103;
+// 59 ragged sequences, 3 drafts, 16/16 heads: 87, 90, 89).
+template <int R>
+__device__ __forceinline__ int unit_cost(int64_t tiles, int ctas) { return R == kTreeTcRows && tiles > ctas ? 2 : 0; }
+
+// The CTAs that the work is dealt out to: as many as there are, and no share empty.
+// CTA c takes [total c / n, total (c + 1) / n).
 __device__ __forceinline__ int64_t share_count(int64_t total, int ctas) { return min(total, static_cast<int64_t>(ctas)); }
 
 // First key of key tile kt of a walk.
@@ -67,10 +75,10 @@ struct TreeWork {
 
 // Where a CTA's share of the work begins, and what it needs to walk it.
 struct TreeStart {
-    int64_t at, end;      // key tiles [at, end) of all
-    int64_t head_tiles;   // of one head
+    int64_t at, end;      // [at, end) of all the work, key tiles and units' costs
+    int64_t head_work;    // of one head
     int64_t before;       // of the head, before sequence b
-    int h, b;
+    int h, b, cost;       // a unit's
     int head_units, units;   // units of one head, and of the head before sequence b
 };
 
@@ -82,39 +90,42 @@ struct TreeWalk {
     __device__ __forceinline__ bool next(TreeWork& w) {
         if (s.at >= s.end) return false;
         const int G = a.Hq / a.Hkv;
-        int64_t in = s.at - s.h * s.head_tiles;
-        if (in >= s.head_tiles) {   // the next head
+        int64_t in = s.at - s.h * s.head_work;
+        if (in >= s.head_work) {   // the next head
             ++s.h;
             s.b = s.units = 0;
             s.before = 0;
-            in -= s.head_tiles;
+            in -= s.head_work;
         }
-        for (;;) {   // ends: the head has more than `in` tiles
+        for (;;) {   // ends: the head has more than `in`
             const int4* p = reinterpret_cast<const int4*>(a.plan.seqs + s.b);
             const int4 x = p[0], y = p[1];
             w.s = TreeSeq{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-            const int64_t tiles = seq_tiles<R>(w.s, G);
-            if (in < s.before + tiles || s.b + 1 >= a.B) break;
-            s.before += tiles;
-            s.units += row_tiles<R>(w.s, G);
+            const int units = row_tiles<R>(w.s, G);
+            const int64_t work = seq_tiles<R>(w.s, G) + static_cast<int64_t>(units) * s.cost;
+            if (in < s.before + work || s.b + 1 >= a.B) break;
+            s.before += work;
+            s.units += units;
             ++s.b;
         }
         const int far = far_tiles<R>(w.s);
         int64_t rest = in - s.before;
-        const int64_t far_all = static_cast<int64_t>(far) * w.s.far_tiles;
+        const int64_t far_all = static_cast<int64_t>(far) * (w.s.far_tiles + s.cost);
         w.far = rest < far_all;
-        const int len = w.far ? w.s.far_tiles : w.s.near_tiles;
+        const int len = (w.far ? w.s.far_tiles : w.s.near_tiles) + s.cost;
         if (!w.far) rest -= far_all;
         const int tile = static_cast<int>(rest / len);   // of its kind
         w.row0 = tile * R + (w.far ? 0 : w.s.far_rows);
         w.rows = min(R, (w.far ? w.s.far_rows : w.s.n * G) - w.row0);
-        w.kt0 = static_cast<int>(rest - static_cast<int64_t>(tile) * len);
-        w.kt1 = static_cast<int>(min(static_cast<int64_t>(len), w.kt0 + s.end - s.at));
+        const int from = static_cast<int>(rest - static_cast<int64_t>(tile) * len);
+        const int to = static_cast<int>(min(static_cast<int64_t>(len), from + s.end - s.at));
+        w.kt0 = max(from - s.cost, 0);
+        w.kt1 = to - s.cost;
         w.b = s.b;
         w.h = s.h;
         w.slot = blockIdx.x + s.h * s.head_units + s.units + tile + (w.far ? 0 : far);
-        s.at += w.kt1 - w.kt0;
-        return true;
+        s.at += to - from;
+        return w.kt1 > w.kt0;   // none: the share ends before the unit's first tile
     }
 };
 
@@ -124,17 +135,28 @@ template <int R>
 __device__ __forceinline__ TreeStart start_walk(const TreeDecodeArgs& a) {
     const int lane = threadIdx.x & 31, G = a.Hq / a.Hkv;
     int64_t total = 0;
+    int all_units = 0;
     TreeSeq mine_seq = {};   // of up to 32 sequences: looked up once
     if (a.B <= 32) {
         if (lane < a.B) mine_seq = a.plan.seqs[lane];
         total = seq_tiles<R>(mine_seq, G);
+        all_units = row_tiles<R>(mine_seq, G);
     } else {
-        for (int i = lane; i < a.B; i += 32) total += seq_tiles<R>(a.plan.seqs[i], G);
+        for (int i = lane; i < a.B; i += 32) {
+            const TreeSeq s = a.plan.seqs[i];
+            total += seq_tiles<R>(s, G);
+            all_units += row_tiles<R>(s, G);
+        }
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    for (int o = 16; o > 0; o >>= 1) {
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+        all_units += __shfl_xor_sync(0xffffffffu, all_units, o);
+    }
     TreeStart w;
-    w.head_tiles = total;
+    w.cost = unit_cost<R>(total * a.Hkv, gridDim.x);
+    w.head_units = all_units;
+    w.head_work = total += static_cast<int64_t>(all_units) * w.cost;
     const int64_t all = total * a.Hkv, ctas = share_count(all, gridDim.x), c = blockIdx.x;
     w.at = c < ctas ? all * c / ctas : 0;
     w.end = c < ctas ? all * (c + 1) / ctas : 0;
@@ -151,8 +173,8 @@ __device__ __forceinline__ TreeStart start_walk(const TreeDecodeArgs& a) {
         int u = 0;
         if (i < a.B) {
             const TreeSeq s = a.B <= 32 ? mine_seq : a.plan.seqs[i];
-            mine = seq_tiles<R>(s, G);
             u = row_tiles<R>(s, G);
+            mine = seq_tiles<R>(s, G) + static_cast<int64_t>(u) * w.cost;
         }
         int64_t sum = mine;
         int usum = u;
@@ -180,10 +202,10 @@ __device__ __forceinline__ TreeStart start_walk(const TreeDecodeArgs& a) {
         before += __shfl_sync(0xffffffffu, sum, 31);
         units += __shfl_sync(0xffffffffu, usum, 31);
     }
-    w.head_units = units;
     if (blockIdx.x == 0 && lane == 0) {
         a.plan.start[a.B] = total;
-        a.plan.unit[a.B] = units;
+        a.plan.unit[a.B] = all_units;
+        a.plan.cost[0] = w.cost;
     }
     return w;
 }
