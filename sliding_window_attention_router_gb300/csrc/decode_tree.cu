@@ -40,6 +40,7 @@ __global__ void __launch_bounds__(kMaxTree) tree_plan_kernel(const __grid_consta
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int b = blockIdx.x, t = threadIdx.x, lane = t & 31, warp = t >> 5;
     if (t == 0) s_bad = 0;
+    const int first = a.starts[b], after = a.starts[b + 1], len = a.seq_lens[b];   // on their way while the others are looked at
     __syncthreads();
     // Sequences must not overlap: the workspace has room for each token once.
     bool bad = t == 0 && (a.starts[0] < 0 || a.starts[a.B] > a.T);
@@ -47,8 +48,7 @@ __global__ void __launch_bounds__(kMaxTree) tree_plan_kernel(const __grid_consta
     if (bad) s_bad = 1;
     __syncthreads();
     bad = s_bad != 0;
-    const int first = a.starts[b], len = a.seq_lens[b];
-    int n = bad ? 0 : a.starts[b + 1] - first;
+    int n = bad ? 0 : after - first;
     if (n > 0 && len != 0 && (n > kMaxTree || len < n || len > (a.max_pages << a.page_lg))) bad = true;
     if (bad || len == 0) n = 0;   // an empty slot has no tokens to look at
     const int base = len - n;
@@ -421,7 +421,10 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(const __grid
     const int64_t head = a.plan.start[a.B], total = head * a.Hkv, start = a.plan.start[b];   // work of a head, of all
     const int unit = a.plan.unit[b], head_units = a.plan.unit[a.B], cost = a.plan.cost[0];
     const int64_t shares = share_count(total, ctas);
-    auto cta_of = [&](int64_t at) { return static_cast<int>(((at + 1) * shares - 1) / total); };
+    auto cta_of = [&](int64_t at) {   // a division of 64 bits takes several times one of 32, and few calls need it
+        const int64_t x = (at + 1) * shares - 1;
+        return static_cast<int>((x | total) >> 32 ? x / total : static_cast<uint32_t>(x) / static_cast<uint32_t>(total));
+    };
     const int far_chunks = (s.far_rows + 31) / 32, chunks = far_chunks + (near_rows + 31) / 32;
     if (threadIdx.x < 2) s_bad[threadIdx.x] = 0;
     __syncthreads();

@@ -517,37 +517,43 @@ __device__ void drain(uint64_t* full, uint32_t filled) {
 }
 
 // ---- Q ---------------------------------------------------------------------------------
+// One warp gathers a unit's rows, kPer of them an instruction; what lies in the tile's
+// others reaches no row but themselves.
 template <int D, bool E4M3>
 __device__ bool q_loader(const TreeDecodeArgs& a, const Ctx<D, E4M3>& c) {
     using Z = Sizes<D, E4M3>;
     constexpr int P = D / 8, kPer = 32 / P;
     const int lane = threadIdx.x & 31, piece = lane % P, G = a.Hq / a.Hkv;
-    const uint32_t col0 = smem_u32(c.smem) + (piece >> 3) * kHalf;
+    // Row i kPer + lane / P of 32: its piece's place but for what i adds and flips.
+    const uint32_t col0 = smem_u32(c.smem) + (piece >> 3) * kHalf + lane / P * 128, swizzle = ((piece & 7) ^ (lane / P)) << 4;
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + piece * 8;
     TreeWalk<R> walk{a, *c.start};
     TreeWork w;
     for (uint32_t u = 0; walk.next(w); ++u) {
         const uint32_t buf = u % Z::kQ, col = col0 + buf * Z::kTile;
+        int at[R / 32];   // the lane's rows of q
+#pragma unroll
+        for (int k = 0; k < R / 32; ++k) {
+            const int in = k * 32 + lane, mine = w.row0 + in;
+            at[k] = in < w.rows ? (w.s.first + a.plan.order[w.s.first + mine / G]) * a.Hq + w.h * G + mine % G : 0;
+        }
         if (!wait_w(&c.bar[c.kQEmpty + buf], (u / Z::kQ & 1) ^ 1, c.abort_flag, a.err)) return false;
-        for (int r0 = 0; r0 < R; r0 += 32) {
-            const int in = r0 + lane, mine = w.row0 + in;
-            int64_t at = -1;   // the lane's row of q
-            if (in < w.rows)
-                at = static_cast<int64_t>(w.s.first + a.plan.order[w.s.first + mine / G]) * a.Hq + w.h * G + mine % G;
-#pragma unroll 4
+#pragma unroll
+        for (int k = 0; k < R / 32; ++k) {
+            if (k * 32 >= w.rows) break;
+#pragma unroll
             for (int i = 0; i < P; ++i) {
-                const int r = i * kPer + lane / P;
-                const int64_t from = __shfl_sync(0xffffffffu, at, r);
-                const uint32_t to = col + (r0 + r) * 128 + (((piece & 7) ^ (r & 7)) << 4);
-                const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + max(from, static_cast<int64_t>(0)) * D + piece * 8;
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(from >= 0 ? 16u : 0u) : "memory");
+                const int row = __shfl_sync(0xffffffffu, at[k], i * kPer + lane / P);
+                const uint32_t to = col + (k * 32 + i * kPer) * 128 + (swizzle ^ ((i * kPer & 7) << 4));
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(q + static_cast<int64_t>(row) * D) : "memory");
             }
         }
         asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
         if (E4M3) {   // every four elements in the order that the pages' come in; each lane its own copies
 #pragma unroll 4
             for (int i = 0; i < R / kPer; ++i) {
-                const int r = i * kPer + lane / P;
-                const uint32_t at = col + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
+                if (i * kPer >= w.rows) break;
+                const uint32_t at = col + i * kPer * 128 + (swizzle ^ ((i * kPer & 7) << 4));
                 const uint4 x = ld_shared_v4(at);
                 st_shared_v4(at, __byte_perm(x.x, x.y, 0x5410), __byte_perm(x.x, x.y, 0x7632), __byte_perm(x.z, x.w, 0x5410),
                              __byte_perm(x.z, x.w, 0x7632));

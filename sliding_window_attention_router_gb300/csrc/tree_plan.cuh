@@ -134,29 +134,43 @@ struct TreeWalk {
 template <int R>
 __device__ __forceinline__ TreeStart start_walk(const TreeDecodeArgs& a) {
     const int lane = threadIdx.x & 31, G = a.Hq / a.Hkv;
-    int64_t total = 0;
-    int all_units = 0;
-    TreeSeq mine_seq = {};   // of up to 32 sequences: looked up once
-    if (a.B <= 32) {
-        if (lane < a.B) mine_seq = a.plan.seqs[lane];
-        total = seq_tiles<R>(mine_seq, G);
-        all_units = row_tiles<R>(mine_seq, G);
-    } else {
-        for (int i = lane; i < a.B; i += 32) {
-            const TreeSeq s = a.plan.seqs[i];
-            total += seq_tiles<R>(s, G);
-            all_units += row_tiles<R>(s, G);
+    // Key tiles and units of up to 32 sequences, and of those before each.
+    struct Sums {
+        int64_t tiles, sum;
+        int units, usum;
+    };
+    auto sums_of = [&](int from) {
+        Sums x = {0, 0, 0, 0};
+        if (from + lane < a.B) {
+            const int4* p = reinterpret_cast<const int4*>(a.plan.seqs + from + lane);
+            const int4 lo = p[0], hi = p[1];
+            const TreeSeq s{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            x.tiles = x.sum = seq_tiles<R>(s, G);
+            x.units = x.usum = row_tiles<R>(s, G);
         }
-    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        total += __shfl_xor_sync(0xffffffffu, total, o);
-        all_units += __shfl_xor_sync(0xffffffffu, all_units, o);
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x.sum, o);
+            const int z = __shfl_up_sync(0xffffffffu, x.usum, o);
+            if (lane >= o) {
+                x.sum += y;
+                x.usum += z;
+            }
+        }
+        return x;
+    };
+    const Sums first = sums_of(0);
+    int64_t tiles = 0;
+    int units = 0;
+    for (int from = 0; from < a.B; from += 32) {
+        const Sums x = from == 0 ? first : sums_of(from);
+        tiles += __shfl_sync(0xffffffffu, x.sum, 31);
+        units += __shfl_sync(0xffffffffu, x.usum, 31);
     }
     TreeStart w;
-    w.cost = unit_cost<R>(total * a.Hkv, gridDim.x);
-    w.head_units = all_units;
-    w.head_work = total += static_cast<int64_t>(all_units) * w.cost;
+    w.cost = unit_cost<R>(tiles * a.Hkv, gridDim.x);
+    w.head_units = units;
+    const int64_t total = w.head_work = tiles + static_cast<int64_t>(units) * w.cost;
     const int64_t all = total * a.Hkv, ctas = share_count(all, gridDim.x), c = blockIdx.x;
     w.at = c < ctas ? all * c / ctas : 0;
     w.end = c < ctas ? all * (c + 1) / ctas : 0;
@@ -165,46 +179,29 @@ __device__ __forceinline__ TreeStart start_walk(const TreeDecodeArgs& a) {
     w.b = w.units = 0;
     const int64_t in = w.at - w.h * total;
     int64_t before = 0;
-    int units = 0;
+    int units_before = 0;
     bool found = false;
-    for (int from = 0; from < a.B; from += 32) {
-        const int i = from + lane;
-        int64_t mine = 0;
-        int u = 0;
-        if (i < a.B) {
-            const TreeSeq s = a.B <= 32 ? mine_seq : a.plan.seqs[i];
-            u = row_tiles<R>(s, G);
-            mine = seq_tiles<R>(s, G) + static_cast<int64_t>(u) * w.cost;
-        }
-        int64_t sum = mine;
-        int usum = u;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
-            const int z = __shfl_up_sync(0xffffffffu, usum, o);
-            if (lane >= o) {
-                sum += y;
-                usum += z;
-            }
-        }
-        if (blockIdx.x == 0 && i < a.B) {
-            a.plan.start[i] = before + sum - mine;
-            a.plan.unit[i] = units + usum - u;
+    for (int from = 0; from < a.B && !(found && blockIdx.x > 0); from += 32) {
+        const Sums x = from == 0 ? first : sums_of(from);
+        const int64_t sum = x.sum + static_cast<int64_t>(x.usum) * w.cost, start = sum - x.tiles - static_cast<int64_t>(x.units) * w.cost;
+        if (blockIdx.x == 0 && from + lane < a.B) {
+            a.plan.start[from + lane] = before + start;
+            a.plan.unit[from + lane] = units_before + x.usum - x.units;
         }
         const unsigned hit = __ballot_sync(0xffffffffu, before + sum > in);
         if (hit && !found) {
             const int who = __ffs(hit) - 1;
             w.b = from + who;
-            w.before = before + __shfl_sync(0xffffffffu, sum - mine, who);
-            w.units = units + __shfl_sync(0xffffffffu, usum - u, who);
+            w.before = before + __shfl_sync(0xffffffffu, start, who);
+            w.units = units_before + __shfl_sync(0xffffffffu, x.usum - x.units, who);
             found = true;
         }
         before += __shfl_sync(0xffffffffu, sum, 31);
-        units += __shfl_sync(0xffffffffu, usum, 31);
+        units_before += __shfl_sync(0xffffffffu, x.usum, 31);
     }
     if (blockIdx.x == 0 && lane == 0) {
         a.plan.start[a.B] = total;
-        a.plan.unit[a.B] = all_units;
+        a.plan.unit[a.B] = units;
         a.plan.cost[0] = w.cost;
     }
     return w;
