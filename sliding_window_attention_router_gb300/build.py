@@ -22,6 +22,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libswiattn.so")
 BINDING = os.path.join(PKG, "_binding.so")
+TORCH = os.path.join(BUILD, "torch_version")   # of the PyTorch that the binding was compiled against
 
 SOURCES = ["swiattn_api.cu", "route.cu", "schedule.cu", "attn_prefill.cu", "attn_simt.cu", "decode.cu",
            "bwd_schedule.cu", "attn_bwd.cu", "bwd_simt.cu", "attn_dual.cu", "rope.cu",
@@ -63,12 +64,23 @@ def _build_binding() -> None:
     if res.returncode != 0:
         raise RuntimeError(f"g++ failed on binding.cpp:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, BINDING)
+    with open(TORCH, "w") as f:
+        f.write(torch.__version__)
+
+
+def _same_torch() -> bool:
+    import torch
+    try:
+        with open(TORCH) as f:
+            return f.read() == torch.__version__
+    except OSError:
+        return False
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compile (if stale) and return the path of libswiattn.so."""
     if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime()
-                         for f in (LIB, BINDING)):
+                         for f in (LIB, BINDING)) and _same_torch():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
