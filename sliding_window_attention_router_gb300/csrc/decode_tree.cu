@@ -29,12 +29,23 @@ namespace {
 constexpr int kWords = kMaxTree / 32;
 
 // ---- the plan ----------------------------------------------------------------
+// The r > 0 lowest set bits of x (a call: 16 copies in line made the plan of trees that do not
+// need it 1 us slower).
+__device__ __noinline__ uint32_t lowest(uint32_t x, int r) {
+    if (r >= __popc(x)) return x;
+    int p = 0;   // the most bits of which no more than r are set
+#pragma unroll
+    for (int step = 16; step > 0; step >>= 1)
+        if (__popc(x & ((1u << (p + step)) - 1)) <= r) p += step;
+    return x & ((1u << p) - 1);
+}
+
 // Block b: sequence b's tokens, one a thread.  The paths come by doubling: after r
 // rounds mask[t] holds the 2^r last tokens of t's path, and up[t] the one before
 // them.
 __global__ void __launch_bounds__(kMaxTree) tree_plan_kernel(const __grid_constant__ TreeDecodeArgs a, int rows, int keys) {
     __shared__ uint32_t s_mask[2][kWords][kMaxTree];
-    __shared__ short s_up[2][kMaxTree], s_depth[kMaxTree];
+    __shared__ short s_up[2][kMaxTree];
     __shared__ int s_count[kMaxTree / 32], s_bad;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -81,7 +92,6 @@ __global__ void __launch_bounds__(kMaxTree) tree_plan_kernel(const __grid_consta
         mask[w] = s_mask[cur][w][t];
         depth += __popc(mask[w]);
     }
-    s_depth[t] = static_cast<short>(depth);
     // Routed tokens first, each kind in its order.
     const unsigned routed = __ballot_sync(0xffffffffu, gate);
     if (lane == 0) s_count[warp] = __popc(routed);
@@ -95,8 +105,17 @@ __global__ void __launch_bounds__(kMaxTree) tree_plan_kernel(const __grid_consta
     before += __popc(routed & ((1u << lane) - 1));   // routed tokens before this one
     if (on) {
         if (!gate && depth >= a.W) {   // the top of the path has left the window
-            for (int u = 0; u < n; ++u)
-                if (s_depth[u] <= depth - a.W && base + s_depth[u] >= a.n_anchor) mask[u >> 5] &= ~(1u << (u & 31));
+            // A path's tokens come in the order of their depths: of them the anchors stay,
+            // and those from depth - W + 1 on.
+            int stay = min(max(a.n_anchor - base, 0), kMaxTree), gone = depth - a.W + 1;
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) {
+                if (w * 32 >= n) break;
+                const uint32_t x = mask[w];
+                mask[w] = x & ((stay > 0 ? lowest(x, stay) : 0u) | ~(gone > 0 ? lowest(x, gone) : 0u));
+                stay -= __popc(x);
+                gone -= __popc(x);
+            }
         }
         a.plan.order[first + (gate ? before : all + t - before)] = t;
         a.plan.lo[first + t] = gate ? 0 : min(max(0, base + depth - a.W + 1), base);
@@ -586,13 +605,16 @@ cudaError_t launch_all(const TreeDecodeArgs& a, int sms, cudaStream_t s) {
     else e = launch_simt<D>(a, ctas, s);
     prof_stop(s);
     if (e != cudaSuccess) return e;
-    // About the chunks of a sequence of mean size (blocks without one cost time too).
-    const int64_t mean = (static_cast<int64_t>(a.T) * (a.Hq / a.Hkv) / a.B / 32 + 1) * a.Hkv;
+    // About the chunks of a sequence of mean size (blocks without one cost time too), or, as
+    // one may be larger, what runs at once (2 ragged sequences of 16K: 31 us, without 44).
+    const int64_t G = a.Hq / a.Hkv, mean = (static_cast<int64_t>(a.T) * G / a.B / 32 + 1) * a.Hkv;
+    const int64_t most = ((std::min(a.T, kMaxTree) * G + 31) / 32 + 1) * a.Hkv;
+    const int64_t y = std::max(mean, std::min<int64_t>(most, 2 * sms / a.B));
     // Many chunks want many blocks at once, few their parts read by more warps (33
     // ragged trees, 1400 chunks: 100 us, by 512 threads each 114; 8 x 32K with 64 rows,
     // 64 chunks: 110 us by 256 threads, 103 by 512).
     const bool many = mean * a.B > 4 * sms;
-    cfg = dependent_launch(dim3(a.B, static_cast<unsigned>(std::min<int64_t>(mean, std::max(1, 8192 / a.B)))), many ? kJoinThreads / 2 : kJoinThreads, s, attr);
+    cfg = dependent_launch(dim3(a.B, static_cast<unsigned>(std::min<int64_t>(y, std::max(1, 8192 / a.B)))), many ? kJoinThreads / 2 : kJoinThreads, s, attr);
     e = cudaLaunchKernelEx(&cfg, tree_join_kernel<KIND, D, kRows>, a, ctas);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
