@@ -191,7 +191,11 @@ __device__ __forceinline__ Row<KIND, D> row_of(const TreeDecodeArgs& a, int whic
 
 // ---- products on CUDA cores ------------------------------------------------------
 // For fp32, exact where the tensor cores are not: 32 rows by 64 keys, a thread 4 x 4
-// scores, then 4 rows by D/16 dimensions.
+// scores, then 4 rows by D/16 dimensions.  A tile's K is copied while the last one's
+// values are added, its V while its scores are formed, one buffer each; four CTAs an SM
+// where they fit, d = 64 (32 ragged sequences of up to 83 drafts, 64/4 heads, d = 64: 151
+// us, by two CTAs that copied first 248; 45 of up to 196, 8/1 heads, d = 128: 440, the
+// same).
 constexpr int kR = kTreeRows, kK = kTreeKeys, kSimtThreads = 128;
 template <int D>
 struct SimtShared {
@@ -251,21 +255,25 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
 #pragma unroll
             for (int c = 0; c < 4 * C; ++c) acc[i][c] = 0.f;
         }
-        for (int kt = w.kt0; kt < w.kt1; ++kt) {
+        // K (0) or V (1) of key tile kt: what no row of the walk reads comes as zeros.
+        auto copy = [&](int which, int kt) {
             const int key0 = tile_key<kK>(w.s, w.far, kt);
-            __syncthreads();
+#pragma unroll 4
             for (int i = tid; i < kK * F; i += kSimtThreads) {
                 const int r = i / F, c = i % F, tok = key0 + r;
-                float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-                if (tok < len && (w.far || tok >= w.s.lo || tok < w.s.na)) {
-                    const int page = page_of(a, w.b, tok);
-                    const Row<KIND, D> k = row_of<KIND, D>(a, 0, page, tok, w.h), v = row_of<KIND, D>(a, 1, page, tok, w.h);
-                    x = four_of<KIND>(k.at, c, k.up);
-                    y = four_of<KIND>(v.at, c, v.up);
-                }
-                reinterpret_cast<float4*>(s.k[r])[c] = x;
-                reinterpret_cast<float4*>(s.v[r])[c] = y;
+                const float* from = static_cast<const float*>(a.q);
+                const bool on = tok < len && (w.far || tok >= w.s.lo || tok < w.s.na);
+                if (on) from = static_cast<const float*>(row_of<KIND, D>(a, which, page_of(a, w.b, tok), tok, w.h).at) + 4 * c;
+                const float* to = (which ? s.v[r] : s.k[r]) + 4 * c;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(on ? 16u : 0u) : "memory");
             }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        copy(0, w.kt0);
+        copy(1, w.kt0);
+        for (int kt = w.kt0; kt < w.kt1; ++kt) {
+            const int key0 = tile_key<kK>(w.s, w.far, kt);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");   // K
             __syncthreads();
             float x[4][4];
 #pragma unroll
@@ -316,7 +324,9 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
                     s.p[r][tx + 16 * j] = p;
                 }
             }
-            __syncwarp();   // a row's weights are written and read by one half-warp
+            asm volatile("cp.async.wait_group 0;" ::: "memory");   // V
+            __syncthreads();   // and K has been read
+            if (kt + 1 < w.kt1) copy(0, kt + 1);
 #pragma unroll 2
             for (int k = 0; k < kK; ++k) {
                 float4 v[C];
@@ -334,7 +344,10 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
                     }
                 }
             }
-            __syncwarp();
+            if (kt + 1 < w.kt1) {
+                __syncthreads();   // V has been read
+                copy(1, kt + 1);
+            }
         }
         static_assert(kPartRows<kR> == kR, "a part has the tile's rows");
         float* part = a.plan.part + static_cast<size_t>(w.slot) * kR * (D + 2);
@@ -599,7 +612,7 @@ cudaError_t launch_all(const TreeDecodeArgs& a, int sms, cudaStream_t s) {
     cudaLaunchConfig_t cfg = dependent_launch(a.B, kMaxTree, s, attr);
     cudaError_t e = cudaLaunchKernelEx(&cfg, tree_plan_kernel, a, kRows, kTc ? kTreeTcKeys : kTreeKeys);
     if (e != cudaSuccess) return e;
-    const int ctas = kTc ? std::min(sms, kTreeTcCtas) : std::min(2 * sms, kTreeCtas);
+    const int ctas = kTc ? std::min(sms, kTreeTcCtas) : std::min(kTreeCtas<D> / 152 * sms, kTreeCtas<D>);
     prof_start(s);
     if constexpr (kTc) e = launch_tree_tc(a, D, KIND == SWIATTN_E4M3, ctas, s);
     else e = launch_simt<D>(a, ctas, s);
@@ -640,7 +653,7 @@ TreeWs tree_ws_layout(int T, int B, int Hq, int Hkv, int d, int dtype) {
     L.part = up(L.mask + sizeof(uint32_t) * kWords * t);
     // Units: a key head's row tiles, of which each sequence with tokens has at most
     // two that are not full.
-    const size_t rows = dtype == SWIATTN_BF16 ? kTreeTcRows : kTreeRows, ctas = dtype == SWIATTN_BF16 ? kTreeTcCtas : kTreeCtas;
+    const size_t rows = dtype == SWIATTN_BF16 ? kTreeTcRows : kTreeRows, ctas = dtype == SWIATTN_BF16 ? kTreeTcCtas : d == 64 ? kTreeCtas<64> : kTreeCtas<128>;
     const size_t units = Hkv * (t * G / rows + 2 * std::min(b, t));
     const size_t part_rows = dtype == SWIATTN_BF16 ? kPartRows<kTreeTcRows> : kPartRows<kTreeRows>;
     L.total = up(L.part + (ctas + units) * part_rows * (d + 2) * sizeof(float));

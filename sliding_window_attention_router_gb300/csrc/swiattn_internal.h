@@ -406,7 +406,9 @@ struct TreeWs {
 };
 // CTAs of a call at most (what fills a GB300), rows and keys of a tile: on CUDA
 // cores, and on the tensor cores.
-constexpr int kTreeCtas = 2 * 152, kTreeRows = 32, kTreeKeys = 64;
+template <int D>
+constexpr int kTreeCtas = (D == 64 ? 4 : 2) * 152;
+constexpr int kTreeRows = 32, kTreeKeys = 64;
 constexpr int kTreeTcCtas = 152, kTreeTcRows = 128, kTreeTcKeys = 128;
 TreeWs tree_ws_layout(int T, int B, int Hq, int Hkv, int d, int dtype);
 cudaError_t launch_decode_tree(const TreeDecodeArgs& a, int d, int page_dtype, int sms, cudaStream_t s);
