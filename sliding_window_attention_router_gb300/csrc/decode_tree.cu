@@ -193,20 +193,22 @@ __device__ __forceinline__ Row<KIND, D> row_of(const TreeDecodeArgs& a, int whic
 // For fp32, exact where the tensor cores are not: 32 rows by 64 keys, a thread 4 x 4
 // scores, then 4 rows by D/16 dimensions.  A tile's K is copied while the last one's
 // values are added, its V while its scores are formed, one buffer each; four CTAs an SM
-// where they fit, d = 64 (32 ragged sequences of up to 83 drafts, 64/4 heads, d = 64: 151
-// us, by two CTAs that copied first 248; 45 of up to 196, 8/1 heads, d = 128: 440, the
-// same).
+// where they fit, d = 64 (32 ragged sequences of up to 83 drafts, 64/4 heads, d = 64: 141
+// us, by two CTAs that copied first 248).  A lane looks one row up, not each piece of it,
+// and takes four keys' weights at once (45 sequences of 196 drafts, 8/1 heads, d = 128: 353
+// us, without 440): eight warps an SM, which is what d = 128 leaves room for, are bound by
+// the instructions beside the products.
 constexpr int kR = kTreeRows, kK = kTreeKeys, kSimtThreads = 128;
 template <int D>
 struct SimtShared {
-    float q[kR][D], k[kK][D + 4], v[kK][D], p[kR][kK + 4];
+    float q[kR][D], k[kK][D + 4], v[kK][D], p[kR][kK + 4];   // rows of 16-byte multiples
     uint32_t mask[kR][kWords];
     int lo[kR];
     TreeStart start;
 };
 
 template <int D>
-__global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_constant__ TreeDecodeArgs a) {
+__global__ void __launch_bounds__(kSimtThreads, kTreeCtas<D> / 152) tree_simt_kernel(const __grid_constant__ TreeDecodeArgs a) {
     extern __shared__ __align__(16) uint8_t raw[];
     SimtShared<D>& s = *reinterpret_cast<SimtShared<D>*>(raw);
     constexpr int F = D / 4;      // float4 of a row
@@ -255,20 +257,27 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
 #pragma unroll
             for (int c = 0; c < 4 * C; ++c) acc[i][c] = 0.f;
         }
-        // K (0) or V (1) of key tile kt: what no row of the walk reads comes as zeros.
+        // K (0) or V (1) of key tile kt, a warp a row at a time or two: 16 rows in all, one
+        // looked up by each lane.  What no row of the walk reads comes as zeros.
         auto copy = [&](int which, int kt) {
-            const int key0 = tile_key<kK>(w.s, w.far, kt);
+            constexpr int H = 32 / F;
+            const int key0 = tile_key<kK>(w.s, w.far, kt), lane = tid & 31, l = lane & 15, first = tid / 32 * H;
+            const int tok = key0 + first + l % H + l / H * (kSimtThreads / 32 * H);
+            unsigned long long row = 0;
+            if (tok < len && (w.far || tok >= w.s.lo || tok < w.s.na))
+                row = reinterpret_cast<unsigned long long>(row_of<KIND, D>(a, which, page_of(a, w.b, tok), tok, w.h).at);
+            const int stride = which ? sizeof(s.v[0]) : sizeof(s.k[0]);
+            uint32_t to = smem_u32(which ? s.v[0] : s.k[0]) + (first + lane / F) * stride + lane % F * 16;
 #pragma unroll 4
-            for (int i = tid; i < kK * F; i += kSimtThreads) {
-                const int r = i / F, c = i % F, tok = key0 + r;
-                const float* from = static_cast<const float*>(a.q);
-                const bool on = tok < len && (w.far || tok >= w.s.lo || tok < w.s.na);
-                if (on) from = static_cast<const float*>(row_of<KIND, D>(a, which, page_of(a, w.b, tok), tok, w.h).at) + 4 * c;
-                const float* to = (which ? s.v[r] : s.k[r]) + 4 * c;
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(on ? 16u : 0u) : "memory");
+            for (int n = 0; n < 16 / H; ++n, to += kSimtThreads / 32 * H * stride) {
+                const unsigned long long from = __shfl_sync(0xffffffffu, row, n * H + lane / F);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to),
+                             "l"(from ? from + lane % F * 16 : reinterpret_cast<unsigned long long>(a.q)), "r"(from ? 16u : 0u)
+                             : "memory");
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
+        static_assert(kK == 16 * (kSimtThreads / 32), "16 rows a warp");
         copy(0, w.kt0);
         copy(1, w.kt0);
         for (int kt = w.kt0; kt < w.kt1; ++kt) {
@@ -327,20 +336,26 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
             asm volatile("cp.async.wait_group 0;" ::: "memory");   // V
             __syncthreads();   // and K has been read
             if (kt + 1 < w.kt1) copy(0, kt + 1);
-#pragma unroll 2
-            for (int k = 0; k < kK; ++k) {
-                float4 v[C];
+#pragma unroll 1
+            for (int k0 = 0; k0 < kK; k0 += 4) {
+                float4 p[4];   // four keys' weights of a row at once
 #pragma unroll
-                for (int c = 0; c < C; ++c) v[c] = reinterpret_cast<const float4*>(s.v[k])[tx + 16 * c];
+                for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(&s.p[ty * 4 + i][k0]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float p = s.p[ty * 4 + i][k];
+                for (int k = 0; k < 4; ++k) {
+                    float4 v[C];
 #pragma unroll
-                    for (int c = 0; c < C; ++c) {
-                        acc[i][4 * c] = fmaf(p, v[c].x, acc[i][4 * c]);
-                        acc[i][4 * c + 1] = fmaf(p, v[c].y, acc[i][4 * c + 1]);
-                        acc[i][4 * c + 2] = fmaf(p, v[c].z, acc[i][4 * c + 2]);
-                        acc[i][4 * c + 3] = fmaf(p, v[c].w, acc[i][4 * c + 3]);
+                    for (int c = 0; c < C; ++c) v[c] = reinterpret_cast<const float4*>(s.v[k0 + k])[tx + 16 * c];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float w = k == 0 ? p[i].x : k == 1 ? p[i].y : k == 2 ? p[i].z : p[i].w;
+#pragma unroll
+                        for (int c = 0; c < C; ++c) {
+                            acc[i][4 * c] = fmaf(w, v[c].x, acc[i][4 * c]);
+                            acc[i][4 * c + 1] = fmaf(w, v[c].y, acc[i][4 * c + 1]);
+                            acc[i][4 * c + 2] = fmaf(w, v[c].z, acc[i][4 * c + 2]);
+                            acc[i][4 * c + 3] = fmaf(w, v[c].w, acc[i][4 * c + 3]);
+                        }
                     }
                 }
             }
