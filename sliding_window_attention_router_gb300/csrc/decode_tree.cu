@@ -435,10 +435,12 @@ __device__ __noinline__ void row_again(const TreeDecodeArgs& a, int b, int h, in
 #pragma unroll
         for (int w = 16; w > 0; w >>= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
         x *= a.scale_log2;
-        const float mn = fmaxf(m, x), f = m == -INFINITY ? 0.f : exp2f(m - mn), p = exp2f(x - mn);
-        l = (m == -INFINITY ? 0.f : l * f) + p;
+        // The maximum passes over a NaN, whose weight is one; nothing is forgotten, whatever the
+        // maximum was, so that it stays.  Scores of -infinity weigh 0 before a finite one, too.
+        const float mn = fmaxf(m, x), ref = mn == -INFINITY ? 0.f : mn, f = exp2f(m - ref), p = exp2f(x - ref);
+        l = l * f + p;
 #pragma unroll
-        for (int i = 0; i < N; ++i) o.x[i] = (m == -INFINITY ? 0.f : o.x[i] * f) + p * vv[i];
+        for (int i = 0; i < N; ++i) o.x[i] = o.x[i] * f + p * vv[i];
         m = mn;
     }
 }
