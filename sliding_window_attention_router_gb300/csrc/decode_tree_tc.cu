@@ -507,7 +507,9 @@ __device__ bool converter(const TreeDecodeArgs& a, const Ctx<D, true>& c, int wh
     }
 }
 
-// The copies in flight of a call that gave up.
+// Waits for a loader's last copies, whether it filled all or gave up: those whose tiles no
+// other warp will wait for, having given up itself, would else write to memory that is the
+// next CTA's by then.  (Where nobody gave up they are there, or about to be.)
 template <int S>
 __device__ void drain(uint64_t* full, uint32_t filled) {
     for (uint32_t back = 1; back <= S && back <= filled; ++back) {
@@ -872,12 +874,13 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) tree_tc_kernel(const __grid
                 converter<D>(a, c, (warp - 12) / kLoaders, (warp - 12) % kLoaders);
             } else {
                 uint32_t filled = 0;
-                if (!loader<D>(a, c, maps.of, box, warp - 12, filled)) drain<Z::kSlots>(&c.bar[c.kFull], filled);
+                loader<D>(a, c, maps.of, box, warp - 12, filled);
+                drain<Z::kSlots>(&c.bar[c.kFull], filled);
             }
         } else if constexpr (E4M3) {
             uint32_t filled = 0;
-            if (!raw_loader<D>(a, c, &maps.of[warp - 10], box, warp - 10, filled))
-                drain<Z::kOwnRaw>(&c.bar[c.kRawFull + (warp - 10) * Z::kOwnRaw], filled);
+            raw_loader<D>(a, c, &maps.of[warp - 10], box, warp - 10, filled);
+            drain<Z::kOwnRaw>(&c.bar[c.kRawFull + (warp - 10) * Z::kOwnRaw], filled);
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     }
