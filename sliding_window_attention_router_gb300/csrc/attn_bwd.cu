@@ -157,7 +157,7 @@ __device__ __forceinline__ uint32_t packed_col(int kk) {
     return static_cast<uint32_t>((kk >> 2) * 64 + (kk & 3) * 8);
 }
 
-// After an abort: waits (bounded) for the loads still in flight on a ring of
+// Waits (bounded) for the loads still in flight, when a producer leaves, on a ring of
 // `slots` full-barriers, of which `issued` have been armed so far.
 __device__ __forceinline__ void drain_ring(uint64_t* bars, uint32_t slots, uint32_t issued) {
     for (uint32_t back = 1; back <= slots && back <= issued; ++back) {
@@ -628,12 +628,12 @@ __global__ void __launch_bounds__(kThreads, 1) dkdv_kernel(const __grid_constant
         }
         __syncwarp();
         KvIssued n_is{0, 0, 0, 0};
-        if (!producer(p, smem, bar, sched, abort_flag, n_is)) {
-            drain_ring(&bar[BAR_Q_FULL], kQSlots, n_is.q);
-            drain_ring(&bar[BAR_DO_FULL], kDSlots, n_is.d);
-            drain_ring(&bar[BAR_K_FULL], 1, n_is.k);
-            drain_ring(&bar[BAR_V_FULL], 1, n_is.v);
-        }
+        producer(p, smem, bar, sched, abort_flag, n_is);
+        // Its last loads, however it left: a role that gave up waits for none.
+        drain_ring(&bar[BAR_Q_FULL], kQSlots, n_is.q);
+        drain_ring(&bar[BAR_DO_FULL], kDSlots, n_is.d);
+        drain_ring(&bar[BAR_K_FULL], 1, n_is.k);
+        drain_ring(&bar[BAR_V_FULL], 1, n_is.v);
         __syncwarp();
     } else if (warp == 9) {
         mma_issuer(p, smem, bar, sched, tmem, abort_flag);
@@ -963,11 +963,10 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
         }
         __syncwarp();
         QIssued n_is{0, 0, 0};
-        if (!producer(p, smem, bar, sched, abort_flag, n_is)) {
-            drain_ring(&bar[BAR_K_FULL], kKSlots, n_is.k);
-            drain_ring(&bar[BAR_V_FULL], kVSlots, n_is.v);
-            drain_ring(&bar[BAR_Q_FULL], 1, n_is.q);
-        }
+        producer(p, smem, bar, sched, abort_flag, n_is);
+        drain_ring(&bar[BAR_K_FULL], kKSlots, n_is.k);
+        drain_ring(&bar[BAR_V_FULL], kVSlots, n_is.v);
+        drain_ring(&bar[BAR_Q_FULL], 1, n_is.q);
         __syncwarp();
     } else if (warp == 9) {
         mma_issuer(p, smem, bar, sched, tmem, abort_flag);

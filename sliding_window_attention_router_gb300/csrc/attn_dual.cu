@@ -617,11 +617,11 @@ __global__ void __launch_bounds__(kThreads, 1) dual_kernel(const __grid_constant
         }
         __syncwarp();
         uint32_t g = 0, q_issued[2] = {0, 0};
-        if (!producer(p, smem, bar, sched, abort_flag, g, q_issued)) {
-            drain_loads(&bar[BAR_KV_FULL], g);
-            for (int x = 0; x < 2; ++x)
-                if (q_issued[x]) mbar_drain(&bar[BAR_Q_FULL + x], (q_issued[x] - 1) & 1u);
-        }
+        producer(p, smem, bar, sched, abort_flag, g, q_issued);
+        // Its last loads, however it left: a role that gave up waits for none.
+        drain_loads(&bar[BAR_KV_FULL], g);
+        for (int x = 0; x < 2; ++x)
+            if (q_issued[x]) mbar_drain(&bar[BAR_Q_FULL + x], (q_issued[x] - 1) & 1u);
         __syncwarp();
     } else if (warp == 9) {
         mma_issuer(p, smem, bar, sched, tmem, abort_flag);

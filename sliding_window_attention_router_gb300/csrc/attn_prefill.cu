@@ -732,11 +732,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         __syncwarp();
         uint32_t g = 0, q_issued[2] = {0, 0};
         bool q_tma_last[2] = {false, false};
-        if (!producer<ANCH>(p, smem, bar, sched, abort_flag, g, q_issued, q_tma_last)) {
-            drain_loads(&bar[BAR_KV_FULL], g);
-            for (int x = 0; x < 2; ++x)
-                if (q_tma_last[x]) mbar_drain(&bar[BAR_Q_FULL + x], (q_issued[x] - 1) & 1u);
-        }
+        producer<ANCH>(p, smem, bar, sched, abort_flag, g, q_issued, q_tma_last);
+        // Its last loads, however it left: a role that gave up waits for none.
+        drain_loads(&bar[BAR_KV_FULL], g);
+        for (int x = 0; x < 2; ++x)
+            if (q_tma_last[x]) mbar_drain(&bar[BAR_Q_FULL + x], (q_issued[x] - 1) & 1u);
         __syncwarp();
     } else if (warp == 9 || warp == 11) {
         mma_issuer<ANCH>(p, smem, bar, sched, tmem, abort_flag, warp == 9 ? 0 : 1);
