@@ -45,15 +45,15 @@ L2_FLUSH_BYTES = 256 << 20
 # has changed since reports null.
 MEASURED_TRAFFIC = {
     # prefill_kernel, long-context prefill N=32768 f=0.13 (far items head by head):
-    # 730 999 040 read + 121 548 800 written
-    ("prefill", "ad2ebe391d3eab42"): 730999040 + 121548800,
+    # 732 170 240 read + 121 753 088 written
+    ("prefill", "2e91631e8c844915"): 732170240 + 121753088,
     # decode_split2_kernel (persistent CTAs), 16 x 32768 decode: 654 431 488 read + 4 102 656 written
     ("decode", "97db57687c228419"): 654431488 + 4102656,
-    # dual_kernel, dual-branch workload B=2 N=8192 GQA 16/4: 143 767 040 read + 271 276 288 written
-    ("dual", "c42c6d9de72c1154"): 143767040 + 271276288,
-    # dkdv_kernel + dq_kernel, backward on the dual workload: (315 331 584 + 22 627 584)
-    # + (254 837 248 + 47 843 584)
-    ("backward", "971f419b64acb641"): 315331584 + 22627584 + 254837248 + 47843584,
+    # dual_kernel, dual-branch workload B=2 N=8192 GQA 16/4: 145 310 720 read + 270 765 056 written
+    ("dual", "8a9adc695d81a736"): 145310720 + 270765056,
+    # dkdv_kernel + dq_kernel, backward on the dual workload: (314 697 984 + 22 407 168)
+    # + (257 711 360 + 47 884 800)
+    ("backward", "0030da35d94c1b9c"): 314697984 + 22407168 + 257711360 + 47884800,
     # route_kernel, 32768 tokens x 2048: 134 248 192 read + 2 795 520 written
     ("route", "4a5c0b7bf6e2d8ed"): 134248192 + 2795520,
     # route_bwd_logit + dh + reduce kernels, 16384 tokens: (201 534 208 + 3 031 552)
