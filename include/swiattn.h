@@ -501,9 +501,11 @@ size_t swiattn_decode_tree_workspace(int T, int B, int Hq, int Hkv, int d, int d
  *    else those at the last W positions and at the first n_anchor.
  *  - q, o [T,Hq,d] of `dtype`; lse (nullable) fp32 [T,Hq]; gate uint8 [T]; pages
  *    of `dtype` (k_exp, v_exp unused, may be NULL) or, with bf16, SWIATTN_E4M3 as
- *    for swiattn_decode_paged_e4m3 (k_exp, v_exp 16-byte aligned); a value of such
- *    a page counts as the bf16 that it is from 2^-133 to below 2^128.  Rows of tokens that no sequence owns are left
- *    as they were, and so are those of an empty slot (seq_lens[b] == 0).
+ *    for swiattn_decode_paged_e4m3 (k_exp, v_exp 16-byte aligned; any byte is
+ *    2^(byte - 127) here, 0 and 255 too); a value of such a page counts as the
+ *    bf16 that it is from 2^-133 to below 2^128.  Rows of tokens that no sequence
+ *    owns are left as they were, and so are those of an empty slot
+ *    (seq_lens[b] == 0).
  *  - Whatever entries that a token does not read hold (NaN included) does not
  *    reach its result; a NaN in one that it reads does.  A token whose result is
  *    not finite costs more time.

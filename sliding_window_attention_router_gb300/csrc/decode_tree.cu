@@ -141,9 +141,10 @@ __global__ void __launch_bounds__(kMaxTree) tree_plan_kernel(const __grid_consta
 }
 
 // ---- elements of a page row ---------------------------------------------------
-// Four elements of a row as floats; `up` is an e4m3 row's power of two.
+// Four elements of a row as floats; `up` is an e4m3 row's power of two, 2^(byte - 127) for every
+// exponent byte as the tensor cores' tiles have it, in two factors as one would not reach its ends.
 template <int KIND>
-__device__ __forceinline__ float4 four_of(const void* row, int at, float up) {
+__device__ __forceinline__ float4 four_of(const void* row, int at, float2 up) {
     if constexpr (KIND == SWIATTN_F32) {
         return reinterpret_cast<const float4*>(row)[at];
     } else if constexpr (KIND == SWIATTN_BF16) {
@@ -157,7 +158,7 @@ __device__ __forceinline__ float4 four_of(const void* row, int at, float up) {
         const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(u >> 16), __NV_E4M3);
         const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&lo));
         const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-        return make_float4(x.x * up, x.y * up, y.x * up, y.y * up);
+        return make_float4(x.x * up.x * up.y, x.y * up.x * up.y, y.x * up.x * up.y, y.y * up.x * up.y);
     }
 }
 template <int KIND>
@@ -175,7 +176,7 @@ __device__ __forceinline__ int page_of(const TreeDecodeArgs& a, int b, int tok) 
 template <int KIND, int D>
 struct Row {
     const void* at;
-    float up;
+    float2 up;
 };
 template <int KIND, int D>
 __device__ __forceinline__ Row<KIND, D> row_of(const TreeDecodeArgs& a, int which, int page, int tok, int h) {
@@ -183,9 +184,11 @@ __device__ __forceinline__ Row<KIND, D> row_of(const TreeDecodeArgs& a, int whic
     const int64_t row = ((static_cast<int64_t>(page) << a.page_lg) + slot) * a.Hkv + h;
     Row<KIND, D> r;
     r.at = static_cast<const char*>(which ? a.v_pages : a.k_pages) + row * (D * bytes_of<KIND>());
-    r.up = 1.f;
-    if (KIND == SWIATTN_E4M3)
-        r.up = __uint_as_float(static_cast<uint32_t>((which ? a.v_exp : a.k_exp)[((static_cast<int64_t>(page) * a.Hkv + h) << a.page_lg) + slot]) << 23);
+    r.up = make_float2(1.f, 1.f);
+    if (KIND == SWIATTN_E4M3) {
+        const uint32_t e = (which ? a.v_exp : a.k_exp)[((static_cast<int64_t>(page) * a.Hkv + h) << a.page_lg) + slot];
+        r.up = make_float2(__uint_as_float((e / 2 + 64) << 23), __uint_as_float((e - e / 2 + 63) << 23));
+    }
     return r;
 }
 
@@ -235,7 +238,7 @@ __global__ void __launch_bounds__(kSimtThreads, kTreeCtas<D> / 152) tree_simt_ke
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < rows) {
                 const int tok = w.s.first + a.plan.order[w.s.first + R / G];
-                x = four_of<KIND>(static_cast<const float*>(a.q) + (static_cast<int64_t>(tok) * a.Hq + w.h * G + R % G) * D, c, 1.f);
+                x = four_of<KIND>(static_cast<const float*>(a.q) + (static_cast<int64_t>(tok) * a.Hq + w.h * G + R % G) * D, c, make_float2(1.f, 1.f));
             }
             reinterpret_cast<float4*>(s.q[r])[c] = x;
         }

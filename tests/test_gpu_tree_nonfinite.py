@@ -78,3 +78,40 @@ def test_leading_scores_of_minus_infinity_weigh_nothing(swa, leading, kind):
     got = c.run(swa)
     assert np.isnan(f64(got[0])[routed][..., 3]).all() and np.isfinite(f64(got[1])).all()
     c.check(got, want)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("case", ["zero rows of 255", "keys of 0", "a key of 255"])
+def test_exponent_bytes_mean_the_same_in_rows_that_are_computed_again(swa, case, d):
+    """2^(byte - 127) for every byte, with and without a neighbour whose NaN has a row computed again."""
+    base, W = 300, 60
+    c = Case([30], [base], 4, 2, d, 16, "e4m3", W, routed=0.25, seed=43,
+             scale={"zero rows of 255": None, "keys of 0": 2.0 ** 18, "a key of 255": 1.0}[case])
+    page_of = lambda j: (c.table[0, j // 16], j % 16)   # noqa: E731
+    codes = [p.view(torch.uint8) for p in c.pages]
+    if case == "zero rows of 255":   # 0 times 2^128
+        for which, j in ((0, 295), (1, 296), (0, 20), (1, 21)):
+            p, s = page_of(j)
+            codes[which][p, s] = 0
+            c.exps[which][p, :, s] = 255
+    elif case == "keys of 0":
+        c.exps[0][:] = 0
+        c.q = torch.ldexp(c.q.double(), torch.tensor(100.0).cuda()).to(c.dtype)
+    else:
+        p, s = page_of(297)
+        codes[0][p, s] = torch.randint(0, 8, codes[0][p, s].shape, dtype=torch.uint8, device="cuda",
+                                       generator=torch.Generator("cuda").manual_seed(1))   # up to 7 * 2^-9
+        c.exps[0][p, :, s] = 255
+        c.q = torch.ldexp(c.q.double(), torch.tensor(-123.0).cuda()).to(c.dtype)
+    values(c)
+    c.check(c.run(swa))
+    put(c, 1, 0, 50, np.nan)   # read by routed rows alone
+    values(c)
+    with np.errstate(invalid="ignore"):
+        want = list(c.reference())
+    routed = c.gate[:30] != 0
+    assert routed.any() and not routed.all()
+    want[1][routed] = np.nan
+    got = c.run(swa)
+    assert np.isnan(f64(got[0])[routed][..., 3]).all()
+    c.check(got, want)
