@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kMaxTree) tree_plan_kernel(const __grid_consta
     __syncthreads();
     bad = s_bad != 0;
     int n = bad ? 0 : after - first;
-    if (n > 0 && len != 0 && (n > kMaxTree || len < n || len > (a.max_pages << a.page_lg))) bad = true;
+    if (!bad && len != 0 && (n > kMaxTree || len < n || len > (a.max_pages << a.page_lg))) bad = true;   // with or without drafts
     if (bad || len == 0) n = 0;   // an empty slot has no tokens to look at
     const int base = len - n;
 

@@ -115,3 +115,14 @@ def test_exponent_bytes_mean_the_same_in_rows_that_are_computed_again(swa, case,
     got = c.run(swa)
     assert np.isnan(f64(got[0])[routed][..., 3]).all()
     c.check(got, want)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_a_bad_length_of_a_sequence_without_drafts_is_reported(swa, kind):
+    c = Case([6, 0, 9], [50, 30, 40], 2, 1, 64, 16, kind, 32, seed=44)
+    want = c.reference()
+    for length, status in ((-1, 1), (c.table.shape[1] * 16 + 1, 1), (-2 ** 31, 1), (0, 0), (c.table.shape[1] * 16, 0)):
+        c.lens[1] = length
+        got = c.run(swa)
+        assert swa.get_device_error() == status, length
+        c.check(got, want)
