@@ -1128,7 +1128,7 @@ int swiattn_accept_tree(void* k_pages, void* v_pages, uint8_t* k_exp, uint8_t* v
     if (ok != SWIATTN_OK) return ok;
     const int64_t n = 4 * (int64_t)B;   // several blocks read what one of them would have overwritten
     if (overlap(lens_out, n, seq_lens, n) || overlap(lens_out, n, leaf, n) || overlap(lens_out, n, starts, n + 4) ||
-        overlap(lens_out, n, block_table, n * max_pages))
+        overlap(lens_out, n, block_table, n * max_pages) || overlap(lens_out, n, parents, 4 * (int64_t)T))
         return SWIATTN_EINVAL;
     DeviceInfo di;
     if (!device_info(di)) return SWIATTN_ECUDA;
