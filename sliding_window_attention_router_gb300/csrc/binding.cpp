@@ -320,9 +320,11 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         }
         const bool interleaved = truth(a[5]);
         const float factor = number(a[6]);
-        if (some.numel()) {
+        // A tensor without elements (no tokens, no heads) has nothing to rotate; the other may.
+        const auto held = [](const Tokens& t) { return t.t && t.t->numel() > 0; };
+        if (held(in[0]) || held(in[1])) {
             const int rot = 2 * static_cast<int>(freq.numel());
-            const auto ptr = [](const Tokens& t) { return t.t ? t.t->data_ptr() : nullptr; };
+            const auto ptr = [&](const Tokens& t) { return held(t) ? t.t->data_ptr() : nullptr; };
             const double* w = static_cast<const double*>(freq.data_ptr());
             const char* where = axes ? (backward ? "swiattn_rope_axes_backward" : "swiattn_rope_axes") : backward ? "swiattn_rope_backward" : "swiattn_rope";
             call(where, index, [&](void* stream) {
