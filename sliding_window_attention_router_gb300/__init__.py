@@ -2,7 +2,8 @@
 
 Every function here marshals arguments to the C ABI declared in
 ``include/swiattn.h`` (same names, without the ``swiattn_`` prefix) and
-returns, some through the compiled module ``_binding`` next to it; all
+returns, some through the compiled module ``_binding`` next to it, or the same
+calls in Python where that is missing or of another PyTorch; all
 computation runs in the library's CUDA kernels.  PyTorch only
 provides device memory and the current stream.  There is no fallback: if the
 shared library is missing, the first call raises.
@@ -13,6 +14,7 @@ import ctypes
 import math
 import os
 import threading
+import warnings
 from typing import Optional
 
 import torch
@@ -555,14 +557,26 @@ _compiled = None
 
 
 def _calls():
-    """The compiled part of this binding (csrc/binding.cpp), which checks and makes the calls below."""
+    """What checks and makes the calls below: the compiled part of this binding (csrc/binding.cpp), or,
+    where that was not built or not against the installed PyTorch, the same in Python, which takes
+    longer on the host."""
     global _compiled
     if _compiled is None:
         lib = _load()
-        from . import _binding
-        _binding.bind({name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
-                       for name in EXPORTS}, SwiAttnError)
-        _compiled = _binding
+        from . import build
+        try:
+            if not build.same_torch():
+                raise ImportError("it was not built, or against another PyTorch")
+            from . import _binding
+            _binding.bind({name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+                           for name in EXPORTS}, SwiAttnError)
+            _compiled = _binding
+        except ImportError as e:
+            warnings.warn(f"the compiled binding is not used ({e}); its calls take longer on the host. "
+                          "Build it: python -c 'import __graft_entry__ as g; g.build()'", RuntimeWarning,
+                          stacklevel=3)
+            from . import _python_calls
+            _compiled = _python_calls
     return _compiled
 
 

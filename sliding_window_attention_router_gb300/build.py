@@ -13,7 +13,9 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,7 +24,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libswiattn.so")
 BINDING = os.path.join(PKG, "_binding.so")
-TORCH = os.path.join(BUILD, "torch_version")   # of the PyTorch that the binding was compiled against
+TORCH = os.path.join(BUILD, "torch_version")   # what the binding was compiled against
 
 SOURCES = ["swiattn_api.cu", "route.cu", "schedule.cu", "attn_prefill.cu", "attn_simt.cu", "decode.cu",
            "bwd_schedule.cu", "attn_bwd.cu", "bwd_simt.cu", "attn_dual.cu", "rope.cu",
@@ -40,15 +42,20 @@ def _nvcc() -> str:
     return cand
 
 
-def _deps_mtime() -> float:
-    paths = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    paths.append(os.path.join(INCLUDE, "swiattn.h"))
-    return max(os.path.getmtime(p) for p in paths)
+_BINDING_SOURCE = "binding.cpp"
+
+
+def _fresh(made: str, sources) -> bool:
+    """Whether `made` is there and no older than its sources in csrc and the header."""
+    paths = [os.path.join(CSRC, f) for f in sources] + [os.path.join(INCLUDE, "swiattn.h")]
+    return os.path.exists(made) and os.path.getmtime(made) >= max(os.path.getmtime(p) for p in paths)
 
 
 def _build_binding() -> None:
     """csrc/binding.cpp against the installed PyTorch, whose own libraries are loaded before it."""
     import torch
+    if os.path.exists(TORCH):   # until the new one is in place, none counts as built
+        os.remove(TORCH)
     root = os.path.dirname(torch.__file__)
     lib = os.path.join(root, "lib")
     tmp = BINDING + f".{os.getpid()}.tmp"
@@ -58,31 +65,49 @@ def _build_binding() -> None:
            *(f"-I{d}" for d in (INCLUDE, os.path.join(root, "include"),
                                 os.path.join(root, "include", "torch", "csrc", "api", "include"),
                                 os.path.join(cuda, "include"), sysconfig.get_path("include"))),
-           os.path.join(CSRC, "binding.cpp"), "-o", tmp, f"-L{lib}", "-ltorch_python", "-ltorch_cpu",
+           os.path.join(CSRC, _BINDING_SOURCE), "-o", tmp, f"-L{lib}", "-ltorch_python", "-ltorch_cpu",
            "-lc10", "-lc10_cuda"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"g++ failed on binding.cpp:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, BINDING)
     with open(TORCH, "w") as f:
-        f.write(torch.__version__)
+        f.write(_against())
 
 
-def _same_torch() -> bool:
+def _against() -> str:
     import torch
+    return f"PyTorch {torch.__version__}, Python {sysconfig.get_python_version()}"
+
+
+def same_torch() -> bool:
+    """Whether the binding was compiled against the installed PyTorch (and Python)."""
     try:
         with open(TORCH) as f:
-            return f.read() == torch.__version__
+            return f.read() == _against()
     except OSError:
         return False
 
 
+def _try_binding() -> None:
+    """Its calls have a form in Python, so that a machine without a C++ compiler or Python's headers
+    does without."""
+    try:
+        _build_binding()
+    except (RuntimeError, OSError) as e:
+        warnings.warn(f"the compiled binding was not built: {e}", RuntimeWarning, stacklevel=2)
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compile (if stale) and return the path of libswiattn.so."""
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime()
-                         for f in (LIB, BINDING)) and _same_torch():
+    binding = force or not (_fresh(BINDING, [_BINDING_SOURCE]) and same_torch())
+    library = force or not _fresh(LIB, [f for f in os.listdir(CSRC) if f != _BINDING_SOURCE])
+    if not binding and not library:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
+    if not library:
+        _try_binding()
+        return LIB
     nvcc = _nvcc()
     extra = ["-Xptxas", "-v"] if ptxas_info else []
 
@@ -97,9 +122,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        binding = ex.submit(_build_binding)
+        beside = ex.submit(_try_binding) if binding else None
         objs = list(ex.map(compile_one, SOURCES))
-        binding.result()
+        if beside:
+            beside.result()
     tmp = LIB + f".{os.getpid()}.tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -110,5 +136,4 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
 
 
 if __name__ == "__main__":
-    import sys
     print(build(force="--force" in sys.argv, verbose=True, ptxas_info="--ptxas" in sys.argv))
