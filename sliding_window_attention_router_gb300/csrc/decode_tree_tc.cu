@@ -507,9 +507,8 @@ __device__ bool converter(const TreeDecodeArgs& a, const Ctx<D, true>& c, int wh
     }
 }
 
-// Waits for a loader's last copies, whether it filled all or gave up: those whose tiles no
-// other warp will wait for, having given up itself, would else write to memory that is the
-// next CTA's by then.  (Where nobody gave up they are there, or about to be.)
+// Waits for a loader's last copies where any warp gave up: those whose tiles none waits for
+// any more would else write to memory that is the next CTA's by then.
 template <int S>
 __device__ void drain(uint64_t* full, uint32_t filled) {
     for (uint32_t back = 1; back <= S && back <= filled; ++back) {
@@ -858,6 +857,7 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) tree_tc_kernel(const __grid
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    uint32_t filled = 0;   // by a loader
     if (warp < 8) {
         warpgroup_reg_inc<kRegsSoftmax<E4M3>>();
         softmax<D, E4M3>(a, c, tmem, warp >> 2, warp & 3);
@@ -873,14 +873,10 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) tree_tc_kernel(const __grid
             if constexpr (E4M3) {
                 converter<D>(a, c, (warp - 12) / kLoaders, (warp - 12) % kLoaders);
             } else {
-                uint32_t filled = 0;
                 loader<D>(a, c, maps.of, box, warp - 12, filled);
-                drain<Z::kSlots>(&c.bar[c.kFull], filled);
             }
         } else if constexpr (E4M3) {
-            uint32_t filled = 0;
             raw_loader<D>(a, c, &maps.of[warp - 10], box, warp - 10, filled);
-            drain<Z::kOwnRaw>(&c.bar[c.kRawFull + (warp - 10) * Z::kOwnRaw], filled);
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     }
@@ -890,6 +886,10 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) tree_tc_kernel(const __grid
     if (warp == 8) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
+    } else if (*c.abort_flag && filled) {   // all have left their roles: it does not change any more
+        // (Behind each loader, aborted or not, e4m3 8 x 32K took 139.7 us, here 137.9.)
+        if constexpr (E4M3) drain<Z::kOwnRaw>(&c.bar[c.kRawFull + (warp - 10) * Z::kOwnRaw], filled);
+        else drain<Z::kSlots>(&c.bar[c.kFull], filled);
     }
 }
 

@@ -8,8 +8,7 @@ import re
 import pytest
 
 CSRC = pathlib.Path(__file__).parent.parent / "sliding_window_attention_router_gb300" / "csrc"
-ROLES = {"decode_tree_tc.cu": ("loader", "raw_loader"), "attn_prefill.cu": ("producer",), "attn_dual.cu": ("producer",),
-         "attn_bwd.cu": ("producer", "producer")}   # two kernels
+ROLES = {"attn_prefill.cu": 1, "attn_dual.cu": 1, "attn_bwd.cu": 2}   # kernels of each
 
 
 def body(text, at):
@@ -21,16 +20,34 @@ def body(text, at):
     return text[at:i]
 
 
-@pytest.mark.parametrize("name", sorted(ROLES))
-def test_a_copying_warp_waits_for_its_last_copies_however_it_left(name):
+def kernel_of(name):
     text = re.sub(r"//[^\n]*", "", (CSRC / name).read_text())
-    kernel = text[text.index("__global__"):]
-    for role in set(ROLES[name]):
-        calls = list(re.finditer(rf"(?<![\w]){role}(<[^;(]*>)?\((?!const )", kernel))   # and not its definition
-        assert len(calls) == ROLES[name].count(role)
-        for call in calls:
-            before = kernel[:call.start()].rstrip()
-            assert before[-1] in ";{}", f"{name}: what follows {role} depends on its result"
-            after = body(kernel, call.start())
-            waits = re.findall(r"drain\w*(?:<[^;(]*>)?\(", after.split(";", 1)[1])
-            assert waits, f"{name}: {role} leaves without waiting for its copies"
+    return text[text.index("__global__"):]
+
+
+def calls_of(kernel, role):
+    """Its calls, not its definition."""
+    return list(re.finditer(rf"(?<![\w]){role}(<[^;(]*>)?\((?!const )", kernel))
+
+
+@pytest.mark.parametrize("name", sorted(ROLES))
+def test_a_producer_waits_for_its_last_copies_however_it_left(name):
+    kernel = kernel_of(name)
+    calls = calls_of(kernel, "producer")
+    assert len(calls) == ROLES[name]
+    for call in calls:
+        assert kernel[:call.start()].rstrip()[-1] in ";{}", "what follows depends on its result"
+        after = body(kernel, call.start())
+        assert re.search(r"drain\w*\(", after.split(";", 1)[1]), "it leaves without waiting for its copies"
+
+
+def test_tree_loaders_wait_for_their_last_copies_when_any_warp_gave_up():
+    """Behind the last barrier, where the flag that any warp raises is final, and not by what the loader
+    itself returned."""
+    kernel = kernel_of("decode_tree_tc.cu")
+    for role in ("loader", "raw_loader"):
+        (call,) = calls_of(kernel, role)
+        assert kernel[:call.start()].rstrip()[-1] in ";{}" and "filled)" in kernel[call.start():].split(";", 1)[0]
+    end = body(kernel, kernel.rindex("__syncthreads();"))
+    assert re.search(r"if \(\*c\.abort_flag && filled\) \{\s*if constexpr \(E4M3\) drain<Z::kOwnRaw>\(&c\.bar\[c\.kRawFull"
+                     r"[^;]*filled\);\s*else drain<Z::kSlots>\(&c\.bar\[c\.kFull\], filled\);", end)
