@@ -479,7 +479,11 @@ int swiattn_decode_paged_e4m3(const void* q, const void* k_pages, const void* v_
                               size_t workspace_bytes, void* stream);
 
 /* Bytes of device workspace swiattn_decode_tree needs for these sizes (0 for
- * invalid sizes). */
+ * invalid sizes).  Most of them are partial results, for bf16 256 rows of d + 2
+ * floats for each of 152 CTAs and for each key head's tile of 128 rows of a
+ * sequence (two tiles more a sequence than its rows fill), however few rows it
+ * has: at d = 128 16 sequences of 16 drafts with 16/16 heads take 88 MiB, 256 of
+ * 8 drafts 1.07 GiB, 1024 of 4 drafts 4.1 GiB. */
 size_t swiattn_decode_tree_workspace(int T, int B, int Hq, int Hkv, int d, int dtype);
 
 /* Attention of drafted tokens over a paged cache, for verifying several tokens of
@@ -601,8 +605,8 @@ const char* swiattn_status_string(int status);
 /* Timing hook.  When both are non-NULL, every later swiattn_prefill,
  * swiattn_decode, swiattn_dual_branch, swiattn_prefill_backward, swiattn_route,
  * swiattn_route_backward, swiattn_rope(_backward), swiattn_rope_axes(_backward),
- * swiattn_append_paged(_at), swiattn_decode_paged_e4m3 and swiattn_decode_tree call
- * records `start` (a cudaEvent_t passed as
+ * swiattn_append_paged(_at), swiattn_decode_paged_e4m3, swiattn_decode_tree,
+ * swiattn_accept_tree and swiattn_fork_paged call records `start` (a cudaEvent_t passed as
  * void*) on its stream immediately before launching its dominant kernel (the
  * attention kernel, the decode split kernel, the tree attention's product kernel, the backward's two attention
  * kernels, dK/dV then dQ, the router GEMV, or the router backward's three

@@ -6,9 +6,10 @@
 // bytes: a tile of 128 keys is 64 KiB (d = 128), 1466 ns of an SM's share of the copy
 // bandwidth, against 1536 tensor cycles (0.8 us) and about as many of the softmax,
 // overlapped: S of the next tile is computed while the weights of this one are.  16
-// sequences of 32K, 16 key heads of one row tile, 4.03 GB: 605 us, 98 % of the copy
-// rate.  33 ragged trees (d = 64, 408 units, 36 key tiles a CTA): 89 us, 20 %, 1.7 us a
-// tile of 128 rows, which is the chain of its softmax, and not its bytes (0.7 us).
+// sequences of 32K, 16 key heads of one row tile, 4.03 GB: 605 to 618 us by the box, 96
+// to 98 % of the copy rate (without a pause, under the power cap, 644 to 671).  33
+// ragged trees (d = 64, 408 units, 36 key tiles a CTA): 88 us, 20 %, 1.7 us a tile of
+// 128 rows, which is the chain of its softmax, and not its bytes (0.7 us).
 // Over e4m3 pages it is bound by instructions: 8 sequences of 32K with 4 key heads of
 // 128 rows, 273 MB: 138 us (29 %); a tile's bytes would take 733 ns, its conversion and
 // its softmax, on the same four schedulers, are about 2600 cycles each.

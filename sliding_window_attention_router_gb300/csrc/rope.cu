@@ -227,8 +227,8 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
 }
 
 // GIVEN: positions on several axes, or an append's tokens with positions of their own
-// (a kernel apart, as its registers cost the others: e4m3 append of 32K tokens 122 us
-// would be 125).
+// (a kernel apart, as its registers cost the others: e4m3 append of 32K tokens, in turn on
+// one box, 122 us without them and 125 with).
 template <typename T, int MODE, int D, bool GIVEN>
 __global__ void __launch_bounds__(kMaxThreads) rotate_kernel(const __grid_constant__ RotateArgs a) {
     constexpr bool kStored = MODE >= kAppend;   // k and v go to pages
